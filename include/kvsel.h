@@ -87,9 +87,13 @@ enum { KVSEL_WO_GROUP_SUM = 0, KVSEL_WO_PER_HEAD = 1 };
  * distance its App. C.3 compares.  L2 is computed through the d x d Gram matrix
  * W_h^T W_h (32x fewer flops at D = 4096); group-sum W_O reading only. */
 enum { KVSEL_NORM_L1 = 0, KVSEL_NORM_L2 = 1 };
-enum { KVSEL_LAYOUT_CONTIGUOUS = 0, KVSEL_LAYOUT_PAGED = 1 };
+/* PACKED (kvsel_attend only): rows [n_rows][head_dim], stride_tok apart, the segments placed by
+ * an offsets array: what kvsel_compact and kvsel_run_layer write. */
+enum { KVSEL_LAYOUT_CONTIGUOUS = 0, KVSEL_LAYOUT_PAGED = 1, KVSEL_LAYOUT_PACKED = 2 };
 
 #define KVSEL_MAX_BATCH 128
+#define KVSEL_MAX_ATTN_BATCH 1024  /* kvsel_attend, kvsel_evict_append */
+#define KVSEL_MAX_ATTN_GROUP 128   /* kvsel_attend */
 
 /* ---- parameters --------------------------------------------------------------------- */
 typedef struct kvsel_params {
@@ -317,7 +321,7 @@ enum {
 };
 
 /* Diagnostics: while `events` is non-NULL, each kernel launched by this thread's
- * subsequent calls is bracketed by cudaEventRecord(events[2*stage]) and
+ * subsequent calls (kvsel_attend and kvsel_evict_append excepted) is bracketed by cudaEventRecord(events[2*stage]) and
  * cudaEventRecord(events[2*stage + 1]) on the launch stream (NULL entries skipped).
  * `events` is a host array of 2*KVSEL_STAGE_COUNT cudaEvent_t created by the caller and
  * must stay valid until the hook is cleared with NULL.  No effect on results. */
@@ -401,6 +405,120 @@ int kvsel_perturbation_workspace_size(const kvsel_params* p, size_t* bytes);
 int kvsel_perturbation(const kvsel_params* p, const void* q, const kvsel_kv* kv, const void* w_o, const int32_t* idx,
                        const int32_t* counts, const int64_t* offsets, float* out, void* ws, size_t ws_bytes,
                        void* stream);
+
+/* ---- the cache in use: attention of new tokens --------------------------------------- */
+
+/* Attention of new tokens over a cache, and the running weight of every cached row.
+ *
+ * A segment is the cache of one (request, KV head); it has n rows, the last m of which are the
+ * m new tokens' own (append them first, e.g. with kvsel_evict_append).  Token t sits at row
+ * r = n - m + t and sees row j when
+ *     j <= r  and  (window == 0  or  j > r - window  or  j < n_sink)      causal = 1
+ *     j < n                                                              causal = 0
+ * Rows count as positions: in a cache that has evicted, "window" means the last `window` rows. */
+typedef struct kvsel_attn_params {
+  int32_t h_kv;          /* KV heads, 1..64                                                  */
+  int32_t group;         /* query heads per KV head, 1..KVSEL_MAX_ATTN_GROUP; query head of
+                            member g of KV head h: h * group + g                             */
+  int32_t head_dim;      /* must be 128                                                      */
+  int32_t batch;         /* requests, 1..KVSEL_MAX_ATTN_BATCH                                */
+  int32_t n_new;         /* new tokens of a request at most, 1..2^20 (q, out, lse hold as
+                            many rows per query head); 1 = a decode step                     */
+  int32_t max_len;       /* rows of a segment at most, 1..2^30: a bound on lens; paged:
+                            max_blocks * block_size must cover it; contiguous: every segment
+                            has memory for as many rows                                      */
+  int32_t causal;        /* 1: the rule above; 0: every token sees all n rows (the new tokens
+                            are not in the cache, e.g. one that kvsel_compact has written)   */
+  int32_t window;        /* rows that a token sees back from its own, its own included;
+                            0 = all.  Needs causal = 1                                       */
+  int32_t n_sink;        /* with a window: the first n_sink rows stay visible                */
+  float scale;           /* logit scale; 0 = 1/sqrt(head_dim)                                */
+  int32_t lens_per_head; /* 0: lens [batch]; 1: lens [batch*h_kv] (always so for PACKED)     */
+  int64_t q_stride_req, q_stride_head, q_stride_tok;   /* q element (b, query head, t, c), in
+                            elements, multiples of 8, c contiguous; all three 0 =
+                            [batch][h_kv*group][n_new][head_dim]                             */
+  int64_t o_stride_req, o_stride_head, o_stride_tok;   /* out, likewise                      */
+  int64_t n_rows;        /* PACKED: rows of k and v                                          */
+  int64_t acc_stride;    /* acc: entries between segments, >= max_len                        */
+  uint64_t wait_cycles;  /* as kvsel_params.wait_cycles                                      */
+} kvsel_attn_params;
+
+/* Bytes of device workspace that kvsel_attend needs on the current device (with_acc: the call
+ * passes acc).  Host-only. */
+int kvsel_attend_workspace_size(const kvsel_attn_params* p, int with_acc, size_t* bytes);
+
+/* out[b][hq][t] = sum_j w_j v_j with w = softmax_j(scale * <q[b][hq][t], k_j>) over the rows that
+ * token t sees; lse the logarithm of that softmax's denominator (natural, of the scaled
+ * logits); acc[seg][j] += sum of w_j over the request's new tokens and the group's heads.
+ *   q        device bf16, strides above, 16-byte aligned
+ *   kv       K/V view: contiguous, paged, or PACKED with `offsets`
+ *   lens     device int32 [batch] or [batch*h_kv]: n of every segment, new tokens included.
+ *            Read on the device, so that a captured call follows the lengths; kvsel_select's
+ *            counts serve directly
+ *   new_lens device int32 [batch], m of every request (0..n_new), or NULL = n_new for all
+ *   offsets  device int64 [batch*h_kv], first row of every segment (PACKED), else NULL
+ *   out      device bf16, strides above, 16-byte aligned; lse device fp32
+ *            [batch][h_kv*group][n_new] or NULL.  Rows of tokens m..n_new-1 are left as they are.
+ *            A token that sees no row (n < m, or an empty segment) gets zeros and -inf
+ *   acc      device fp32 [batch*h_kv][acc_stride] or NULL; entries 0..n-1 of a segment are added
+ *            to, the others left as they are
+ *   ws       workspace of kvsel_attend_workspace_size bytes, 256-byte aligned, its status word
+ *            zeroed by kvsel_workspace_init; one per call that may run at the same time (two
+ *            graphs that replay at the same time included)
+ * Softmax statistics and sums are fp32; out is rounded once to bf16.  Two calls with the same
+ * inputs give the same bits on the same kind of device.  K/V rows that no new token sees may
+ * hold anything and pages without a visible row are not looked up; rows that some token of
+ * the request sees must be finite.  A length, offset or block-table entry out of range is
+ * recorded in the status word (KVSEL_EDEVICE through kvsel_get_device_status): lengths are
+ * clamped, a segment at a bad offset counts as empty, a row in a bad block as zeros. */
+int kvsel_attend(const kvsel_attn_params* p, const void* q, const kvsel_kv* kv, const int32_t* lens,
+                 const int32_t* new_lens, const int64_t* offsets, void* out, float* lse, float* acc, void* ws,
+                 size_t ws_bytes, void* stream);
+
+/* ---- the cache in use: eviction by accumulated weight --------------------------------- */
+
+/* A cache that stays within `budget` rows per segment while tokens keep arriving: before new
+ * tokens enter, the rows with the least accumulated attention weight (kvsel_attend's acc) leave.
+ * Per segment the caller keeps, on the device: lens (rows in use), seen (tokens that have
+ * entered so far, evicted ones included), pos [capacity] (token position of each row) and acc
+ * [capacity].  After a compaction: pos = the kept idx, acc = their scores, seen = n_ctx. */
+typedef struct kvsel_evict_params {
+  int32_t h_kv;          /* KV heads, 1..64                                                  */
+  int32_t head_dim;      /* must be 128                                                      */
+  int32_t batch;         /* requests, 1..KVSEL_MAX_ATTN_BATCH                                */
+  int32_t n_new;         /* new rows of a segment at most; 0 = evict only                    */
+  int32_t capacity;      /* rows that a segment has memory for (K/V, pos, acc), 1..2^30      */
+  int32_t budget;        /* rows of a segment after the call at most, <= capacity            */
+  int32_t n_sink;        /* positions below n_sink always stay                               */
+  int32_t n_recent;      /* the most recent n_recent positions, the new ones included, always
+                            stay.  n_sink + max(n_recent, n_new) <= budget, else KVSEL_EBUDGET */
+  int64_t new_stride_req, new_stride_head, new_stride_tok;   /* k_new and v_new element (b, h, t,
+                            c), in elements, multiples of 8; all three 0 =
+                            [batch][h_kv][n_new][head_dim]                                   */
+} kvsel_evict_params;
+
+/* Bytes of device workspace that kvsel_evict_append needs.  Host-only. */
+int kvsel_evict_append_workspace_size(const kvsel_evict_params* p, size_t* bytes);
+
+/* Make room for m new rows in every segment and append them.  With n = lens[seg] rows,
+ * keep = min(n, budget - m) of them stay: protected positions first (pos < n_sink or
+ * pos >= seen + m - n_recent), then by acc descending, ties by row ascending (NaN ranks
+ * last).  Evicted rows below `keep` are refilled by the kept rows at or behind `keep`, both in
+ * ascending order, with their pos and acc; no other row moves.  New row i goes to row
+ * keep + i with pos = seen + i and acc = 0; then lens = keep + m and seen += m.  Rows, pos and
+ * acc at or behind the new lens are left as they are.  K and V rows are copied bit-exact.
+ *   kv       contiguous or paged, written in place; no two segments may share memory
+ *   lens, seen  device int32 [batch*h_kv], read and written
+ *   pos, acc    device int32 / fp32 [batch*h_kv][capacity], read and written
+ *   k_new, v_new  device bf16, strides above, 16-byte aligned; NULL when n_new = 0
+ *   new_lens device int32 [batch], m of every request (0..n_new), or NULL = n_new for all
+ *   ws       workspace of kvsel_evict_append_workspace_size bytes, 256-byte aligned, as
+ *            kvsel_attend's (the two calls may share one)
+ * A length out of range is clamped, a row in a block out of range is not copied; both are
+ * recorded in the status word. */
+int kvsel_evict_append(const kvsel_evict_params* p, const kvsel_kv* kv, int32_t* lens, int32_t* seen, int32_t* pos,
+                       float* acc, const void* k_new, const void* v_new, const int32_t* new_lens, void* ws,
+                       size_t ws_bytes, void* stream);
 
 /* Static description of an error code. */
 const char* kvsel_strerror(int code);

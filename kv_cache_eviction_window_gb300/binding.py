@@ -28,7 +28,7 @@ POOL = {"none": 0, "max": 1, "avg": 2}
 BUDGET = {"head": 0, "layer": 1, "anchor": 2}
 WO_MODE = {"group_sum": 0, "per_head": 1}
 VALUE_NORM = {"l1": 0, "l2": 1}
-LAYOUT_CONTIGUOUS, LAYOUT_PAGED = 0, 1
+LAYOUT_CONTIGUOUS, LAYOUT_PAGED, LAYOUT_PACKED = 0, 1, 2
 MAX_BATCH = 128
 
 EXPORTS = ("kvsel_workspace_size", "kvsel_output_size", "kvsel_workspace_init", "kvsel_score",
@@ -36,7 +36,9 @@ EXPORTS = ("kvsel_workspace_size", "kvsel_output_size", "kvsel_workspace_init", 
            "kvsel_set_stage_events", "kvsel_strerror", "kvsel_version",
            "kvsel_score_noalloc", "kvsel_launch_count", "kvsel_head_scores", "kvsel_anchor_project",
            "kvsel_run_anchors", "kvsel_perturbation_workspace_size", "kvsel_perturbation",
-           "kvsel_query_agnostic_split", "kvsel_prepared_w_o_size", "kvsel_prepare_w_o")
+           "kvsel_query_agnostic_split", "kvsel_prepared_w_o_size", "kvsel_prepare_w_o",
+           "kvsel_attend_workspace_size", "kvsel_attend", "kvsel_evict_append_workspace_size",
+           "kvsel_evict_append")
 NOALLOC_SCRATCH_BYTES = 16 << 20
 STAGES = ("rowstats", "keysum", "wbar", "vnorm", "finalize", "select", "compact", "project", "perturb")
 
@@ -76,6 +78,26 @@ class kvsel_kv(ctypes.Structure):
     ]
 
 
+class kvsel_attn_params(ctypes.Structure):
+    _fields_ = [
+        ("h_kv", ctypes.c_int32), ("group", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("batch", ctypes.c_int32),
+        ("n_new", ctypes.c_int32), ("max_len", ctypes.c_int32), ("causal", ctypes.c_int32), ("window", ctypes.c_int32),
+        ("n_sink", ctypes.c_int32), ("scale", ctypes.c_float), ("lens_per_head", ctypes.c_int32),
+        ("q_stride_req", ctypes.c_int64), ("q_stride_head", ctypes.c_int64), ("q_stride_tok", ctypes.c_int64),
+        ("o_stride_req", ctypes.c_int64), ("o_stride_head", ctypes.c_int64), ("o_stride_tok", ctypes.c_int64),
+        ("n_rows", ctypes.c_int64), ("acc_stride", ctypes.c_int64), ("wait_cycles", ctypes.c_uint64),
+    ]
+
+
+class kvsel_evict_params(ctypes.Structure):
+    _fields_ = [
+        ("h_kv", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("batch", ctypes.c_int32), ("n_new", ctypes.c_int32),
+        ("capacity", ctypes.c_int32), ("budget", ctypes.c_int32), ("n_sink", ctypes.c_int32),
+        ("n_recent", ctypes.c_int32),
+        ("new_stride_req", ctypes.c_int64), ("new_stride_head", ctypes.c_int64), ("new_stride_tok", ctypes.c_int64),
+    ]
+
+
 _lib = None
 
 
@@ -92,6 +114,7 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
     except OSError as e:  # pragma: no cover - depends on the machine
         raise KvselUnavailable(f"cannot load {p}: {e}") from e
     P, K = ctypes.POINTER(kvsel_params), ctypes.POINTER(kvsel_kv)
+    PA, PE = ctypes.POINTER(kvsel_attn_params), ctypes.POINTER(kvsel_evict_params)
     vp, sz, i64p = ctypes.c_void_p, ctypes.c_size_t, ctypes.POINTER(ctypes.c_int64)
     sig = {
         "kvsel_workspace_size": ([P, ctypes.POINTER(sz)], ctypes.c_int),
@@ -115,6 +138,10 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
                                        ctypes.c_int),
         "kvsel_anchor_project": ([P, K] + [vp] * 10 + [sz, vp], ctypes.c_int),
         "kvsel_run_anchors": ([P, vp, K] + [vp] * 12 + [sz, vp], ctypes.c_int),
+        "kvsel_attend_workspace_size": ([PA, ctypes.c_int, ctypes.POINTER(sz)], ctypes.c_int),
+        "kvsel_attend": ([PA, vp, K] + [vp] * 7 + [sz, vp], ctypes.c_int),
+        "kvsel_evict_append_workspace_size": ([PE, ctypes.POINTER(sz)], ctypes.c_int),
+        "kvsel_evict_append": ([PE, K] + [vp] * 8 + [sz, vp], ctypes.c_int),
         "kvsel_perturbation_workspace_size": ([P, ctypes.POINTER(sz)], ctypes.c_int),
         "kvsel_perturbation": ([P, vp, K, vp, vp, vp, vp, vp, vp, sz, vp], ctypes.c_int),
     }
@@ -171,6 +198,27 @@ def params_from_workload(wl, n_ctx_per_req: Optional[Sequence[int]] = None, **ov
     return make_params(**kw)
 
 
+def make_attn_params(*, h_kv: int, group: int, batch: int, max_len: int, n_new: int = 1, head_dim: int = 128,
+                     causal: bool = True, window: int = 0, n_sink: int = 0, scale: float = 0.0,
+                     lens_per_head: bool = False, q_strides: Sequence[int] = (0, 0, 0),
+                     o_strides: Sequence[int] = (0, 0, 0), n_rows: int = 0, acc_stride: int = 0,
+                     wait_cycles: int = 0) -> kvsel_attn_params:
+    """q_strides / o_strides: (request, query head, token) in elements; zeros = dense
+    [batch][h_kv*group][n_new][head_dim]."""
+    return kvsel_attn_params(h_kv, group, head_dim, batch, n_new, max_len, int(bool(causal)), window, n_sink, scale,
+                             int(bool(lens_per_head)), *[int(x) for x in q_strides], *[int(x) for x in o_strides],
+                             n_rows, acc_stride, int(wait_cycles))
+
+
+def make_evict_params(*, h_kv: int, batch: int, capacity: int, budget: int, n_new: int = 1, head_dim: int = 128,
+                      n_sink: int = 4, n_recent: int = 32,
+                      new_strides: Sequence[int] = (0, 0, 0)) -> kvsel_evict_params:
+    """new_strides: (request, KV head, token) of k_new and v_new in elements; zeros = dense
+    [batch][h_kv][n_new][head_dim]."""
+    return kvsel_evict_params(h_kv, head_dim, batch, n_new, capacity, budget, n_sink, n_recent,
+                              *[int(x) for x in new_strides])
+
+
 def make_kv_contiguous(k, v, *, stride_req: int = 0) -> kvsel_kv:
     """K/V tensors [H][n][d] (one request) or [B][H][n][d] (bf16, CUDA)."""
     kv = kvsel_kv()
@@ -191,6 +239,16 @@ def make_kv_paged(k_pool, v_pool, block_table) -> kvsel_kv:
     kv.block_size = k_pool.shape[1]
     kv.max_blocks = block_table.shape[1]
     kv.num_blocks = k_pool.shape[0]
+    return kv
+
+
+def make_kv_packed(k, v) -> kvsel_kv:
+    """Rows [n_rows][d] bf16 (CUDA) of segments placed by an offsets array, as kvsel_compact
+    writes them (kvsel_attend only)."""
+    kv = kvsel_kv()
+    kv.k, kv.v = _ptr(k), _ptr(v)
+    kv.layout = LAYOUT_PACKED
+    kv.stride_tok = k.stride(0)
     return kv
 
 
@@ -361,6 +419,36 @@ def kvsel_perturbation(params, q, kv: kvsel_kv, w_o, idx, counts, offsets, out, 
     _check(load().kvsel_perturbation(ctypes.byref(params), _ptr(q), ctypes.byref(kv), _ptr(w_o), _ptr(idx),
                                      _ptr(counts), _ptr(offsets), _ptr(out), _ptr(ws), ws.numel() * ws.element_size(),
                                      _stream(stream)), "kvsel_perturbation")
+
+
+def kvsel_attend_workspace_size(params: kvsel_attn_params, acc: bool = False) -> int:
+    out = ctypes.c_size_t()
+    _check(load().kvsel_attend_workspace_size(ctypes.byref(params), int(bool(acc)), ctypes.byref(out)),
+           "kvsel_attend_workspace_size")
+    return out.value
+
+
+def kvsel_attend(params: kvsel_attn_params, q, kv: kvsel_kv, lens, out, ws, new_lens=None, offsets=None, lse=None,
+                 acc=None, stream=None) -> None:
+    """Attention of new tokens over the cache; with acc every cached row's weight is added."""
+    _check(load().kvsel_attend(ctypes.byref(params), _ptr(q), ctypes.byref(kv), _ptr(lens), _ptr(new_lens),
+                               _ptr(offsets), _ptr(out), _ptr(lse), _ptr(acc), _ptr(ws),
+                               ws.numel() * ws.element_size(), _stream(stream)), "kvsel_attend")
+
+
+def kvsel_evict_append_workspace_size(params: kvsel_evict_params) -> int:
+    out = ctypes.c_size_t()
+    _check(load().kvsel_evict_append_workspace_size(ctypes.byref(params), ctypes.byref(out)),
+           "kvsel_evict_append_workspace_size")
+    return out.value
+
+
+def kvsel_evict_append(params: kvsel_evict_params, kv: kvsel_kv, lens, seen, pos, acc, k_new, v_new, ws,
+                       new_lens=None, stream=None) -> None:
+    """Evict by accumulated weight until the new rows fit the budget, then append them."""
+    _check(load().kvsel_evict_append(ctypes.byref(params), ctypes.byref(kv), _ptr(lens), _ptr(seen), _ptr(pos),
+                                     _ptr(acc), _ptr(k_new), _ptr(v_new), _ptr(new_lens), _ptr(ws),
+                                     ws.numel() * ws.element_size(), _stream(stream)), "kvsel_evict_append")
 
 
 def kvsel_get_device_status(ws, stream=None) -> int:

@@ -1,0 +1,219 @@
+// Shared by the kernels of kvsel_attend: the arguments, the key range that a block of query
+// rows sees, and the division of all (block, key tile) pairs over the grid.
+//
+// Query rows of a segment (request b, KV head h) are numbered r = t * G + g: token t of the
+// request's new tokens, member g of the head's group.  An item is a block of TR rows of one
+// segment; it is worked through in tiles of TK cached rows.
+#pragma once
+#include "internal.cuh"
+
+namespace kvsel {
+
+struct AttnArgs {
+  int B, H, G, m;                 // requests, KV heads, group, new tokens of a request at most
+  int max_len;                    // rows of a segment at most
+  int causal, window, n_sink;
+  int per_head;                   // lens [B*H] instead of [B]
+  float s2;                       // logit scale * log2(e)
+  const int32_t* lens;
+  const int32_t* new_lens;        // [B] or null: m for every request
+  const int64_t* offsets;         // packed cache: first row of every segment
+  long long n_rows;               // packed cache: rows in all
+  const uint16_t* q;
+  long long q_req, q_head, q_tok;
+  uint16_t* out;
+  long long o_req, o_head, o_tok;
+  float* lse;                     // [B][H*G][m] natural log, or null
+  float* lse2;                    // [B][H][m*G] log2 units, for the weights, or null
+  float* acc;                     // [B*H][acc_stride] or null
+  long long acc_stride;
+  KvSource src;
+  const uint16_t* k;
+  const uint16_t* v;
+  long long stride_req, stride_head, stride_tok;
+  int rt;                         // row blocks (items) per segment
+  // partial results of items that several CTAs share: two slots per CTA
+  float* part_o;                  // [2 * grid][rows][128]
+  float2* part_ml;                // [2 * grid][rows]: reference (log2 units) and sum
+  int4* rec;                      // [grid]: item that starts here and goes on, CTAs that follow
+  WaitCtl wc;
+};
+
+// Rows of segment (b, h) and new tokens of request b, as the caller's device arrays give them;
+// values out of range are flagged and clamped.
+struct SegLen {
+  int n, m;
+  long long row0;                 // packed cache: first row
+};
+__device__ __forceinline__ SegLen seg_len(const AttnArgs& a, int b, int h) {
+  SegLen s;
+  const int raw = __ldg(a.lens + (a.per_head ? b * a.H + h : b));
+  s.n = min(max(raw, 0), a.max_len);
+  const int mr = a.new_lens ? __ldg(a.new_lens + b) : a.m;
+  s.m = min(max(mr, 0), a.m);
+  bool bad = s.n != raw || s.m != mr;
+  s.row0 = 0;
+  if (a.offsets) {
+    s.row0 = __ldg(a.offsets + b * a.H + h);
+    if (s.row0 < 0 || s.row0 + s.n > a.n_rows) {
+      bad = true;
+      s.n = 0;
+      s.row0 = 0;
+    }
+  }
+  if (bad) atomicOr(a.wc.status, DEV_BAD_INDEX);
+  return s;
+}
+
+// Key tiles of an item.  A row block sees [0, sink) and [lo, hi) of the cached rows (some row
+// of it does); tiles [0, ns) cover the first range, the others [lo, hi).  Where the two
+// meet, or without a window, lo = 0 and ns = 0.
+struct ItemRange {
+  int seg, b, h, rt;
+  int n, m;                       // cached rows, new tokens
+  int rows;                       // valid query rows of the block
+  int p0, p1;                     // cache row of the block's first and last token
+  int lo, hi, sink, ns, tiles;
+  long long row0;
+};
+template <int TR, int TK>
+__device__ __forceinline__ ItemRange item_range(const AttnArgs& a, int item) {
+  ItemRange x;
+  x.seg = item / a.rt;
+  x.rt = item - x.seg * a.rt;
+  x.b = x.seg / a.H;
+  x.h = x.seg - x.b * a.H;
+  const SegLen s = seg_len(a, x.b, x.h);
+  x.n = s.n;
+  x.m = s.m;
+  x.row0 = s.row0;
+  const int R = s.m * a.G, r0 = x.rt * TR;
+  x.rows = min(TR, R - r0);
+  x.lo = x.ns = x.sink = x.hi = x.tiles = x.p0 = x.p1 = 0;
+  if (x.rows <= 0) {
+    x.rows = 0;
+    return x;
+  }
+  if (a.causal) {
+    x.p0 = s.n - s.m + r0 / a.G;
+    x.p1 = s.n - s.m + (r0 + x.rows - 1) / a.G;
+    x.hi = max(0, x.p1 + 1);
+  } else {
+    x.p0 = x.p1 = s.n - 1;
+    x.hi = s.n;
+  }
+  if (a.window > 0) {
+    const int lo = max(0, x.p0 - a.window + 1);
+    // pages behind the window may be gone: a tile starts with the first page that is seen
+    const int al = a.src.paged ? lo - lo % a.src.block_size : lo;
+    const int sink = min(a.n_sink, x.hi);
+    const int ns = (sink + TK - 1) / TK;
+    if (lo > sink && al > ns * TK) {
+      x.lo = al;
+      x.sink = sink;
+      x.ns = ns;
+    }
+  }
+  // a block that sees nothing (fewer rows than new tokens) still has its empty result to write
+  x.tiles = max(1, x.ns + (x.hi - x.lo + TK - 1) / TK);
+  return x;
+}
+// First row of tile ti and the end of the rows that it covers.
+template <int TK>
+__device__ __forceinline__ void tile_rows(const ItemRange& x, int ti, int& j0, int& j1) {
+  if (ti < x.ns) {
+    j0 = ti * TK;
+    j1 = x.sink;
+  } else {
+    j0 = x.lo + (ti - x.ns) * TK;
+    j1 = x.hi;
+  }
+}
+
+// The share of CTA `cta` of the grid in all tiles of all items, in item order: tiles
+// [total * cta / grid, total * (cta + 1) / grid).  Lengths live on the device, so every CTA
+// adds up the items itself (a thread takes consecutive items, then a block-wide scan).
+struct Share {
+  long long total;
+  long long begin, end;           // this CTA's tiles
+  int grid;                       // CTAs with work: min(gridDim.x, total)
+  int item;                       // item of tile `begin`
+  long long item_base;            // its first tile
+};
+template <int TR, int TK, int THREADS>
+__device__ __forceinline__ Share share_of(const AttnArgs& a, int cta) {
+  __shared__ long long s_warp[THREADS / 32];
+  __shared__ long long s_base;
+  __shared__ int s_item;
+  const int items = a.B * a.H * a.rt;
+  const int per = (items + THREADS - 1) / THREADS;
+  const int i0 = min(items, static_cast<int>(threadIdx.x) * per), i1 = min(items, i0 + per);
+  long long sum = 0;
+  for (int i = i0; i < i1; ++i) sum += item_range<TR, TK>(a, i).tiles;
+  long long inc = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, inc, o);
+    if ((threadIdx.x & 31) >= o) inc += y;
+  }
+  if ((threadIdx.x & 31) == 31) s_warp[threadIdx.x >> 5] = inc;
+  __syncthreads();
+  long long before = inc - sum, total = 0;
+  for (int w = 0; w < THREADS / 32; ++w) {
+    if (w < static_cast<int>(threadIdx.x >> 5)) before += s_warp[w];
+    total += s_warp[w];
+  }
+  Share sh;
+  sh.total = total;
+  sh.grid = static_cast<int>(min(static_cast<long long>(gridDim.x), total));
+  sh.begin = sh.end = 0;
+  sh.item = 0;
+  sh.item_base = 0;
+  if (cta < sh.grid) {
+    sh.begin = total * cta / sh.grid;
+    sh.end = total * (cta + 1) / sh.grid;
+    if (sum > 0 && sh.begin >= before && sh.begin < before + sum) {
+      long long at = before;
+      int i = i0;
+      for (; i < i1; ++i) {
+        const int c = item_range<TR, TK>(a, i).tiles;
+        if (sh.begin < at + c) break;
+        at += c;
+      }
+      s_item = i;
+      s_base = at;
+    }
+  }
+  __syncthreads();
+  if (cta < sh.grid) {
+    sh.item = s_item;
+    sh.item_base = s_base;
+  }
+  return sh;
+}
+// The last CTA with a tile of an item that ends before tile `e`.
+__device__ __forceinline__ int last_cta(const Share& sh, long long e) {
+  return static_cast<int>((e * sh.grid - 1) / sh.total);
+}
+
+// whether row p sees cached row j (j < hi of its tile)
+__device__ __forceinline__ bool sees(const AttnArgs& a, int p, int j) {
+  if (!a.causal) return true;
+  return j <= p && (a.window <= 0 || j > p - a.window || j < a.n_sink);
+}
+// element offset of cached row j, or -1 (a block-table entry out of range)
+__device__ __forceinline__ long long row_elem(const AttnArgs& a, int b, int h, long long row0, int j) {
+  if (!a.src.paged)
+    return b * a.stride_req + h * a.stride_head + (row0 + static_cast<long long>(j)) * a.stride_tok;
+  const int bs = a.src.block_size;
+  const int pb = __ldg(a.src.block_table + static_cast<size_t>(b) * a.src.max_blocks + j / bs);
+  if (pb < 0 || pb >= a.src.num_blocks) return -1;
+  return ((static_cast<long long>(pb) * bs + (j % bs)) * a.H + h) * kHeadDim;
+}
+
+cudaError_t launch_attend_rows(const AttnArgs& a, int grid, cudaStream_t st);
+cudaError_t launch_attend_weights(const AttnArgs& a, cudaStream_t st);
+int attend_rows_tile();           // query rows per item of launch_attend_rows
+int attend_rows_ctas_per_sm();
+
+}  // namespace kvsel

@@ -1,0 +1,493 @@
+// Attention of a few query rows (single tokens, drafted tokens) over a long cache:
+//   out_r = sum_j p_rj v_j / sum_j p_rj,  p_rj = exp2(s2 * <q_r, k_j> - ref_r),
+// with the reference ref_r within 8 of the running maximum (in log2 units), so that the
+// accumulator is rescaled only when the maximum has grown by more than that; sums and
+// accumulators in fp32.
+//
+// Bound: HBM.  A cached row costs 512 B and 512 flop per query row, so with at most 16 rows
+// the tensor cores are idle most of the time and mma.sync m16n8k16, whose operands come
+// straight from registers, is enough: a tcgen05 tile would have 128 rows to fill.  Every warp
+// streams its own 16-row units of K and V through its own three-stage cp.async ring, without a
+// block-wide barrier inside an item, and keeps its own reference, sum and accumulator; the
+// four warps are merged once per item.  cp.async writes zeros for rows that no query row
+// sees, so nothing that lies behind a segment's end can reach a product.
+//
+// Items (16 query rows of one segment) are cut along the cache so that every CTA of the grid
+// gets the same number of tiles whatever the lengths are (share_of); the pieces of an item
+// that was cut are joined by attend_join_kernel, in cache order.
+#include <algorithm>
+
+#include "attend.cuh"
+
+namespace kvsel {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr int kTR = 16;                              // query rows per item
+constexpr int kUnit = 16;                            // cached rows per warp and step
+constexpr int kTK = kUnit * kWarps;                  // cached rows per tile
+constexpr int kStages = 3;
+constexpr int kUnitBytes = kUnit * 256;              // one side (K or V) of a unit
+constexpr int kStageBytes = 2 * kUnitBytes;
+constexpr int kOPad = 132;                           // floats per accumulator row when merging
+constexpr size_t kSmem = kWarps * kStages * kStageBytes;
+static_assert(kWarps * kTR * kOPad * 4 <= kSmem, "the merge reuses the ring");
+
+__device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void* src, bool live) {
+  const int n = live ? 16 : 0;
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst),
+               "l"(static_cast<unsigned long long>(__cvta_generic_to_global(src))), "r"(n)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t r[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t addr, uint32_t r[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void mma16816(float c[4], const uint32_t a[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+__global__ void __launch_bounds__(kThreads, 2) attend_rows_kernel(const AttnArgs a) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  __shared__ float s_m[kWarps][kTR], s_l[kWarps][kTR];
+  const int warp = warp_id(), lane = lane_id();
+  const int quad = lane >> 2, ql = lane & 3;
+  if (threadIdx.x == 0) a.rec[blockIdx.x] = make_int4(-1, 0, 0, 0);
+  const Share sh = share_of<kTR, kTK, kThreads>(a, blockIdx.x);
+  if (static_cast<int>(blockIdx.x) >= sh.grid) return;
+  const uint32_t ring = smem_u32(smem) + warp * (kStages * kStageBytes);
+  float* s_o = reinterpret_cast<float*>(smem);
+
+  long long base = sh.item_base, at = sh.begin;
+  for (int item = sh.item; at < sh.end; ++item) {
+    const ItemRange x = item_range<kTR, kTK>(a, item);
+    if (x.tiles == 0) continue;
+    const int ta = static_cast<int>(at - base);
+    const int tb = static_cast<int>(min(static_cast<long long>(x.tiles), sh.end - base));
+    const int cnt = tb - ta;
+
+    // query rows as mma A fragments: rows quad and quad + 8, two neighbouring columns each
+    uint32_t qf[8][4];
+    const int r0 = x.rt * kTR;
+    int pos[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int r = r0 + quad + 8 * u;
+      const int t = r / a.G, g = r - t * a.G;
+      const bool live = quad + 8 * u < x.rows;
+      pos[u] = live ? (a.causal ? x.n - x.m + t : x.n - 1) : -1;
+      const uint16_t* src = a.q + x.b * a.q_req + static_cast<long long>(x.h * a.G + g) * a.q_head +
+                            static_cast<long long>(t) * a.q_tok;
+#pragma unroll
+      for (int kk = 0; kk < 8; ++kk) {
+        qf[kk][u] = live ? __ldg(reinterpret_cast<const uint32_t*>(src + kk * 16 + ql * 2)) : 0u;
+        qf[kk][u + 2] = live ? __ldg(reinterpret_cast<const uint32_t*>(src + kk * 16 + 8 + ql * 2)) : 0u;
+      }
+    }
+
+    float o[16][4];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    float ref[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
+
+    // element offset of the cached row that this lane looks up for unit u (rows 0..15: lanes l
+    // and l + 16), one unit ahead of the copies that use it; -1 where there is none
+    auto lookup = [&](int u) -> long long {
+      if (u >= cnt) return -1;
+      int j0, j1;
+      tile_rows<kTK>(x, ta + u, j0, j1);
+      const int j = j0 + warp * kUnit + (lane & 15);
+      if (j >= j1) return -1;
+      // rows before the window of the block's first token are not read
+      if (a.window > 0 && a.causal && j <= x.p0 - a.window && j >= a.n_sink) return -1;
+      const long long e = row_elem(a, x.b, x.h, x.row0, j);
+      if (e < 0) atomicOr(a.wc.status, DEV_BAD_INDEX);
+      return e;
+    };
+    auto issue = [&](int u, long long off) {
+      if (u < cnt) {
+        const uint32_t dst = ring + (u % kStages) * kStageBytes;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int row = i * 2 + (lane >> 4), c = lane & 15;
+          const long long e = __shfl_sync(0xffffffffu, off, row);
+          const long long s = e < 0 ? 0 : e + c * 8;
+          const uint32_t d = dst + row * 256 + ((c ^ (row & 7)) << 4);
+          cp_async16_zfill(d, a.k + s, e >= 0);
+          cp_async16_zfill(d + kUnitBytes, a.v + s, e >= 0);
+        }
+      }
+      cp_async_commit();
+    };
+    long long ahead = lookup(0);
+#pragma unroll
+    for (int u = 0; u < kStages - 1; ++u) {
+      const long long off = ahead;
+      ahead = lookup(u + 1);
+      issue(u, off);
+    }
+
+    for (int u = 0; u < cnt; ++u) {
+      cp_async_wait<kStages - 2>();
+      __syncwarp();
+      {
+        const long long off = ahead;
+        ahead = lookup(u + kStages);
+        issue(u + kStages - 1, off);
+      }
+      const uint32_t sk = ring + (u % kStages) * kStageBytes, sv = sk + kUnitBytes;
+      float c[2][4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) c[0][i] = c[1][i] = 0.f;
+      {
+        const int row = (lane & 7) + ((lane >> 4) << 3);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {
+          uint32_t b[4];
+          ldmatrix4(sk + row * 256 + (((kk * 2 + ((lane >> 3) & 1)) ^ (row & 7)) << 4), b);
+          mma16816(c[0], qf[kk], b[0], b[1]);
+          mma16816(c[1], qf[kk], b[2], b[3]);
+        }
+      }
+      int j0, j1;
+      tile_rows<kTK>(x, ta + u, j0, j1);
+      j0 += warp * kUnit;
+      // every row of the block sees all 16 cached rows: no element masks
+      const bool whole =
+          j0 + kUnit <= j1 &&
+          (!a.causal || (j0 + kUnit <= x.p0 + 1 && (a.window <= 0 || j0 > x.p1 - a.window || j0 + kUnit <= a.n_sink)));
+      float p[2][4];
+      float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float y = c[nt][i] * a.s2;
+          if (!whole) {
+            const int j = j0 + nt * 8 + ql * 2 + (i & 1);
+            if (j >= j1 || !sees(a, pos[i >> 1], j)) y = -INFINITY;
+          }
+          p[nt][i] = y;
+          top[i >> 1] = fmaxf(top[i >> 1], y);
+        }
+#pragma unroll
+      for (int u2 = 0; u2 < 2; ++u2) {
+        top[u2] = fmaxf(top[u2], __shfl_xor_sync(0xffffffffu, top[u2], 1));
+        top[u2] = fmaxf(top[u2], __shfl_xor_sync(0xffffffffu, top[u2], 2));
+      }
+      if (__any_sync(0xffffffffu, top[0] > ref[0] + 8.f || top[1] > ref[1] + 8.f)) {
+        float f[2];
+#pragma unroll
+        for (int u2 = 0; u2 < 2; ++u2) {
+          const float r2 = fmaxf(ref[u2], top[u2]);
+          f[u2] = ref[u2] == -INFINITY ? 0.f : exp2f(ref[u2] - r2);
+          ref[u2] = r2;
+          sum[u2] *= f[u2];
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          o[i][0] *= f[0];
+          o[i][1] *= f[0];
+          o[i][2] *= f[1];
+          o[i][3] *= f[1];
+        }
+      }
+      const float base0 = ref[0] == -INFINITY ? 0.f : ref[0], base1 = ref[1] == -INFINITY ? 0.f : ref[1];
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt) {
+        p[nt][0] = ex2_approx(p[nt][0] - base0);
+        p[nt][1] = ex2_approx(p[nt][1] - base0);
+        p[nt][2] = ex2_approx(p[nt][2] - base1);
+        p[nt][3] = ex2_approx(p[nt][3] - base1);
+        sum[0] += p[nt][0] + p[nt][1];
+        sum[1] += p[nt][2] + p[nt][3];
+      }
+      // the weights enter the second product as a bf16 high part and remainder: the tensor
+      // cores are idle here, and the result then carries the output's rounding alone
+      uint32_t hi[4], lo[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float y0 = p[i >> 1][(i & 1) * 2], y1 = p[i >> 1][(i & 1) * 2 + 1];
+        const __nv_bfloat162 h2 = __floats2bfloat162_rn(y0, y1);
+        const float2 hf = __bfloat1622float2(h2);
+        hi[i] = *reinterpret_cast<const uint32_t*>(&h2);
+        lo[i] = pack_bf16(y0 - hf.x, y1 - hf.y);
+      }
+      {
+        const int row = (lane & 7) + (((lane >> 3) & 1) << 3);
+#pragma unroll
+        for (int nd = 0; nd < 8; ++nd) {
+          uint32_t b[4];
+          ldmatrix4_trans(sv + row * 256 + (((nd * 2 + (lane >> 4)) ^ (row & 7)) << 4), b);
+          mma16816(o[nd * 2], hi, b[0], b[1]);
+          mma16816(o[nd * 2 + 1], hi, b[2], b[3]);
+          mma16816(o[nd * 2], lo, b[0], b[1]);
+          mma16816(o[nd * 2 + 1], lo, b[2], b[3]);
+        }
+      }
+      __syncwarp();   // the stage is refilled after every lane has read it
+    }
+
+    // merge the four warps: common reference, rescaled sums and accumulators
+    cp_async_wait<0>();
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      sum[u] += __shfl_xor_sync(0xffffffffu, sum[u], 1);
+      sum[u] += __shfl_xor_sync(0xffffffffu, sum[u], 2);
+      if (ql == 0) {
+        s_m[warp][quad + 8 * u] = ref[u];
+        s_l[warp][quad + 8 * u] = sum[u];
+      }
+    }
+    __syncthreads();   // the rings are free
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float* d = s_o + (warp * kTR + quad) * kOPad + i * 8 + ql * 2;
+      if (quad < x.rows) *reinterpret_cast<float2*>(d) = make_float2(o[i][0], o[i][1]);
+      if (quad + 8 < x.rows) *reinterpret_cast<float2*>(d + 8 * kOPad) = make_float2(o[i][2], o[i][3]);
+    }
+    __syncthreads();
+    const bool first = ta == 0, last = tb == x.tiles;
+    const int slot = 2 * blockIdx.x + (first ? 1 : 0);
+    for (int r = warp; r < x.rows; r += kWarps) {
+      float M = -INFINITY, L = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w][r]);
+      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float f = s_m[w][r] == -INFINITY ? 0.f : exp2f(s_m[w][r] - M);
+        const float4 z = *reinterpret_cast<const float4*>(s_o + (w * kTR + r) * kOPad + lane * 4);
+        L += f * s_l[w][r];
+        y.x += f * z.x;
+        y.y += f * z.y;
+        y.z += f * z.z;
+        y.w += f * z.w;
+      }
+      if (first && last) {
+        const int rr = r0 + r, t = rr / a.G, g = rr - t * a.G;
+        const float inv = L > 0.f ? 1.f / L : 0.f;
+        uint16_t* dst = a.out + x.b * a.o_req + static_cast<long long>(x.h * a.G + g) * a.o_head +
+                        static_cast<long long>(t) * a.o_tok;
+        *reinterpret_cast<uint2*>(dst + lane * 4) = make_uint2(pack_bf16(y.x * inv, y.y * inv), pack_bf16(y.z * inv, y.w * inv));
+        if (lane == 0) {
+          const float e2 = L > 0.f ? M + log2f(L) : -INFINITY;
+          if (a.lse) a.lse[(static_cast<long long>(x.b) * a.H * a.G + x.h * a.G + g) * a.m + t] = e2 * 0.6931471805599453f;
+          if (a.lse2) a.lse2[static_cast<long long>(x.seg) * a.m * a.G + rr] = e2;
+        }
+      } else {
+        *reinterpret_cast<float4*>(a.part_o + (static_cast<long long>(slot) * kTR + r) * kHeadDim + lane * 4) = y;
+        if (lane == 0) a.part_ml[static_cast<long long>(slot) * kTR + r] = make_float2(M, L);
+      }
+    }
+    if (first && !last && threadIdx.x == 0)
+      a.rec[blockIdx.x] = make_int4(item, last_cta(sh, base + x.tiles) - blockIdx.x, 0, 0);
+    __syncthreads();   // s_m, s_l and the accumulators are read before the next item
+    base += x.tiles;
+    at = base;
+  }
+}
+
+// Joins the pieces of an item that several CTAs of attend_rows_kernel share: CTA x owns the
+// item that starts in the first kernel's CTA x, y the query row of it.
+__global__ void __launch_bounds__(128) attend_join_kernel(const AttnArgs a, int tr) {
+  __shared__ float4 s_y[4][32];
+  __shared__ float s_M[4], s_L[4];
+  const int4 rec = a.rec[blockIdx.x];
+  if (rec.x < 0) return;
+  const int seg = rec.x / a.rt, rt = rec.x - seg * a.rt;
+  const int b = seg / a.H, h = seg - b * a.H;
+  const int mr = a.new_lens ? __ldg(a.new_lens + b) : a.m;
+  const int R = min(max(mr, 0), a.m) * a.G;
+  const int r = blockIdx.y, rr = rt * tr + r;
+  if (rr >= R) return;
+  const int warp = warp_id(), lane = lane_id();
+  // piece 0 sits in slot 1 of this CTA, piece c > 0 in slot 0 of CTA x + c
+  float M = -INFINITY, L = 0.f;
+  float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int c = warp; c <= rec.y; c += 4) {
+    const long long slot = c == 0 ? 2ll * blockIdx.x + 1 : 2ll * (blockIdx.x + c);
+    const float2 ml = a.part_ml[slot * tr + r];
+    const float4 z = *reinterpret_cast<const float4*>(a.part_o + (slot * tr + r) * kHeadDim + lane * 4);
+    const float M2 = fmaxf(M, ml.x);
+    if (M2 == -INFINITY) continue;
+    const float f = exp2f(M - M2), g = exp2f(ml.x - M2);
+    M = M2;
+    L = L * f + ml.y * g;
+    y.x = y.x * f + z.x * g;
+    y.y = y.y * f + z.y * g;
+    y.z = y.z * f + z.z * g;
+    y.w = y.w * f + z.w * g;
+  }
+  s_y[warp][lane] = y;
+  if (lane == 0) {
+    s_M[warp] = M;
+    s_L[warp] = L;
+  }
+  __syncthreads();
+  if (warp) return;
+  M = fmaxf(fmaxf(s_M[0], s_M[1]), fmaxf(s_M[2], s_M[3]));
+  L = 0.f;
+  y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const float f = s_M[w] == -INFINITY ? 0.f : exp2f(s_M[w] - M);
+    const float4 z = s_y[w][lane];
+    L += f * s_L[w];
+    y.x += f * z.x;
+    y.y += f * z.y;
+    y.z += f * z.z;
+    y.w += f * z.w;
+  }
+  const int t = rr / a.G, g = rr - t * a.G;
+  const float inv = L > 0.f ? 1.f / L : 0.f;
+  uint16_t* dst = a.out + b * a.o_req + static_cast<long long>(h * a.G + g) * a.o_head + static_cast<long long>(t) * a.o_tok;
+  *reinterpret_cast<uint2*>(dst + lane * 4) = make_uint2(pack_bf16(y.x * inv, y.y * inv), pack_bf16(y.z * inv, y.w * inv));
+  if (lane == 0) {
+    const float e2 = L > 0.f ? M + log2f(L) : -INFINITY;
+    if (a.lse) a.lse[(static_cast<long long>(b) * a.H * a.G + h * a.G + g) * a.m + t] = e2 * 0.6931471805599453f;
+    if (a.lse2) a.lse2[static_cast<long long>(seg) * a.m * a.G + rr] = e2;
+  }
+}
+
+// Accumulated weights: acc_j += sum over query rows r of exp2(s2 <q_r, k_j> - lse2_r).  A CTA
+// owns 64 cached rows of one segment (16 per warp, the mma's A operand, loaded once into
+// registers) and streams the query rows that see any of them; each thread adds up its own
+// cached rows, so the order of additions is fixed.
+constexpr int kWRows = 64;                           // query rows per step
+__global__ void __launch_bounds__(kThreads) attend_weights_kernel(const AttnArgs a) {
+  __shared__ __align__(128) uint8_t s_q[kWRows * 256];
+  __shared__ float s_e[kWRows];
+  const int seg = blockIdx.y, b = seg / a.H, h = seg - b * a.H;
+  const SegLen s = seg_len(a, b, h);
+  const int jb = blockIdx.x * kTK;
+  if (jb >= s.n || s.m == 0) return;
+  const int warp = warp_id(), lane = lane_id(), quad = lane >> 2, ql = lane & 3;
+  const int first = s.n - s.m;                       // cache row of token 0
+  // tokens that see a row of [jb, jend)
+  const int jend = min(jb + kTK, s.n);
+  int t0 = 0, t1 = s.m;
+  if (a.causal) {
+    t0 = max(0, jb - first);
+    if (a.window > 0 && jb >= a.n_sink) t1 = static_cast<int>(min(static_cast<long long>(s.m), static_cast<long long>(jend) - 1 + a.window - first));
+  }
+  if (t0 >= t1) return;
+  int j[2];
+  uint32_t kf[8][4];
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    j[u] = jb + warp * kUnit + quad + 8 * u;
+    // a page that no token sees may be gone: looked up only inside the tokens' reach
+    bool live = j[u] < s.n;
+    if (live && a.causal && a.window > 0 && j[u] >= a.n_sink && j[u] <= max(first, 0) - a.window) live = false;
+    long long e = -1;
+    if (live) {
+      e = row_elem(a, b, h, s.row0, j[u]);
+      if (e < 0) atomicOr(a.wc.status, DEV_BAD_INDEX);
+    }
+    const uint16_t* src = a.k + (e < 0 ? 0 : e);
+#pragma unroll
+    for (int kk = 0; kk < 8; ++kk) {
+      kf[kk][u] = e >= 0 ? __ldg(reinterpret_cast<const uint32_t*>(src + kk * 16 + ql * 2)) : 0u;
+      kf[kk][u + 2] = e >= 0 ? __ldg(reinterpret_cast<const uint32_t*>(src + kk * 16 + 8 + ql * 2)) : 0u;
+    }
+  }
+  float w[2] = {0.f, 0.f};
+  const uint32_t sq = smem_u32(s_q);
+  for (int rb = t0 * a.G; rb < t1 * a.G; rb += kWRows) {
+    __syncthreads();
+    for (int i = threadIdx.x; i < kWRows * 16; i += kThreads) {
+      const int row = i >> 4, c = i & 15, r = rb + row;
+      uint4 z = make_uint4(0u, 0u, 0u, 0u);
+      if (r < t1 * a.G) {
+        const int t = r / a.G, g = r - t * a.G;
+        z = __ldg(reinterpret_cast<const uint4*>(a.q + b * a.q_req + static_cast<long long>(h * a.G + g) * a.q_head +
+                                                 static_cast<long long>(t) * a.q_tok) + c);
+      }
+      *reinterpret_cast<uint4*>(s_q + row * 256 + ((c ^ (row & 7)) << 4)) = z;
+    }
+    if (threadIdx.x < kWRows) {
+      const int r = rb + threadIdx.x;
+      s_e[threadIdx.x] = r < t1 * a.G ? __ldg(a.lse2 + static_cast<long long>(seg) * a.m * a.G + r) : -INFINITY;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int nb = 0; nb < kWRows / 16; ++nb) {
+      float c[2][4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) c[0][i] = c[1][i] = 0.f;
+      const int row = nb * 16 + (lane & 7) + ((lane >> 4) << 3);
+#pragma unroll
+      for (int kk = 0; kk < 8; ++kk) {
+        uint32_t f[4];
+        ldmatrix4(sq + row * 256 + (((kk * 2 + ((lane >> 3) & 1)) ^ (row & 7)) << 4), f);
+        mma16816(c[0], kf[kk], f[0], f[1]);
+        mma16816(c[1], kf[kk], f[2], f[3]);
+      }
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int rl = nb * 16 + nt * 8 + ql * 2 + (i & 1);
+          const float e2 = s_e[rl];
+          const int p = first + (rb + rl) / a.G;
+          if (e2 != -INFINITY && sees(a, p, j[i >> 1])) w[i >> 1] += ex2_approx(c[nt][i] * a.s2 - e2);
+        }
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    w[u] += __shfl_xor_sync(0xffffffffu, w[u], 1);
+    w[u] += __shfl_xor_sync(0xffffffffu, w[u], 2);
+    if (ql == 0 && j[u] < s.n) {
+      float* d = a.acc + seg * a.acc_stride + j[u];
+      *d += w[u];
+    }
+  }
+}
+
+}  // namespace
+
+int attend_rows_tile() { return kTR; }
+int attend_rows_ctas_per_sm() { return 2; }
+
+cudaError_t launch_attend_rows(const AttnArgs& a, int grid, cudaStream_t st) {
+  cudaError_t e = ensure_smem(reinterpret_cast<const void*>(attend_rows_kernel), kSmem);
+  if (e != cudaSuccess) return e;
+  attend_rows_kernel<<<grid, kThreads, kSmem, st>>>(a);
+  note_launch();
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  attend_join_kernel<<<dim3(grid, std::min(kTR, a.m * a.G)), 128, 0, st>>>(a, kTR);
+  note_launch();
+  return cudaGetLastError();
+}
+
+cudaError_t launch_attend_weights(const AttnArgs& a, cudaStream_t st) {
+  const dim3 grid((a.max_len + kTK - 1) / kTK, a.B * a.H);
+  attend_weights_kernel<<<grid, kThreads, 0, st>>>(a);
+  note_launch();
+  return cudaGetLastError();
+}
+
+}  // namespace kvsel

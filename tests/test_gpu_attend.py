@@ -1,0 +1,240 @@
+"""kvsel_attend against the fp64 oracle: single tokens and chunks, every cache layout, lengths
+from nothing to many tiles, windows with first tokens, and the running weights."""
+import numpy as np
+import pytest
+
+from tests import cache_harness as CH
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    import __graft_entry__
+
+    __graft_entry__.build()
+    from kv_cache_eviction_window_gb300 import binding
+
+    binding.load()
+    yield
+
+
+def run(acc=True, **kw):
+    c = CH.Case(**kw).upload()
+    ws = c.call(acc=acc)
+    assert CH.status(ws) == 0
+    c.check(acc=acc)
+    return c
+
+
+@pytest.mark.parametrize("layout,block", [("contiguous", 0), ("packed", 0), ("paged", 8), ("paged", 16), ("paged", 32),
+                                          ("paged", 64)])
+@pytest.mark.parametrize("n", [1, 2, 15, 16, 17, 63, 64, 65, 127, 129, 300, 1111])
+def test_single_tokens(layout, block, n):
+    run(layout=layout, block=block, lens=n, H=2, G=4, seed=n)
+
+
+@pytest.mark.parametrize("G", [1, 2, 3, 5, 7, 8, 13, 16, 17, 32, 100, 128])
+def test_groups(G):
+    run(G=G, H=1, lens=333, seed=G)
+
+
+@pytest.mark.parametrize("m", [2, 3, 5, 16, 17, 31, 64, 65, 128, 200, 257])
+@pytest.mark.parametrize("G,layout", [(1, "contiguous"), (4, "paged"), (7, "packed")])
+def test_chunks(G, layout, m):
+    run(G=G, H=2, m=m, lens=m + 190, layout=layout, seed=m)
+
+
+@pytest.mark.parametrize("m,G", [(1, 3), (40, 7), (129, 1), (300, 4)])
+def test_a_chunk_that_is_the_whole_cache(m, G):
+    run(m=m, G=G, lens=m, layout="paged", block=8, seed=m)
+
+
+@pytest.mark.parametrize("layout", ["contiguous", "paged", "packed"])
+@pytest.mark.parametrize("m,G", [(1, 4), (6, 7), (50, 4), (130, 2)])
+def test_ragged_batches(layout, m, G):
+    g = CH.rng(m)
+    new = g.integers(0, m + 1, 5)
+    lens = np.array([0, 1, 700, 64, 259]) + new
+    lens[0] = 0
+    run(B=5, H=2, G=G, m=m, new=new, lens=lens if layout != "packed" else np.repeat(lens[:, None], 2, 1), layout=layout,
+        token_major=True, seed=m)
+
+
+def test_lengths_per_head():
+    g = CH.rng(3)
+    for m, layout in ((1, "contiguous"), (3, "paged"), (40, "paged"), (70, "contiguous")):
+        run(B=3, H=4, G=4, m=m, lens=g.integers(m, 900, (3, 4)), per_head=True, layout=layout, pad_rows=5, seed=m)
+
+
+@pytest.mark.parametrize("window,n_sink", [(1, 0), (1, 4), (5, 1), (16, 4), (100, 64), (128, 200), (1000, 4), (4096, 0),
+                                           (50, 1000)])
+@pytest.mark.parametrize("m,G,layout,block", [(1, 4, "paged", 16), (1, 8, "contiguous", 0), (9, 3, "paged", 64),
+                                              (70, 4, "paged", 8), (300, 2, "contiguous", 0)])
+def test_windows(window, n_sink, m, G, layout, block):
+    run(B=2, H=2, G=G, m=m, lens=[1201, m + 7], window=window, n_sink=n_sink, layout=layout, block=block, seed=window)
+
+
+@pytest.mark.parametrize("m,G", [(1, 4), (5, 3), (90, 4)])
+def test_every_row_visible(m, G):
+    # the new tokens are not in the cache: every token sees all rows, an empty cache none
+    run(B=3, G=G, m=m, lens=[0, 77, 500], causal=False, seed=m)
+
+
+@pytest.mark.parametrize("m,G", [(4, 4), (40, 4), (150, 2)])
+def test_fewer_rows_than_tokens(m, G):
+    # tokens in front of the cache see nothing: zeros, and a log-sum-exp of -inf
+    run(B=3, G=G, m=m, lens=[0, 1, m - 2], seed=m)
+
+
+def test_scale_and_far_logits():
+    run(lens=700, scale=1.0, logit=3.0, seed=1)                 # a softmax of almost one row
+    run(lens=700, scale=1e-3, seed=2)                           # an almost even one
+    run(lens=700, m=40, scale=0.5, logit=3.0, seed=3)
+    # logits that rise along the cache: the running maximum moves in every tile
+    for m in (1, 40):
+        c = CH.Case(lens=1500, m=m, H=1, seed=4)
+        c.k[0][0] = CH.bf16(c.k[0][0] + np.linspace(0, 4, 1500)[:, None] * c.q[0, 0, 0, 0][None])
+        c.upload()
+        ws = c.call(acc=True)
+        assert CH.status(ws) == 0
+        c.check(acc=True)
+
+
+def test_work_cut_over_many_blocks():
+    # one long segment, and many short ones: pieces of one item in many places, many items in one
+    run(H=1, G=8, lens=20011, seed=1)
+    run(B=64, H=8, G=4, lens=np.arange(64) * 5 + 1, layout="paged", seed=2, acc=False)
+    run(B=300, H=2, G=2, lens=np.arange(300) % 7, seed=3)
+    run(B=2, H=2, G=4, m=100, lens=[5000, 130], layout="paged", seed=4)
+
+
+def test_weights_add_up_over_calls_and_results_repeat():
+    import torch
+
+    for m in (1, 33):
+        c = CH.Case(lens=900, m=m, B=2, seed=m).upload()
+        ws = c.call(acc=True)
+        first = c.t["out"].clone(), c.t["acc"].clone()
+        c.call(acc=True, ws=ws)
+        assert torch.equal(first[0], c.t["out"])
+        c.check(acc=True, calls=2)
+        # without acc and lse: the same outputs
+        c.call(acc=False, lse=False)
+        assert torch.equal(first[0], c.t["out"])
+        c.t["acc"].zero_()
+        c.call(acc=True)
+        assert torch.equal(first[1], c.t["acc"])
+
+
+def test_lengths_are_read_by_a_captured_call():
+    import torch
+
+    c = CH.Case(lens=[900, 650], B=2, m=2, per_head=False, seed=5).upload()
+    from kv_cache_eviction_window_gb300 import binding as L
+
+    ws = CH.workspace(L.kvsel_attend_workspace_size(L.make_attn_params(**c.params), True))
+    lens = c.t["lens"].clone()
+    c.t["lens"].fill_(3)
+    g = torch.cuda.CUDAGraph()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        c.call(acc=True, ws=ws, stream=s)
+        with torch.cuda.graph(g, stream=s):
+            c.call(acc=True, ws=ws, stream=torch.cuda.current_stream())
+    torch.cuda.current_stream().wait_stream(s)
+    c.t["acc"].zero_()
+    c.t["lens"].copy_(lens)
+    g.replay()
+    assert CH.status(ws) == 0
+    c.check(acc=True)
+
+
+def test_calls_side_by_side():
+    import torch
+
+    cases = [CH.Case(lens=3000 + 100 * i, H=2, m=1 + 40 * (i % 2), seed=i).upload() for i in range(4)]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    from kv_cache_eviction_window_gb300 import binding as L
+
+    wss = [CH.workspace(L.kvsel_attend_workspace_size(L.make_attn_params(**c.params), True)) for c in cases]
+    torch.cuda.synchronize()
+    for c, s, ws in zip(cases, streams, wss):
+        c.call(acc=True, ws=ws, stream=s)
+    torch.cuda.synchronize()
+    for c, ws in zip(cases, wss):
+        assert CH.status(ws) == 0
+        c.check(acc=True)
+
+
+def test_bad_lengths_blocks_and_offsets_are_reported():
+    import torch
+
+    for m in (1, 40):
+        c = CH.Case(lens=200, m=m, layout="paged", seed=1).upload()
+        ora = c.oracle()
+        c.t["lens"].fill_(c.max_len + 9)        # clamped to max_len
+        ws = c.call(acc=True)
+        assert CH.status(ws) == -7
+        c.check(ora, acc=True)
+        c.t["lens"].fill_(-4)                    # counts as empty
+        ws = c.call(ws=ws)
+        assert CH.status(ws) == -7
+        assert torch.all(c.t["out"] == 0) and torch.all(torch.isneginf(c.t["lse"]))
+        # a block out of range: its rows read as zeros
+        c = CH.Case(lens=200, m=m, layout="paged", seed=1)
+        for h in range(c.H):
+            c.k[0][h][48:64] = 0.0
+            c.v[0][h][48:64] = 0.0
+        c.upload()
+        c.keep[2][0, 3] = c.keep[2].numel() + 5
+        ws = c.call(acc=True)
+        assert CH.status(ws) == -7
+        c.check(acc=True)
+        c = CH.Case(lens=200, m=m, layout="packed", seed=2).upload()
+        c.offsets[1] += 1                         # the last segment would end one row too late
+        ws = c.call()
+        assert CH.status(ws) == -7
+        out = CH.to_f64(c.t["out"]).reshape(1, c.H, c.G, m, CH.D)
+        assert np.all(out[0, 1] == 0)
+        assert np.isfinite(out).all()
+
+
+def test_attention_over_what_a_layer_call_kept():
+    """run_layer's compacted cache goes straight into the attention: the query tokens attend to
+    the kept rows only, and to the whole cache when everything is kept."""
+    import torch
+
+    from kv_cache_eviction_window_gb300 import binding as L
+    from kv_cache_eviction_window_gb300 import datagen
+    from oracle import cache_oracle as CO
+    from tests import gpu_harness as GH
+
+    wl = datagen.WORKLOADS[3].replace(layers=1, h_kv=2, window=32)
+    inp = datagen.make_layer(wl, 0, n_ctx=2500)
+    p = L.params_from_workload(wl, n_ctx=2500)
+    q, k, v = (GH.torch_bf16(x) for x in (inp["q"], inp["k"][0], inp["v"][0]))
+    buf = L.LayerBuffers(p)
+    L.kvsel_run_layer(p, q, L.make_kv_contiguous(k, v), None, buf.s_attn, buf.s_val, buf.idx, buf.counts, buf.offsets,
+                      buf.k_out, buf.v_out, buf.ws)
+    G, W = wl.group, 3
+    pa = L.make_attn_params(h_kv=2, group=G, batch=1, n_new=W, max_len=2500, causal=False, n_rows=buf.n_kept)
+    out = torch.empty((1, 2 * G, W, 128), dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty((1, 2 * G, W), device="cuda")
+    # (scoring and attention calls take turns on one workspace)
+    ws = CH.workspace(max(L.kvsel_attend_workspace_size(pa), L.kvsel_workspace_size(p)))
+    qn = q.reshape(1, 2 * G, 32, 128)[:, :, -W:].contiguous()
+    for _ in range(2):
+        L.kvsel_attend(pa, qn, L.make_kv_packed(buf.k_out, buf.v_out), buf.counts, out, ws, offsets=buf.offsets, lse=lse)
+        L.kvsel_run_layer(p, q, L.make_kv_contiguous(k, v), None, buf.s_attn, buf.s_val, buf.idx, buf.counts, buf.offsets,
+                          buf.k_out, buf.v_out, ws)
+    assert CH.status(ws) == 0
+    counts, offs = buf.counts.cpu().numpy(), buf.offsets.cpu().numpy()
+    for h in range(2):
+        idx = buf.idx.cpu().numpy()[offs[h]:offs[h] + counts[h]]
+        o = CO.attend_segment(CH.to_f64(qn)[0, h * G:(h + 1) * G], CH.to_f64(k)[h][idx], CH.to_f64(v)[h][idx], causal=False)
+        e = 132 * 2.0 ** -23 * o["abs_logit"] + 2.0 ** -14
+        tol = (2 * e[..., None] + 2.0 ** -8) * o["mean_abs"] + 2.0 ** -8 * np.abs(o["out"])
+        assert np.all(np.abs(CH.to_f64(out)[0, h * G:(h + 1) * G] - o["out"]) <= tol)
