@@ -31,7 +31,8 @@ struct AttnArgs {
   const uint16_t* k;
   const uint16_t* v;
   long long stride_req, stride_head, stride_tok;
-  int rt;                         // row blocks (items) per segment
+  int tr;                         // query rows of an item
+  int rt;                         // items per segment
   // partial results of items that several CTAs share: two slots per CTA
   float* part_o;                  // [2 * grid][rows][128]
   float2* part_ml;                // [2 * grid][rows]: reference (log2 units) and sum
@@ -76,9 +77,10 @@ struct ItemRange {
   int lo, hi, sink, ns, tiles;
   long long row0;
 };
-template <int TR, int TK>
+template <int TK>
 __device__ __forceinline__ ItemRange item_range(const AttnArgs& a, int item) {
   ItemRange x;
+  const int TR = a.tr;
   x.seg = item / a.rt;
   x.rt = item - x.seg * a.rt;
   x.b = x.seg / a.H;
@@ -140,7 +142,7 @@ struct Share {
   int item;                       // item of tile `begin`
   long long item_base;            // its first tile
 };
-template <int TR, int TK, int THREADS>
+template <int TK, int THREADS>
 __device__ __forceinline__ Share share_of(const AttnArgs& a, int cta) {
   __shared__ long long s_warp[THREADS / 32];
   __shared__ long long s_base;
@@ -149,7 +151,7 @@ __device__ __forceinline__ Share share_of(const AttnArgs& a, int cta) {
   const int per = (items + THREADS - 1) / THREADS;
   const int i0 = min(items, static_cast<int>(threadIdx.x) * per), i1 = min(items, i0 + per);
   long long sum = 0;
-  for (int i = i0; i < i1; ++i) sum += item_range<TR, TK>(a, i).tiles;
+  for (int i = i0; i < i1; ++i) sum += item_range<TK>(a, i).tiles;
   long long inc = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -176,7 +178,7 @@ __device__ __forceinline__ Share share_of(const AttnArgs& a, int cta) {
       long long at = before;
       int i = i0;
       for (; i < i1; ++i) {
-        const int c = item_range<TR, TK>(a, i).tiles;
+        const int c = item_range<TK>(a, i).tiles;
         if (sh.begin < at + c) break;
         at += c;
       }
@@ -211,9 +213,39 @@ __device__ __forceinline__ long long row_elem(const AttnArgs& a, int b, int h, l
   return ((static_cast<long long>(pb) * bs + (j % bs)) * a.H + h) * kHeadDim;
 }
 
+// a row that no cached row is read for: behind the tile's end, or before the window of the
+// item's first token (and not among the first rows that stay visible)
+__device__ __forceinline__ bool unseen(const AttnArgs& a, const ItemRange& x, int j, int j1) {
+  return j >= j1 || (a.window > 0 && j >= a.n_sink && j <= x.p0 - a.window);
+}
+
+// Log-sum-exp of query row rr of a segment from its reference M (log2 units) and sum L.
+__device__ __forceinline__ void write_lse(const AttnArgs& a, int b, int h, int rr, float M, float L) {
+  const int t = rr / a.G, g = rr - t * a.G;
+  const float e2 = L > 0.f ? M + log2f(L) : -INFINITY;
+  if (a.lse) a.lse[(static_cast<long long>(b) * a.H * a.G + h * a.G + g) * a.m + t] = e2 * 0.6931471805599453f;
+  if (a.lse2) a.lse2[static_cast<long long>(b * a.H + h) * a.m * a.G + rr] = e2;
+}
+__device__ __forceinline__ uint16_t* out_row(const AttnArgs& a, int b, int h, int rr) {
+  const int t = rr / a.G, g = rr - t * a.G;
+  return a.out + b * a.o_req + static_cast<long long>(h * a.G + g) * a.o_head + static_cast<long long>(t) * a.o_tok;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// a few rows per item (a.tr = attend_rows_tile())
 cudaError_t launch_attend_rows(const AttnArgs& a, int grid, cudaStream_t st);
-cudaError_t launch_attend_weights(const AttnArgs& a, cudaStream_t st);
-int attend_rows_tile();           // query rows per item of launch_attend_rows
+int attend_rows_tile();
 int attend_rows_ctas_per_sm();
+// tcgen05 tiles: two blocks of `block` query rows per item that share the cached rows, or, with
+// `split`, one block whose even and odd key tiles run side by side
+cudaError_t launch_attend_tile(const AttnArgs& a, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                               int block, bool split, int grid, cudaStream_t st);
+int attend_tile_keys();           // cached rows per tile
+// joins the pieces of items that several CTAs of either kernel share
+cudaError_t launch_attend_join(const AttnArgs& a, int grid, cudaStream_t st);
+cudaError_t launch_attend_weights(const AttnArgs& a, cudaStream_t st);
 
 }  // namespace kvsel

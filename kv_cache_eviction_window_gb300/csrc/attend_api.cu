@@ -27,7 +27,9 @@ int device_sms(int* sms) {
 }
 
 struct AttnPlan {
-  int grid = 0, rt = 1;
+  int grid = 0, tr = 0, rt = 1;
+  bool tiled = false, split = false;
+  int block = 0;                 // tiled: query rows per block, whole tokens of the group
   size_t rec = 0, ml = 0, o = 0, lse2 = 0, total = 0;
 };
 
@@ -41,6 +43,7 @@ int check_attn(const kvsel_attn_params* p) {
   if (p->group > KVSEL_MAX_ATTN_GROUP || p->batch > KVSEL_MAX_ATTN_BATCH) return KVSEL_EUNSUPPORTED;
   if (p->n_new > (1 << 20) || p->max_len > kMaxRows) return KVSEL_EUNSUPPORTED;
   if (static_cast<long long>(p->n_new) * p->group * p->h_kv * p->batch > kMaxRows) return KVSEL_EUNSUPPORTED;
+  if (p->n_rows > (1ll << 31) - 1) return KVSEL_EUNSUPPORTED;
   if (p->causal < 0 || p->causal > 1 || p->lens_per_head < 0 || p->lens_per_head > 1) return KVSEL_EINVAL;
   if (p->window < 0 || p->window > kMaxRows || p->n_sink < 0 || p->n_sink > kMaxRows) return KVSEL_EINVAL;
   if (p->window > 0 && !p->causal) return KVSEL_EUNSUPPORTED;
@@ -60,17 +63,27 @@ int plan_attn(const kvsel_attn_params* p, bool with_acc, AttnPlan& pl) {
   if (rc) return rc;
   int sms = 0;
   if ((rc = device_sms(&sms))) return rc;
-  const int tr = attend_rows_tile();
-  pl.rt = (p->n_new * p->group + tr - 1) / tr;
-  pl.grid = sms * attend_rows_ctas_per_sm();
+  const int R = p->n_new * p->group;
+  if (R <= attend_rows_tile()) {
+    // single tokens and the like: HBM-bound, 16 query rows per item
+    pl.tr = attend_rows_tile();
+    pl.grid = sms * attend_rows_ctas_per_sm();
+  } else {
+    pl.tiled = true;
+    pl.block = 128 / p->group * p->group;
+    pl.split = R <= pl.block;
+    pl.tr = pl.split ? pl.block : 2 * pl.block;
+    pl.grid = sms;
+  }
+  pl.rt = (R + pl.tr - 1) / pl.tr;
   // behind the status word and the counters that the scoring calls keep in a shared workspace
   size_t off = kStatusBytes + kCounterBytes;
   pl.rec = off;
   off = align256(off + sizeof(int4) * pl.grid);
   pl.ml = off;
-  off = align256(off + sizeof(float2) * 2 * pl.grid * tr);
+  off = align256(off + sizeof(float2) * 2 * pl.grid * pl.tr);
   pl.o = off;
-  off = align256(off + sizeof(float) * 2 * pl.grid * tr * kHeadDim);
+  off = align256(off + sizeof(float) * 2 * pl.grid * pl.tr * kHeadDim);
   if (with_acc) {
     pl.lse2 = off;
     off = align256(off + sizeof(float) * p->batch * p->h_kv * p->n_new * p->group);
@@ -96,6 +109,37 @@ int check_cache(const kvsel_kv* kv, int B, int H, long long rows, const int64_t*
     return KVSEL_EINVAL;
   }
   return KVSEL_OK;
+}
+
+// Query tiles: 64 columns x the group's heads x whole tokens.
+bool query_map(CUtensorMap* m, const AttnArgs& a, int block) {
+  const cuuint64_t hq = static_cast<cuuint64_t>(a.H) * a.G;
+  const cuuint64_t dims[4] = {kHeadDim, hq, static_cast<cuuint64_t>(a.m), static_cast<cuuint64_t>(a.B)};
+  // the stride of a dimension with one entry is not used; any valid one will do
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(hq > 1 ? a.q_head : kHeadDim) * 2,
+                                 static_cast<cuuint64_t>(a.m > 1 ? a.q_tok : kHeadDim) * 2,
+                                 static_cast<cuuint64_t>(a.B > 1 ? a.q_req : kHeadDim) * 2};
+  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(a.G), static_cast<cuuint32_t>(block / a.G), 1};
+  return encode_bf16_map(m, a.q, 4, dims, strides, box);
+}
+
+// K or V tiles: 64 columns x 128 rows of one segment (contiguous, packed) or x one page.
+bool cache_map(CUtensorMap* m, const void* base, const kvsel_kv* kv, const kvsel_attn_params* p) {
+  const cuuint64_t H = p->h_kv, B = p->batch;
+  if (kv->layout == KVSEL_LAYOUT_PAGED) {
+    const cuuint64_t bs = kv->block_size;
+    const cuuint64_t dims[4] = {kHeadDim, H, bs, static_cast<cuuint64_t>(kv->num_blocks)};
+    const cuuint64_t strides[3] = {kHeadDim * 2, H * kHeadDim * 2, bs * H * kHeadDim * 2};
+    const cuuint32_t box[4] = {64, 1, static_cast<cuuint32_t>(bs), 1};
+    return encode_bf16_map(m, base, 4, dims, strides, box);
+  }
+  const bool packed = kv->layout == KVSEL_LAYOUT_PACKED;
+  const cuuint64_t rows = packed ? p->n_rows : p->max_len, tok = static_cast<cuuint64_t>(kv->stride_tok) * 2;
+  const cuuint64_t dims[4] = {kHeadDim, rows, packed ? 1 : H, packed ? 1 : B};
+  const cuuint64_t strides[3] = {tok, !packed && H > 1 ? static_cast<cuuint64_t>(kv->stride_head) * 2 : tok,
+                                 !packed && B > 1 ? static_cast<cuuint64_t>(kv->stride_req) * 2 : tok};
+  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(attend_tile_keys()), 1, 1};
+  return encode_bf16_map(m, base, 4, dims, strides, box);
 }
 
 KvSource source_of(const kvsel_kv* kv) {
@@ -204,13 +248,21 @@ int kvsel_attend(const kvsel_attn_params* p, const void* q, const kvsel_kv* kv, 
     a.stride_req = kv->stride_req;
     a.stride_head = kv->stride_head;
   }
+  a.tr = pl.tr;
   a.rt = pl.rt;
   a.part_o = reinterpret_cast<float*>(wsb + pl.o);
   a.part_ml = reinterpret_cast<float2*>(wsb + pl.ml);
   a.rec = reinterpret_cast<int4*>(wsb + pl.rec);
   a.wc = WaitCtl{p->wait_cycles ? p->wait_cycles : kDefaultWaitCycles, static_cast<int*>(ws)};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if ((rc = launch_rc(launch_attend_rows(a, pl.grid, st)))) return rc;
+  if (!pl.tiled) {
+    rc = launch_rc(launch_attend_rows(a, pl.grid, st));
+  } else {
+    CUtensorMap tq, tk, tv;
+    if (!query_map(&tq, a, pl.block) || !cache_map(&tk, kv->k, kv, p) || !cache_map(&tv, kv->v, kv, p)) return KVSEL_EINVAL;
+    rc = launch_rc(launch_attend_tile(a, tq, tk, tv, pl.block, pl.split, pl.grid, st));
+  }
+  if (rc) return rc;
   return acc ? launch_rc(launch_attend_weights(a, st)) : KVSEL_OK;
 }
 

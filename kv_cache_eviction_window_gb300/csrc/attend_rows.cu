@@ -15,8 +15,6 @@
 // Items (16 query rows of one segment) are cut along the cache so that every CTA of the grid
 // gets the same number of tiles whatever the lengths are (share_of); the pieces of an item
 // that was cut are joined by attend_join_kernel, in cache order.
-#include <algorithm>
-
 #include "attend.cuh"
 
 namespace kvsel {
@@ -63,10 +61,6 @@ __device__ __forceinline__ void mma16816(float c[4], const uint32_t a[4], uint32
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
 
 __global__ void __launch_bounds__(kThreads, 2) attend_rows_kernel(const AttnArgs a) {
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -74,14 +68,14 @@ __global__ void __launch_bounds__(kThreads, 2) attend_rows_kernel(const AttnArgs
   const int warp = warp_id(), lane = lane_id();
   const int quad = lane >> 2, ql = lane & 3;
   if (threadIdx.x == 0) a.rec[blockIdx.x] = make_int4(-1, 0, 0, 0);
-  const Share sh = share_of<kTR, kTK, kThreads>(a, blockIdx.x);
+  const Share sh = share_of<kTK, kThreads>(a, blockIdx.x);
   if (static_cast<int>(blockIdx.x) >= sh.grid) return;
   const uint32_t ring = smem_u32(smem) + warp * (kStages * kStageBytes);
   float* s_o = reinterpret_cast<float*>(smem);
 
   long long base = sh.item_base, at = sh.begin;
   for (int item = sh.item; at < sh.end; ++item) {
-    const ItemRange x = item_range<kTR, kTK>(a, item);
+    const ItemRange x = item_range<kTK>(a, item);
     if (x.tiles == 0) continue;
     const int ta = static_cast<int>(at - base);
     const int tb = static_cast<int>(min(static_cast<long long>(x.tiles), sh.end - base));
@@ -118,9 +112,7 @@ __global__ void __launch_bounds__(kThreads, 2) attend_rows_kernel(const AttnArgs
       int j0, j1;
       tile_rows<kTK>(x, ta + u, j0, j1);
       const int j = j0 + warp * kUnit + (lane & 15);
-      if (j >= j1) return -1;
-      // rows before the window of the block's first token are not read
-      if (a.window > 0 && a.causal && j <= x.p0 - a.window && j >= a.n_sink) return -1;
+      if (unseen(a, x, j, j1)) return -1;
       const long long e = row_elem(a, x.b, x.h, x.row0, j);
       if (e < 0) atomicOr(a.wc.status, DEV_BAD_INDEX);
       return e;
@@ -200,7 +192,7 @@ __global__ void __launch_bounds__(kThreads, 2) attend_rows_kernel(const AttnArgs
         float f[2];
 #pragma unroll
         for (int u2 = 0; u2 < 2; ++u2) {
-          const float r2 = fmaxf(ref[u2], top[u2]);
+          const float r2 = top[u2] > ref[u2] + 8.f ? top[u2] : ref[u2];
           f[u2] = ref[u2] == -INFINITY ? 0.f : exp2f(ref[u2] - r2);
           ref[u2] = r2;
           sum[u2] *= f[u2];
@@ -286,16 +278,10 @@ __global__ void __launch_bounds__(kThreads, 2) attend_rows_kernel(const AttnArgs
         y.w += f * z.w;
       }
       if (first && last) {
-        const int rr = r0 + r, t = rr / a.G, g = rr - t * a.G;
         const float inv = L > 0.f ? 1.f / L : 0.f;
-        uint16_t* dst = a.out + x.b * a.o_req + static_cast<long long>(x.h * a.G + g) * a.o_head +
-                        static_cast<long long>(t) * a.o_tok;
-        *reinterpret_cast<uint2*>(dst + lane * 4) = make_uint2(pack_bf16(y.x * inv, y.y * inv), pack_bf16(y.z * inv, y.w * inv));
-        if (lane == 0) {
-          const float e2 = L > 0.f ? M + log2f(L) : -INFINITY;
-          if (a.lse) a.lse[(static_cast<long long>(x.b) * a.H * a.G + x.h * a.G + g) * a.m + t] = e2 * 0.6931471805599453f;
-          if (a.lse2) a.lse2[static_cast<long long>(x.seg) * a.m * a.G + rr] = e2;
-        }
+        *reinterpret_cast<uint2*>(out_row(a, x.b, x.h, r0 + r) + lane * 4) =
+            make_uint2(pack_bf16(y.x * inv, y.y * inv), pack_bf16(y.z * inv, y.w * inv));
+        if (lane == 0) write_lse(a, x.b, x.h, r0 + r, M, L);
       } else {
         *reinterpret_cast<float4*>(a.part_o + (static_cast<long long>(slot) * kTR + r) * kHeadDim + lane * 4) = y;
         if (lane == 0) a.part_ml[static_cast<long long>(slot) * kTR + r] = make_float2(M, L);
@@ -306,68 +292,6 @@ __global__ void __launch_bounds__(kThreads, 2) attend_rows_kernel(const AttnArgs
     __syncthreads();   // s_m, s_l and the accumulators are read before the next item
     base += x.tiles;
     at = base;
-  }
-}
-
-// Joins the pieces of an item that several CTAs of attend_rows_kernel share: CTA x owns the
-// item that starts in the first kernel's CTA x, y the query row of it.
-__global__ void __launch_bounds__(128) attend_join_kernel(const AttnArgs a, int tr) {
-  __shared__ float4 s_y[4][32];
-  __shared__ float s_M[4], s_L[4];
-  const int4 rec = a.rec[blockIdx.x];
-  if (rec.x < 0) return;
-  const int seg = rec.x / a.rt, rt = rec.x - seg * a.rt;
-  const int b = seg / a.H, h = seg - b * a.H;
-  const int mr = a.new_lens ? __ldg(a.new_lens + b) : a.m;
-  const int R = min(max(mr, 0), a.m) * a.G;
-  const int r = blockIdx.y, rr = rt * tr + r;
-  if (rr >= R) return;
-  const int warp = warp_id(), lane = lane_id();
-  // piece 0 sits in slot 1 of this CTA, piece c > 0 in slot 0 of CTA x + c
-  float M = -INFINITY, L = 0.f;
-  float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int c = warp; c <= rec.y; c += 4) {
-    const long long slot = c == 0 ? 2ll * blockIdx.x + 1 : 2ll * (blockIdx.x + c);
-    const float2 ml = a.part_ml[slot * tr + r];
-    const float4 z = *reinterpret_cast<const float4*>(a.part_o + (slot * tr + r) * kHeadDim + lane * 4);
-    const float M2 = fmaxf(M, ml.x);
-    if (M2 == -INFINITY) continue;
-    const float f = exp2f(M - M2), g = exp2f(ml.x - M2);
-    M = M2;
-    L = L * f + ml.y * g;
-    y.x = y.x * f + z.x * g;
-    y.y = y.y * f + z.y * g;
-    y.z = y.z * f + z.z * g;
-    y.w = y.w * f + z.w * g;
-  }
-  s_y[warp][lane] = y;
-  if (lane == 0) {
-    s_M[warp] = M;
-    s_L[warp] = L;
-  }
-  __syncthreads();
-  if (warp) return;
-  M = fmaxf(fmaxf(s_M[0], s_M[1]), fmaxf(s_M[2], s_M[3]));
-  L = 0.f;
-  y = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    const float f = s_M[w] == -INFINITY ? 0.f : exp2f(s_M[w] - M);
-    const float4 z = s_y[w][lane];
-    L += f * s_L[w];
-    y.x += f * z.x;
-    y.y += f * z.y;
-    y.z += f * z.z;
-    y.w += f * z.w;
-  }
-  const int t = rr / a.G, g = rr - t * a.G;
-  const float inv = L > 0.f ? 1.f / L : 0.f;
-  uint16_t* dst = a.out + b * a.o_req + static_cast<long long>(h * a.G + g) * a.o_head + static_cast<long long>(t) * a.o_tok;
-  *reinterpret_cast<uint2*>(dst + lane * 4) = make_uint2(pack_bf16(y.x * inv, y.y * inv), pack_bf16(y.z * inv, y.w * inv));
-  if (lane == 0) {
-    const float e2 = L > 0.f ? M + log2f(L) : -INFINITY;
-    if (a.lse) a.lse[(static_cast<long long>(b) * a.H * a.G + h * a.G + g) * a.m + t] = e2 * 0.6931471805599453f;
-    if (a.lse2) a.lse2[static_cast<long long>(seg) * a.m * a.G + rr] = e2;
   }
 }
 
@@ -478,9 +402,7 @@ cudaError_t launch_attend_rows(const AttnArgs& a, int grid, cudaStream_t st) {
   attend_rows_kernel<<<grid, kThreads, kSmem, st>>>(a);
   note_launch();
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  attend_join_kernel<<<dim3(grid, std::min(kTR, a.m * a.G)), 128, 0, st>>>(a, kTR);
-  note_launch();
-  return cudaGetLastError();
+  return launch_attend_join(a, grid, st);
 }
 
 cudaError_t launch_attend_weights(const AttnArgs& a, cudaStream_t st) {

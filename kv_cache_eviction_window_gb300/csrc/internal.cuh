@@ -204,6 +204,10 @@ int perturb_slices(int D);   // 256-feature slices of W_O rows in the projection
 // (KVSEL_OK, or KVSEL_ECUDA when it cannot be looked up).
 int noalloc_scratch_address(cudaStream_t st, void** out);
 
+// Tensor map over bf16 data: 128-byte swizzle, zeros outside; false when it cannot be encoded.
+bool encode_bf16_map(CUtensorMap* m, const void* ptr, int rank, const cuuint64_t* dims, const cuuint64_t* strides_bytes,
+                     const cuuint32_t* box);
+
 // Raise a kernel's dynamic shared-memory limit once per device (cached).
 cudaError_t ensure_smem(const void* func, size_t bytes);
 

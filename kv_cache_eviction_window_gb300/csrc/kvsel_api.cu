@@ -380,6 +380,17 @@ bool encode(CUtensorMap* m, const void* ptr, int rank, const cuuint64_t* dims, c
   return r == CUDA_SUCCESS;
 }
 
+}  // namespace
+
+namespace kvsel {
+bool encode_bf16_map(CUtensorMap* m, const void* ptr, int rank, const cuuint64_t* dims, const cuuint64_t* strides_bytes,
+                     const cuuint32_t* box) {
+  return encode(m, ptr, rank, dims, strides_bytes, box);
+}
+}  // namespace kvsel
+
+namespace {
+
 // K or V tiles of `rows` tokens.
 bool kv_map(CUtensorMap* m, const void* base, const kvsel_kv* kv, const Plan& pl, int rows) {
   if (kv->layout == KVSEL_LAYOUT_CONTIGUOUS) {

@@ -127,6 +127,24 @@ def test_weights_add_up_over_calls_and_results_repeat():
         assert torch.equal(first[1], c.t["acc"])
 
 
+@pytest.mark.parametrize("m,G", [(1, 7), (6, 7), (100, 7), (200, 3)])
+def test_a_result_does_not_depend_on_the_rest_of_the_batch(m, G):
+    # (groups that do not fill a tile; logits that make the running maxima move)
+    import torch
+
+    c = CH.Case(B=2, G=G, H=1, m=m, lens=[900, 900], scale=0.6, seed=m).upload()
+    c.call(acc=True)
+    first = c.t["out"].clone(), c.t["lse"].clone(), c.t["acc"].clone()
+    for _ in range(5):
+        junk = torch.randn(1 << 22, device="cuda") * 1e30      # another content of the shared memories
+        (junk.view(2048, 2048) @ junk.view(2048, 2048)).sum()
+        c.t["acc"].zero_()
+        c.t["q"][1] *= 1.25
+        c.call(acc=True)
+        for x, y in zip(first, (c.t["out"], c.t["lse"], c.t["acc"])):
+            assert torch.equal(x[0], y[0])
+
+
 def test_lengths_are_read_by_a_captured_call():
     import torch
 
