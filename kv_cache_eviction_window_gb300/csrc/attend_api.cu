@@ -105,6 +105,8 @@ int check_cache(const kvsel_kv* kv, int B, int H, long long rows, const int64_t*
     const int bs = kv->block_size;
     if (!kv->block_table || !aligned(kv->block_table, 4) || !(bs == 8 || bs == 16 || bs == 32 || bs == 64)) return KVSEL_EINVAL;
     if (kv->num_blocks < 1 || kv->max_blocks < (rows + bs - 1) / bs) return KVSEL_EINVAL;
+    // rows of the pool are counted in 32 bits
+    if ((static_cast<long long>(kv->num_blocks) + 1) * bs * H > (1ll << 31) - 1) return KVSEL_EUNSUPPORTED;
   } else {
     return KVSEL_EINVAL;
   }
@@ -127,11 +129,13 @@ bool query_map(CUtensorMap* m, const AttnArgs& a, int block) {
 bool cache_map(CUtensorMap* m, const void* base, const kvsel_kv* kv, const kvsel_attn_params* p) {
   const cuuint64_t H = p->h_kv, B = p->batch;
   if (kv->layout == KVSEL_LAYOUT_PAGED) {
-    const cuuint64_t bs = kv->block_size;
-    const cuuint64_t dims[4] = {kHeadDim, H, bs, static_cast<cuuint64_t>(kv->num_blocks)};
-    const cuuint64_t strides[3] = {kHeadDim * 2, H * kHeadDim * 2, bs * H * kHeadDim * 2};
-    const cuuint32_t box[4] = {64, 1, static_cast<cuuint32_t>(bs), 1};
-    return encode_bf16_map(m, base, 4, dims, strides, box);
+    // a page whole, in atoms of 8 rows x 64 columns: columns, rows of an atom, column halves, atoms of
+    // the page; the last dimension, rows of the pool, places the page and the head in one coordinate
+    const cuuint64_t bs = kv->block_size, row = H * kHeadDim * 2;
+    const cuuint64_t dims[5] = {64, 8, 2, bs / 8, static_cast<cuuint64_t>(kv->num_blocks) * bs * H};
+    const cuuint64_t strides[4] = {row, 128, 8 * row, kHeadDim * 2};
+    const cuuint32_t box[5] = {64, 8, 2, static_cast<cuuint32_t>(bs / 8), 1};
+    return encode_bf16_map(m, base, 5, dims, strides, box);
   }
   const bool packed = kv->layout == KVSEL_LAYOUT_PACKED;
   const cuuint64_t rows = packed ? p->n_rows : p->max_len, tok = static_cast<cuuint64_t>(kv->stride_tok) * 2;

@@ -5,14 +5,22 @@
 // unrounded weights.  P is rounded to bf16 (2^-9 relative at most per weight): V is bf16 and
 // both operands of the product need one type.
 //
-// A CTA works on two streams, each with 128 rows of S and O in TMEM (2 x 128 + 2 x 128 of 512
-// columns; P overwrites the first half of its S):
+// A CTA works on two streams of 128 query rows.  Each has O in TMEM (128 columns) and two S
+// buffers of 64 keys (P overwrites the first half of its S), 512 columns in all: a key tile of
+// 128 is taken in two steps, and the tensor cores form the next step's S while the softmax warps
+// work on this one.  (One buffer of 128 keys per stream had its next product wait for the last
+// one's P: a dependent group of UMMAs costs about 480 cycles beyond its own 64 per UMMA, and a
+// tile pair took 3700-4250 cycles for 2048 of tensor work.  At 64 keys Q K^T is bound by shared
+// memory, 48 cycles per UMMA instead of 32, so a tile pair takes 2560 at least.)
 //   SPLIT = false  an item has two blocks of query rows; both read the same K and V tiles
 //   SPLIT = true   an item has one block; its even and odd key tiles are the two streams, whose
 //                  results are added at the end
 // While one stream's four warps form the weights of a tile, the tensor cores run the other
 // stream's products.  A thread owns one query row, so a row's maximum and sum need no shuffle.
-// Roles: warps 0-3 and 4-7 the streams' softmax, warp 8 issues the UMMAs, warp 9 the TMA loads.
+// Roles: warps 0-3 and 4-7 the streams' softmax; warps 8 and 9 issue the streams' Q K^T, warps 10
+// and 11 their P V; warp 12 the TMA loads.  (A wait behind a group of UMMAs returns only when the
+// group has left its warp's issue queue, about 300 cycles: one warp for all products took 2800
+// cycles per step of both streams, one per stream 2200.)
 //
 // A block holds T = 128 / G tokens (T * G rows, the group's heads side by side), so that K and V
 // tiles serve the whole group.  Items are cut along the cache as in attend_rows_kernel.
@@ -25,11 +33,11 @@ namespace kvsel {
 namespace {
 
 constexpr int kTK = 128;                             // cached rows per tile
-constexpr int kMmaWarp = 8, kLoadWarp = 9;
-constexpr int kThreads = 384;                        // three warpgroups; warps 10 and 11 idle
-// registers per thread: 168 at launch (3 x 168 x 32 per sub-partition), then 208 for the two
-// softmax warpgroups, whose threads hold a row of S, and 88 for the third: 2 x 208 + 88 = 3 x 168
-constexpr int kSoftRegs = 208, kOtherRegs = 88;
+constexpr int kQkWarp = 8, kPvWarp = 10, kLoadWarp = 12;   // + stream
+constexpr int kThreads = 512;                        // four warpgroups; warps 13 to 15 idle
+// registers per thread: 128 at launch (4 x 128 x 32 per sub-partition), then 184 for the two
+// softmax warpgroups and 72 for the others: 2 x 184 + 2 x 72 = 4 x 128
+constexpr int kSoftRegs = 184, kOtherRegs = 72;
 constexpr int kTile = 128 * 256;                     // bytes of one 128 x 128 bf16 tile
 constexpr int kHalf = 128 * 128;                     // its 64-column half
 constexpr int kStages = 5;
@@ -45,13 +53,43 @@ __device__ __forceinline__ void umma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, u
       "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// MN-major operand, 128-byte swizzle: stored [K rows][64 MN elements], 8-row atoms 1024 B apart, the
-// next 64 MN elements one half tile further
-__device__ __forceinline__ uint64_t sdesc_mnmajor(uint32_t saddr) {
+// one lane of a converged warp, the same one every time
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+// K and V stages, 128-byte swizzle: atoms of 8 rows x 64 columns (1024 B).  Contiguous and packed
+// caches: the 16 atoms of columns 0-63, then those of columns 64-127.  Paged: the two atoms of 8
+// rows side by side, so that one box brings a page whole.  (A box costs about 53 cycles beyond 5
+// per 128-byte row: with a box per page and column half, 16-row pages came at 4300 cycles per K
+// and V tile, and 16-byte copies by four warps at 4900.)
+struct StageLayout {
+  uint32_t group, half;                              // bytes to the next 8 rows, to the other 64 columns
+};
+__device__ __forceinline__ StageLayout stage_layout(const AttnArgs& a) {
+  return a.src.paged ? StageLayout{2048u, 1024u} : StageLayout{1024u, static_cast<uint32_t>(kHalf)};
+}
+// K-major operand in such a stage
+__device__ __forceinline__ uint64_t sdesc_stage_k(uint32_t saddr, const StageLayout& l) {
   uint64_t d = 0;
   d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
-  d |= static_cast<uint64_t>(kHalf >> 4) << 16;
-  d |= static_cast<uint64_t>(1024u >> 4) << 32;
+  d |= static_cast<uint64_t>(1u) << 16;
+  d |= static_cast<uint64_t>(l.group >> 4) << 32;
+  d |= static_cast<uint64_t>(1u) << 46;
+  d |= static_cast<uint64_t>(2u) << 61;
+  return d;
+}
+// MN-major operand in such a stage
+__device__ __forceinline__ uint64_t sdesc_stage_v(uint32_t saddr, const StageLayout& l) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(l.half >> 4) << 16;
+  d |= static_cast<uint64_t>(l.group >> 4) << 32;
   d |= static_cast<uint64_t>(1u) << 46;
   d |= static_cast<uint64_t>(2u) << 61;
   return d;
@@ -112,8 +150,8 @@ __device__ __forceinline__ void load_tile(const AttnArgs& a, const ItemRange& x,
   if (lane == 0) mbar_arrive_expect_tx(bar, pages * bs * 256);
   __syncwarp();
   if (live) {
-    tma_load_4d(dst + lane * bs * 128, map, bar, 0, x.h, 0, pb);
-    tma_load_4d(dst + kHalf + lane * bs * 128, map, bar, 64, x.h, 0, pb);
+    // the last dimension counts rows of the pool: (block, slot 0, head)
+    tma_load_5d(dst + lane * bs * 256, map, bar, 0, 0, 0, 0, pb * (bs * a.H) + x.h);
   }
 }
 
@@ -125,8 +163,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* smem = smem_align1024(smem_raw);
   uint8_t* sQ = smem;                                // two blocks (SPLIT: one, then the exchange buffer)
   uint8_t* sKV = smem + 2 * kTile;
-  __shared__ __align__(8) uint64_t qfull, qempty, kvfull[kStages], kvempty[kStages], sfull[2], pfull[2], pv[2], done;
-  __shared__ __align__(8) uint64_t xfull, xempty;
+  __shared__ __align__(8) uint64_t qfull, qempty, kvfull[kStages], kvempty[kStages], sfull[2][2], pfull[2][2], pv[2][2], done;
+  __shared__ __align__(8) uint64_t xfull, xempty, vfix[4];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   __shared__ float2 s_ml[128];
@@ -135,17 +173,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     a.rec[blockIdx.x] = make_int4(-1, 0, 0, 0);
     mbar_init(&qfull, 1);
-    mbar_init(&qempty, 1);
+    mbar_init(&qempty, 2);
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&kvfull[s], 1);
-      mbar_init(&kvempty[s], 1);
+      mbar_init(&kvempty[s], SPLIT ? 1 : 2);         // both streams read a tile, or one
     }
-    for (int w = 0; w < 2; ++w) {
-      mbar_init(&sfull[w], 1);
-      mbar_init(&pfull[w], 4);
-      mbar_init(&pv[w], 1);
-    }
-    mbar_init(&done, 1);
+    for (int u = 0; u < 4; ++u) mbar_init(&vfix[u], 4);
+    for (int w = 0; w < 2; ++w)
+      for (int u = 0; u < 2; ++u) {
+        mbar_init(&sfull[w][u], 1);
+        mbar_init(&pfull[w][u], 4);
+        mbar_init(&pv[w][u], 1);
+      }
+    mbar_init(&done, 4);
     mbar_init(&xfull, 4);
     mbar_init(&xempty, 4);
     s_abort = 0;
@@ -153,17 +193,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   const Share sh = share_of<kTK, kThreads>(a, blockIdx.x);
   if (static_cast<int>(blockIdx.x) >= sh.grid) return;   // the whole CTA
-  if (warp == kMmaWarp) {
+  if (warp == kQkWarp) {
     tmem_alloc(&s_tmem, 512);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tbase = s_tmem;                     // S0, S1: columns 0, 128; O0, O1: 256, 384
+  const uint32_t tbase = s_tmem;                     // S of stream w, buffer u: column 128 w + 64 u; O: 256 + 128 w
   constexpr int nblk = SPLIT ? 1 : 2;                // query blocks per item
+  constexpr int nstr = SPLIT ? 2 : 1;                // key tiles that the streams take at a time
 
-  if (warp >= kMmaWarp) regs_down<kOtherRegs>();
+  if (warp >= kQkWarp) regs_down<kOtherRegs>();
   if (warp == kLoadWarp) {
     if (lane == 0) {
       tma_prefetch_desc(&tq);
@@ -201,11 +242,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++use;
       };
       // the order in which the MMA warp takes the tiles
-      constexpr int ahead = SPLIT ? 2 : 1;
-      for (int i = 0; i < ahead && i < cnt && ok; ++i) load(i, false);
-      for (int i = 0; i < cnt && ok; ++i) {
-        load(i, true);
-        if (ok && i + ahead < cnt) load(i + ahead, false);
+      for (int i = 0; i < cnt && ok; i += nstr) {
+        for (int w = 0; w < nstr && i + w < cnt && ok; ++w) load(i + w, false);
+        for (int w = 0; w < nstr && i + w < cnt && ok; ++w) load(i + w, true);
       }
       base += x.tiles;
       at = base;
@@ -219,119 +258,89 @@ __global__ void __launch_bounds__(kThreads, 1)
         ring_tail(&qempty, 1, piece, &s_abort, a.wc);
       }
     }
-  } else if (warp == kMmaWarp) {
-    if (lane == 0) {
-      constexpr uint32_t idesc_s = idesc_bf16_f32(128, 128);
-      constexpr uint32_t idesc_o = idesc_bf16_f32(128, 128) | (1u << 16);   // B (V) MN-major
-      int use = 0, piece = 0;
-      int np[2] = {0, 0};                            // tiles of each stream so far
-      bool ok = true;
-      auto wait_stage = [&](int u) {
-        ok = ok && mbar_wait(&kvfull[u % kStages], (u / kStages) & 1, &s_abort, a.wc);
-        tc_fence_after();
-      };
-      auto qk = [&](int w, int u) {
-        const uint64_t qd = sdesc_kmajor_sw128(smem_u32(sQ + (SPLIT ? 0 : w) * kTile));
-        const uint64_t kd = sdesc_kmajor_sw128(smem_u32(sKV + (u % kStages) * kTile));
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const uint32_t off = ((k >> 2) * kHalf + (k & 3) * 32) >> 4;
-          umma_bf16(tbase + w * 128, qd + off, kd + off, idesc_s, k ? 1u : 0u);
-        }
-        umma_commit(&sfull[w]);
-      };
-      // O_w (+)= P_w V once the weights are in TMEM
-      auto pvm = [&](int w, int u, bool first) {
-        ok = ok && mbar_wait(&pfull[w], np[w] & 1, &s_abort, a.wc);
-        if (!ok) return;
-        tc_fence_after();
-        const uint32_t vb = smem_u32(sKV + (u % kStages) * kTile);
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          umma_bf16_ta(tbase + 256 + w * 128, tbase + w * 128 + k * 8, sdesc_mnmajor(vb + k * 2048), idesc_o,
-                       (first && k == 0) ? 0u : 1u);
-        umma_commit(&pv[w]);
-        ++np[w];
-      };
-      // S_w is written again only after the product that reads P_w in its place
-      auto wait_pv = [&](int w) {
-        if (np[w]) ok = ok && mbar_wait(&pv[w], (np[w] - 1) & 1, &s_abort, a.wc);
-        tc_fence_after();
-      };
-      auto release = [&](int u) { umma_commit(&kvempty[u % kStages]); };
-      long long base = sh.item_base, at = sh.begin;
-      for (int item = sh.item; ok && at < sh.end; ++item) {
-        const ItemRange x = item_range<kTK>(a, item);
-        if (x.tiles == 0) continue;
-        const int cnt = static_cast<int>(min(static_cast<long long>(x.tiles), sh.end - base) - (at - base));
-        ok = mbar_wait(&qfull, piece & 1, &s_abort, a.wc);
-        if (!ok) break;
-        tc_fence_after();
-        ++piece;
-        if (SPLIT) {
-          for (int w = 0; w < 2 && w < cnt && ok; ++w) {
-            wait_stage(use);
-            wait_pv(w);
-            if (!ok) break;
-            qk(w, use);
-            release(use++);
-          }
-          for (int i = 0; i < cnt && ok; ++i) {
-            const int w = i & 1;
-            wait_stage(use);
-            pvm(w, use, i < 2);
-            if (!ok) break;
-            release(use++);
-            if (i + 2 < cnt) {
-              wait_stage(use);
-              wait_pv(w);
-              if (!ok) break;
-              qk(w, use);
-              release(use++);
-            }
-          }
-        } else {
-          wait_stage(use);
-          for (int w = 0; w < 2 && ok; ++w) {
-            wait_pv(w);
-            if (ok) qk(w, use);
-          }
+  } else if (warp >= kQkWarp && warp < kLoadWarp) {
+    // the whole warp follows the loop and one elected lane issues, so that descriptors stay in
+    // uniform registers
+    const int w = warp & 1;
+    const bool is_qk = warp < kPvWarp;
+    constexpr uint32_t idesc_s = idesc_bf16_f32(128, 64);
+    constexpr uint32_t idesc_o = idesc_bf16_f32(128, 128) | (1u << 16);   // B (V) MN-major
+    int use = 0, piece = 0, g = 0;                   // ring uses before this piece; pieces; steps
+    bool ok = true;                                  // the same in every lane
+    auto wait = [&](uint64_t* bar, int phase) {
+      ok = __all_sync(0xffffffffu, ok && mbar_wait(bar, static_cast<uint32_t>(phase & 1), &s_abort, a.wc));
+    };
+    auto commit = [&](uint64_t* bar) {
+      if (elect_one()) umma_commit(bar);
+      __syncwarp();
+    };
+    const uint64_t qd = sdesc_kmajor_sw128(smem_u32(sQ + (SPLIT ? 0 : w) * kTile));
+    const StageLayout lay = stage_layout(a);
+    const uint64_t kd0 = sdesc_stage_k(smem_u32(sKV), lay), vd0 = sdesc_stage_v(smem_u32(sKV), lay);
+    const uint32_t sub_step = (8 * lay.group) >> 4, k_step = (2 * lay.group) >> 4, khalf = lay.half >> 4;   // 64 rows, 16 rows
+    const uint32_t tS = tbase + w * 128, tO = tbase + 256 + w * 128;
+    long long base = sh.item_base, at = sh.begin;
+    for (int item = sh.item; ok && at < sh.end; ++item) {
+      const ItemRange x = item_range<kTK>(a, item);
+      if (x.tiles == 0) continue;
+      const int cnt = static_cast<int>(min(static_cast<long long>(x.tiles), sh.end - base) - (at - base));
+      const int steps = 2 * (SPLIT ? (cnt + 1 - w) / 2 : cnt);   // of this stream: key tile n / 2, buffer n & 1
+      if (is_qk) {
+        wait(&qfull, piece);
+        for (int n = 0; n < steps && ok; ++n, ++g) {
+          const int c = n >> 1, u = n & 1, k = use + (SPLIT ? 4 * c + w : 2 * c);   // ring use of the K tile
+          if (u == 0) wait(&kvfull[k % kStages], k / kStages);
+          // the buffer is free when the product that read the last P in it is done
+          if (g >= 2) wait(&pv[w][u], (g >> 1) - 1);
           if (!ok) break;
-          release(use++);
-          for (int i = 0; i < cnt && ok; ++i) {
-            const int uv = use;
-            const bool more = i + 1 < cnt;
-            wait_stage(uv);
-            for (int w = 0; w < 2 && ok; ++w) {
-              pvm(w, uv, i == 0);
-              if (!ok) break;
-              if (w == 1) release(uv);
-              if (more) {
-                if (w == 0) wait_stage(uv + 1);
-                wait_pv(w);
-                if (ok) qk(w, uv + 1);
-              }
+          tc_fence_after();
+          const uint64_t kd = kd0 + (k % kStages) * (kTile >> 4) + u * sub_step;
+          if (elect_one()) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const uint32_t in = ((i & 3) * 32) >> 4;
+              umma_bf16(tS + u * 64, qd + (i >> 2) * (kHalf >> 4) + in, kd + (i >> 2) * khalf + in, idesc_s, i ? 1u : 0u);
             }
-            if (!ok) break;
-            if (more) release(uv + 1);
-            use += more ? 2 : 1;
+            umma_commit(&sfull[w][u]);
+            if (u == 1) umma_commit(&kvempty[k % kStages]);
           }
+          __syncwarp();
         }
-        if (!ok) break;
-        umma_commit(&qempty);
-        base += x.tiles;
-        at = base;
+        if (ok) commit(&qempty);
+      } else {
+        for (int n = 0; n < steps && ok; ++n, ++g) {
+          const int c = n >> 1, u = n & 1;
+          const int v = use + (SPLIT ? (2 * c + 1 < cnt ? 4 * c + 2 + w : 4 * c + 1) : 2 * c + 1);
+          if (u == 0) wait(&kvfull[v % kStages], v / kStages);
+          wait(&pfull[w][u], g >> 1);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t vd = vd0 + (v % kStages) * (kTile >> 4) + u * sub_step;
+          if (elect_one()) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              umma_bf16_ta(tO, tS + u * 64 + i * 8, vd + i * k_step, idesc_o, (n == 0 && i == 0) ? 0u : 1u);
+            umma_commit(&pv[w][u]);
+            if (u == 1) umma_commit(&kvempty[v % kStages]);
+          }
+          __syncwarp();
+        }
       }
-      // every product issued has been done before TMEM is freed
-      umma_commit(&done);
-      mbar_drain(&done, 0, a.wc.status);
+      ++piece;
+      use += 2 * cnt;
+      base += x.tiles;
+      at = base;
     }
-  } else if (warp < kMmaWarp) {
+    // every product issued has been done before TMEM is freed
+    commit(&done);
+    if (lane == 0 && warp == kQkWarp) mbar_drain(&done, 0, a.wc.status);
+  } else if (warp < kQkWarp) {
     regs_up<kSoftRegs>();
     const int w = warp >> 2, row = threadIdx.x & 127;   // stream, query row within the block (TMEM lane)
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t tS = tbase + w * 128 + lanes, tO = tbase + 256 + w * 128 + lanes;
-    int np = 0, use = 0, nx = 0;                     // tiles of this stream; ring uses before this piece; exchanges
+    const uint32_t tS0 = tbase + w * 128 + lanes, tO = tbase + 256 + w * 128 + lanes;
+    // steps of this stream; ring uses before this piece; exchanges; tiles with unseen rows
+    int g = 0, use = 0, nx = 0, nfix = 0;
     bool ok = true;                                  // the same in every lane of a warp
     auto wait = [&](uint64_t* bar, int phase) {
       ok = __all_sync(0xffffffffu, ok && mbar_wait(bar, static_cast<uint32_t>(phase & 1), &s_abort, a.wc));
@@ -351,39 +360,41 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int pa = a.causal ? x.n - x.m + (x.rt * a.tr + first_row) / a.G : x.n - 1;
       const int pb = a.causal ? x.n - x.m + (x.rt * a.tr + first_row + max(rows, 1) - 1) / a.G : x.n - 1;
       float ref = -INFINITY, sum = 0.f;
-      int mine = 0;                                  // tiles of this piece so far
-      for (int i = SPLIT ? w : 0; i < cnt; i += SPLIT ? 2 : 1) {
+      int mine = 0;                                  // steps of this piece so far
+      const int steps = 2 * (SPLIT ? (cnt + 1 - w) / 2 : cnt);
+      for (; mine < steps; ++mine, ++g) {
+        const int u = mine & 1, i = SPLIT ? (mine & ~1) + w : mine >> 1;   // buffer; tile of the piece
+        const uint32_t tS = tS0 + u * 64;
         int j0, j1;
         tile_rows<kTK>(x, ta + i, j0, j1);
-        wait(&sfull[w], np);
+        const int js = j0 + u * 64;                  // first key of the step
+        wait(&sfull[w][u], g >> 1);
         if (!ok) break;
         tc_fence_after();
-        float s[128];
+        float s[64];
         tmem_ld32(tS, s);
         tmem_ld32(tS + 32, s + 32);
-        tmem_ld32(tS + 64, s + 64);
-        tmem_ld32(tS + 96, s + 96);
         tmem_ld_wait();
-        const bool whole = j0 + kTK <= j1 && (!a.causal || (j0 + kTK <= pa + 1 &&
-                                                            (a.window <= 0 || j0 > pb - a.window || j0 + kTK <= a.n_sink)));
+        const bool whole = js + 64 <= j1 && (!a.causal || (js + 64 <= pa + 1 &&
+                                                           (a.window <= 0 || js > pb - a.window || js + 64 <= a.n_sink)));
         if (!whole) {
           // a row sees columns [0, hi) and, with a window, of these [lo, hi) and those below `first`
-          const int hi = min(j1, a.causal ? p + 1 : j1) - j0;
-          const int lo = a.window > 0 ? p - a.window + 1 - j0 : -1, first = a.window > 0 ? a.n_sink - j0 : 0;
+          const int hi = min(j1, a.causal ? p + 1 : j1) - js;
+          const int lo = a.window > 0 ? p - a.window + 1 - js : -1, first = a.window > 0 ? a.n_sink - js : 0;
 #pragma unroll
-          for (int c = 0; c < 128; ++c)
+          for (int c = 0; c < 64; ++c)
             if (c >= hi || (c < lo && c >= first)) s[c] = -INFINITY;
         }
         float t0 = s[0], t1 = s[1], t2 = s[2], t3 = s[3];
 #pragma unroll
-        for (int c = 4; c < 124; c += 8) {
+        for (int c = 4; c < 60; c += 8) {
           t0 = fmax3(t0, s[c], s[c + 1]);
           t1 = fmax3(t1, s[c + 2], s[c + 3]);
           t2 = fmax3(t2, s[c + 4], s[c + 5]);
           t3 = fmax3(t3, s[c + 6], s[c + 7]);
         }
-        t0 = fmax3(t0, s[124], s[125]);
-        t1 = fmax3(t1, s[126], s[127]);
+        t0 = fmax3(t0, s[60], s[61]);
+        t1 = fmax3(t1, s[62], s[63]);
         const float top = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)) * a.s2;
         if (__any_sync(0xffffffffu, top > ref + 8.f)) {
           // each row by its own maximum: a result does not depend on the rows next to it
@@ -392,7 +403,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           ref = r2;
           sum *= f;
           if (mine > 0) {
-            // the products that wrote O are done: S of this tile was formed after them
+            // after the product of the step before, the last that writes O until this P is there
+            wait(&pv[w][u ^ 1], (g - 1) >> 1);
+            if (!ok) break;
+            tc_fence_after();
 #pragma unroll
             for (int c0 = 0; c0 < 128; c0 += 16) {
               uint32_t y[16];
@@ -408,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t sc2 = pack2(a.s2, a.s2), off2 = pack2(off, off);
         uint64_t acc0 = pack2(0.f, 0.f), acc1 = acc0;
 #pragma unroll
-        for (int c0 = 0; c0 < 128; c0 += 32) {
+        for (int c0 = 0; c0 < 64; c0 += 32) {
           uint32_t pk[16];
 #pragma unroll
           for (int c = 0; c < 32; c += 2) {
@@ -430,36 +444,42 @@ __global__ void __launch_bounds__(kThreads, 1)
           sum += y0 + y1;
         }
         // V rows that the item does not see may hold anything; their weights are zero, and the
-        // rows become zero before the product reads them.  (!SPLIT: stream 0 does it for both,
-        // its product is issued first.)
-        if ((SPLIT || w == 0) &&
-            (j0 + kTK > j1 || (a.window > 0 && j0 <= x.p0 - a.window && j0 + kTK > a.n_sink))) {
-          // ring use of this tile's V
-          const int uv = SPLIT ? use + min(cnt, 2) + i + max(0, min(i, cnt - 2)) : use + 1 + 2 * i;
-          wait(&kvfull[uv % kStages], uv / kStages);
-          if (!ok) break;
-          if (unseen(a, x, j0 + row, j1)) {
-            uint8_t* d = sKV + (uv % kStages) * kTile + row * 128;
+        // rows become zero before the tile's first product reads them.  Without SPLIT stream 0 does
+        // it for both; it is at most two tiles ahead, so four barriers in turn tell stream 1.
+        if (u == 0 && (j0 + kTK > j1 || (a.window > 0 && j0 <= x.p0 - a.window && j0 + kTK > a.n_sink))) {
+          if (SPLIT || w == 0) {
+            const int uv = use + (SPLIT ? (i - w + 1 < cnt ? 2 * (i - w) + 2 + w : 2 * (i - w) + 1) : 2 * i + 1);
+            wait(&kvfull[uv % kStages], uv / kStages);
+            if (!ok) break;
+            if (unseen(a, x, j0 + row, j1)) {
+              const StageLayout lay = stage_layout(a);
+              uint8_t* d = sKV + (uv % kStages) * kTile + (row >> 3) * lay.group + (row & 7) * 128;
 #pragma unroll
-            for (int c = 0; c < 8; ++c) {
-              *reinterpret_cast<uint4*>(d + c * 16) = make_uint4(0u, 0u, 0u, 0u);
-              *reinterpret_cast<uint4*>(d + kHalf + c * 16) = make_uint4(0u, 0u, 0u, 0u);
+              for (int c = 0; c < 8; ++c) {
+                *reinterpret_cast<uint4*>(d + c * 16) = make_uint4(0u, 0u, 0u, 0u);
+                *reinterpret_cast<uint4*>(d + lay.half + c * 16) = make_uint4(0u, 0u, 0u, 0u);
+              }
             }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (!SPLIT && lane == 0) mbar_arrive(&vfix[nfix & 3]);
+          } else {
+            wait(&vfix[nfix & 3], nfix >> 2);
+            if (!ok) break;
+            fence_proxy_async_smem();
           }
-          fence_proxy_async_smem();
+          ++nfix;
         }
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&pfull[w]);
-        ++np;
-        ++mine;
+        if (lane == 0) mbar_arrive(&pfull[w][u]);
       }
       use += 2 * cnt;                                // a K and a V tile each
 
       // results of this piece
       const bool first = ta == 0, last = tb == x.tiles, direct = first && last;
-      if (mine > 0) wait(&pv[w], np - 1);
+      if (mine > 0) wait(&pv[w][1], (g - 1) >> 1);
       if (!ok) break;
       tc_fence_after();
       const bool live = row < rows && (!SPLIT || w == 0);
@@ -546,7 +566,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (warp == kMmaWarp) {
+  if (warp == kQkWarp) {
     tc_fence_after();
     tmem_dealloc(tbase, 512);
   }
