@@ -25,6 +25,8 @@ struct AttnArgs {
   long long o_req, o_head, o_tok;
   float* lse;                     // [B][H*G][m] natural log, or null
   float* lse2;                    // [B][H][m*G] log2 units, for the weights, or null
+  float* logits;                  // [B*H][m*G][logit_stride], log2 units, masked: -inf (m*G <= 16), or null
+  long long logit_stride;
   float* acc;                     // [B*H][acc_stride] or null
   long long acc_stride;
   KvSource src;
@@ -106,8 +108,9 @@ __device__ __forceinline__ ItemRange item_range(const AttnArgs& a, int item) {
   }
   if (a.window > 0) {
     const int lo = max(0, x.p0 - a.window + 1);
-    // pages behind the window may be gone: a tile starts with the first page that is seen
-    const int al = a.src.paged ? lo - lo % a.src.block_size : lo;
+    // pages behind the window may be gone: a tile starts with the first page that is seen; at an
+    // even row otherwise (two logits are kept at a time)
+    const int al = lo - lo % (a.src.paged ? a.src.block_size : 2);
     const int sink = min(a.n_sink, x.hi);
     const int ns = (sink + TK - 1) / TK;
     if (lo > sink && al > ns * TK) {
@@ -142,16 +145,15 @@ struct Share {
   int item;                       // item of tile `begin`
   long long item_base;            // its first tile
 };
-template <int TK, int THREADS>
-__device__ __forceinline__ Share share_of(const AttnArgs& a, int cta) {
+template <int THREADS, class Tiles>
+__device__ __forceinline__ Share share_of(int items, Tiles tiles, int cta) {
   __shared__ long long s_warp[THREADS / 32];
   __shared__ long long s_base;
   __shared__ int s_item;
-  const int items = a.B * a.H * a.rt;
   const int per = (items + THREADS - 1) / THREADS;
   const int i0 = min(items, static_cast<int>(threadIdx.x) * per), i1 = min(items, i0 + per);
   long long sum = 0;
-  for (int i = i0; i < i1; ++i) sum += item_range<TK>(a, i).tiles;
+  for (int i = i0; i < i1; ++i) sum += tiles(i);
   long long inc = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -178,7 +180,7 @@ __device__ __forceinline__ Share share_of(const AttnArgs& a, int cta) {
       long long at = before;
       int i = i0;
       for (; i < i1; ++i) {
-        const int c = item_range<TK>(a, i).tiles;
+        const int c = tiles(i);
         if (sh.begin < at + c) break;
         at += c;
       }
@@ -235,6 +237,94 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// K and V stages of the UMMA kernels, 128-byte swizzle: atoms of 8 rows x 64 columns (1024 B).
+// Contiguous and packed caches: the 16 atoms of columns 0-63, then those of columns 64-127.
+// Paged: the two atoms of 8 rows side by side, so that one box brings a page whole.  (A box costs
+// about 53 cycles beyond 5 per 128-byte row: with a box per page and column half, 16-row pages
+// came at 4300 cycles per K and V tile, and 16-byte copies by four warps at 4900.)
+constexpr int kTileBytes = 128 * 256;                // one 128 x 128 bf16 tile
+constexpr int kHalfBytes = 128 * 128;                // its 64-column half
+struct StageLayout {
+  uint32_t group, half;                              // bytes to the next 8 rows, to the other 64 columns
+};
+__device__ __forceinline__ StageLayout stage_layout(const AttnArgs& a) {
+  return a.src.paged ? StageLayout{2048u, 1024u} : StageLayout{1024u, static_cast<uint32_t>(kHalfBytes)};
+}
+// K-major operand in such a stage
+__device__ __forceinline__ uint64_t sdesc_stage_k(uint32_t saddr, const StageLayout& l) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(1u) << 16;
+  d |= static_cast<uint64_t>(l.group >> 4) << 32;
+  d |= static_cast<uint64_t>(1u) << 46;
+  d |= static_cast<uint64_t>(2u) << 61;
+  return d;
+}
+// 128 rows of a segment from row j0 (those below j1) into such a stage, by the lanes of a warp.
+// live(first, last): whether any row of a page is seen; other pages are not looked up.
+template <class Live>
+__device__ __forceinline__ void load_rows_tile(const AttnArgs& a, int b, int h, long long row0, const CUtensorMap* map,
+                                               int j0, int j1, uint8_t* dst, uint64_t* bar, Live seen) {
+  const int lane = lane_id();
+  if (!a.src.paged) {
+    if (lane == 0) {
+      mbar_arrive_expect_tx(bar, kTileBytes);
+      const int row = static_cast<int>(row0) + j0;
+      tma_load_4d(dst, map, bar, 0, row, a.offsets ? 0 : h, a.offsets ? 0 : b);
+      tma_load_4d(dst + kHalfBytes, map, bar, 64, row, a.offsets ? 0 : h, a.offsets ? 0 : b);
+    }
+    return;
+  }
+  const int bs = a.src.block_size, at = j0 + lane * bs;   // lane i: page i of the tile
+  const bool live = lane < 128 / bs && at < j1 && seen(at, at + bs - 1);
+  int pb = 0;
+  if (live) {
+    pb = __ldg(a.src.block_table + static_cast<size_t>(b) * a.src.max_blocks + at / bs);
+    if (pb < 0 || pb >= a.src.num_blocks) {
+      atomicOr(a.wc.status, DEV_BAD_INDEX);
+      pb = a.src.num_blocks;                         // outside the pool: zeros
+    }
+  }
+  const unsigned pages = __popc(__ballot_sync(0xffffffffu, live));
+  if (lane == 0) mbar_arrive_expect_tx(bar, pages * bs * 256);
+  __syncwarp();
+  // the last dimension counts rows of the pool: (block, slot 0, head)
+  if (live) tma_load_5d(dst + lane * bs * 256, map, bar, 0, 0, 0, 0, pb * (bs * a.H) + h);
+}
+// one lane of a converged warp, the same one every time
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
+// Programmatic dependent launch: a kernel's CTAs may start while the one before it on the stream
+// ends; what that one wrote is read behind after_previous().  Every CTA calls it, so that a
+// kernel's end implies the end of all before it.
+__device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+template <class... Params, class... Args>
+cudaError_t launch_after(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t st, Args... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+  if (e != cudaSuccess) return e;
+  note_launch();
+  return cudaGetLastError();
+}
+
 // a few rows per item (a.tr = attend_rows_tile())
 cudaError_t launch_attend_rows(const AttnArgs& a, int grid, cudaStream_t st);
 int attend_rows_tile();
@@ -246,6 +336,11 @@ cudaError_t launch_attend_tile(const AttnArgs& a, const CUtensorMap& tq, const C
 int attend_tile_keys();           // cached rows per tile
 // joins the pieces of items that several CTAs of either kernel share
 cudaError_t launch_attend_join(const AttnArgs& a, int grid, cudaStream_t st);
-cudaError_t launch_attend_weights(const AttnArgs& a, cudaStream_t st);
+// acc += the weights of every cached row: from the logits that attend_rows_kernel kept ...
+cudaError_t launch_weights_kept(const AttnArgs& a, cudaStream_t st);
+// ... or from Q K^T formed again on tcgen05 (rec, part_ml as for the tile kernel: they are free
+// again; part: [2 * grid][256])
+cudaError_t launch_weights_tile(const AttnArgs& a, const CUtensorMap& tq, const CUtensorMap& tk, int block, float* part,
+                                int grid, cudaStream_t st);
 
 }  // namespace kvsel

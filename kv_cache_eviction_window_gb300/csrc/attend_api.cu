@@ -30,7 +30,8 @@ struct AttnPlan {
   int grid = 0, tr = 0, rt = 1;
   bool tiled = false, split = false;
   int block = 0;                 // tiled: query rows per block, whole tokens of the group
-  size_t rec = 0, ml = 0, o = 0, lse2 = 0, total = 0;
+  size_t rec = 0, ml = 0, o = 0, lse2 = 0, wpart = 0, logits = 0, total = 0;
+  long long logit_stride = 0;
 };
 
 // a stride matters only where its dimension has more than one entry
@@ -86,7 +87,16 @@ int plan_attn(const kvsel_attn_params* p, bool with_acc, AttnPlan& pl) {
   off = align256(off + sizeof(float) * 2 * pl.grid * pl.tr * kHeadDim);
   if (with_acc) {
     pl.lse2 = off;
-    off = align256(off + sizeof(float) * p->batch * p->h_kv * p->n_new * p->group);
+    const size_t rows = static_cast<size_t>(p->batch) * p->h_kv * R;
+    off = align256(off + sizeof(float) * rows);
+    if (pl.tiled) {
+      pl.wpart = off;
+      off = align256(off + sizeof(float) * 2 * pl.grid * 256);
+    } else {
+      pl.logits = off;
+      pl.logit_stride = (static_cast<long long>(p->max_len) + 7) / 8 * 8;
+      off = align256(off + sizeof(float) * rows * pl.logit_stride);
+    }
   }
   pl.total = off;
   return KVSEL_OK;
@@ -242,6 +252,8 @@ int kvsel_attend(const kvsel_attn_params* p, const void* q, const kvsel_kv* kv, 
   a.o_tok = od ? kHeadDim : p->o_stride_tok;
   a.lse = lse;
   a.lse2 = acc ? reinterpret_cast<float*>(wsb + pl.lse2) : nullptr;
+  a.logits = acc && !pl.tiled ? reinterpret_cast<float*>(wsb + pl.logits) : nullptr;
+  a.logit_stride = pl.logit_stride;
   a.acc = acc;
   a.acc_stride = p->acc_stride;
   a.src = source_of(kv);
@@ -261,13 +273,13 @@ int kvsel_attend(const kvsel_attn_params* p, const void* q, const kvsel_kv* kv, 
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (!pl.tiled) {
     rc = launch_rc(launch_attend_rows(a, pl.grid, st));
-  } else {
-    CUtensorMap tq, tk, tv;
-    if (!query_map(&tq, a, pl.block) || !cache_map(&tk, kv->k, kv, p) || !cache_map(&tv, kv->v, kv, p)) return KVSEL_EINVAL;
-    rc = launch_rc(launch_attend_tile(a, tq, tk, tv, pl.block, pl.split, pl.grid, st));
+    return rc || !acc ? rc : launch_rc(launch_weights_kept(a, st));
   }
-  if (rc) return rc;
-  return acc ? launch_rc(launch_attend_weights(a, st)) : KVSEL_OK;
+  CUtensorMap tq, tk, tv;
+  if (!query_map(&tq, a, pl.block) || !cache_map(&tk, kv->k, kv, p) || !cache_map(&tv, kv->v, kv, p)) return KVSEL_EINVAL;
+  rc = launch_rc(launch_attend_tile(a, tq, tk, tv, pl.block, pl.split, pl.grid, st));
+  if (rc || !acc) return rc;
+  return launch_rc(launch_weights_tile(a, tq, tk, pl.block, reinterpret_cast<float*>(wsb + pl.wpart), pl.grid, st));
 }
 
 int kvsel_evict_append_workspace_size(const kvsel_evict_params* p, size_t* bytes) {

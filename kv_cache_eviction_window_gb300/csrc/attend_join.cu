@@ -33,6 +33,8 @@ template <int WPR>
 __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(const AttnArgs a) {
   __shared__ float4 s_y[kJoinWarps][32];
   __shared__ float2 s_ml[kJoinWarps];
+  let_next_start();
+  after_previous();
   const int4 rec = a.rec[blockIdx.x];
   if (rec.x < 0) return;
   const int seg = rec.x / a.rt, rt = rec.x - seg * a.rt;
@@ -76,11 +78,8 @@ cudaError_t launch_attend_join(const AttnArgs& a, int grid, cudaStream_t st) {
   const int rows = static_cast<int>(std::min<long long>(a.tr, static_cast<long long>(a.m) * a.G));
   // pieces per item: about grid / items
   if (static_cast<long long>(a.B) * a.H * a.rt * 8 < grid)
-    attend_join_kernel<4><<<dim3(grid, std::min(rows, 64)), kJoinWarps * 32, 0, st>>>(a);
-  else
-    attend_join_kernel<1><<<dim3(grid, std::min((rows + 3) / 4, 16)), kJoinWarps * 32, 0, st>>>(a);
-  note_launch();
-  return cudaGetLastError();
+    return launch_after(attend_join_kernel<4>, dim3(grid, std::min(rows, 64)), kJoinWarps * 32, 0, st, a);
+  return launch_after(attend_join_kernel<1>, dim3(grid, std::min((rows + 3) / 4, 16)), kJoinWarps * 32, 0, st, a);
 }
 
 }  // namespace kvsel

@@ -68,7 +68,9 @@ __global__ void __launch_bounds__(kThreads, 2) attend_rows_kernel(const AttnArgs
   const int warp = warp_id(), lane = lane_id();
   const int quad = lane >> 2, ql = lane & 3;
   if (threadIdx.x == 0) a.rec[blockIdx.x] = make_int4(-1, 0, 0, 0);
-  const Share sh = share_of<kTK, kThreads>(a, blockIdx.x);
+  let_next_start();
+  const Share sh =
+      share_of<kThreads>(a.B * a.H * a.rt, [&](int i) { return item_range<kTK>(a, i).tiles; }, blockIdx.x);
   if (static_cast<int>(blockIdx.x) >= sh.grid) return;
   const uint32_t ring = smem_u32(smem) + warp * (kStages * kStageBytes);
   float* s_o = reinterpret_cast<float*>(smem);
@@ -188,6 +190,21 @@ __global__ void __launch_bounds__(kThreads, 2) attend_rows_kernel(const AttnArgs
         top[u2] = fmaxf(top[u2], __shfl_xor_sync(0xffffffffu, top[u2], 1));
         top[u2] = fmaxf(top[u2], __shfl_xor_sync(0xffffffffu, top[u2], 2));
       }
+      if (a.logits) {
+        // kept for the weights, which need the whole row's sum first (4 B per row and query row
+        // instead of reading K again)
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+          for (int u2 = 0; u2 < 2; ++u2) {
+            const int r = quad + 8 * u2, j = j0 + nt * 8 + ql * 2;
+            float* d = a.logits + (static_cast<long long>(x.seg) * a.m * a.G + r) * a.logit_stride + j;
+            if (r < x.rows && j + 1 < j1)
+              *reinterpret_cast<float2*>(d) = make_float2(p[nt][2 * u2], p[nt][2 * u2 + 1]);
+            else if (r < x.rows && j < j1)
+              *d = p[nt][2 * u2];
+          }
+      }
       if (__any_sync(0xffffffffu, top[0] > ref[0] + 8.f || top[1] > ref[1] + 8.f)) {
         float f[2];
 #pragma unroll
@@ -295,100 +312,28 @@ __global__ void __launch_bounds__(kThreads, 2) attend_rows_kernel(const AttnArgs
   }
 }
 
-// Accumulated weights: acc_j += sum over query rows r of exp2(s2 <q_r, k_j> - lse2_r).  A CTA
-// owns 64 cached rows of one segment (16 per warp, the mma's A operand, loaded once into
-// registers) and streams the query rows that see any of them; each thread adds up its own
-// cached rows, so the order of additions is fixed.
-constexpr int kWRows = 64;                           // query rows per step
-__global__ void __launch_bounds__(kThreads) attend_weights_kernel(const AttnArgs a) {
-  __shared__ __align__(128) uint8_t s_q[kWRows * 256];
-  __shared__ float s_e[kWRows];
-  const int seg = blockIdx.y, b = seg / a.H, h = seg - b * a.H;
-  const SegLen s = seg_len(a, b, h);
-  const int jb = blockIdx.x * kTK;
-  if (jb >= s.n || s.m == 0) return;
-  const int warp = warp_id(), lane = lane_id(), quad = lane >> 2, ql = lane & 3;
-  const int first = s.n - s.m;                       // cache row of token 0
-  // tokens that see a row of [jb, jend)
-  const int jend = min(jb + kTK, s.n);
-  int t0 = 0, t1 = s.m;
-  if (a.causal) {
-    t0 = max(0, jb - first);
-    if (a.window > 0 && jb >= a.n_sink) t1 = static_cast<int>(min(static_cast<long long>(s.m), static_cast<long long>(jend) - 1 + a.window - first));
+// Accumulated weights from the kept logits: acc_j += sum over query rows r of
+// exp2(logit_rj - lse2_r).  A thread owns a cached row, so the order of additions is fixed.
+// Bound: the logits, 4 B per cached row and query row, mostly from L2.
+__global__ void __launch_bounds__(256) weights_kept_kernel(const AttnArgs a) {
+  __shared__ float s_e[kTR];
+  after_previous();
+  const int seg = blockIdx.y, R = a.m * a.G;
+  const ItemRange x = item_range<kTK>(a, seg);       // one item per segment: R <= 16
+  if (static_cast<int>(blockIdx.x) * 256 >= x.n || x.rows == 0) return;
+  if (static_cast<int>(threadIdx.x) < x.rows) s_e[threadIdx.x] = a.lse2[static_cast<long long>(seg) * R + threadIdx.x];
+  __syncthreads();
+  const int j = blockIdx.x * 256 + threadIdx.x;
+  // rows outside the item's tiles have no logits: no query row sees them
+  const int in_first = min(x.sink, x.ns * kTK);
+  if (j >= x.n || !((j < in_first) || (j >= x.lo && j < x.hi))) return;
+  const float* lg = a.logits + static_cast<long long>(seg) * R * a.logit_stride + j;
+  float w = 0.f;
+  for (int r = 0; r < x.rows; ++r) {
+    const float e2 = s_e[r];
+    if (e2 != -INFINITY) w += ex2_approx(lg[r * a.logit_stride] - e2);
   }
-  if (t0 >= t1) return;
-  int j[2];
-  uint32_t kf[8][4];
-#pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    j[u] = jb + warp * kUnit + quad + 8 * u;
-    // a page that no token sees may be gone: looked up only inside the tokens' reach
-    bool live = j[u] < s.n;
-    if (live && a.causal && a.window > 0 && j[u] >= a.n_sink && j[u] <= max(first, 0) - a.window) live = false;
-    long long e = -1;
-    if (live) {
-      e = row_elem(a, b, h, s.row0, j[u]);
-      if (e < 0) atomicOr(a.wc.status, DEV_BAD_INDEX);
-    }
-    const uint16_t* src = a.k + (e < 0 ? 0 : e);
-#pragma unroll
-    for (int kk = 0; kk < 8; ++kk) {
-      kf[kk][u] = e >= 0 ? __ldg(reinterpret_cast<const uint32_t*>(src + kk * 16 + ql * 2)) : 0u;
-      kf[kk][u + 2] = e >= 0 ? __ldg(reinterpret_cast<const uint32_t*>(src + kk * 16 + 8 + ql * 2)) : 0u;
-    }
-  }
-  float w[2] = {0.f, 0.f};
-  const uint32_t sq = smem_u32(s_q);
-  for (int rb = t0 * a.G; rb < t1 * a.G; rb += kWRows) {
-    __syncthreads();
-    for (int i = threadIdx.x; i < kWRows * 16; i += kThreads) {
-      const int row = i >> 4, c = i & 15, r = rb + row;
-      uint4 z = make_uint4(0u, 0u, 0u, 0u);
-      if (r < t1 * a.G) {
-        const int t = r / a.G, g = r - t * a.G;
-        z = __ldg(reinterpret_cast<const uint4*>(a.q + b * a.q_req + static_cast<long long>(h * a.G + g) * a.q_head +
-                                                 static_cast<long long>(t) * a.q_tok) + c);
-      }
-      *reinterpret_cast<uint4*>(s_q + row * 256 + ((c ^ (row & 7)) << 4)) = z;
-    }
-    if (threadIdx.x < kWRows) {
-      const int r = rb + threadIdx.x;
-      s_e[threadIdx.x] = r < t1 * a.G ? __ldg(a.lse2 + static_cast<long long>(seg) * a.m * a.G + r) : -INFINITY;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int nb = 0; nb < kWRows / 16; ++nb) {
-      float c[2][4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) c[0][i] = c[1][i] = 0.f;
-      const int row = nb * 16 + (lane & 7) + ((lane >> 4) << 3);
-#pragma unroll
-      for (int kk = 0; kk < 8; ++kk) {
-        uint32_t f[4];
-        ldmatrix4(sq + row * 256 + (((kk * 2 + ((lane >> 3) & 1)) ^ (row & 7)) << 4), f);
-        mma16816(c[0], kf[kk], f[0], f[1]);
-        mma16816(c[1], kf[kk], f[2], f[3]);
-      }
-#pragma unroll
-      for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int rl = nb * 16 + nt * 8 + ql * 2 + (i & 1);
-          const float e2 = s_e[rl];
-          const int p = first + (rb + rl) / a.G;
-          if (e2 != -INFINITY && sees(a, p, j[i >> 1])) w[i >> 1] += ex2_approx(c[nt][i] * a.s2 - e2);
-        }
-    }
-  }
-#pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    w[u] += __shfl_xor_sync(0xffffffffu, w[u], 1);
-    w[u] += __shfl_xor_sync(0xffffffffu, w[u], 2);
-    if (ql == 0 && j[u] < s.n) {
-      float* d = a.acc + seg * a.acc_stride + j[u];
-      *d += w[u];
-    }
-  }
+  a.acc[seg * a.acc_stride + j] += w;
 }
 
 }  // namespace
@@ -405,11 +350,8 @@ cudaError_t launch_attend_rows(const AttnArgs& a, int grid, cudaStream_t st) {
   return launch_attend_join(a, grid, st);
 }
 
-cudaError_t launch_attend_weights(const AttnArgs& a, cudaStream_t st) {
-  const dim3 grid((a.max_len + kTK - 1) / kTK, a.B * a.H);
-  attend_weights_kernel<<<grid, kThreads, 0, st>>>(a);
-  note_launch();
-  return cudaGetLastError();
+cudaError_t launch_weights_kept(const AttnArgs& a, cudaStream_t st) {
+  return launch_after(weights_kept_kernel, dim3((a.max_len + 255) / 256, a.B * a.H), 256, 0, st, a);
 }
 
 }  // namespace kvsel

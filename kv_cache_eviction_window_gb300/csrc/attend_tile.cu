@@ -38,8 +38,7 @@ constexpr int kThreads = 512;                        // four warpgroups; warps 1
 // registers per thread: 128 at launch (4 x 128 x 32 per sub-partition), then 184 for the two
 // softmax warpgroups and 72 for the others: 2 x 184 + 2 x 72 = 4 x 128
 constexpr int kSoftRegs = 184, kOtherRegs = 72;
-constexpr int kTile = 128 * 256;                     // bytes of one 128 x 128 bf16 tile
-constexpr int kHalf = 128 * 128;                     // its 64-column half
+constexpr int kTile = kTileBytes, kHalf = kHalfBytes;
 constexpr int kStages = 5;
 constexpr size_t kSmem = 1024 + 2 * kTile + kStages * kTile;
 
@@ -52,37 +51,6 @@ __device__ __forceinline__ void umma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, u
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
       "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
-}
-// one lane of a converged warp, the same one every time
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "elect.sync _|p, 0xffffffff;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(p));
-  return p != 0;
-}
-// K and V stages, 128-byte swizzle: atoms of 8 rows x 64 columns (1024 B).  Contiguous and packed
-// caches: the 16 atoms of columns 0-63, then those of columns 64-127.  Paged: the two atoms of 8
-// rows side by side, so that one box brings a page whole.  (A box costs about 53 cycles beyond 5
-// per 128-byte row: with a box per page and column half, 16-row pages came at 4300 cycles per K
-// and V tile, and 16-byte copies by four warps at 4900.)
-struct StageLayout {
-  uint32_t group, half;                              // bytes to the next 8 rows, to the other 64 columns
-};
-__device__ __forceinline__ StageLayout stage_layout(const AttnArgs& a) {
-  return a.src.paged ? StageLayout{2048u, 1024u} : StageLayout{1024u, static_cast<uint32_t>(kHalf)};
-}
-// K-major operand in such a stage
-__device__ __forceinline__ uint64_t sdesc_stage_k(uint32_t saddr, const StageLayout& l) {
-  uint64_t d = 0;
-  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
-  d |= static_cast<uint64_t>(1u) << 16;
-  d |= static_cast<uint64_t>(l.group >> 4) << 32;
-  d |= static_cast<uint64_t>(1u) << 46;
-  d |= static_cast<uint64_t>(2u) << 61;
-  return d;
 }
 // MN-major operand in such a stage
 __device__ __forceinline__ uint64_t sdesc_stage_v(uint32_t saddr, const StageLayout& l) {
@@ -120,41 +88,6 @@ __device__ __forceinline__ void regs_down() {
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// The K or V rows of one tile into a 128B-swizzled stage, by the lanes of the load warp.
-__device__ __forceinline__ void load_tile(const AttnArgs& a, const ItemRange& x, const CUtensorMap* map, int j0, int j1,
-                                          uint8_t* dst, uint64_t* bar) {
-  const int lane = lane_id();
-  if (!a.src.paged) {
-    if (lane == 0) {
-      mbar_arrive_expect_tx(bar, kTile);
-      const int row = static_cast<int>(x.row0) + j0;
-      const int h = a.offsets ? 0 : x.h, b = a.offsets ? 0 : x.b;
-      tma_load_4d(dst, map, bar, 0, row, h, b);
-      tma_load_4d(dst + kHalf, map, bar, 64, row, h, b);
-    }
-    return;
-  }
-  // lane i: page i of the tile; pages without a row that the item sees are not looked up
-  const int bs = a.src.block_size, at = j0 + lane * bs;
-  bool live = lane < kTK / bs && at < j1;
-  if (live && a.window > 0 && at >= a.n_sink && at + bs - 1 <= x.p0 - a.window) live = false;
-  int pb = 0;
-  if (live) {
-    pb = __ldg(a.src.block_table + static_cast<size_t>(x.b) * a.src.max_blocks + at / bs);
-    if (pb < 0 || pb >= a.src.num_blocks) {
-      atomicOr(a.wc.status, DEV_BAD_INDEX);
-      pb = a.src.num_blocks;                         // outside the pool: zeros
-    }
-  }
-  const unsigned pages = __popc(__ballot_sync(0xffffffffu, live));
-  if (lane == 0) mbar_arrive_expect_tx(bar, pages * bs * 256);
-  __syncwarp();
-  if (live) {
-    // the last dimension counts rows of the pool: (block, slot 0, head)
-    tma_load_5d(dst + lane * bs * 256, map, bar, 0, 0, 0, 0, pb * (bs * a.H) + x.h);
-  }
-}
-
 template <bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
     attend_tile_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
@@ -191,7 +124,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     s_abort = 0;
     fence_mbar_init();
   }
-  const Share sh = share_of<kTK, kThreads>(a, blockIdx.x);
+  let_next_start();
+  const Share sh =
+      share_of<kThreads>(a.B * a.H * a.rt, [&](int i) { return item_range<kTK>(a, i).tiles; }, blockIdx.x);
   if (static_cast<int>(blockIdx.x) >= sh.grid) return;   // the whole CTA
   if (warp == kQkWarp) {
     tmem_alloc(&s_tmem, 512);
@@ -238,7 +173,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) return;
         int j0, j1;
         tile_rows<kTK>(x, ta + ti, j0, j1);
-        load_tile(a, x, is_v ? &tv : &tk, j0, j1, sKV + s * kTile, &kvfull[s]);
+        load_rows_tile(a, x.b, x.h, x.row0, is_v ? &tv : &tk, j0, j1, sKV + s * kTile, &kvfull[s], [&](int from, int to) {
+          return a.window <= 0 || from < a.n_sink || to > x.p0 - a.window;
+        });
         ++use;
       };
       // the order in which the MMA warp takes the tiles
