@@ -238,7 +238,7 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 }
 
 // K and V stages of the UMMA kernels, 128-byte swizzle: atoms of 8 rows x 64 columns (1024 B).
-// Contiguous and packed caches: the 16 atoms of columns 0-63, then those of columns 64-127.
+// Contiguous and packed caches: the atoms of columns 0-63, then those of columns 64-127.
 // Paged: the two atoms of 8 rows side by side, so that one box brings a page whole.  (A box costs
 // about 53 cycles beyond 5 per 128-byte row: with a box per page and column half, 16-row pages
 // came at 4300 cycles per K and V tile, and 16-byte copies by four warps at 4900.)
@@ -247,8 +247,8 @@ constexpr int kHalfBytes = 128 * 128;                // its 64-column half
 struct StageLayout {
   uint32_t group, half;                              // bytes to the next 8 rows, to the other 64 columns
 };
-__device__ __forceinline__ StageLayout stage_layout(const AttnArgs& a) {
-  return a.src.paged ? StageLayout{2048u, 1024u} : StageLayout{1024u, static_cast<uint32_t>(kHalfBytes)};
+__device__ __forceinline__ StageLayout stage_layout(const AttnArgs& a, int rows) {
+  return a.src.paged ? StageLayout{2048u, 1024u} : StageLayout{1024u, rows * 128u};
 }
 // K-major operand in such a stage
 __device__ __forceinline__ uint64_t sdesc_stage_k(uint32_t saddr, const StageLayout& l) {
@@ -260,23 +260,27 @@ __device__ __forceinline__ uint64_t sdesc_stage_k(uint32_t saddr, const StageLay
   d |= static_cast<uint64_t>(2u) << 61;
   return d;
 }
-// 128 rows of a segment from row j0 (those below j1) into such a stage, by the lanes of a warp.
-// live(first, last): whether any row of a page is seen; other pages are not looked up.
-template <class Live>
-__device__ __forceinline__ void load_rows_tile(const AttnArgs& a, int b, int h, long long row0, const CUtensorMap* map,
-                                               int j0, int j1, uint8_t* dst, uint64_t* bar, Live seen) {
+// ROWS (64 or 128) rows of a segment from row j0 (those below j1) into such a stage, by the lanes of
+// a warp.  seen(first, last): whether any row of a page is seen; other pages are not looked up.
+constexpr int kBoxRows = 64;                         // rows of a box of a contiguous or packed cache
+template <int ROWS, class Seen>
+__device__ __forceinline__ void load_rows(const AttnArgs& a, int b, int h, long long row0, const CUtensorMap* map,
+                                          int j0, int j1, uint8_t* dst, uint64_t* bar, Seen seen) {
   const int lane = lane_id();
   if (!a.src.paged) {
     if (lane == 0) {
-      mbar_arrive_expect_tx(bar, kTileBytes);
+      mbar_arrive_expect_tx(bar, ROWS * 256);
       const int row = static_cast<int>(row0) + j0;
-      tma_load_4d(dst, map, bar, 0, row, a.offsets ? 0 : h, a.offsets ? 0 : b);
-      tma_load_4d(dst + kHalfBytes, map, bar, 64, row, a.offsets ? 0 : h, a.offsets ? 0 : b);
+#pragma unroll
+      for (int r = 0; r < ROWS; r += kBoxRows) {
+        tma_load_4d(dst + r * 128, map, bar, 0, row + r, a.offsets ? 0 : h, a.offsets ? 0 : b);
+        tma_load_4d(dst + (ROWS + r) * 128, map, bar, 64, row + r, a.offsets ? 0 : h, a.offsets ? 0 : b);
+      }
     }
     return;
   }
-  const int bs = a.src.block_size, at = j0 + lane * bs;   // lane i: page i of the tile
-  const bool live = lane < 128 / bs && at < j1 && seen(at, at + bs - 1);
+  const int bs = a.src.block_size, at = j0 + lane * bs;   // lane i: page i of the rows
+  const bool live = lane < ROWS / bs && at < j1 && seen(at, at + bs - 1);
   int pb = 0;
   if (live) {
     pb = __ldg(a.src.block_table + static_cast<size_t>(b) * a.src.max_blocks + at / bs);
@@ -290,6 +294,7 @@ __device__ __forceinline__ void load_rows_tile(const AttnArgs& a, int b, int h, 
   __syncwarp();
   // the last dimension counts rows of the pool: (block, slot 0, head)
   if (live) tma_load_5d(dst + lane * bs * 256, map, bar, 0, 0, 0, 0, pb * (bs * a.H) + h);
+  __syncwarp();
 }
 // one lane of a converged warp, the same one every time
 __device__ __forceinline__ bool elect_one() {
@@ -302,29 +307,6 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
-// Programmatic dependent launch: a kernel's CTAs may start while the one before it on the stream
-// ends; what that one wrote is read behind after_previous().  Every CTA calls it, so that a
-// kernel's end implies the end of all before it.
-__device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-template <class... Params, class... Args>
-cudaError_t launch_after(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t st, Args... args) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
-  if (e != cudaSuccess) return e;
-  note_launch();
-  return cudaGetLastError();
-}
-
 // a few rows per item (a.tr = attend_rows_tile())
 cudaError_t launch_attend_rows(const AttnArgs& a, int grid, cudaStream_t st);
 int attend_rows_tile();
@@ -333,7 +315,6 @@ int attend_rows_ctas_per_sm();
 // `split`, one block whose even and odd key tiles run side by side
 cudaError_t launch_attend_tile(const AttnArgs& a, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                                int block, bool split, int grid, cudaStream_t st);
-int attend_tile_keys();           // cached rows per tile
 // joins the pieces of items that several CTAs of either kernel share
 cudaError_t launch_attend_join(const AttnArgs& a, int grid, cudaStream_t st);
 // acc += the weights of every cached row: from the logits that attend_rows_kernel kept ...

@@ -152,7 +152,7 @@ bool cache_map(CUtensorMap* m, const void* base, const kvsel_kv* kv, const kvsel
   const cuuint64_t dims[4] = {kHeadDim, rows, packed ? 1 : H, packed ? 1 : B};
   const cuuint64_t strides[3] = {tok, !packed && H > 1 ? static_cast<cuuint64_t>(kv->stride_head) * 2 : tok,
                                  !packed && B > 1 ? static_cast<cuuint64_t>(kv->stride_req) * 2 : tok};
-  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(attend_tile_keys()), 1, 1};
+  const cuuint32_t box[4] = {64, kBoxRows, 1, 1};
   return encode_bf16_map(m, base, 4, dims, strides, box);
 }
 

@@ -68,7 +68,6 @@ __global__ void __launch_bounds__(kThreads, 2) attend_rows_kernel(const AttnArgs
   const int warp = warp_id(), lane = lane_id();
   const int quad = lane >> 2, ql = lane & 3;
   if (threadIdx.x == 0) a.rec[blockIdx.x] = make_int4(-1, 0, 0, 0);
-  let_next_start();
   const Share sh =
       share_of<kThreads>(a.B * a.H * a.rt, [&](int i) { return item_range<kTK>(a, i).tiles; }, blockIdx.x);
   if (static_cast<int>(blockIdx.x) >= sh.grid) return;
@@ -317,7 +316,6 @@ __global__ void __launch_bounds__(kThreads, 2) attend_rows_kernel(const AttnArgs
 // Bound: the logits, 4 B per cached row and query row, mostly from L2.
 __global__ void __launch_bounds__(256) weights_kept_kernel(const AttnArgs a) {
   __shared__ float s_e[kTR];
-  after_previous();
   const int seg = blockIdx.y, R = a.m * a.G;
   const ItemRange x = item_range<kTK>(a, seg);       // one item per segment: R <= 16
   if (static_cast<int>(blockIdx.x) * 256 >= x.n || x.rows == 0) return;
@@ -351,7 +349,9 @@ cudaError_t launch_attend_rows(const AttnArgs& a, int grid, cudaStream_t st) {
 }
 
 cudaError_t launch_weights_kept(const AttnArgs& a, cudaStream_t st) {
-  return launch_after(weights_kept_kernel, dim3((a.max_len + 255) / 256, a.B * a.H), 256, 0, st, a);
+  weights_kept_kernel<<<dim3((a.max_len + 255) / 256, a.B * a.H), 256, 0, st>>>(a);
+  note_launch();
+  return cudaGetLastError();
 }
 
 }  // namespace kvsel

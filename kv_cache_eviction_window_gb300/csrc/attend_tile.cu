@@ -14,7 +14,9 @@
 // memory, 48 cycles per UMMA instead of 32, so a tile pair takes 2560 at least.)
 //   SPLIT = false  an item has two blocks of query rows; both read the same K and V tiles
 //   SPLIT = true   an item has one block; its even and odd key tiles are the two streams, whose
-//                  results are added at the end
+//                  results are added at the end.  Each stream has a K/V ring of its own: a wait for a
+//                  phase of a stage is only sound for a warp that knows the phase before to be over,
+//                  and with one ring that phase could be the other stream's, still on its way
 // While one stream's four warps form the weights of a tile, the tensor cores run the other
 // stream's products.  A thread owns one query row, so a row's maximum and sum need no shuffle.
 // Roles: warps 0-3 and 4-7 the streams' softmax; warps 8 and 9 issue the streams' Q K^T, warps 10
@@ -39,7 +41,7 @@ constexpr int kThreads = 512;                        // four warpgroups; warps 1
 // softmax warpgroups and 72 for the others: 2 x 184 + 2 x 72 = 4 x 128
 constexpr int kSoftRegs = 184, kOtherRegs = 72;
 constexpr int kTile = kTileBytes, kHalf = kHalfBytes;
-constexpr int kStages = 5;
+constexpr int kStages = 5;                           // of 128 rows; SPLIT: per stream, of 64 rows
 constexpr size_t kSmem = 1024 + 2 * kTile + kStages * kTile;
 
 // A operand in TMEM
@@ -96,7 +98,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* smem = smem_align1024(smem_raw);
   uint8_t* sQ = smem;                                // two blocks (SPLIT: one, then the exchange buffer)
   uint8_t* sKV = smem + 2 * kTile;
-  __shared__ __align__(8) uint64_t qfull, qempty, kvfull[kStages], kvempty[kStages], sfull[2][2], pfull[2][2], pv[2][2], done;
+  __shared__ __align__(8) uint64_t qfull, qempty, kvfull[2][kStages], kvempty[2][kStages], sfull[2][2], pfull[2][2], pv[2][2], done;
   __shared__ __align__(8) uint64_t xfull, xempty, vfix[4];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
@@ -108,8 +110,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&qfull, 1);
     mbar_init(&qempty, 2);
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(&kvfull[s], 1);
-      mbar_init(&kvempty[s], SPLIT ? 1 : 2);         // both streams read a tile, or one
+      for (int w = 0; w < 2; ++w) {
+        mbar_init(&kvfull[w][s], 1);
+        mbar_init(&kvempty[w][s], SPLIT ? 1 : 2);    // both streams read a tile, or one
+      }
     }
     for (int u = 0; u < 4; ++u) mbar_init(&vfix[u], 4);
     for (int w = 0; w < 2; ++w)
@@ -124,7 +128,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     s_abort = 0;
     fence_mbar_init();
   }
-  let_next_start();
   const Share sh =
       share_of<kThreads>(a.B * a.H * a.rt, [&](int i) { return item_range<kTK>(a, i).tiles; }, blockIdx.x);
   if (static_cast<int>(blockIdx.x) >= sh.grid) return;   // the whole CTA
@@ -137,8 +140,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tbase = s_tmem;                     // S of stream w, buffer u: column 128 w + 64 u; O: 256 + 128 w
   constexpr int nblk = SPLIT ? 1 : 2;                // query blocks per item
-  constexpr int nstr = SPLIT ? 2 : 1;                // key tiles that the streams take at a time
+  constexpr int nring = SPLIT ? 2 : 1;
+  constexpr int kStageRows = SPLIT ? 64 : 128, kStageBytes = kStageRows * 256;
+  auto stage = [&](int ring, int use) { return sKV + (ring * kStages + use % kStages) * kStageBytes; };
 
+  __syncwarp();
   if (warp >= kQkWarp) regs_down<kOtherRegs>();
   if (warp == kLoadWarp) {
     if (lane == 0) {
@@ -146,7 +152,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tma_prefetch_desc(&tk);
       tma_prefetch_desc(&tv);
     }
-    int use = 0, piece = 0;                          // ring uses issued, pieces begun
+    int use[2] = {0, 0}, piece = 0;                  // ring uses issued, pieces begun
     bool ok = true;                                  // the same in every lane
     long long base = sh.item_base, at = sh.begin;
     for (int item = sh.item; ok && at < sh.end; ++item) {
@@ -167,31 +173,45 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       ++piece;
       __syncwarp();
-      auto load = [&](int ti, bool is_v) {
-        const int s = use % kStages;
-        ok = __all_sync(0xffffffffu, mbar_wait(&kvempty[s], ((use / kStages) & 1) ^ 1, &s_abort, a.wc));
+      auto load = [&](int ring, int ti, int sub, bool is_v) {
+        const int u = use[ring], s = u % kStages;
+        ok = __all_sync(0xffffffffu, ok && mbar_wait(&kvempty[ring][s], ((u / kStages) & 1) ^ 1, &s_abort, a.wc));
         if (!ok) return;
         int j0, j1;
         tile_rows<kTK>(x, ta + ti, j0, j1);
-        load_rows_tile(a, x.b, x.h, x.row0, is_v ? &tv : &tk, j0, j1, sKV + s * kTile, &kvfull[s], [&](int from, int to) {
-          return a.window <= 0 || from < a.n_sink || to > x.p0 - a.window;
-        });
-        ++use;
+        load_rows<kStageRows>(a, x.b, x.h, x.row0, is_v ? &tv : &tk, j0 + sub * 64, j1, stage(ring, u), &kvfull[ring][s],
+                              [&](int from, int to) { return a.window <= 0 || from < a.n_sink || to > x.p0 - a.window; });
+        ++use[ring];
       };
-      // the order in which the MMA warp takes the tiles
-      for (int i = 0; i < cnt && ok; i += nstr) {
-        for (int w = 0; w < nstr && i + w < cnt && ok; ++w) load(i + w, false);
-        for (int w = 0; w < nstr && i + w < cnt && ok; ++w) load(i + w, true);
+      // K, then V, in the order in which the UMMA warps take them
+      if (SPLIT) {
+        for (int i = 0; i < cnt && ok; i += 2)
+          for (int sub = 0; sub < 2; ++sub)
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+              if (i + w >= cnt) break;
+              load(w, i + w, sub, false);
+              if (ok) load(w, i + w, sub, true);
+            }
+      } else {
+        for (int i = 0; i < cnt && ok; ++i) {
+          load(0, i, 0, false);
+          if (ok) load(0, i, 0, true);
+        }
       }
       base += x.tiles;
       at = base;
     }
     // copies in flight land, and the last releases arrive, before the CTA ends
     if (lane == 0) {
-      for (int u = max(0, use - kStages); u < use; ++u) mbar_drain(&kvfull[u % kStages], (u / kStages) & 1, a.wc.status);
+#pragma unroll
+      for (int r = 0; r < nring; ++r)
+        for (int u = max(0, use[r] - kStages); u < use[r]; ++u)
+          mbar_drain(&kvfull[r][u % kStages], (u / kStages) & 1, a.wc.status);
       if (piece) mbar_drain(&qfull, (piece - 1) & 1, a.wc.status);
       if (ok) {
-        ring_tail(kvempty, kStages, use, &s_abort, a.wc);
+#pragma unroll
+        for (int r = 0; r < nring; ++r) ring_tail(kvempty[r], kStages, use[r], &s_abort, a.wc);
         ring_tail(&qempty, 1, piece, &s_abort, a.wc);
       }
     }
@@ -212,8 +232,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     };
     const uint64_t qd = sdesc_kmajor_sw128(smem_u32(sQ + (SPLIT ? 0 : w) * kTile));
-    const StageLayout lay = stage_layout(a);
-    const uint64_t kd0 = sdesc_stage_k(smem_u32(sKV), lay), vd0 = sdesc_stage_v(smem_u32(sKV), lay);
+    const int ring = SPLIT ? w : 0;
+    const StageLayout lay = stage_layout(a, kStageRows);
+    const uint32_t base0 = smem_u32(stage(ring, 0));
+    const uint64_t kd0 = sdesc_stage_k(base0, lay), vd0 = sdesc_stage_v(base0, lay);
     const uint32_t sub_step = (8 * lay.group) >> 4, k_step = (2 * lay.group) >> 4, khalf = lay.half >> 4;   // 64 rows, 16 rows
     const uint32_t tS = tbase + w * 128, tO = tbase + 256 + w * 128;
     long long base = sh.item_base, at = sh.begin;
@@ -225,13 +247,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (is_qk) {
         wait(&qfull, piece);
         for (int n = 0; n < steps && ok; ++n, ++g) {
-          const int c = n >> 1, u = n & 1, k = use + (SPLIT ? 4 * c + w : 2 * c);   // ring use of the K tile
-          if (u == 0) wait(&kvfull[k % kStages], k / kStages);
+          const int u = n & 1, k = use + (SPLIT ? 2 * n : 2 * (n >> 1));   // ring use of the K rows
+          if (SPLIT || u == 0) wait(&kvfull[ring][k % kStages], k / kStages);
           // the buffer is free when the product that read the last P in it is done
           if (g >= 2) wait(&pv[w][u], (g >> 1) - 1);
           if (!ok) break;
           tc_fence_after();
-          const uint64_t kd = kd0 + (k % kStages) * (kTile >> 4) + u * sub_step;
+          const uint64_t kd = kd0 + (k % kStages) * (kStageBytes >> 4) + (SPLIT ? 0 : u) * sub_step;
           if (elect_one()) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -239,32 +261,31 @@ __global__ void __launch_bounds__(kThreads, 1)
               umma_bf16(tS + u * 64, qd + (i >> 2) * (kHalf >> 4) + in, kd + (i >> 2) * khalf + in, idesc_s, i ? 1u : 0u);
             }
             umma_commit(&sfull[w][u]);
-            if (u == 1) umma_commit(&kvempty[k % kStages]);
+            if (SPLIT || u == 1) umma_commit(&kvempty[ring][k % kStages]);
           }
           __syncwarp();
         }
         if (ok) commit(&qempty);
       } else {
         for (int n = 0; n < steps && ok; ++n, ++g) {
-          const int c = n >> 1, u = n & 1;
-          const int v = use + (SPLIT ? (2 * c + 1 < cnt ? 4 * c + 2 + w : 4 * c + 1) : 2 * c + 1);
-          if (u == 0) wait(&kvfull[v % kStages], v / kStages);
+          const int u = n & 1, v = use + (SPLIT ? 2 * n : 2 * (n >> 1)) + 1;
+          if (SPLIT || u == 0) wait(&kvfull[ring][v % kStages], v / kStages);
           wait(&pfull[w][u], g >> 1);
           if (!ok) break;
           tc_fence_after();
-          const uint64_t vd = vd0 + (v % kStages) * (kTile >> 4) + u * sub_step;
+          const uint64_t vd = vd0 + (v % kStages) * (kStageBytes >> 4) + (SPLIT ? 0 : u) * sub_step;
           if (elect_one()) {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
               umma_bf16_ta(tO, tS + u * 64 + i * 8, vd + i * k_step, idesc_o, (n == 0 && i == 0) ? 0u : 1u);
             umma_commit(&pv[w][u]);
-            if (u == 1) umma_commit(&kvempty[v % kStages]);
+            if (SPLIT || u == 1) umma_commit(&kvempty[ring][v % kStages]);
           }
           __syncwarp();
         }
       }
       ++piece;
-      use += 2 * cnt;
+      use += SPLIT ? 2 * steps : 2 * cnt;
       base += x.tiles;
       at = base;
     }
@@ -308,6 +329,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         wait(&sfull[w][u], g >> 1);
         if (!ok) break;
         tc_fence_after();
+        __syncwarp();                                // (the TMEM instructions want a converged warp)
         float s[64];
         tmem_ld32(tS, s);
         tmem_ld32(tS + 32, s + 32);
@@ -344,6 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             wait(&pv[w][u ^ 1], (g - 1) >> 1);
             if (!ok) break;
             tc_fence_after();
+            __syncwarp();
 #pragma unroll
             for (int c0 = 0; c0 < 128; c0 += 16) {
               uint32_t y[16];
@@ -358,6 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float off = ref == -INFINITY ? 0.f : -ref;
         const uint64_t sc2 = pack2(a.s2, a.s2), off2 = pack2(off, off);
         uint64_t acc0 = pack2(0.f, 0.f), acc1 = acc0;
+        __syncwarp();
 #pragma unroll
         for (int c0 = 0; c0 < 64; c0 += 32) {
           uint32_t pk[16];
@@ -383,19 +407,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         // V rows that the item does not see may hold anything; their weights are zero, and the
         // rows become zero before the tile's first product reads them.  Without SPLIT stream 0 does
         // it for both; it is at most two tiles ahead, so four barriers in turn tell stream 1.
-        if (u == 0 && (j0 + kTK > j1 || (a.window > 0 && j0 <= x.p0 - a.window && j0 + kTK > a.n_sink))) {
+        const int jv = SPLIT ? js : j0;              // rows of the V stage
+        if ((SPLIT || u == 0) &&
+            (jv + kStageRows > j1 || (a.window > 0 && jv <= x.p0 - a.window && jv + kStageRows > a.n_sink))) {
           if (SPLIT || w == 0) {
-            const int uv = use + (SPLIT ? (i - w + 1 < cnt ? 2 * (i - w) + 2 + w : 2 * (i - w) + 1) : 2 * i + 1);
-            wait(&kvfull[uv % kStages], uv / kStages);
+            const int ring = SPLIT ? w : 0, uv = use + (SPLIT ? 2 * mine : 2 * i) + 1;
+            wait(&kvfull[ring][uv % kStages], uv / kStages);
             if (!ok) break;
-            if (unseen(a, x, j0 + row, j1)) {
-              const StageLayout lay = stage_layout(a);
-              uint8_t* d = sKV + (uv % kStages) * kTile + (row >> 3) * lay.group + (row & 7) * 128;
+            // a thread a row, or a column half of one
+            const int r = row & (kStageRows - 1);
+            if (unseen(a, x, jv + r, j1)) {
+              const StageLayout lay = stage_layout(a, kStageRows);
+              uint8_t* d = stage(ring, uv) + (r >> 3) * lay.group + (r & 7) * 128;
 #pragma unroll
-              for (int c = 0; c < 8; ++c) {
-                *reinterpret_cast<uint4*>(d + c * 16) = make_uint4(0u, 0u, 0u, 0u);
-                *reinterpret_cast<uint4*>(d + lay.half + c * 16) = make_uint4(0u, 0u, 0u, 0u);
-              }
+              for (int hf = 0; hf < 2; ++hf)
+                if (!SPLIT || hf == row >> 6)
+#pragma unroll
+                  for (int c = 0; c < 8; ++c)
+                    *reinterpret_cast<uint4*>(d + hf * lay.half + c * 16) = make_uint4(0u, 0u, 0u, 0u);
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -407,12 +436,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           ++nfix;
         }
+        __syncwarp();
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&pfull[w][u]);
+        __syncwarp();
       }
-      use += 2 * cnt;                                // a K and a V tile each
+      use += SPLIT ? 2 * steps : 2 * cnt;                                // a K and a V tile each
 
       // results of this piece
       const bool first = ta == 0, last = tb == x.tiles, direct = first && last;
@@ -427,6 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int c0 = 0; c0 < 128; c0 += 32) {
         float y[32];
+        __syncwarp();
         if (mine > 0) {
           tmem_ld32(tO + c0, y);
           tmem_ld_wait();
@@ -510,8 +542,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 }  // namespace
-
-int attend_tile_keys() { return kTK; }
 
 cudaError_t launch_attend_tile(const AttnArgs& a, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                                int block, bool split, int grid, cudaStream_t st) {

@@ -87,8 +87,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     s_abort = 0;
     fence_mbar_init();
   }
-  after_previous();
-  let_next_start();
   if (threadIdx.x == 0) a.rec[blockIdx.x] = make_int4(-1, 0, 0, 0);
   const Share sh = share_of<kThreads>(a.B * a.H * per_seg,
                                       [&](int i) { return key_item(a, i, per_seg, tok).blocks; }, blockIdx.x);
@@ -118,7 +116,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = __all_sync(0xffffffffu, mbar_wait(&kempty, (piece & 1) ^ 1, &s_abort, a.wc));
       if (!ok) break;
       for (int w = 0; w < 2; ++w)
-        load_rows_tile(a, x.b, x.h, x.row0, &tk, x.jb + w * 128, x.n, sK + w * kTileBytes, &kfull, [&](int from, int to) {
+        load_rows<128>(a, x.b, x.h, x.row0, &tk, x.jb + w * 128, x.n, sK + w * kTileBytes, &kfull, [&](int from, int to) {
           return a.window <= 0 || !a.causal || from < a.n_sink || to > x.first - a.window;
         });
       ++piece;
@@ -159,7 +157,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == kMmaWarp) {
     constexpr uint32_t idesc = idesc_bf16_f32(128, 128);
-    const StageLayout lay = stage_layout(a);
+    const StageLayout lay = stage_layout(a, 128);
     const uint64_t kd0 = sdesc_stage_k(smem_u32(sK), lay), qd0 = sdesc_kmajor_sw128(smem_u32(sQ));
     const uint32_t khalf = lay.half >> 4;
     int use = 0, piece = 0;
@@ -238,6 +236,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool whole = __all_sync(0xffffffffu, lo == 0 && hi >= block);
         uint64_t acc0 = pack2(0.f, 0.f), acc1 = acc0;
         float masked = 0.f;
+        __syncwarp();
 #pragma unroll
         for (int c0 = 0; c0 < 128; c0 += 64) {
           float y[64];
@@ -272,6 +271,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive(&lempty[w][u]);
           mbar_arrive(&qempty[s]);
         }
+        __syncwarp();
       }
       if (!ok) break;
       const bool first = ta == 0, last = tb == x.blocks;
@@ -297,7 +297,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Items that several CTAs share: the partials in order (slots as in attend_join.cu).
 __global__ void __launch_bounds__(kKeys) weights_join_kernel(const AttnArgs a, const float* part) {
-  after_previous();
   const int4 rec = a.rec[blockIdx.x];
   if (rec.x < 0) return;
   const int per_seg = (a.max_len + kKeys - 1) / kKeys;
@@ -315,9 +314,12 @@ cudaError_t launch_weights_tile(const AttnArgs& a, const CUtensorMap& tq, const 
                                 int grid, cudaStream_t st) {
   cudaError_t e = ensure_smem(reinterpret_cast<const void*>(weights_tile_kernel), kSmem);
   if (e != cudaSuccess) return e;
-  e = launch_after(weights_tile_kernel, dim3(grid), kThreads, kSmem, st, tq, tk, a, block, part);
-  if (e != cudaSuccess) return e;
-  return launch_after(weights_join_kernel, dim3(grid), kKeys, 0, st, a, static_cast<const float*>(part));
+  weights_tile_kernel<<<grid, kThreads, kSmem, st>>>(tq, tk, a, block, part);
+  note_launch();
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  weights_join_kernel<<<grid, kKeys, 0, st>>>(a, part);
+  note_launch();
+  return cudaGetLastError();
 }
 
 }  // namespace kvsel

@@ -145,6 +145,22 @@ def test_a_result_does_not_depend_on_the_rest_of_the_batch(m, G):
             assert torch.equal(x[0], y[0])
 
 
+@pytest.mark.parametrize("m,G,H,block", [(6, 7, 4, 32), (1, 7, 4, 32), (70, 7, 2, 16), (20, 1, 8, 64)])
+def test_back_to_back_calls_repeat_bit_for_bit(m, G, H, block):
+    # ragged lengths, calls without a pause: the warps of a CTA drift apart in every way
+    import torch
+
+    c = CH.Case(B=4, G=G, H=H, m=m, lens=[3001, 1900, 517, 2222], layout="paged", block=block, seed=m).upload()
+    ws = c.call()
+    first = c.t["out"].clone(), c.t["lse"].clone()
+    for _ in range(20):
+        for _ in range(50):
+            c.call(ws=ws)
+        assert CH.status(ws) == 0
+        assert torch.equal(first[0], c.t["out"]) and torch.equal(first[1], c.t["lse"])
+    c.check()
+
+
 def test_lengths_are_read_by_a_captured_call():
     import torch
 
