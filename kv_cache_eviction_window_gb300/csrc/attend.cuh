@@ -38,7 +38,11 @@ struct AttnArgs {
   // partial results of items that several CTAs share: two slots per CTA
   float* part_o;                  // [2 * grid][rows][128]
   float2* part_ml;                // [2 * grid][rows]: reference (log2 units) and sum
-  int4* rec;                      // [grid]: item that starts here and goes on, CTAs that follow
+// who joins what.  by_item (fewer items than CTAs): rec[item] = {CTA of the first piece, or -1 when
+  // the item is done, CTAs that follow}; else rec[CTA] = {item that starts there and goes on, or
+  // -1, CTAs that follow}
+  int2* rec;                      // [grid]
+  int by_item;
   WaitCtl wc;
 };
 
@@ -200,6 +204,19 @@ __device__ __forceinline__ int last_cta(const Share& sh, long long e) {
   return static_cast<int>((e * sh.grid - 1) / sh.total);
 }
 
+// Records for attend_join_kernel: at a kernel's start, and by the CTA that works on an item's first tile
+// (`follow` CTAs work on the others).
+__device__ __forceinline__ void rec_clear(const AttnArgs& a) {
+  if (threadIdx.x == 0 && !a.by_item) a.rec[blockIdx.x] = make_int2(-1, 0);
+}
+__device__ __forceinline__ void rec_first(const AttnArgs& a, int item, int follow) {
+  if (threadIdx.x != 0) return;
+  if (a.by_item)
+    a.rec[item] = make_int2(follow > 0 ? static_cast<int>(blockIdx.x) : -1, follow);
+  else if (follow > 0)
+    a.rec[blockIdx.x] = make_int2(item, follow);
+}
+
 // whether row p sees cached row j (j < hi of its tile)
 __device__ __forceinline__ bool sees(const AttnArgs& a, int p, int j) {
   if (!a.causal) return true;
@@ -262,7 +279,6 @@ __device__ __forceinline__ uint64_t sdesc_stage_k(uint32_t saddr, const StageLay
 }
 // ROWS (64 or 128) rows of a segment from row j0 (those below j1) into such a stage, by the lanes of
 // a warp.  seen(first, last): whether any row of a page is seen; other pages are not looked up.
-constexpr int kBoxRows = 64;                         // rows of a box of a contiguous or packed cache
 template <int ROWS, class Seen>
 __device__ __forceinline__ void load_rows(const AttnArgs& a, int b, int h, long long row0, const CUtensorMap* map,
                                           int j0, int j1, uint8_t* dst, uint64_t* bar, Seen seen) {
@@ -271,11 +287,8 @@ __device__ __forceinline__ void load_rows(const AttnArgs& a, int b, int h, long 
     if (lane == 0) {
       mbar_arrive_expect_tx(bar, ROWS * 256);
       const int row = static_cast<int>(row0) + j0;
-#pragma unroll
-      for (int r = 0; r < ROWS; r += kBoxRows) {
-        tma_load_4d(dst + r * 128, map, bar, 0, row + r, a.offsets ? 0 : h, a.offsets ? 0 : b);
-        tma_load_4d(dst + (ROWS + r) * 128, map, bar, 64, row + r, a.offsets ? 0 : h, a.offsets ? 0 : b);
-      }
+      tma_load_4d(dst, map, bar, 0, row, a.offsets ? 0 : h, a.offsets ? 0 : b);
+      tma_load_4d(dst + ROWS * 128, map, bar, 64, row, a.offsets ? 0 : h, a.offsets ? 0 : b);
     }
     return;
   }
@@ -310,6 +323,7 @@ __device__ __forceinline__ bool elect_one() {
 // a few rows per item (a.tr = attend_rows_tile())
 cudaError_t launch_attend_rows(const AttnArgs& a, int grid, cudaStream_t st);
 int attend_rows_tile();
+int attend_tile_rows(bool split);  // rows of a K/V stage, and of a box of its maps
 int attend_rows_ctas_per_sm();
 // tcgen05 tiles: two blocks of `block` query rows per item that share the cached rows, or, with
 // `split`, one block whose even and odd key tiles run side by side

@@ -80,7 +80,7 @@ int plan_attn(const kvsel_attn_params* p, bool with_acc, AttnPlan& pl) {
   // behind the status word and the counters that the scoring calls keep in a shared workspace
   size_t off = kStatusBytes + kCounterBytes;
   pl.rec = off;
-  off = align256(off + sizeof(int4) * pl.grid);
+  off = align256(off + sizeof(int2) * pl.grid);
   pl.ml = off;
   off = align256(off + sizeof(float2) * 2 * pl.grid * pl.tr);
   pl.o = off;
@@ -135,8 +135,8 @@ bool query_map(CUtensorMap* m, const AttnArgs& a, int block) {
   return encode_bf16_map(m, a.q, 4, dims, strides, box);
 }
 
-// K or V tiles: 64 columns x 128 rows of one segment (contiguous, packed) or x one page.
-bool cache_map(CUtensorMap* m, const void* base, const kvsel_kv* kv, const kvsel_attn_params* p) {
+// K or V tiles: 64 columns x `box_rows` rows of one segment (contiguous, packed) or a page.
+bool cache_map(CUtensorMap* m, const void* base, const kvsel_kv* kv, const kvsel_attn_params* p, int box_rows) {
   const cuuint64_t H = p->h_kv, B = p->batch;
   if (kv->layout == KVSEL_LAYOUT_PAGED) {
     // a page whole, in atoms of 8 rows x 64 columns: columns, rows of an atom, column halves, atoms of
@@ -152,7 +152,7 @@ bool cache_map(CUtensorMap* m, const void* base, const kvsel_kv* kv, const kvsel
   const cuuint64_t dims[4] = {kHeadDim, rows, packed ? 1 : H, packed ? 1 : B};
   const cuuint64_t strides[3] = {tok, !packed && H > 1 ? static_cast<cuuint64_t>(kv->stride_head) * 2 : tok,
                                  !packed && B > 1 ? static_cast<cuuint64_t>(kv->stride_req) * 2 : tok};
-  const cuuint32_t box[4] = {64, kBoxRows, 1, 1};
+  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(box_rows), 1, 1};
   return encode_bf16_map(m, base, 4, dims, strides, box);
 }
 
@@ -268,7 +268,10 @@ int kvsel_attend(const kvsel_attn_params* p, const void* q, const kvsel_kv* kv, 
   a.rt = pl.rt;
   a.part_o = reinterpret_cast<float*>(wsb + pl.o);
   a.part_ml = reinterpret_cast<float2*>(wsb + pl.ml);
-  a.rec = reinterpret_cast<int4*>(wsb + pl.rec);
+  a.rec = reinterpret_cast<int2*>(wsb + pl.rec);
+  // few rows in all: the join starts a CTA for each (128 items of 256 rows: 119 us, by CTAs 27 us)
+  const long long items = static_cast<long long>(p->batch) * p->h_kv * pl.rt;
+  a.by_item = items <= pl.grid && items * std::min(pl.tr, p->n_new * p->group) <= 4096;
   a.wc = WaitCtl{p->wait_cycles ? p->wait_cycles : kDefaultWaitCycles, static_cast<int*>(ws)};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (!pl.tiled) {
@@ -276,9 +279,12 @@ int kvsel_attend(const kvsel_attn_params* p, const void* q, const kvsel_kv* kv, 
     return rc || !acc ? rc : launch_rc(launch_weights_kept(a, st));
   }
   CUtensorMap tq, tk, tv;
-  if (!query_map(&tq, a, pl.block) || !cache_map(&tk, kv->k, kv, p) || !cache_map(&tv, kv->v, kv, p)) return KVSEL_EINVAL;
+  const int box = attend_tile_rows(pl.split);
+  if (!query_map(&tq, a, pl.block) || !cache_map(&tk, kv->k, kv, p, box) || !cache_map(&tv, kv->v, kv, p, box))
+    return KVSEL_EINVAL;
   rc = launch_rc(launch_attend_tile(a, tq, tk, tv, pl.block, pl.split, pl.grid, st));
   if (rc || !acc) return rc;
+  if (pl.split && !cache_map(&tk, kv->k, kv, p, attend_tile_rows(false))) return KVSEL_EINVAL;
   return launch_rc(launch_weights_tile(a, tq, tk, pl.block, reinterpret_cast<float*>(wsb + pl.wpart), pl.grid, st));
 }
 

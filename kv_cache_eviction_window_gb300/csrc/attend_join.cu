@@ -1,12 +1,13 @@
 // Joins the pieces of items that several CTAs of attend_rows_kernel or attend_tile_kernel
 // share.  Piece c of an item that starts in CTA x sits in slot 1 of CTA x (c = 0) or slot 0 of
-// CTA x + c: unnormalised rows, their references (log2 units) and sums.  The factors of all
-// pieces are formed first, so that the rows' loads do not wait for one another; pieces are
-// added in a fixed order, so results repeat.
+// CTA x + c: unnormalised rows, their references (log2 units) and sums.  The loads of a row's
+// pieces do not wait for one another; pieces are added in a fixed order, so results repeat.
 //
-// Bound: latency (the pieces are in L2).  WPR warps work on a row: one where an item has few
-// pieces, eight where it may have one per CTA.  (The same work by the CTA that finishes an
-// item's last piece, without a second launch, took 38 us longer for 73 pieces of 7 rows.)
+// Bound: latency (the pieces are in L2).  Few items (by_item): a CTA per row, eight warps over its
+// pieces, of which there may be one per CTA of the grid.  Many items, of two or three pieces: a
+// warp per row, five CTAs for each CTA before; those whose number starts no shared item end at once.
+// (Joining in the CTA that finishes an item's last piece, without a second launch, took 38 us
+// longer for 73 pieces of 7 rows.)
 #include <algorithm>
 
 #include "attend.cuh"
@@ -16,96 +17,116 @@ namespace {
 
 constexpr int kJoinWarps = 8;
 
-template <int WPR>
-__global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(const AttnArgs a) {
+struct Joined {
+  float M, L;
+  float4 y;
+};
+__device__ __forceinline__ Joined nothing() { return Joined{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)}; }
+// N more pieces: references and sums ml (-inf, 0 where there is none) and rows z
+template <int N>
+__device__ __forceinline__ void add_pieces(Joined& p, const float2* ml, const float4* z) {
+  float m2 = p.M;
+#pragma unroll
+  for (int i = 0; i < N; ++i) m2 = fmaxf(m2, ml[i].x);
+  const float old = p.M == -INFINITY ? 0.f : exp2f(p.M - m2);
+  p.M = m2;
+  p.L *= old;
+  p.y = make_float4(p.y.x * old, p.y.y * old, p.y.z * old, p.y.w * old);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float f = ml[i].x == -INFINITY ? 0.f : exp2f(ml[i].x - m2);
+    p.L += f * ml[i].y;
+    p.y.x += f * z[i].x;
+    p.y.y += f * z[i].y;
+    p.y.z += f * z[i].z;
+    p.y.w += f * z[i].w;
+  }
+}
+struct JoinItem {
+  int b, h, rt, rows, leader, pieces;
+};
+__device__ __forceinline__ JoinItem join_item(const AttnArgs& a, int item, int leader, int follow) {
+  JoinItem x;
+  const int seg = item / a.rt;
+  x.rt = item - seg * a.rt;
+  x.b = seg / a.H;
+  x.h = seg - x.b * a.H;
+  const int mr = a.new_lens ? __ldg(a.new_lens + x.b) : a.m;
+  x.rows = min(a.tr, min(max(mr, 0), a.m) * a.G - x.rt * a.tr);
+  x.leader = leader;
+  x.pieces = follow + 1;
+  return x;
+}
+// pieces c, c + step, ... (N of them at most) of row r
+template <int N>
+__device__ __forceinline__ void fetch(const AttnArgs& a, const JoinItem& x, int r, int c, int step, float2* ml, float4* z) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int ci = c + i * step;
+    ml[i] = make_float2(-INFINITY, 0.f);
+    z[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (r < x.rows && ci < x.pieces) {
+      const long long at = (ci == 0 ? 2ll * x.leader + 1 : 2ll * (x.leader + ci)) * a.tr + r;
+      ml[i] = a.part_ml[at];
+      z[i] = *reinterpret_cast<const float4*>(a.part_o + at * kHeadDim + lane_id() * 4);
+    }
+  }
+}
+__device__ __forceinline__ void finish(const AttnArgs& a, const JoinItem& x, int r, const Joined& p) {
+  const int rr = x.rt * a.tr + r;
+  const float inv = p.L > 0.f ? 1.f / p.L : 0.f;
+  *reinterpret_cast<uint2*>(out_row(a, x.b, x.h, rr) + lane_id() * 4) =
+      make_uint2(pack_bf16(p.y.x * inv, p.y.y * inv), pack_bf16(p.y.z * inv, p.y.w * inv));
+  if (lane_id() == 0) write_lse(a, x.b, x.h, rr, p.M, p.L);
+}
+
+// grid (item, row)
+__global__ void __launch_bounds__(kJoinWarps * 32) join_items_kernel(const AttnArgs a) {
   __shared__ float4 s_y[kJoinWarps][32];
   __shared__ float2 s_ml[kJoinWarps];
-  const int4 rec = a.rec[blockIdx.x];
+  const int warp = warp_id(), lane = lane_id(), r = blockIdx.y;
+  // an item without rows has no record
+  const int2 rec = a.rec[blockIdx.x];
+  const JoinItem x = join_item(a, blockIdx.x, rec.x, rec.y);
+  if (r >= x.rows || rec.x < 0) return;
+  Joined p = nothing();
+  for (int c = warp; c < x.pieces; c += 8 * kJoinWarps) {
+    float2 ml[8];
+    float4 z[8];
+    fetch<8>(a, x, r, c, kJoinWarps, ml, z);
+    add_pieces<8>(p, ml, z);
+  }
+  s_y[warp][lane] = p.y;
+  if (lane == 0) s_ml[warp] = make_float2(p.M, p.L);
+  __syncthreads();
+  if (warp) return;
+  p = nothing();
+  float2 ml[kJoinWarps];
+  float4 z[kJoinWarps];
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) {
+    ml[w] = s_ml[w];
+    z[w] = s_y[w][lane];
+  }
+  add_pieces<kJoinWarps>(p, ml, z);
+  finish(a, x, r, p);
+}
+
+// grid (CTA of the kernel before, share of its rows): all CTAs resident at once, a row per warp
+constexpr int kShares = 5;
+__global__ void __launch_bounds__(kJoinWarps * 32, kShares) join_ctas_kernel(const AttnArgs a) {
+  const int2 rec = a.rec[blockIdx.x];
   if (rec.x < 0) return;
-  const int seg = rec.x / a.rt, rt = rec.x - seg * a.rt;
-  const int b = seg / a.H, h = seg - b * a.H;
-  const int mr = a.new_lens ? __ldg(a.new_lens + b) : a.m;
-  const int rows = min(a.tr, min(max(mr, 0), a.m) * a.G - rt * a.tr);
-  const int warp = warp_id(), lane = lane_id(), part = warp % WPR, pieces = rec.y + 1;
-  constexpr int kRowsPer = kJoinWarps / WPR;
-  auto place = [&](int c, int r) { return (c == 0 ? 2ll * blockIdx.x + 1 : 2ll * (blockIdx.x + c)) * a.tr + r; };
-  for (int r0 = blockIdx.y * kRowsPer; r0 < rows; r0 += gridDim.y * kRowsPer) {
-    const int r = r0 + warp / WPR;
-    float M = -INFINITY, L = 0.f;
-    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-    // this warp's pieces are part, part + WPR, ...: 32 at a time, lane i the factor of the i-th
-    for (int c0 = part; c0 < pieces && r < rows; c0 += 32 * WPR) {
-      const int c = c0 + lane * WPR;
-      float2 ml = make_float2(-INFINITY, 0.f);
-      if (c < pieces) ml = a.part_ml[place(c, r)];
-      const int cnt = min(32, (pieces - c0 + WPR - 1) / WPR);
-      float4 z[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i < cnt) z[i] = *reinterpret_cast<const float4*>(a.part_o + place(c0 + i * WPR, r) * kHeadDim + lane * 4);
-      float m2 = ml.x;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) m2 = fmaxf(m2, __shfl_xor_sync(0xffffffffu, m2, o));
-      m2 = fmaxf(m2, M);
-      const float f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - m2);
-      float l = f * ml.y;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-      const float old = M == -INFINITY ? 0.f : exp2f(M - m2);
-      M = m2;
-      L = L * old + l;
-      y.x *= old;
-      y.y *= old;
-      y.z *= old;
-      y.w *= old;
-      for (int i0 = 0; i0 < cnt; i0 += 8) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (i0 + i < cnt) {
-            const float g = __shfl_sync(0xffffffffu, f, i0 + i);
-            y.x += g * z[i].x;
-            y.y += g * z[i].y;
-            y.z += g * z[i].z;
-            y.w += g * z[i].w;
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (i0 + 8 + i < cnt)
-            z[i] = *reinterpret_cast<const float4*>(a.part_o + place(c0 + (i0 + 8 + i) * WPR, r) * kHeadDim + lane * 4);
-      }
+  const JoinItem x = join_item(a, rec.x, blockIdx.x, rec.y);
+  for (int r = blockIdx.y * kJoinWarps + warp_id(); r < x.rows; r += kShares * kJoinWarps) {
+    Joined p = nothing();
+    for (int c = 0; c < x.pieces; c += 4) {
+      float2 ml[4];
+      float4 z[4];
+      fetch<4>(a, x, r, c, 1, ml, z);
+      add_pieces<4>(p, ml, z);
     }
-    if (WPR > 1) {
-      s_y[warp][lane] = y;
-      if (lane == 0) s_ml[warp] = make_float2(M, L);
-      __syncthreads();
-      if (part == 0) {
-        float m2 = M;
-        for (int w = 1; w < WPR; ++w) m2 = fmaxf(m2, s_ml[warp + w].x);
-        const float old = M == -INFINITY ? 0.f : exp2f(M - m2);
-        L *= old;
-        y = make_float4(y.x * old, y.y * old, y.z * old, y.w * old);
-        for (int w = 1; w < WPR; ++w) {
-          const float2 ml = s_ml[warp + w];
-          const float g = ml.x == -INFINITY ? 0.f : exp2f(ml.x - m2);
-          const float4 z = s_y[warp + w][lane];
-          L += g * ml.y;
-          y.x += g * z.x;
-          y.y += g * z.y;
-          y.z += g * z.z;
-          y.w += g * z.w;
-        }
-        M = m2;
-      }
-      __syncthreads();
-    }
-    if (r < rows && part == 0) {
-      const int rr = rt * a.tr + r;
-      const float inv = L > 0.f ? 1.f / L : 0.f;
-      *reinterpret_cast<uint2*>(out_row(a, b, h, rr) + lane * 4) =
-          make_uint2(pack_bf16(y.x * inv, y.y * inv), pack_bf16(y.z * inv, y.w * inv));
-      if (lane == 0) write_lse(a, b, h, rr, M, L);
-    }
+    finish(a, x, r, p);
   }
 }
 
@@ -113,11 +134,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(const Attn
 
 cudaError_t launch_attend_join(const AttnArgs& a, int grid, cudaStream_t st) {
   const int rows = static_cast<int>(std::min<long long>(a.tr, static_cast<long long>(a.m) * a.G));
-  // pieces per item: about grid / items
-  if (static_cast<long long>(a.B) * a.H * a.rt * 8 < grid)
-    attend_join_kernel<8><<<dim3(grid, std::min(rows, 64)), kJoinWarps * 32, 0, st>>>(a);
+  if (a.by_item)
+    join_items_kernel<<<dim3(a.B * a.H * a.rt, rows), kJoinWarps * 32, 0, st>>>(a);
   else
-    attend_join_kernel<1><<<dim3(grid, std::min((rows + 7) / 8, 16)), kJoinWarps * 32, 0, st>>>(a);
+    join_ctas_kernel<<<dim3(grid, kShares), kJoinWarps * 32, 0, st>>>(a);
   note_launch();
   return cudaGetLastError();
 }

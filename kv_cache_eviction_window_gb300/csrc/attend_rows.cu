@@ -67,7 +67,7 @@ __global__ void __launch_bounds__(kThreads, 2) attend_rows_kernel(const AttnArgs
   __shared__ float s_m[kWarps][kTR], s_l[kWarps][kTR];
   const int warp = warp_id(), lane = lane_id();
   const int quad = lane >> 2, ql = lane & 3;
-  if (threadIdx.x == 0) a.rec[blockIdx.x] = make_int4(-1, 0, 0, 0);
+  rec_clear(a);
   const Share sh =
       share_of<kThreads>(a.B * a.H * a.rt, [&](int i) { return item_range<kTK>(a, i).tiles; }, blockIdx.x);
   if (static_cast<int>(blockIdx.x) >= sh.grid) return;
@@ -303,8 +303,7 @@ __global__ void __launch_bounds__(kThreads, 2) attend_rows_kernel(const AttnArgs
         if (lane == 0) a.part_ml[static_cast<long long>(slot) * kTR + r] = make_float2(M, L);
       }
     }
-    if (first && !last && threadIdx.x == 0)
-      a.rec[blockIdx.x] = make_int4(item, last_cta(sh, base + x.tiles) - blockIdx.x, 0, 0);
+    if (first) rec_first(a, item, last ? 0 : last_cta(sh, base + x.tiles) - static_cast<int>(blockIdx.x));
     __syncthreads();   // s_m, s_l and the accumulators are read before the next item
     base += x.tiles;
     at = base;

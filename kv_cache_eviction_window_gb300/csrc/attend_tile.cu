@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int warp = warp_id(), lane = lane_id();
   if (threadIdx.x == 0) {
-    a.rec[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    rec_clear(a);
     mbar_init(&qfull, 1);
     mbar_init(&qempty, 2);
     for (int s = 0; s < kStages; ++s) {
@@ -525,8 +525,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         else
           a.part_ml[static_cast<long long>(slot) * a.tr + first_row + row] = make_float2(ref, sum);
       }
-      if (first && !last && threadIdx.x == 0)
-        a.rec[blockIdx.x] = make_int4(item, last_cta(sh, base + x.tiles) - blockIdx.x, 0, 0);
+      if (first) rec_first(a, item, last ? 0 : last_cta(sh, base + x.tiles) - static_cast<int>(blockIdx.x));
       tc_fence_before();                             // O is read before the next piece's products
       base += x.tiles;
       at = base;
@@ -542,6 +541,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 }  // namespace
+
+int attend_tile_rows(bool split) { return split ? 64 : 128; }
 
 cudaError_t launch_attend_tile(const AttnArgs& a, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                                int block, bool split, int grid, cudaStream_t st) {

@@ -87,7 +87,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     s_abort = 0;
     fence_mbar_init();
   }
-  if (threadIdx.x == 0) a.rec[blockIdx.x] = make_int4(-1, 0, 0, 0);
+  if (threadIdx.x == 0) a.rec[blockIdx.x] = make_int2(-1, 0);
   const Share sh = share_of<kThreads>(a.B * a.H * per_seg,
                                       [&](int i) { return key_item(a, i, per_seg, tok).blocks; }, blockIdx.x);
   if (static_cast<int>(blockIdx.x) >= sh.grid) return;   // the whole CTA
@@ -280,7 +280,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else {
         part[(2ll * blockIdx.x + (first ? 1 : 0)) * kKeys + key] = sum;
         if (first && threadIdx.x == 0)
-          a.rec[blockIdx.x] = make_int4(item, last_cta(sh, base + x.blocks) - blockIdx.x, 0, 0);
+          a.rec[blockIdx.x] = make_int2(item, last_cta(sh, base + x.blocks) - static_cast<int>(blockIdx.x));
       }
       base += x.blocks;
       at = base;
@@ -297,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Items that several CTAs share: the partials in order (slots as in attend_join.cu).
 __global__ void __launch_bounds__(kKeys) weights_join_kernel(const AttnArgs a, const float* part) {
-  const int4 rec = a.rec[blockIdx.x];
+  const int2 rec = a.rec[blockIdx.x];
   if (rec.x < 0) return;
   const int per_seg = (a.max_len + kKeys - 1) / kKeys;
   const int seg = rec.x / per_seg, j = (rec.x - seg * per_seg) * kKeys + threadIdx.x;
