@@ -253,21 +253,25 @@ def make_kv_packed(k, v) -> kvsel_kv:
 
 
 def _ptr(t) -> Optional[int]:
-    if t is None:
-        return None
-    if isinstance(t, int):
-        return t
-    return t.data_ptr()
+    return t if t is None or isinstance(t, int) else t.data_ptr()
 
 
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        import torch
-
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
+def _current_stream() -> int:
+    """Handle of torch's current stream (the raw getter: a Stream object costs more than a launch)."""
+    import torch
+
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if raw is None:
+        return torch.cuda.current_stream().cuda_stream
+    return raw(torch.cuda.current_device())
 
 
 def _check(rc: int, where: str) -> None:
@@ -431,9 +435,10 @@ def kvsel_attend_workspace_size(params: kvsel_attn_params, acc: bool = False) ->
 def kvsel_attend(params: kvsel_attn_params, q, kv: kvsel_kv, lens, out, ws, new_lens=None, offsets=None, lse=None,
                  acc=None, stream=None) -> None:
     """Attention of new tokens over the cache; with acc every cached row's weight is added."""
-    _check(load().kvsel_attend(ctypes.byref(params), _ptr(q), ctypes.byref(kv), _ptr(lens), _ptr(new_lens),
-                               _ptr(offsets), _ptr(out), _ptr(lse), _ptr(acc), _ptr(ws),
-                               ws.numel() * ws.element_size(), _stream(stream)), "kvsel_attend")
+    rc = (_lib or load()).kvsel_attend(params, _ptr(q), kv, _ptr(lens), _ptr(new_lens), _ptr(offsets), _ptr(out),
+                                       _ptr(lse), _ptr(acc), ws.data_ptr(), ws.nbytes, _stream(stream))
+    if rc:
+        _check(rc, "kvsel_attend")
 
 
 def kvsel_evict_append_workspace_size(params: kvsel_evict_params) -> int:
@@ -446,9 +451,10 @@ def kvsel_evict_append_workspace_size(params: kvsel_evict_params) -> int:
 def kvsel_evict_append(params: kvsel_evict_params, kv: kvsel_kv, lens, seen, pos, acc, k_new, v_new, ws,
                        new_lens=None, stream=None) -> None:
     """Evict by accumulated weight until the new rows fit the budget, then append them."""
-    _check(load().kvsel_evict_append(ctypes.byref(params), ctypes.byref(kv), _ptr(lens), _ptr(seen), _ptr(pos),
-                                     _ptr(acc), _ptr(k_new), _ptr(v_new), _ptr(new_lens), _ptr(ws),
-                                     ws.numel() * ws.element_size(), _stream(stream)), "kvsel_evict_append")
+    rc = (_lib or load()).kvsel_evict_append(params, kv, _ptr(lens), _ptr(seen), _ptr(pos), _ptr(acc), _ptr(k_new),
+                                             _ptr(v_new), _ptr(new_lens), ws.data_ptr(), ws.nbytes, _stream(stream))
+    if rc:
+        _check(rc, "kvsel_evict_append")
 
 
 def kvsel_get_device_status(ws, stream=None) -> int:

@@ -5,11 +5,15 @@
 // order; the new rows follow at `keep`.  So a row moves only when it has to, nothing that is
 // read is written by another slot, and the new rows are the segment's last.
 //
-// evict_select_kernel: one CTA per segment ranks the slots (three-digit radix selection of
-// the keep-th largest key, then an ordered scan for ties, holes and fills).
+// evict_few_kernel: up to four rows to evict (a decode step): one CTA per segment finds them by
+// as many block-wide minima and moves the rows itself.  Bound: latency.
+// evict_select_kernel: one CTA per segment ranks the slots: the keep-th largest key by a radix
+// selection in three digits, then ordered scans for ties, holes and fills.  The keys stay in
+// shared memory (up to 49,152 slots); a thread owns an odd number of consecutive slots, so that
+// its walk through them meets no bank twice and equal neighbours cost one count.
 // evict_move_kernel: slot keep + i of a segment is handled by one half warp per side: its old
-// row goes to its hole, then new row i takes the slot.  Bound by HBM: 8 B per slot read, 512 B
-// per moved or new row read and written.
+// row goes to its hole, then new row i takes the slot.  Bound: HBM, 512 B per moved or new row
+// read and written (and 8 B per slot before).
 #include <algorithm>
 
 #include "evict.cuh"
@@ -46,11 +50,11 @@ __device__ __forceinline__ Seg seg_of(const EvictArgs& a, int seg) {
 }
 __device__ __forceinline__ uint32_t slot_key(const EvictArgs& a, const Seg& s, long long base, int i) {
   const int p = a.pos[base + i];
-  if (p < a.n_sink || p >= s.recent0) return 0xFFFFFFFFu;
-  return weight_key(a.acc[base + i]);
+  const float w = a.acc[base + i];                   // (both loads before the test)
+  return p < a.n_sink || p >= s.recent0 ? 0xFFFFFFFFu : weight_key(w);
 }
 
-// inclusive block-wide scan of three counters packed in 21-bit fields
+// inclusive block-wide scan
 __device__ __forceinline__ unsigned long long block_scan(unsigned long long v, unsigned long long* s_w,
                                                          unsigned long long& total) {
   const int lane = lane_id(), warp = warp_id();
@@ -61,37 +65,46 @@ __device__ __forceinline__ unsigned long long block_scan(unsigned long long v, u
   }
   if (lane == 31) s_w[warp] = v;
   __syncthreads();
-  if (warp == 0) {
-    unsigned long long y = s_w[lane];
+  unsigned long long y = s_w[lane];                  // every warp scans the 32 sums
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const unsigned long long z = __shfl_up_sync(0xffffffffu, y, o);
-      if (lane >= o) y += z;
-    }
-    s_w[lane] = y;
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned long long z = __shfl_up_sync(0xffffffffu, y, o);
+    if (lane >= o) y += z;
   }
-  __syncthreads();
-  if (warp > 0) v += s_w[warp - 1];
-  total = s_w[31];
+  total = __shfl_sync(0xffffffffu, y, 31);
+  if (warp > 0) v += __shfl_sync(0xffffffffu, y, warp - 1);
   __syncthreads();
   return v;
 }
 
+constexpr int kKeptSlots = 49152;                    // slots whose keys fit into shared memory
+
+// KEPT: the keys are in shared memory, else formed again from pos and acc in every pass
+template <bool KEPT>
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictArgs a) {
+  extern __shared__ uint32_t s_key[];
   __shared__ int s_hist[2048];
   __shared__ unsigned long long s_w[32];
   __shared__ uint32_t s_prefix;
   __shared__ int s_need;
-  const int seg = blockIdx.x;
+  const int seg = blockIdx.x, tid = threadIdx.x;
   const Seg s = seg_of(a, seg);
   const long long base = static_cast<long long>(seg) * a.capacity;
   __syncthreads();   // every thread has read lens and seen
-  if (threadIdx.x == 0) {
+  if (tid == 0) {
     a.head[seg] = make_int4(s.keep, s.n, s.m, s.seen);
     a.lens[seg] = s.keep + s.m;
     a.seen[seg] = s.seen + s.m;
   }
   if (s.keep == s.n) return;
+  if (KEPT) {
+#pragma unroll 8
+    for (int i = tid; i < s.n; i += kSelThreads) s_key[i] = slot_key(a, s, base, i);
+  }
+  const int run = ((s.n + kSelThreads - 1) / kSelThreads) | 1;
+  const int i0 = static_cast<int>(min(static_cast<long long>(s.n), static_cast<long long>(tid) * run));
+  const int i1 = static_cast<int>(min(static_cast<long long>(s.n), static_cast<long long>(i0) + run));
+  auto key = [&](int i) { return KEPT ? s_key[i] : slot_key(a, s, base, i); };
 
   // the keep-th largest key, by digits of 11, 11 and 10 bits from the top
   uint32_t prefix = 0, mask = 0;
@@ -99,23 +112,33 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
   if (s.keep == 0) prefix = 0xFFFFFFFFu, mask = 0xFFFFFFFFu, need = 0;
   for (int pass = 0; pass < 3 && s.keep > 0; ++pass) {
     const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), bins = pass == 2 ? 1024 : 2048;
-    for (int i = threadIdx.x; i < bins; i += kSelThreads) s_hist[i] = 0;
+    for (int i = tid; i < bins; i += kSelThreads) s_hist[i] = 0;
     __syncthreads();
-    for (int i = threadIdx.x; i < s.n; i += kSelThreads) {
-      const uint32_t k = slot_key(a, s, base, i);
-      if ((k & mask) == prefix) atomicAdd(&s_hist[(k >> shift) & (bins - 1)], 1);
+    int bin = -1, cnt = 0;
+#pragma unroll 4
+    for (int i = i0; i < i1; ++i) {
+      const uint32_t k = key(i);
+      if ((k & mask) != prefix) continue;
+      const int d = static_cast<int>((k >> shift) & (bins - 1));
+      if (d != bin) {
+        if (cnt) atomicAdd(&s_hist[bin], cnt);
+        bin = d;
+        cnt = 0;
+      }
+      ++cnt;
     }
+    if (cnt) atomicAdd(&s_hist[bin], cnt);
     __syncthreads();
     // thread t owns bins 2t and 2t + 1 counted from the top
     const int per = bins / kSelThreads;
     int own = 0;
-    for (int u = 0; u < per; ++u) own += s_hist[bins - 1 - (threadIdx.x * per + u)];
+    for (int u = 0; u < per; ++u) own += s_hist[bins - 1 - (tid * per + u)];
     unsigned long long total;
     int before = static_cast<int>(block_scan(own, s_w, total)) - own;
     for (int u = 0; u < per; ++u) {
-      const int bin = bins - 1 - (threadIdx.x * per + u), c = s_hist[bin];
+      const int d = bins - 1 - (tid * per + u), c = s_hist[d];
       if (before < need && need <= before + c) {
-        s_prefix = prefix | (static_cast<uint32_t>(bin) << shift);
+        s_prefix = prefix | (static_cast<uint32_t>(d) << shift);
         s_need = need - before;
       }
       before += c;
@@ -124,26 +147,31 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
     prefix = s_prefix;
     need = s_need;
     mask |= static_cast<uint32_t>(bins - 1) << shift;
-    __syncthreads();
   }
   // keys above `prefix` stay, and the first `need` slots whose key equals it
-  int ties = 0, hole = 0, fill = 0;                  // before this block of slots
-  for (int i0 = 0; i0 < s.n; i0 += kSelThreads) {
-    const int i = i0 + threadIdx.x;
-    const bool in = i < s.n;
-    const uint32_t k = in ? slot_key(a, s, base, i) : 0u;
-    const bool tie = in && k == prefix;
-    unsigned long long total;
-    const int tr = ties + static_cast<int>(block_scan(tie, s_w, total));   // ties up to and with i
-    ties += static_cast<int>(total);
-    const bool kept = in && (k > prefix || (tie && tr <= need));
-    const bool is_hole = in && !kept && i < s.keep, is_fill = kept && i >= s.keep;
-    const unsigned long long v = (static_cast<unsigned long long>(is_hole) << 32) | (is_fill ? 1u : 0u);
-    const unsigned long long sc = block_scan(v, s_w, total);
-    if (is_hole) a.holes[base + hole + static_cast<int>(sc >> 32) - 1] = i;
-    if (in && i >= s.keep) a.fills[base + i - s.keep] = is_fill ? fill + static_cast<int>(sc & 0xFFFFFFFFu) - 1 : -1;
-    hole += static_cast<int>(total >> 32);
-    fill += static_cast<int>(total & 0xFFFFFFFFu);
+  __syncthreads();
+  int ties = 0;
+#pragma unroll 4
+  for (int i = i0; i < i1; ++i) ties += key(i) == prefix;
+  unsigned long long total;
+  const int ties0 = static_cast<int>(block_scan(ties, s_w, total)) - ties;
+  unsigned long long v = 0;                          // holes above, fills below
+  int t = ties0;
+#pragma unroll 4
+  for (int i = i0; i < i1; ++i) {
+    const uint32_t k = key(i);
+    const bool kept = k > prefix || (k == prefix && t++ < need);
+    if (!kept && i < s.keep) v += 1ull << 32;
+    if (kept && i >= s.keep) v += 1;
+  }
+  const unsigned long long sc = block_scan(v, s_w, total) - v;
+  int hole = static_cast<int>(sc >> 32), fill = static_cast<int>(sc & 0xFFFFFFFFu);
+  t = ties0;
+  for (int i = i0; i < i1; ++i) {
+    const uint32_t k = key(i);
+    const bool kept = k > prefix || (k == prefix && t++ < need);
+    if (!kept && i < s.keep) a.holes[base + hole++] = i;
+    if (i >= s.keep) a.fills[base + i - s.keep] = kept ? fill++ : -1;
   }
 }
 
@@ -155,43 +183,122 @@ __device__ __forceinline__ long long slot_elem(const EvictArgs& a, int b, int h,
   return ((static_cast<long long>(pb) * bs + (i % bs)) * a.H + h) * kHeadDim;
 }
 
+// Slot i of a segment, by one warp: its old row to slot `to` (-1: it does not stay, or stays where it
+// is), then new row `fresh` (-1: none) in its place.
+__device__ __forceinline__ void move_slot(const EvictArgs& a, int b, int h, long long base, int i, int to, int fresh,
+                                          int seen) {
+  const int lane = lane_id(), side = lane >> 4, piece = lane & 15;
+  uint16_t* cache = side ? a.v : a.k;
+  const long long e = slot_elem(a, b, h, i);
+  bool bad = e < 0;
+  if (to >= 0) {
+    const long long ed = slot_elem(a, b, h, to);
+    bad |= ed < 0;
+    if (e >= 0 && ed >= 0)
+      *(reinterpret_cast<uint4*>(cache + ed) + piece) = *(reinterpret_cast<const uint4*>(cache + e) + piece);
+    if (lane == 0) {
+      a.pos[base + to] = a.pos[base + i];
+      a.acc[base + to] = a.acc[base + i];
+    }
+  }
+  __syncwarp();
+  if (fresh >= 0) {
+    if (e >= 0)
+      *(reinterpret_cast<uint4*>(cache + e) + piece) =
+          __ldg(reinterpret_cast<const uint4*>((side ? a.v_new : a.k_new) + b * a.new_req + h * a.new_head +
+                                               static_cast<long long>(fresh) * a.new_tok) + piece);
+    if (lane == 0) {
+      a.pos[base + i] = seen + fresh;
+      a.acc[base + i] = 0.f;
+    }
+  }
+  if (bad && lane == 0) atomicOr(a.status, DEV_BAD_INDEX);
+}
+
+// At most kFew rows to evict and to append.  A slot ranks by (key, then the later slot first): the
+// first of that order leave.  A thread keeps the kFew lowest of its own slots, sorted.
+constexpr int kFew = 4;
+__global__ void __launch_bounds__(kSelThreads) evict_few_kernel(const EvictArgs a) {
+  __shared__ unsigned long long s_min[kFew][32];
+  const int seg = blockIdx.x, b = seg / a.H, h = seg - b * a.H;
+  const Seg s = seg_of(a, seg);
+  const long long base = static_cast<long long>(seg) * a.capacity;
+  const int gone = s.n - s.keep;                     // rows that leave
+  int out[kFew];
+#pragma unroll
+  for (int i = 0; i < kFew; ++i) out[i] = 0x7FFFFFFF;
+  if (gone > 0) {
+    unsigned long long low[kFew];
+#pragma unroll
+    for (int i = 0; i < kFew; ++i) low[i] = ~0ull;
+#pragma unroll 4
+    for (int i = threadIdx.x; i < s.n; i += kSelThreads) {
+      unsigned long long k = (static_cast<unsigned long long>(slot_key(a, s, base, i)) << 32) | (0xFFFFFFFFu - i);
+#pragma unroll
+      for (int u = 0; u < kFew; ++u) {
+        const unsigned long long x = min(low[u], k);
+        k = max(low[u], k);
+        low[u] = x;
+      }
+    }
+    for (int r = 0; r < gone; ++r) {
+      unsigned long long m = low[0];
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) m = min(m, __shfl_xor_sync(0xffffffffu, m, o));
+      if (lane_id() == 0) s_min[r][warp_id()] = m;
+      __syncthreads();
+      m = s_min[r][lane_id()];
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) m = min(m, __shfl_xor_sync(0xffffffffu, m, o));
+      if (low[0] == m) {                             // its owner goes on with its next one
+#pragma unroll
+        for (int u = 0; u + 1 < kFew; ++u) low[u] = low[u + 1];
+        low[kFew - 1] = ~0ull;
+      }
+      // the slots that leave, in ascending order
+      int x = static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(m));
+#pragma unroll
+      for (int u = 0; u < kFew; ++u) {
+        const int y = min(out[u], x);
+        x = max(out[u], x);
+        out[u] = y;
+      }
+    }
+  }
+  __syncthreads();   // every thread has read lens and seen
+  if (threadIdx.x == 0) {
+    a.lens[seg] = s.keep + s.m;
+    a.seen[seg] = s.seen + s.m;
+  }
+  // warp u: slot keep + u; the f-th kept slot behind `keep` fills the f-th hole
+  const int u = warp_id();
+  if (u >= max(gone, s.m)) return;
+  auto leaves = [&](int i) {
+    bool y = false;
+#pragma unroll
+    for (int v = 0; v < kFew; ++v) y |= out[v] == i;
+    return y;
+  };
+  int to = -1;
+  if (u < gone && !leaves(s.keep + u)) {
+    int f = 0;
+    for (int v = 0; v < u; ++v) f += !leaves(s.keep + v);
+#pragma unroll
+    for (int v = 0; v < kFew; ++v)
+      if (v == f) to = out[v];                       // holes are the lowest of the slots that leave
+  }
+  move_slot(a, b, h, base, s.keep + u, to, u < s.m ? u : -1, s.seen);
+}
+
 __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArgs a) {
   const int seg = blockIdx.y, b = seg / a.H, h = seg - b * a.H;
   const int4 hd = a.head[seg];
   const int keep = hd.x, n = hd.y, m = hd.z, seen = hd.w;
   const long long base = static_cast<long long>(seg) * a.capacity;
-  const int lane = lane_id(), side = lane >> 4, piece = lane & 15;
-  uint16_t* cache = side ? a.v : a.k;
-  const uint16_t* fresh = side ? a.v_new : a.k_new;
   const int slots = max(n - keep, m);
   for (int u = blockIdx.x * kMoveSlots + warp_id(); u < slots; u += gridDim.x * kMoveSlots) {
-    const int i = keep + u;
-    const long long e = slot_elem(a, b, h, i);
     const int rank = u < n - keep ? a.fills[base + u] : -1;
-    int bad = e < 0;
-    if (rank >= 0) {
-      const int d = a.holes[base + rank];
-      const long long ed = slot_elem(a, b, h, d);
-      bad |= ed < 0;
-      if (e >= 0 && ed >= 0)
-        *(reinterpret_cast<uint4*>(cache + ed) + piece) = *(reinterpret_cast<const uint4*>(cache + e) + piece);
-      if (lane == 0) {
-        a.pos[base + d] = a.pos[base + i];
-        a.acc[base + d] = a.acc[base + i];
-      }
-    }
-    __syncwarp();
-    if (u < m) {
-      if (e >= 0)
-        *(reinterpret_cast<uint4*>(cache + e) + piece) =
-            __ldg(reinterpret_cast<const uint4*>(fresh + b * a.new_req + h * a.new_head +
-                                                 static_cast<long long>(u) * a.new_tok) + piece);
-      if (lane == 0) {
-        a.pos[base + i] = seen + u;
-        a.acc[base + i] = 0.f;
-      }
-    }
-    if (bad && lane == 0) atomicOr(a.status, DEV_BAD_INDEX);
+    move_slot(a, b, h, base, keep + u, rank >= 0 ? a.holes[base + rank] : -1, u < m ? u : -1, seen);
   }
 }
 
@@ -199,12 +306,23 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArg
 
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t st) {
   const int segs = a.B * a.H;
-  evict_select_kernel<<<segs, kSelThreads, 0, st>>>(a);
+  const int most = a.capacity - a.budget + a.m;      // rows to evict, and slots behind the kept range, at most
+  // one launch for a few rows, two otherwise
+  if (most <= kFew) {
+    evict_few_kernel<<<segs, kSelThreads, 0, st>>>(a);
+    note_launch();
+    return cudaGetLastError();
+  }
+  cudaError_t e;
+  if (a.capacity <= kKeptSlots) {
+    const size_t smem = static_cast<size_t>(a.capacity) * sizeof(uint32_t);
+    if ((e = ensure_smem(reinterpret_cast<const void*>(evict_select_kernel<true>), smem)) != cudaSuccess) return e;
+    evict_select_kernel<true><<<segs, kSelThreads, smem, st>>>(a);
+  } else {
+    evict_select_kernel<false><<<segs, kSelThreads, 0, st>>>(a);
+  }
   note_launch();
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  const int most = std::max(a.capacity - a.budget + a.m, a.m);
-  if (most <= 0) return cudaSuccess;
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const int gx = std::min((most + kMoveSlots - 1) / kMoveSlots, 65535);
   evict_move_kernel<<<dim3(gx, segs), kMoveThreads, 0, st>>>(a);
   note_launch();
