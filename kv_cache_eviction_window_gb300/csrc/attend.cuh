@@ -217,6 +217,12 @@ __device__ __forceinline__ void rec_first(const AttnArgs& a, int item, int follo
     a.rec[blockIdx.x] = make_int2(item, follow);
 }
 
+// How far (log2 units) a row's running maximum may rise above the reference that its weights are
+// scaled by before sum and accumulator are rescaled.  Floating point loses nothing by the scale; 16
+// leaves 2^94 for the values at 2^17 rows.  (8 rescaled in one step of eight on keys of log-normal
+// norms, 750 cycles each.)
+constexpr float kSlack = 16.f;
+
 // whether row p sees cached row j (j < hi of its tile)
 __device__ __forceinline__ bool sees(const AttnArgs& a, int p, int j) {
   if (!a.causal) return true;

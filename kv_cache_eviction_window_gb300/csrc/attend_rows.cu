@@ -1,6 +1,6 @@
 // Attention of a few query rows (single tokens, drafted tokens) over a long cache:
 //   out_r = sum_j p_rj v_j / sum_j p_rj,  p_rj = exp2(s2 * <q_r, k_j> - ref_r),
-// with the reference ref_r within 8 of the running maximum (in log2 units), so that the
+// with the reference ref_r within kSlack of the running maximum (in log2 units), so that the
 // accumulator is rescaled only when the maximum has grown by more than that; sums and
 // accumulators in fp32.
 //
@@ -204,11 +204,11 @@ __global__ void __launch_bounds__(kThreads, 2) attend_rows_kernel(const AttnArgs
               *d = p[nt][2 * u2];
           }
       }
-      if (__any_sync(0xffffffffu, top[0] > ref[0] + 8.f || top[1] > ref[1] + 8.f)) {
+      if (__any_sync(0xffffffffu, top[0] > ref[0] + kSlack || top[1] > ref[1] + kSlack)) {
         float f[2];
 #pragma unroll
         for (int u2 = 0; u2 < 2; ++u2) {
-          const float r2 = top[u2] > ref[u2] + 8.f ? top[u2] : ref[u2];
+          const float r2 = top[u2] > ref[u2] + kSlack ? top[u2] : ref[u2];
           f[u2] = ref[u2] == -INFINITY ? 0.f : exp2f(ref[u2] - r2);
           ref[u2] = r2;
           sum[u2] *= f[u2];

@@ -1,7 +1,7 @@
 // Attention of many query rows (a chunk of new tokens) over a cache, on tcgen05:
 //   S = Q K^T (fp32 in TMEM), P = exp2(s2 * S - ref) rounded to bf16 into TMEM, O += P V.
-// The reference of a row stays within 8 of its running maximum (log2 units), so O, which stays
-// in TMEM, is rescaled only when the maximum has grown by more; row sums are fp32 over the
+// The reference of a row stays within kSlack = 16 of its running maximum (log2 units), so O, which
+// stays in TMEM, is rescaled only when the maximum has grown by more; row sums are fp32 over the
 // unrounded weights.  P is rounded to bf16 (2^-9 relative at most per weight): V is bf16 and
 // both operands of the product need one type.
 //
@@ -355,9 +355,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         t0 = fmax3(t0, s[60], s[61]);
         t1 = fmax3(t1, s[62], s[63]);
         const float top = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)) * a.s2;
-        if (__any_sync(0xffffffffu, top > ref + 8.f)) {
+        if (__any_sync(0xffffffffu, top > ref + kSlack)) {
           // each row by its own maximum: a result does not depend on the rows next to it
-          const float r2 = top > ref + 8.f ? top : ref;
+          const float r2 = top > ref + kSlack ? top : ref;
           const float f = ref == -INFINITY ? 0.f : exp2f(ref - r2);
           ref = r2;
           sum *= f;
