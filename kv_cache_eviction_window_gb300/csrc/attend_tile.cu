@@ -301,6 +301,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     int g = 0, use = 0, nx = 0, nfix = 0;
     bool ok = true;                                  // the same in every lane of a warp
     auto wait = [&](uint64_t* bar, int phase) {
+      // (the test alone is cheaper than a try_wait that succeeds)
+      if (__all_sync(0xffffffffu, ok && mbar_test(bar, static_cast<uint32_t>(phase & 1)))) return;
       ok = __all_sync(0xffffffffu, ok && mbar_wait(bar, static_cast<uint32_t>(phase & 1), &s_abort, a.wc));
     };
     long long base = sh.item_base, at = sh.begin;
