@@ -421,7 +421,7 @@ typedef struct kvsel_attn_params {
   int32_t group;         /* query heads per KV head, 1..KVSEL_MAX_ATTN_GROUP; query head of
                             member g of KV head h: h * group + g                             */
   int32_t head_dim;      /* must be 128                                                      */
-  int32_t batch;         /* requests, 1..KVSEL_MAX_ATTN_BATCH                                */
+  int32_t batch;         /* requests, 1..KVSEL_MAX_ATTN_BATCH; batch * h_kv <= 65535         */
   int32_t n_new;         /* new tokens of a request at most, 1..2^20 (q, out, lse hold as
                             many rows per query head); 1 = a decode step                     */
   int32_t max_len;       /* rows of a segment at most, 1..2^30: a bound on lens; paged:
@@ -444,7 +444,9 @@ typedef struct kvsel_attn_params {
 } kvsel_attn_params;
 
 /* Bytes of device workspace that kvsel_attend needs on the current device (with_acc: the call
- * passes acc).  Host-only. */
+ * passes acc).  Tens of MB at most, but with acc and n_new * group <= 16 also
+ * 4 * batch * h_kv * n_new * group * max_len bytes (the logits), so keep max_len near the real
+ * lengths.  Host-only. */
 int kvsel_attend_workspace_size(const kvsel_attn_params* p, int with_acc, size_t* bytes);
 
 /* out[b][hq][t] = sum_j w_j v_j with w = softmax_j(scale * <q[b][hq][t], k_j>) over the rows that
@@ -470,7 +472,8 @@ int kvsel_attend_workspace_size(const kvsel_attn_params* p, int with_acc, size_t
  * hold anything and pages without a visible row are not looked up; rows that some token of
  * the request sees must be finite.  A length, offset or block-table entry out of range is
  * recorded in the status word (KVSEL_EDEVICE through kvsel_get_device_status): lengths are
- * clamped, a segment at a bad offset counts as empty, a row in a bad block as zeros. */
+ * clamped, a segment at a bad offset counts as empty, a row in a bad block as zeros.  A bounded
+ * wait that ran out (KVSEL_ETIMEOUT) leaves out, lse and acc undefined. */
 int kvsel_attend(const kvsel_attn_params* p, const void* q, const kvsel_kv* kv, const int32_t* lens,
                  const int32_t* new_lens, const int64_t* offsets, void* out, float* lse, float* acc, void* ws,
                  size_t ws_bytes, void* stream);
@@ -485,7 +488,7 @@ int kvsel_attend(const kvsel_attn_params* p, const void* q, const kvsel_kv* kv, 
 typedef struct kvsel_evict_params {
   int32_t h_kv;          /* KV heads, 1..64                                                  */
   int32_t head_dim;      /* must be 128                                                      */
-  int32_t batch;         /* requests, 1..KVSEL_MAX_ATTN_BATCH                                */
+  int32_t batch;         /* requests, 1..KVSEL_MAX_ATTN_BATCH; batch * h_kv <= 65535         */
   int32_t n_new;         /* new rows of a segment at most; 0 = evict only                    */
   int32_t capacity;      /* rows that a segment has memory for (K/V, pos, acc), 1..2^30      */
   int32_t budget;        /* rows of a segment after the call at most, <= capacity            */
@@ -497,7 +500,8 @@ typedef struct kvsel_evict_params {
                             [batch][h_kv][n_new][head_dim]                                   */
 } kvsel_evict_params;
 
-/* Bytes of device workspace that kvsel_evict_append needs.  Host-only. */
+/* Bytes of device workspace that kvsel_evict_append needs: about 8 per row of capacity, whatever the
+ * budget and n_new.  Host-only. */
 int kvsel_evict_append_workspace_size(const kvsel_evict_params* p, size_t* bytes);
 
 /* Make room for m new rows in every segment and append them.  With n = lens[seg] rows,

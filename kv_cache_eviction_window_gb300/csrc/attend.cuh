@@ -43,6 +43,7 @@ struct AttnArgs {
   // -1, CTAs that follow}
   int2* rec;                      // [grid]
   int by_item;
+  int grid;                       // CTAs of the kernel that works on the items
   WaitCtl wc;
 };
 

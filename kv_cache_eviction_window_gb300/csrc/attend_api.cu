@@ -14,6 +14,7 @@ namespace {
 
 constexpr unsigned long long kDefaultWaitCycles = 2000000000ull;   // ~1 s at the boost clock
 constexpr long long kMaxRows = 1ll << 30;
+constexpr int kMaxSegments = 65535;                  // a grid dimension
 
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 bool aligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -42,6 +43,7 @@ int check_attn(const kvsel_attn_params* p) {
   if (p->head_dim != kHeadDim) return KVSEL_EUNSUPPORTED;
   if (p->h_kv < 1 || p->h_kv > 64 || p->group < 1 || p->batch < 1 || p->n_new < 1 || p->max_len < 1) return KVSEL_EINVAL;
   if (p->group > KVSEL_MAX_ATTN_GROUP || p->batch > KVSEL_MAX_ATTN_BATCH) return KVSEL_EUNSUPPORTED;
+  if (p->batch * p->h_kv > kMaxSegments) return KVSEL_EUNSUPPORTED;
   if (p->n_new > (1 << 20) || p->max_len > kMaxRows) return KVSEL_EUNSUPPORTED;
   if (static_cast<long long>(p->n_new) * p->group * p->h_kv * p->batch > kMaxRows) return KVSEL_EUNSUPPORTED;
   if (p->n_rows > (1ll << 31) - 1) return KVSEL_EUNSUPPORTED;
@@ -174,7 +176,8 @@ int check_evict(const kvsel_evict_params* p) {
   if (!p) return KVSEL_EINVAL;
   if (p->head_dim != kHeadDim) return KVSEL_EUNSUPPORTED;
   if (p->h_kv < 1 || p->h_kv > 64 || p->batch < 1 || p->n_new < 0 || p->capacity < 1 || p->budget < 1) return KVSEL_EINVAL;
-  if (p->batch > KVSEL_MAX_ATTN_BATCH || p->capacity > kMaxRows) return KVSEL_EUNSUPPORTED;
+  if (p->batch > KVSEL_MAX_ATTN_BATCH || p->batch * p->h_kv > kMaxSegments || p->capacity > kMaxRows)
+    return KVSEL_EUNSUPPORTED;
   if (p->n_sink < 0 || p->n_recent < 0 || p->budget > p->capacity) return KVSEL_EINVAL;
   if (static_cast<long long>(p->n_sink) + std::max(p->n_recent, p->n_new) > p->budget) return KVSEL_EBUDGET;
   if (p->new_stride_req || p->new_stride_head || p->new_stride_tok)
@@ -185,6 +188,7 @@ int check_evict(const kvsel_evict_params* p) {
 }
 
 struct EvictLayout {
+  int most = 0;
   size_t head = 0, holes = 0, fills = 0, total = 0;
 };
 EvictLayout evict_layout(const kvsel_evict_params* p) {
@@ -192,8 +196,12 @@ EvictLayout evict_layout(const kvsel_evict_params* p) {
   const size_t segs = static_cast<size_t>(p->batch) * p->h_kv;
   L.head = kStatusBytes + kCounterBytes;
   L.holes = align256(L.head + segs * sizeof(int4));
-  L.fills = align256(L.holes + segs * p->capacity * sizeof(int32_t));
-  L.total = align256(L.fills + segs * p->capacity * sizeof(int32_t));
+  // at most so many rows leave a segment, and so many slots lie behind its kept range
+  L.most = p->capacity - p->budget + p->n_new;
+  // (room for any budget, so that one workspace serves a cache for good)
+  const size_t list = segs * p->capacity * sizeof(int32_t);
+  L.fills = align256(L.holes + list);
+  L.total = align256(L.fills + list);
   return L;
 }
 
@@ -269,6 +277,7 @@ int kvsel_attend(const kvsel_attn_params* p, const void* q, const kvsel_kv* kv, 
   a.part_o = reinterpret_cast<float*>(wsb + pl.o);
   a.part_ml = reinterpret_cast<float2*>(wsb + pl.ml);
   a.rec = reinterpret_cast<int2*>(wsb + pl.rec);
+  a.grid = pl.grid;
   // few rows in all: the join starts a CTA for each (128 items of 256 rows: 119 us, by CTAs 27 us)
   const long long items = static_cast<long long>(p->batch) * p->h_kv * pl.rt;
   a.by_item = items <= pl.grid && items * std::min(pl.tr, p->n_new * p->group) <= 4096;
@@ -338,6 +347,7 @@ int kvsel_evict_append(const kvsel_evict_params* p, const kvsel_kv* kv, int32_t*
   a.head = reinterpret_cast<int4*>(wsb + L.head);
   a.holes = reinterpret_cast<int32_t*>(wsb + L.holes);
   a.fills = reinterpret_cast<int32_t*>(wsb + L.fills);
+  a.most = L.most;
   a.status = static_cast<int*>(ws);
   return launch_rc(launch_evict(a, static_cast<cudaStream_t>(stream)));
 }

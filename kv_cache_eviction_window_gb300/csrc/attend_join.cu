@@ -87,8 +87,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_items_kernel(const AttnA
   const int warp = warp_id(), lane = lane_id(), r = blockIdx.y;
   // an item without rows has no record
   const int2 rec = a.rec[blockIdx.x];
+  // (nor one whose kernel gave up on a wait: what lies there then is not followed)
   const JoinItem x = join_item(a, blockIdx.x, rec.x, rec.y);
-  if (r >= x.rows || rec.x < 0) return;
+  if (r >= x.rows || rec.x < 0 || rec.y < 0 || rec.x + rec.y >= a.grid || rec.x >= a.grid) return;
   Joined p = nothing();
   for (int c = warp; c < x.pieces; c += 8 * kJoinWarps) {
     float2 ml[8];

@@ -15,6 +15,8 @@
 // Items (16 query rows of one segment) are cut along the cache so that every CTA of the grid
 // gets the same number of tiles whatever the lengths are (share_of); the pieces of an item
 // that was cut are joined by attend_join_kernel, in cache order.
+#include <algorithm>
+
 #include "attend.cuh"
 
 namespace kvsel {
@@ -317,20 +319,22 @@ __global__ void __launch_bounds__(256) weights_kept_kernel(const AttnArgs a) {
   __shared__ float s_e[kTR];
   const int seg = blockIdx.y, R = a.m * a.G;
   const ItemRange x = item_range<kTK>(a, seg);       // one item per segment: R <= 16
-  if (static_cast<int>(blockIdx.x) * 256 >= x.n || x.rows == 0) return;
+  if (static_cast<long long>(blockIdx.x) * 256 >= x.n || x.rows == 0) return;
   if (static_cast<int>(threadIdx.x) < x.rows) s_e[threadIdx.x] = a.lse2[static_cast<long long>(seg) * R + threadIdx.x];
   __syncthreads();
-  const int j = blockIdx.x * 256 + threadIdx.x;
   // rows outside the item's tiles have no logits: no query row sees them
   const int in_first = min(x.sink, x.ns * kTK);
-  if (j >= x.n || !((j < in_first) || (j >= x.lo && j < x.hi))) return;
-  const float* lg = a.logits + static_cast<long long>(seg) * R * a.logit_stride + j;
-  float w = 0.f;
-  for (int r = 0; r < x.rows; ++r) {
-    const float e2 = s_e[r];
-    if (e2 != -INFINITY) w += ex2_approx(lg[r * a.logit_stride] - e2);
+  for (long long jj = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; jj < x.n; jj += gridDim.x * 256ll) {
+    const int j = static_cast<int>(jj);
+    if (!(j < in_first || (j >= x.lo && j < x.hi))) continue;
+    const float* lg = a.logits + static_cast<long long>(seg) * R * a.logit_stride + j;
+    float w = 0.f;
+    for (int r = 0; r < x.rows; ++r) {
+      const float e2 = s_e[r];
+      if (e2 != -INFINITY) w += ex2_approx(lg[r * a.logit_stride] - e2);
+    }
+    a.acc[seg * a.acc_stride + j] += w;
   }
-  a.acc[seg * a.acc_stride + j] += w;
 }
 
 }  // namespace
@@ -348,7 +352,9 @@ cudaError_t launch_attend_rows(const AttnArgs& a, int grid, cudaStream_t st) {
 }
 
 cudaError_t launch_weights_kept(const AttnArgs& a, cudaStream_t st) {
-  weights_kept_kernel<<<dim3((a.max_len + 255) / 256, a.B * a.H), 256, 0, st>>>(a);
+  const int segs = a.B * a.H;
+  const int gx = std::min((a.max_len + 255) / 256, std::max(1, 16384 / segs));
+  weights_kept_kernel<<<dim3(gx, segs), 256, 0, st>>>(a);
   note_launch();
   return cudaGetLastError();
 }

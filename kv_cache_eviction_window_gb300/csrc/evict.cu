@@ -165,13 +165,14 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
     if (kept && i >= s.keep) v += 1;
   }
   const unsigned long long sc = block_scan(v, s_w, total) - v;
+  const long long list = static_cast<long long>(seg) * a.most;
   int hole = static_cast<int>(sc >> 32), fill = static_cast<int>(sc & 0xFFFFFFFFu);
   t = ties0;
   for (int i = i0; i < i1; ++i) {
     const uint32_t k = key(i);
     const bool kept = k > prefix || (k == prefix && t++ < need);
-    if (!kept && i < s.keep) a.holes[base + hole++] = i;
-    if (i >= s.keep) a.fills[base + i - s.keep] = kept ? fill++ : -1;
+    if (!kept && i < s.keep) a.holes[list + hole++] = i;
+    if (i >= s.keep) a.fills[list + i - s.keep] = kept ? fill++ : -1;
   }
 }
 
@@ -294,21 +295,21 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArg
   const int seg = blockIdx.y, b = seg / a.H, h = seg - b * a.H;
   const int4 hd = a.head[seg];
   const int keep = hd.x, n = hd.y, m = hd.z, seen = hd.w;
-  const long long base = static_cast<long long>(seg) * a.capacity;
+  const long long base = static_cast<long long>(seg) * a.capacity, list = static_cast<long long>(seg) * a.most;
   const int slots = max(n - keep, m);
   for (int u = blockIdx.x * kMoveSlots + warp_id(); u < slots; u += gridDim.x * kMoveSlots) {
-    const int rank = u < n - keep ? a.fills[base + u] : -1;
-    move_slot(a, b, h, base, keep + u, rank >= 0 ? a.holes[base + rank] : -1, u < m ? u : -1, seen);
+    const int rank = u < n - keep ? a.fills[list + u] : -1;
+    move_slot(a, b, h, base, keep + u, rank >= 0 ? a.holes[list + rank] : -1, u < m ? u : -1, seen);
   }
 }
 
 }  // namespace
 
+bool evict_in_one_launch(int most) { return most <= kFew; }
+
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t st) {
   const int segs = a.B * a.H;
-  const int most = a.capacity - a.budget + a.m;      // rows to evict, and slots behind the kept range, at most
-  // one launch for a few rows, two otherwise
-  if (most <= kFew) {
+  if (evict_in_one_launch(a.most)) {
     evict_few_kernel<<<segs, kSelThreads, 0, st>>>(a);
     note_launch();
     return cudaGetLastError();
@@ -323,7 +324,7 @@ cudaError_t launch_evict(const EvictArgs& a, cudaStream_t st) {
   }
   note_launch();
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  const int gx = std::min((most + kMoveSlots - 1) / kMoveSlots, 65535);
+  const int gx = std::min((a.most + kMoveSlots - 1) / kMoveSlots, std::max(1, 16384 / segs));
   evict_move_kernel<<<dim3(gx, segs), kMoveThreads, 0, st>>>(a);
   note_launch();
   return cudaGetLastError();

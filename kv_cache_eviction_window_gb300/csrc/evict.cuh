@@ -22,10 +22,12 @@ struct EvictArgs {
   // workspace: the segment's numbers for the second launch, its holes, and the rank among the
   // kept ones (or -1) of every slot behind the kept range
   int4* head;                     // [B*H]: rows kept, rows before, new rows, tokens seen before
-  int32_t* holes;                 // [B*H][capacity]
-  int32_t* fills;                 // [B*H][capacity]
+  int most;                       // rows to evict, and slots behind the kept range, at most
+  int32_t* holes;                 // [B*H][most]
+  int32_t* fills;                 // [B*H][most]
   int* status;
 };
+bool evict_in_one_launch(int most);   // then holes and fills are not used
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t st);
 
 }  // namespace kvsel

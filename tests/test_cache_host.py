@@ -77,7 +77,8 @@ def paged(B, **kw):
     (dict(max_len=0), -1), (dict(max_len=(1 << 30) + 1), -3), (dict(window=-1), -1), (dict(n_sink=-1), -1),
     (dict(window=5, causal=False), -3), (dict(scale=-1.0), -1), (dict(scale=float("inf")), -1),
     (dict(scale=float("nan")), -1), (dict(q_strides=(0, 128, 4), n_new=2), -1), (dict(o_strides=(0, 0, 128), n_new=2), -1),
-    (dict(q_strides=(-8, 128, 128), batch=2), -1), (dict(n_new=1 << 20, group=128, h_kv=64), -3)])
+    (dict(q_strides=(-8, 128, 128), batch=2), -1), (dict(n_new=1 << 20, group=128, h_kv=64), -3),
+    (dict(batch=1024, h_kv=64), -3)])
 def test_attend_refuses_parameters(B, kw, code):
     assert attend(B, **kw) == code
 
@@ -117,7 +118,8 @@ def evict(B, kv=None, ptr=None, ws_bytes=1 << 40, **kw):
     (dict(head_dim=64), -3), (dict(h_kv=0), -1), (dict(h_kv=65), -1), (dict(batch=0), -1), (dict(batch=1025), -3),
     (dict(n_new=-1), -1), (dict(capacity=0), -1), (dict(budget=0), -1), (dict(budget=101), -1), (dict(n_sink=-1), -1),
     (dict(n_recent=-1), -1), (dict(n_sink=60, n_recent=41), -2), (dict(n_new=97), -2), (dict(n_new=101, n_sink=0), -2),
-    (dict(new_strides=(0, 128, 100), n_new=2), -1)])
+    (dict(new_strides=(0, 128, 100), n_new=2), -1),
+    (dict(batch=1024, h_kv=64), -3)])
 def test_evict_refuses_parameters(B, kw, code):
     assert evict(B, **kw) == code
     if "new_strides" not in kw:
@@ -131,6 +133,11 @@ def test_evict_refuses_parameters(B, kw, code):
                                       (dict(ws=None), -4), (dict(ws=GOOD + 16), -4)])
 def test_evict_refuses_pointers(B, ptr, code):
     assert evict(B, ptr=ptr) == code
+
+
+def test_evict_workspace_serves_a_cache_for_good(B):
+    size = lambda **kw: B.kvsel_evict_append_workspace_size(B.make_evict_params(h_kv=8, batch=4, capacity=4096, **kw))   # noqa: E731
+    assert size(budget=4096, n_new=1) == size(budget=100, n_new=50) == size(budget=4000, n_new=0)
 
 
 def test_evict_refuses_caches_and_small_workspaces(B):

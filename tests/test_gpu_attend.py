@@ -272,3 +272,77 @@ def test_attention_over_what_a_layer_call_kept():
         e = 132 * 2.0 ** -23 * o["abs_logit"] + 2.0 ** -14
         tol = (2 * e[..., None] + 2.0 ** -8) * o["mean_abs"] + 2.0 ** -8 * np.abs(o["out"])
         assert np.all(np.abs(CH.to_f64(out)[0, h * G:(h + 1) * G] - o["out"]) <= tol)
+
+
+@pytest.mark.parametrize("G,m", [(100, 3), (128, 5), (65, 9), (43, 8), (3, 400)])
+def test_wide_groups_in_chunks(G, m):
+    # groups that fill a tile alone, or leave most of one empty
+    run(G=G, m=m, H=2, lens=[m + 301], layout="paged", block=16, seed=G)
+
+
+@pytest.mark.parametrize("m,G,acc", [(6, 7, False), (300, 4, False), (300, 4, True)])
+def test_a_wait_that_runs_out_is_reported(m, G, acc):
+    """wait_cycles = 1 makes every wait that is not already satisfied give up: the call ends with
+    KVSEL_ETIMEOUT in the status word, and the next call on the same workspace is sound."""
+    import torch
+
+    c = CH.Case(B=2, G=G, H=2, m=m, lens=[2000, 900], layout="paged", seed=m).upload()
+    good = dict(c.params)
+    c.params["wait_cycles"] = 1
+    ws = c.call(acc=acc)
+    assert CH.status(ws) == -6
+    c.params = good
+    c.t["out"].fill_(7.0)
+    c.t["lse"].fill_(7.0)
+    c.t["acc"].zero_()
+    c.call(acc=acc, ws=ws)
+    assert CH.status(ws) == 0
+    c.check(acc=acc)
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("m", [1, 40])
+def test_caches_beyond_2_to_the_32_elements(m):
+    """Blocks and rows whose element offset passes 32 bits, in a paged and in a packed cache, and a
+    token-major contiguous one ([token][head][d])."""
+    import torch
+
+    from kv_cache_eviction_window_gb300 import binding as L
+
+    G, H, n, bs = 4, 4, 200, 16
+    c = CH.Case(G=G, H=H, m=m, lens=n, seed=m)
+    ora = c.oracle()
+    q = CH.to_gpu_bf16(c.q.reshape(1, H * G, m, CH.D))
+    k, v = (CH.to_gpu_bf16(np.stack(x[0])) for x in (c.k, c.v))          # [H][n][d]
+    blocks = (1 << 32) // (bs * H * CH.D) + 64
+    pools = [torch.empty((blocks, bs, H, CH.D), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    used = -(-n // bs)
+    table = torch.arange(blocks - used, blocks, dtype=torch.int32, device="cuda").flip(0).reshape(1, used).contiguous()
+    for pool, x in zip(pools, (k, v)):
+        rows = torch.zeros((used * bs, H, CH.D), dtype=torch.bfloat16, device="cuda")
+        rows[:n] = x.permute(1, 0, 2)
+        pool[table[0].long()] = rows.view(used, bs, H, CH.D)
+    flat = [p.view(-1, CH.D) for p in pools]                             # the same memory as packed rows
+    base = flat[0].shape[0] - H * n
+    packed = [x.clone() for x in (k, v)]
+    strided = [torch.empty((n, H, CH.D), dtype=torch.bfloat16, device="cuda").copy_(x.permute(1, 0, 2)) for x in (k, v)]
+    for kind in ("paged", "strided", "packed"):
+        p = L.make_attn_params(h_kv=H, group=G, batch=1, n_new=m, max_len=n, n_rows=flat[0].shape[0] if kind == "packed" else 0,
+                               acc_stride=n, lens_per_head=kind == "packed")
+        offsets = None
+        if kind == "paged":
+            kv = L.make_kv_paged(pools[0], pools[1], table)
+        elif kind == "strided":
+            kv = L.make_kv_contiguous(*(x.permute(1, 0, 2) for x in strided))
+        else:
+            for f, x in zip(flat, packed):
+                f[base:] = x.reshape(H * n, CH.D)
+            offsets = torch.arange(H, device="cuda", dtype=torch.int64) * n + base
+            kv = L.make_kv_packed(flat[0], flat[1])
+        lens = torch.full((H,) if kind == "packed" else (1,), n, dtype=torch.int32, device="cuda")
+        c.t = dict(out=torch.empty((1, H * G, m, CH.D), dtype=torch.bfloat16, device="cuda"),
+                   lse=torch.empty((1, H * G, m), device="cuda"), acc=torch.zeros((1, H, n), device="cuda"))
+        ws = CH.workspace(L.kvsel_attend_workspace_size(p, True))
+        L.kvsel_attend(p, q, kv, lens, c.t["out"], ws, offsets=offsets, lse=c.t["lse"], acc=c.t["acc"])
+        assert CH.status(ws) == 0
+        c.check(ora, acc=True)

@@ -178,6 +178,48 @@ def test_bad_lengths_and_blocks_are_reported():
     assert L.kvsel_get_device_status(ws) == 0
 
 
+@pytest.mark.parametrize("n,m", [(60000, 5), (60000, 0), (49152, 300), (49153, 300)])
+def test_caches_beyond_shared_memory(n, m):
+    c = Cache(H=1, capacity=n, lens=n, m=m, seed=n, ties=True)
+    ws = c.step(CH.rng(1), budget=n - 1000, n_sink=4, n_recent=300)
+    assert CH.status(ws) == 0
+    c.check()
+
+
+@pytest.mark.parametrize("m", [1, 30])
+def test_a_captured_call_follows_the_lengths(m):
+    import torch
+
+    from kv_cache_eviction_window_gb300 import binding as L
+
+    c = Cache(B=2, H=2, capacity=100, lens=[[100, 40], [99, 71]], m=m, seed=m)
+    g = CH.rng(1)
+    kn, vn = (CH.bf16(g.standard_normal((2, 2, m, CH.D))) for _ in range(2))
+    kd, vd = CH.to_gpu_bf16(kn), CH.to_gpu_bf16(vn)
+    p = L.make_evict_params(h_kv=2, batch=2, capacity=100, budget=100, n_new=m, n_sink=2, n_recent=m)
+    ws = CH.workspace(L.kvsel_evict_append_workspace_size(p))
+    d = c.dev
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        L.kvsel_evict_append(p, c.kv, d["lens"], d["seen"], d["pos"], d["acc"], kd, vd, ws)
+    for _ in range(3):
+        graph.replay()
+        for b in range(2):
+            for h in range(2):
+                n, seen = int(c.lens[b, h]), int(c.seen[b, h])
+                order = CO.evict_segment(c.pos[b, h, :n], c.acc[b, h, :n], seen, m, budget=100, n_sink=2, n_recent=m)
+                keep = len(order)
+                for x in (c.pos, c.acc, c.k, c.v):
+                    x[b, h, :keep] = x[b, h, order]
+                c.pos[b, h, keep:keep + m] = seen + np.arange(m)
+                c.acc[b, h, keep:keep + m] = 0
+                c.k[b, h, keep:keep + m] = kn[b, h]
+                c.v[b, h, keep:keep + m] = vn[b, h]
+                c.lens[b, h], c.seen[b, h] = keep + m, seen + m
+    assert CH.status(ws) == 0
+    c.check()
+
+
 def test_decode_loop_with_eviction():
     """A prompt is compacted, then tokens arrive one by one (and in a chunk): evict and append,
     attend with running weights.  The copy follows with the oracle; the weights that the next
