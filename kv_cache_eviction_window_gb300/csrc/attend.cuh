@@ -9,8 +9,28 @@
 
 namespace kvsel {
 
+// Division of 0 <= n < 2^31 by a number known at the launch: n * m >> p with p = 31 + ceil(log2 d) and
+// m = ceil(2^p / d), exact for these n.  (The plan of a call is a chain of divisions.)
+struct Div {
+  unsigned int m;
+  int p;
+  __host__ static Div by(int d) {
+    Div x;
+    int k = 0;
+    while ((1ll << k) < d) ++k;
+    x.p = 31 + k;
+    x.m = static_cast<unsigned int>(((1ull << x.p) + d - 1) / d);
+    return x;
+  }
+  __device__ __forceinline__ int operator()(int n) const {
+    return static_cast<int>((static_cast<unsigned long long>(n) * m) >> p);
+  }
+};
+
 struct AttnArgs {
   int B, H, G, m;                 // requests, KV heads, group, new tokens of a request at most
+  Div by_rt, by_H, by_G;          // items per segment, heads, group
+  int page_shift;                 // paged: log2 of the rows of a page
   int max_len;                    // rows of a segment at most
   int causal, window, n_sink;
   int per_head;                   // lens [B*H] instead of [B]
@@ -88,9 +108,9 @@ template <int TK>
 __device__ __forceinline__ ItemRange item_range(const AttnArgs& a, int item) {
   ItemRange x;
   const int TR = a.tr;
-  x.seg = item / a.rt;
+  x.seg = a.by_rt(item);
   x.rt = item - x.seg * a.rt;
-  x.b = x.seg / a.H;
+  x.b = a.by_H(x.seg);
   x.h = x.seg - x.b * a.H;
   const SegLen s = seg_len(a, x.b, x.h);
   x.n = s.n;
@@ -104,8 +124,8 @@ __device__ __forceinline__ ItemRange item_range(const AttnArgs& a, int item) {
     return x;
   }
   if (a.causal) {
-    x.p0 = s.n - s.m + r0 / a.G;
-    x.p1 = s.n - s.m + (r0 + x.rows - 1) / a.G;
+    x.p0 = s.n - s.m + a.by_G(r0);
+    x.p1 = s.n - s.m + a.by_G(r0 + x.rows - 1);
     x.hi = max(0, x.p1 + 1);
   } else {
     x.p0 = x.p1 = s.n - 1;
@@ -115,7 +135,7 @@ __device__ __forceinline__ ItemRange item_range(const AttnArgs& a, int item) {
     const int lo = max(0, x.p0 - a.window + 1);
     // pages behind the window may be gone: a tile starts with the first page that is seen; at an
     // even row otherwise (two logits are kept at a time)
-    const int al = lo - lo % (a.src.paged ? a.src.block_size : 2);
+    const int al = lo & -(a.src.paged ? 1 << a.page_shift : 2);
     const int sink = min(a.n_sink, x.hi);
     const int ns = (sink + TK - 1) / TK;
     if (lo > sink && al > ns * TK) {
@@ -143,22 +163,31 @@ __device__ __forceinline__ void tile_rows(const ItemRange& x, int ti, int& j0, i
 // The share of CTA `cta` of the grid in all tiles of all items, in item order: tiles
 // [total * cta / grid, total * (cta + 1) / grid).  Lengths live on the device, so every CTA
 // adds up the items itself (a thread takes consecutive items, then a block-wide scan).
+template <class Item>
 struct Share {
   long long total;
   long long begin, end;           // this CTA's tiles
   int grid;                       // CTAs with work: min(gridDim.x, total)
   int item;                       // item of tile `begin`
   long long item_base;            // its first tile
+  Item first;                     // and its range
 };
-template <int THREADS, class Tiles>
-__device__ __forceinline__ Share share_of(int items, Tiles tiles, int cta) {
+// range(i): the range of item i, with its number of tiles
+template <int THREADS, class Range>
+__device__ __forceinline__ auto share_of(int items, Range range, int cta) -> Share<decltype(range(0))> {
+  using Item = decltype(range(0));
   __shared__ long long s_warp[THREADS / 32];
   __shared__ long long s_base;
   __shared__ int s_item;
+  __shared__ Item s_first;
   const int per = (items + THREADS - 1) / THREADS;
   const int i0 = min(items, static_cast<int>(threadIdx.x) * per), i1 = min(items, i0 + per);
   long long sum = 0;
-  for (int i = i0; i < i1; ++i) sum += tiles(i);
+  Item mine{};                                       // the last of this thread's items (the only one, as a rule)
+  for (int i = i0; i < i1; ++i) {
+    mine = range(i);
+    sum += mine.tiles;
+  }
   long long inc = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -172,7 +201,7 @@ __device__ __forceinline__ Share share_of(int items, Tiles tiles, int cta) {
     if (w < static_cast<int>(threadIdx.x >> 5)) before += s_warp[w];
     total += s_warp[w];
   }
-  Share sh;
+  Share<Item> sh;
   sh.total = total;
   sh.grid = static_cast<int>(min(static_cast<long long>(gridDim.x), total));
   sh.begin = sh.end = 0;
@@ -184,24 +213,29 @@ __device__ __forceinline__ Share share_of(int items, Tiles tiles, int cta) {
     if (sum > 0 && sh.begin >= before && sh.begin < before + sum) {
       long long at = before;
       int i = i0;
-      for (; i < i1; ++i) {
-        const int c = tiles(i);
-        if (sh.begin < at + c) break;
-        at += c;
+      if (per > 1) {
+        for (; i < i1; ++i) {
+          mine = range(i);
+          if (sh.begin < at + mine.tiles) break;
+          at += mine.tiles;
+        }
       }
       s_item = i;
       s_base = at;
+      s_first = mine;
     }
   }
   __syncthreads();
   if (cta < sh.grid) {
     sh.item = s_item;
     sh.item_base = s_base;
+    sh.first = s_first;
   }
   return sh;
 }
 // The last CTA with a tile of an item that ends before tile `e`.
-__device__ __forceinline__ int last_cta(const Share& sh, long long e) {
+template <class Item>
+__device__ __forceinline__ int last_cta(const Share<Item>& sh, long long e) {
   return static_cast<int>((e * sh.grid - 1) / sh.total);
 }
 
@@ -233,10 +267,10 @@ __device__ __forceinline__ bool sees(const AttnArgs& a, int p, int j) {
 __device__ __forceinline__ long long row_elem(const AttnArgs& a, int b, int h, long long row0, int j) {
   if (!a.src.paged)
     return b * a.stride_req + h * a.stride_head + (row0 + static_cast<long long>(j)) * a.stride_tok;
-  const int bs = a.src.block_size;
-  const int pb = __ldg(a.src.block_table + static_cast<size_t>(b) * a.src.max_blocks + j / bs);
+  const int page = j >> a.page_shift;
+  const int pb = __ldg(a.src.block_table + static_cast<size_t>(b) * a.src.max_blocks + page);
   if (pb < 0 || pb >= a.src.num_blocks) return -1;
-  return ((static_cast<long long>(pb) * bs + (j % bs)) * a.H + h) * kHeadDim;
+  return (((static_cast<long long>(pb) << a.page_shift) + (j - (page << a.page_shift))) * a.H + h) * kHeadDim;
 }
 
 // a row that no cached row is read for: behind the tile's end, or before the window of the
@@ -247,13 +281,13 @@ __device__ __forceinline__ bool unseen(const AttnArgs& a, const ItemRange& x, in
 
 // Log-sum-exp of query row rr of a segment from its reference M (log2 units) and sum L.
 __device__ __forceinline__ void write_lse(const AttnArgs& a, int b, int h, int rr, float M, float L) {
-  const int t = rr / a.G, g = rr - t * a.G;
+  const int t = a.by_G(rr), g = rr - t * a.G;
   const float e2 = L > 0.f ? M + log2f(L) : -INFINITY;
   if (a.lse) a.lse[(static_cast<long long>(b) * a.H * a.G + h * a.G + g) * a.m + t] = e2 * 0.6931471805599453f;
   if (a.lse2) a.lse2[static_cast<long long>(b * a.H + h) * a.m * a.G + rr] = e2;
 }
 __device__ __forceinline__ uint16_t* out_row(const AttnArgs& a, int b, int h, int rr) {
-  const int t = rr / a.G, g = rr - t * a.G;
+  const int t = a.by_G(rr), g = rr - t * a.G;
   return a.out + b * a.o_req + static_cast<long long>(h * a.G + g) * a.o_head + static_cast<long long>(t) * a.o_tok;
 }
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
@@ -300,10 +334,10 @@ __device__ __forceinline__ void load_rows(const AttnArgs& a, int b, int h, long 
     return;
   }
   const int bs = a.src.block_size, at = j0 + lane * bs;   // lane i: page i of the rows
-  const bool live = lane < ROWS / bs && at < j1 && seen(at, at + bs - 1);
+  const bool live = lane < (ROWS >> a.page_shift) && at < j1 && seen(at, at + bs - 1);
   int pb = 0;
   if (live) {
-    pb = __ldg(a.src.block_table + static_cast<size_t>(b) * a.src.max_blocks + at / bs);
+    pb = __ldg(a.src.block_table + static_cast<size_t>(b) * a.src.max_blocks + (at >> a.page_shift));
     if (pb < 0 || pb >= a.src.num_blocks) {
       atomicOr(a.wc.status, DEV_BAD_INDEX);
       pb = a.src.num_blocks;                         // outside the pool: zeros

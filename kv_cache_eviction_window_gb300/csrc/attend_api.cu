@@ -272,6 +272,10 @@ int kvsel_attend(const kvsel_attn_params* p, const void* q, const kvsel_kv* kv, 
     a.stride_req = kv->stride_req;
     a.stride_head = kv->stride_head;
   }
+  a.by_rt = Div::by(pl.rt);
+  a.by_H = Div::by(p->h_kv);
+  a.by_G = Div::by(p->group);
+  while (a.src.paged && (1 << a.page_shift) < a.src.block_size) ++a.page_shift;
   a.tr = pl.tr;
   a.rt = pl.rt;
   a.part_o = reinterpret_cast<float*>(wsb + pl.o);

@@ -47,9 +47,9 @@ struct JoinItem {
 };
 __device__ __forceinline__ JoinItem join_item(const AttnArgs& a, int item, int leader, int follow) {
   JoinItem x;
-  const int seg = item / a.rt;
+  const int seg = a.by_rt(item);
   x.rt = item - seg * a.rt;
-  x.b = seg / a.H;
+  x.b = a.by_H(seg);
   x.h = seg - x.b * a.H;
   const int mr = a.new_lens ? __ldg(a.new_lens + x.b) : a.m;
   x.rows = min(a.tr, min(max(mr, 0), a.m) * a.G - x.rt * a.tr);

@@ -70,43 +70,18 @@ __global__ void __launch_bounds__(kThreads, 2) attend_rows_kernel(const AttnArgs
   const int warp = warp_id(), lane = lane_id();
   const int quad = lane >> 2, ql = lane & 3;
   rec_clear(a);
-  const Share sh =
-      share_of<kThreads>(a.B * a.H * a.rt, [&](int i) { return item_range<kTK>(a, i).tiles; }, blockIdx.x);
+  const auto sh = share_of<kThreads>(a.B * a.H * a.rt, [&](int i) { return item_range<kTK>(a, i); }, blockIdx.x);
   if (static_cast<int>(blockIdx.x) >= sh.grid) return;
   const uint32_t ring = smem_u32(smem) + warp * (kStages * kStageBytes);
   float* s_o = reinterpret_cast<float*>(smem);
 
   long long base = sh.item_base, at = sh.begin;
   for (int item = sh.item; at < sh.end; ++item) {
-    const ItemRange x = item_range<kTK>(a, item);
+    const ItemRange x = item == sh.item ? sh.first : item_range<kTK>(a, item);
     if (x.tiles == 0) continue;
     const int ta = static_cast<int>(at - base);
     const int tb = static_cast<int>(min(static_cast<long long>(x.tiles), sh.end - base));
     const int cnt = tb - ta;
-
-    // query rows as mma A fragments: rows quad and quad + 8, two neighbouring columns each
-    uint32_t qf[8][4];
-    const int r0 = x.rt * kTR;
-    int pos[2];
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int r = r0 + quad + 8 * u;
-      const int t = r / a.G, g = r - t * a.G;
-      const bool live = quad + 8 * u < x.rows;
-      pos[u] = live ? (a.causal ? x.n - x.m + t : x.n - 1) : -1;
-      const uint16_t* src = a.q + x.b * a.q_req + static_cast<long long>(x.h * a.G + g) * a.q_head +
-                            static_cast<long long>(t) * a.q_tok;
-#pragma unroll
-      for (int kk = 0; kk < 8; ++kk) {
-        qf[kk][u] = live ? __ldg(reinterpret_cast<const uint32_t*>(src + kk * 16 + ql * 2)) : 0u;
-        qf[kk][u + 2] = live ? __ldg(reinterpret_cast<const uint32_t*>(src + kk * 16 + 8 + ql * 2)) : 0u;
-      }
-    }
-
-    float o[16][4];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-    float ref[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
 
     // element offset of the cached row that this lane looks up for unit u (rows 0..15: lanes l
     // and l + 16), one unit ahead of the copies that use it; -1 where there is none
@@ -142,6 +117,30 @@ __global__ void __launch_bounds__(kThreads, 2) attend_rows_kernel(const AttnArgs
       ahead = lookup(u + 1);
       issue(u, off);
     }
+
+    // query rows as mma A fragments: rows quad and quad + 8, two neighbouring columns each
+    uint32_t qf[8][4];
+    const int r0 = x.rt * kTR;
+    int pos[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int r = r0 + quad + 8 * u;
+      const int t = a.by_G(r), g = r - t * a.G;
+      const bool live = quad + 8 * u < x.rows;
+      pos[u] = live ? (a.causal ? x.n - x.m + t : x.n - 1) : -1;
+      const uint16_t* src = a.q + x.b * a.q_req + static_cast<long long>(x.h * a.G + g) * a.q_head +
+                            static_cast<long long>(t) * a.q_tok;
+#pragma unroll
+      for (int kk = 0; kk < 8; ++kk) {
+        qf[kk][u] = live ? __ldg(reinterpret_cast<const uint32_t*>(src + kk * 16 + ql * 2)) : 0u;
+        qf[kk][u + 2] = live ? __ldg(reinterpret_cast<const uint32_t*>(src + kk * 16 + 8 + ql * 2)) : 0u;
+      }
+    }
+
+    float o[16][4];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    float ref[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
 
     for (int u = 0; u < cnt; ++u) {
       cp_async_wait<kStages - 2>();

@@ -128,8 +128,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     s_abort = 0;
     fence_mbar_init();
   }
-  const Share sh =
-      share_of<kThreads>(a.B * a.H * a.rt, [&](int i) { return item_range<kTK>(a, i).tiles; }, blockIdx.x);
+  const auto sh = share_of<kThreads>(a.B * a.H * a.rt, [&](int i) { return item_range<kTK>(a, i); }, blockIdx.x);
   if (static_cast<int>(blockIdx.x) >= sh.grid) return;   // the whole CTA
   if (warp == kQkWarp) {
     tmem_alloc(&s_tmem, 512);
@@ -156,7 +155,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;                                  // the same in every lane
     long long base = sh.item_base, at = sh.begin;
     for (int item = sh.item; ok && at < sh.end; ++item) {
-      const ItemRange x = item_range<kTK>(a, item);
+      const ItemRange x = item == sh.item ? sh.first : item_range<kTK>(a, item);
       if (x.tiles == 0) continue;
       const int ta = static_cast<int>(at - base);
       const int cnt = static_cast<int>(min(static_cast<long long>(x.tiles), sh.end - base)) - ta;
@@ -240,7 +239,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tS = tbase + w * 128, tO = tbase + 256 + w * 128;
     long long base = sh.item_base, at = sh.begin;
     for (int item = sh.item; ok && at < sh.end; ++item) {
-      const ItemRange x = item_range<kTK>(a, item);
+      const ItemRange x = item == sh.item ? sh.first : item_range<kTK>(a, item);
       if (x.tiles == 0) continue;
       const int cnt = static_cast<int>(min(static_cast<long long>(x.tiles), sh.end - base) - (at - base));
       const int steps = 2 * (SPLIT ? (cnt + 1 - w) / 2 : cnt);   // of this stream: key tile n / 2, buffer n & 1
@@ -307,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     long long base = sh.item_base, at = sh.begin;
     for (int item = sh.item; ok && at < sh.end; ++item) {
-      const ItemRange x = item_range<kTK>(a, item);
+      const ItemRange x = item == sh.item ? sh.first : item_range<kTK>(a, item);
       if (x.tiles == 0) continue;
       const int ta = static_cast<int>(at - base);
       const int tb = static_cast<int>(min(static_cast<long long>(x.tiles), sh.end - base));
@@ -315,10 +314,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int first_row = SPLIT ? 0 : w * block;   // of the item
       const int rows = min(block, x.rows - first_row);
       const int rr = x.rt * a.tr + first_row + row;  // row of the segment
-      const int p = a.causal ? x.n - x.m + rr / a.G : x.n - 1;
+      const int p = a.causal ? x.n - x.m + a.by_G(rr) : x.n - 1;
       // cache rows of the block's first and last token
-      const int pa = a.causal ? x.n - x.m + (x.rt * a.tr + first_row) / a.G : x.n - 1;
-      const int pb = a.causal ? x.n - x.m + (x.rt * a.tr + first_row + max(rows, 1) - 1) / a.G : x.n - 1;
+      const int pa = a.causal ? x.n - x.m + a.by_G(x.rt * a.tr + first_row) : x.n - 1;
+      const int pb = a.causal ? x.n - x.m + a.by_G(x.rt * a.tr + first_row + max(rows, 1) - 1) : x.n - 1;
       float ref = -INFINITY, sum = 0.f;
       int mine = 0;                                  // steps of this piece so far
       const int steps = 2 * (SPLIT ? (cnt + 1 - w) / 2 : cnt);

@@ -24,21 +24,21 @@ constexpr size_t kSmem = 1024 + 2 * kTileBytes + kStages * kTileBytes;
 struct KeyItem {
   int seg, b, h, jb;              // first cached row
   int n, m, first;                // rows, new tokens, row of token 0
-  int q0, blocks;                 // first query block, query blocks that see a row of the item
+  int q0, tiles;                  // first query block, query blocks that see a row of the item
   long long row0;
 };
 __device__ __forceinline__ KeyItem key_item(const AttnArgs& a, int item, int per_seg, int tok) {
   KeyItem x;
   x.seg = item / per_seg;
   x.jb = (item - x.seg * per_seg) * kKeys;
-  x.b = x.seg / a.H;
+  x.b = a.by_H(x.seg);
   x.h = x.seg - x.b * a.H;
   const SegLen s = seg_len(a, x.b, x.h);
   x.n = s.n;
   x.m = s.m;
   x.row0 = s.row0;
   x.first = s.n - s.m;
-  x.q0 = x.blocks = 0;
+  x.q0 = x.tiles = 0;
   if (x.jb >= s.n || s.m == 0) return x;
   int t0 = 0, t1 = s.m;           // tokens that see a row of the item
   if (a.causal) {
@@ -49,7 +49,7 @@ __device__ __forceinline__ KeyItem key_item(const AttnArgs& a, int item, int per
   }
   if (t0 >= t1) return x;
   x.q0 = t0 / tok;
-  x.blocks = (t1 + tok - 1) / tok - x.q0;
+  x.tiles = (t1 + tok - 1) / tok - x.q0;
   return x;
 }
 
@@ -88,8 +88,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_mbar_init();
   }
   if (threadIdx.x == 0) a.rec[blockIdx.x] = make_int2(-1, 0);
-  const Share sh = share_of<kThreads>(a.B * a.H * per_seg,
-                                      [&](int i) { return key_item(a, i, per_seg, tok).blocks; }, blockIdx.x);
+  const auto sh =
+      share_of<kThreads>(a.B * a.H * per_seg, [&](int i) { return key_item(a, i, per_seg, tok); }, blockIdx.x);
   if (static_cast<int>(blockIdx.x) >= sh.grid) return;   // the whole CTA
   if (warp == kMmaWarp) {
     tmem_alloc(&s_tmem, 512);
@@ -109,10 +109,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     long long base = sh.item_base, at = sh.begin;
     for (int item = sh.item; ok && at < sh.end; ++item) {
-      const KeyItem x = key_item(a, item, per_seg, tok);
-      if (x.blocks == 0) continue;
+      const KeyItem x = item == sh.item ? sh.first : key_item(a, item, per_seg, tok);
+      if (x.tiles == 0) continue;
       const int ta = static_cast<int>(at - base);
-      const int tb = static_cast<int>(min(static_cast<long long>(x.blocks), sh.end - base));
+      const int tb = static_cast<int>(min(static_cast<long long>(x.tiles), sh.end - base));
       ok = __all_sync(0xffffffffu, mbar_wait(&kempty, (piece & 1) ^ 1, &s_abort, a.wc));
       if (!ok) break;
       for (int w = 0; w < 2; ++w)
@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(&qfull[s]);
         ++use;
       }
-      base += x.blocks;
+      base += x.tiles;
       at = base;
     }
     if (lane == 0) {
@@ -167,9 +167,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     long long base = sh.item_base, at = sh.begin;
     for (int item = sh.item; ok && at < sh.end; ++item) {
-      const KeyItem x = key_item(a, item, per_seg, tok);
-      if (x.blocks == 0) continue;
-      const int cnt = static_cast<int>(min(static_cast<long long>(x.blocks), sh.end - base) - (at - base));
+      const KeyItem x = item == sh.item ? sh.first : key_item(a, item, per_seg, tok);
+      if (x.tiles == 0) continue;
+      const int cnt = static_cast<int>(min(static_cast<long long>(x.tiles), sh.end - base) - (at - base));
       wait(&kfull, piece++);
       for (int i = 0; i < cnt && ok; ++i, ++use) {
         const int s = use % kStages, u = use & 1;
@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       if (elect_one()) umma_commit(&kempty);
       __syncwarp();
-      base += x.blocks;
+      base += x.tiles;
       at = base;
     }
     if (elect_one()) umma_commit(&done);
@@ -212,10 +212,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     long long base = sh.item_base, at = sh.begin;
     for (int item = sh.item; ok && at < sh.end; ++item) {
-      const KeyItem x = key_item(a, item, per_seg, tok);
-      if (x.blocks == 0) continue;
+      const KeyItem x = item == sh.item ? sh.first : key_item(a, item, per_seg, tok);
+      if (x.tiles == 0) continue;
       const int ta = static_cast<int>(at - base);
-      const int tb = static_cast<int>(min(static_cast<long long>(x.blocks), sh.end - base));
+      const int tb = static_cast<int>(min(static_cast<long long>(x.tiles), sh.end - base));
       const int j = x.jb + key;
       // query rows [r0, r1) of the segment see the cached row
       long long r0 = 0, r1 = j < x.n ? static_cast<long long>(x.m) * a.G : 0;
@@ -274,15 +274,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
       }
       if (!ok) break;
-      const bool first = ta == 0, last = tb == x.blocks;
+      const bool first = ta == 0, last = tb == x.tiles;
       if (first && last) {
         if (j < x.n) a.acc[x.seg * a.acc_stride + j] += sum;
       } else {
         part[(2ll * blockIdx.x + (first ? 1 : 0)) * kKeys + key] = sum;
         if (first && threadIdx.x == 0)
-          a.rec[blockIdx.x] = make_int2(item, last_cta(sh, base + x.blocks) - static_cast<int>(blockIdx.x));
+          a.rec[blockIdx.x] = make_int2(item, last_cta(sh, base + x.tiles) - static_cast<int>(blockIdx.x));
       }
-      base += x.blocks;
+      base += x.tiles;
       at = base;
     }
   }
