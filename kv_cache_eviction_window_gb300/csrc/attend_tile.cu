@@ -54,6 +54,26 @@ __device__ __forceinline__ void umma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, u
       "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
+// Transposes four 16-byte words over four neighbouring lanes: lane q's v[k] becomes lane k's v[q].
+__device__ __forceinline__ void quad_transpose(uint4 (&v)[4]) {
+#pragma unroll
+  for (int s = 1; s < 4; s <<= 1) {
+    const bool up = lane_id() & s;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (k & s) continue;
+      uint4 y = up ? v[k] : v[k | s];
+      y.x = __shfl_xor_sync(0xffffffffu, y.x, s);
+      y.y = __shfl_xor_sync(0xffffffffu, y.y, s);
+      y.z = __shfl_xor_sync(0xffffffffu, y.z, s);
+      y.w = __shfl_xor_sync(0xffffffffu, y.w, s);
+      if (up)
+        v[k] = y;
+      else
+        v[k | s] = y;
+    }
+  }
+}
 // MN-major operand in such a stage
 __device__ __forceinline__ uint64_t sdesc_stage_v(uint32_t saddr, const StageLayout& l) {
   uint64_t d = 0;
@@ -128,6 +148,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     s_abort = 0;
     fence_mbar_init();
   }
+  if (threadIdx.x == kLoadWarp * 32) {
+    tma_prefetch_desc(&tq);
+    tma_prefetch_desc(&tk);
+    tma_prefetch_desc(&tv);
+  }
   const auto sh = share_of<kThreads>(a.B * a.H * a.rt, [&](int i) { return item_range<kTK>(a, i); }, blockIdx.x);
   if (static_cast<int>(blockIdx.x) >= sh.grid) return;   // the whole CTA
   if (warp == kQkWarp) {
@@ -146,11 +171,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncwarp();
   if (warp >= kQkWarp) regs_down<kOtherRegs>();
   if (warp == kLoadWarp) {
-    if (lane == 0) {
-      tma_prefetch_desc(&tq);
-      tma_prefetch_desc(&tk);
-      tma_prefetch_desc(&tv);
-    }
     int use[2] = {0, 0}, piece = 0;                  // ring uses issued, pieces begun
     bool ok = true;                                  // the same in every lane
     long long base = sh.item_base, at = sh.begin;
@@ -453,10 +473,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       const bool live = row < rows && (!SPLIT || w == 0);
       const int slot = 2 * blockIdx.x + (first ? 1 : 0);
-      float* po = a.part_o + (static_cast<long long>(slot) * a.tr + first_row + row) * kHeadDim;
-      uint16_t* dst = live && direct ? out_row(a, x.b, x.h, rr) : nullptr;
-      float f0 = 1.f, f1 = 0.f, inv = sum > 0.f ? 1.f / sum : 0.f;
+      // Results leave by quads of lanes, 64 bytes of four rows in turn (a row per thread took 6000 to
+      // 12000 cycles for a piece: 32 lines touched by each store)
+      const int q0 = row & ~3;
+      float* po = a.part_o + (static_cast<long long>(slot) * a.tr + first_row + q0) * kHeadDim + (lane & 3) * 4;
+      uint16_t* dst[4];
 #pragma unroll
+      for (int k = 0; k < 4; ++k)
+        dst[k] = direct ? out_row(a, x.b, x.h, x.rt * a.tr + first_row + q0 + k) + (lane & 3) * 8 : nullptr;
+      float f0 = 1.f, f1 = 0.f, inv = sum > 0.f ? 1.f / sum : 0.f;
+#pragma unroll 1
       for (int c0 = 0; c0 < 128; c0 += 32) {
         float y[32];
         __syncwarp();
@@ -505,17 +531,32 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           ++nx;
         }
-        if (live) {
+        if (!SPLIT || w == 0) {
+          uint4 v[4];
           if (direct) {
 #pragma unroll
-            for (int c = 0; c < 32; c += 8)
-              *reinterpret_cast<uint4*>(dst + c0 + c) =
-                  make_uint4(pack_bf16(y[c] * inv, y[c + 1] * inv), pack_bf16(y[c + 2] * inv, y[c + 3] * inv),
-                             pack_bf16(y[c + 4] * inv, y[c + 5] * inv), pack_bf16(y[c + 6] * inv, y[c + 7] * inv));
+            for (int c = 0; c < 4; ++c) {
+              const float* z = y + c * 8;
+              v[c] = make_uint4(pack_bf16(z[0] * inv, z[1] * inv), pack_bf16(z[2] * inv, z[3] * inv),
+                                pack_bf16(z[4] * inv, z[5] * inv), pack_bf16(z[6] * inv, z[7] * inv));
+            }
+            quad_transpose(v);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (q0 + k < rows) *reinterpret_cast<uint4*>(dst[k] + c0) = v[k];
           } else {
 #pragma unroll
-            for (int c = 0; c < 32; c += 4)
-              *reinterpret_cast<float4*>(po + c0 + c) = make_float4(y[c], y[c + 1], y[c + 2], y[c + 3]);
+            for (int hf = 0; hf < 2; ++hf) {
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                const float* z = y + hf * 16 + c * 4;
+                v[c] = make_uint4(__float_as_uint(z[0]), __float_as_uint(z[1]), __float_as_uint(z[2]), __float_as_uint(z[3]));
+              }
+              quad_transpose(v);
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                if (q0 + k < rows) *reinterpret_cast<uint4*>(po + k * kHeadDim + c0 + hf * 16) = v[k];
+            }
           }
         }
       }
