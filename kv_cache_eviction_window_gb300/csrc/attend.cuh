@@ -63,6 +63,7 @@ struct AttnArgs {
   // -1, CTAs that follow}
   int2* rec;                      // [grid]
   int by_item;
+  int start;                      // attend_tile_kernel: units for the start of an item
   int grid;                       // CTAs of the kernel that works on the items
   WaitCtl wc;
 };
@@ -160,33 +161,36 @@ __device__ __forceinline__ void tile_rows(const ItemRange& x, int ti, int& j0, i
   }
 }
 
-// The share of CTA `cta` of the grid in all tiles of all items, in item order: tiles
-// [total * cta / grid, total * (cta + 1) / grid).  Lengths live on the device, so every CTA
-// adds up the items itself (a thread takes consecutive items, then a block-wide scan).
+// The share of CTA `cta` of the grid in all tiles of all items, in item order: units
+// [total * cta / grid, total * (cta + 1) / grid).  An item has `start` units for what beginning it
+// costs, then one per tile; a CTA whose share ends within the former leaves it to the next.
+// Lengths live on the device, so every CTA adds up the items itself (a thread takes consecutive
+// items, then a block-wide scan).
 template <class Item>
 struct Share {
   long long total;
-  long long begin, end;           // this CTA's tiles
+  long long begin, end;           // this CTA's units
   int grid;                       // CTAs with work: min(gridDim.x, total)
-  int item;                       // item of tile `begin`
-  long long item_base;            // its first tile
+  int start;
+  int item;                       // item of unit `begin`
+  long long item_base;            // its first unit
   Item first;                     // and its range
 };
-// range(i): the range of item i, with its number of tiles
+// range(i): the range of item i, with its number of tiles.  The result stays in shared memory; kept in
+// registers through attend_tile_kernel it costs the softmax warps' inner loop 2% (spills).
 template <int THREADS, class Range>
-__device__ __forceinline__ auto share_of(int items, Range range, int cta) -> Share<decltype(range(0))> {
+__device__ __forceinline__ auto share_of(int items, Range range, int cta, int start = 0) -> const Share<decltype(range(0))>& {
   using Item = decltype(range(0));
+  const auto units = [&](const Item& x) { return x.tiles > 0 ? x.tiles + start : 0; };
   __shared__ long long s_warp[THREADS / 32];
-  __shared__ long long s_base;
-  __shared__ int s_item;
-  __shared__ Item s_first;
+  __shared__ Share<Item> s_sh;
   const int per = (items + THREADS - 1) / THREADS;
   const int i0 = min(items, static_cast<int>(threadIdx.x) * per), i1 = min(items, i0 + per);
   long long sum = 0;
   Item mine{};                                       // the last of this thread's items (the only one, as a rule)
   for (int i = i0; i < i1; ++i) {
     mine = range(i);
-    sum += mine.tiles;
+    sum += units(mine);
   }
   long long inc = sum;
 #pragma unroll
@@ -201,39 +205,43 @@ __device__ __forceinline__ auto share_of(int items, Range range, int cta) -> Sha
     if (w < static_cast<int>(threadIdx.x >> 5)) before += s_warp[w];
     total += s_warp[w];
   }
-  Share<Item> sh;
-  sh.total = total;
-  sh.grid = static_cast<int>(min(static_cast<long long>(gridDim.x), total));
-  sh.begin = sh.end = 0;
-  sh.item = 0;
-  sh.item_base = 0;
-  if (cta < sh.grid) {
-    sh.begin = total * cta / sh.grid;
-    sh.end = total * (cta + 1) / sh.grid;
-    if (sum > 0 && sh.begin >= before && sh.begin < before + sum) {
+  const int grid = static_cast<int>(min(static_cast<long long>(gridDim.x), total));
+  if (threadIdx.x == 0) s_sh.grid = grid;
+  if (cta < grid) {
+    const long long begin = total * cta / grid;
+    if (sum > 0 && begin >= before && begin < before + sum) {
       long long at = before;
       int i = i0;
       if (per > 1) {
         for (; i < i1; ++i) {
           mine = range(i);
-          if (sh.begin < at + mine.tiles) break;
-          at += mine.tiles;
+          if (begin < at + units(mine)) break;
+          at += units(mine);
         }
       }
-      s_item = i;
-      s_base = at;
-      s_first = mine;
+      s_sh.total = total;
+      s_sh.begin = begin;
+      s_sh.end = total * (cta + 1) / grid;
+      s_sh.start = start;
+      s_sh.item = i;
+      s_sh.item_base = at;
+      s_sh.first = mine;
     }
   }
   __syncthreads();
-  if (cta < sh.grid) {
-    sh.item = s_item;
-    sh.item_base = s_base;
-    sh.first = s_first;
-  }
-  return sh;
+  return s_sh;
 }
-// The last CTA with a tile of an item that ends before tile `e`.
+// The tiles [ta, tb) of an item that this CTA works on; `base`, the item's first unit, moves to the next
+// item's.  False: none.
+template <class Item>
+__device__ __forceinline__ bool next_piece(const Share<Item>& sh, int item, int tiles, long long& base, int& ta, int& tb) {
+  if (tiles == 0) return false;
+  ta = item == sh.item ? max(0, static_cast<int>(sh.begin - base) - sh.start) : 0;
+  tb = static_cast<int>(min(static_cast<long long>(tiles), sh.end - base - sh.start));
+  base += tiles + sh.start;
+  return ta < tb;
+}
+// The last CTA with a unit of an item that ends before unit `e`.
 template <class Item>
 __device__ __forceinline__ int last_cta(const Share<Item>& sh, long long e) {
   return static_cast<int>((e * sh.grid - 1) / sh.total);
@@ -251,6 +259,11 @@ __device__ __forceinline__ void rec_first(const AttnArgs& a, int item, int follo
   else if (follow > 0)
     a.rec[blockIdx.x] = make_int2(item, follow);
 }
+
+// What the start of an item costs in attend_tile_kernel, in key tiles, when there are more items than
+// CTAs: results written, Q loaded, an empty pipeline, some 6000 cycles.  (2048 tokens over an empty
+// cache, whose first items have one tile: 75 us without it, 62 at two tiles, 60 at three.)
+constexpr int kStartUnits = 3;
 
 // How far (log2 units) a row's running maximum may rise above the reference that its weights are
 // scaled by before sum and accumulator are rescaled.  Floating point loses nothing by the scale; 16

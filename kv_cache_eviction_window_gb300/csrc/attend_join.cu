@@ -5,7 +5,8 @@
 //
 // Bound: latency (the pieces are in L2).  Few items (by_item): a CTA per row, eight warps over its
 // pieces, of which there may be one per CTA of the grid.  Many items, of two or three pieces: a
-// warp per row, five CTAs for each CTA before; those whose number starts no shared item end at once.
+// warp per two rows (one row at a time took 2 to 3 us longer), five CTAs for each CTA before; those
+// whose number starts no shared item end at once.
 // (Joining in the CTA that finishes an item's last piece, without a second launch, took 38 us
 // longer for 73 pieces of 7 rows.)
 #include <algorithm>
@@ -113,21 +114,25 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_items_kernel(const AttnA
   finish(a, x, r, p);
 }
 
-// grid (CTA of the kernel before, share of its rows): all CTAs resident at once, a row per warp
+// grid (CTA of the kernel before, share of its rows): all CTAs resident at once, two rows per warp at a time
 constexpr int kShares = 5;
 __global__ void __launch_bounds__(kJoinWarps * 32, kShares) join_ctas_kernel(const AttnArgs a) {
   const int2 rec = a.rec[blockIdx.x];
   if (rec.x < 0) return;
   const JoinItem x = join_item(a, rec.x, blockIdx.x, rec.y);
-  for (int r = blockIdx.y * kJoinWarps + warp_id(); r < x.rows; r += kShares * kJoinWarps) {
-    Joined p = nothing();
-    for (int c = 0; c < x.pieces; c += 4) {
+  constexpr int kStep = kShares * kJoinWarps;
+  for (int r = blockIdx.y * kJoinWarps + warp_id(); r < x.rows; r += 2 * kStep) {
+    Joined p = nothing(), p2 = nothing();
+    for (int c = 0; c < x.pieces; c += 2) {
       float2 ml[4];
       float4 z[4];
-      fetch<4>(a, x, r, c, 1, ml, z);
-      add_pieces<4>(p, ml, z);
+      fetch<2>(a, x, r, c, 1, ml, z);
+      fetch<2>(a, x, r + kStep, c, 1, ml + 2, z + 2);
+      add_pieces<2>(p, ml, z);
+      add_pieces<2>(p2, ml + 2, z + 2);
     }
     finish(a, x, r, p);
+    if (r + kStep < x.rows) finish(a, x, r + kStep, p2);
   }
 }
 

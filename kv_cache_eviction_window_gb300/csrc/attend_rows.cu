@@ -75,12 +75,11 @@ __global__ void __launch_bounds__(kThreads, 2) attend_rows_kernel(const AttnArgs
   const uint32_t ring = smem_u32(smem) + warp * (kStages * kStageBytes);
   float* s_o = reinterpret_cast<float*>(smem);
 
-  long long base = sh.item_base, at = sh.begin;
-  for (int item = sh.item; at < sh.end; ++item) {
+  long long base = sh.item_base;
+  for (int item = sh.item; base < sh.end; ++item) {
     const ItemRange x = item == sh.item ? sh.first : item_range<kTK>(a, item);
-    if (x.tiles == 0) continue;
-    const int ta = static_cast<int>(at - base);
-    const int tb = static_cast<int>(min(static_cast<long long>(x.tiles), sh.end - base));
+    int ta, tb;
+    if (!next_piece(sh, item, x.tiles, base, ta, tb)) continue;
     const int cnt = tb - ta;
 
     // element offset of the cached row that this lane looks up for unit u (rows 0..15: lanes l
@@ -304,10 +303,8 @@ __global__ void __launch_bounds__(kThreads, 2) attend_rows_kernel(const AttnArgs
         if (lane == 0) a.part_ml[static_cast<long long>(slot) * kTR + r] = make_float2(M, L);
       }
     }
-    if (first) rec_first(a, item, last ? 0 : last_cta(sh, base + x.tiles) - static_cast<int>(blockIdx.x));
+    if (first) rec_first(a, item, last ? 0 : last_cta(sh, base) - static_cast<int>(blockIdx.x));
     __syncthreads();   // s_m, s_l and the accumulators are read before the next item
-    base += x.tiles;
-    at = base;
   }
 }
 

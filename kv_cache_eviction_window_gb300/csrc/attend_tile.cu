@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&tk);
     tma_prefetch_desc(&tv);
   }
-  const auto sh = share_of<kThreads>(a.B * a.H * a.rt, [&](int i) { return item_range<kTK>(a, i); }, blockIdx.x);
+  const auto& sh = share_of<kThreads>(a.B * a.H * a.rt, [&](int i) { return item_range<kTK>(a, i); }, blockIdx.x, a.start);
   if (static_cast<int>(blockIdx.x) >= sh.grid) return;   // the whole CTA
   if (warp == kQkWarp) {
     tmem_alloc(&s_tmem, 512);
@@ -173,12 +173,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kLoadWarp) {
     int use[2] = {0, 0}, piece = 0;                  // ring uses issued, pieces begun
     bool ok = true;                                  // the same in every lane
-    long long base = sh.item_base, at = sh.begin;
-    for (int item = sh.item; ok && at < sh.end; ++item) {
+    long long base = sh.item_base;
+    for (int item = sh.item; ok && base < sh.end; ++item) {
       const ItemRange x = item == sh.item ? sh.first : item_range<kTK>(a, item);
-      if (x.tiles == 0) continue;
-      const int ta = static_cast<int>(at - base);
-      const int cnt = static_cast<int>(min(static_cast<long long>(x.tiles), sh.end - base)) - ta;
+      int ta, tb;
+      if (!next_piece(sh, item, x.tiles, base, ta, tb)) continue;
+      const int cnt = tb - ta;
       ok = __all_sync(0xffffffffu, mbar_wait(&qempty, (piece & 1) ^ 1, &s_abort, a.wc));
       if (!ok) break;
       if (lane == 0) {
@@ -218,8 +218,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (ok) load(0, i, 0, true);
         }
       }
-      base += x.tiles;
-      at = base;
     }
     // copies in flight land, and the last releases arrive, before the CTA ends
     if (lane == 0) {
@@ -257,11 +255,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t kd0 = sdesc_stage_k(base0, lay), vd0 = sdesc_stage_v(base0, lay);
     const uint32_t sub_step = (8 * lay.group) >> 4, k_step = (2 * lay.group) >> 4, khalf = lay.half >> 4;   // 64 rows, 16 rows
     const uint32_t tS = tbase + w * 128, tO = tbase + 256 + w * 128;
-    long long base = sh.item_base, at = sh.begin;
-    for (int item = sh.item; ok && at < sh.end; ++item) {
+    long long base = sh.item_base;
+    for (int item = sh.item; ok && base < sh.end; ++item) {
       const ItemRange x = item == sh.item ? sh.first : item_range<kTK>(a, item);
-      if (x.tiles == 0) continue;
-      const int cnt = static_cast<int>(min(static_cast<long long>(x.tiles), sh.end - base) - (at - base));
+      int ta, tb;
+      if (!next_piece(sh, item, x.tiles, base, ta, tb)) continue;
+      const int cnt = tb - ta;
       const int steps = 2 * (SPLIT ? (cnt + 1 - w) / 2 : cnt);   // of this stream: key tile n / 2, buffer n & 1
       if (is_qk) {
         wait(&qfull, piece);
@@ -305,8 +304,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       ++piece;
       use += SPLIT ? 2 * steps : 2 * cnt;
-      base += x.tiles;
-      at = base;
     }
     // every product issued has been done before TMEM is freed
     commit(&done);
@@ -324,12 +321,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (__all_sync(0xffffffffu, ok && mbar_test(bar, static_cast<uint32_t>(phase & 1)))) return;
       ok = __all_sync(0xffffffffu, ok && mbar_wait(bar, static_cast<uint32_t>(phase & 1), &s_abort, a.wc));
     };
-    long long base = sh.item_base, at = sh.begin;
-    for (int item = sh.item; ok && at < sh.end; ++item) {
+    long long base = sh.item_base;
+    for (int item = sh.item; ok && base < sh.end; ++item) {
       const ItemRange x = item == sh.item ? sh.first : item_range<kTK>(a, item);
-      if (x.tiles == 0) continue;
-      const int ta = static_cast<int>(at - base);
-      const int tb = static_cast<int>(min(static_cast<long long>(x.tiles), sh.end - base));
+      int ta, tb;
+      if (!next_piece(sh, item, x.tiles, base, ta, tb)) continue;
       const int cnt = tb - ta;
       const int first_row = SPLIT ? 0 : w * block;   // of the item
       const int rows = min(block, x.rows - first_row);
@@ -567,10 +563,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         else
           a.part_ml[static_cast<long long>(slot) * a.tr + first_row + row] = make_float2(ref, sum);
       }
-      if (first) rec_first(a, item, last ? 0 : last_cta(sh, base + x.tiles) - static_cast<int>(blockIdx.x));
+      if (first) rec_first(a, item, last ? 0 : last_cta(sh, base) - static_cast<int>(blockIdx.x));
       tc_fence_before();                             // O is read before the next piece's products
-      base += x.tiles;
-      at = base;
     }
   }
   __syncwarp();

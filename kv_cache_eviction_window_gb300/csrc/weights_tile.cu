@@ -107,12 +107,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     int use = 0, piece = 0;
     bool ok = true;
-    long long base = sh.item_base, at = sh.begin;
-    for (int item = sh.item; ok && at < sh.end; ++item) {
+    long long base = sh.item_base;
+    for (int item = sh.item; ok && base < sh.end; ++item) {
       const KeyItem x = item == sh.item ? sh.first : key_item(a, item, per_seg, tok);
-      if (x.tiles == 0) continue;
-      const int ta = static_cast<int>(at - base);
-      const int tb = static_cast<int>(min(static_cast<long long>(x.tiles), sh.end - base));
+      int ta, tb;
+      if (!next_piece(sh, item, x.tiles, base, ta, tb)) continue;
       ok = __all_sync(0xffffffffu, mbar_wait(&kempty, (piece & 1) ^ 1, &s_abort, a.wc));
       if (!ok) break;
       for (int w = 0; w < 2; ++w)
@@ -144,8 +143,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(&qfull[s]);
         ++use;
       }
-      base += x.tiles;
-      at = base;
     }
     if (lane == 0) {
       for (int u = max(0, use - kStages); u < use; ++u) mbar_drain(&qfull[u % kStages], (u / kStages) & 1, a.wc.status);
@@ -165,11 +162,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto wait = [&](uint64_t* bar, int phase) {
       ok = __all_sync(0xffffffffu, ok && mbar_wait(bar, static_cast<uint32_t>(phase & 1), &s_abort, a.wc));
     };
-    long long base = sh.item_base, at = sh.begin;
-    for (int item = sh.item; ok && at < sh.end; ++item) {
+    long long base = sh.item_base;
+    for (int item = sh.item; ok && base < sh.end; ++item) {
       const KeyItem x = item == sh.item ? sh.first : key_item(a, item, per_seg, tok);
-      if (x.tiles == 0) continue;
-      const int cnt = static_cast<int>(min(static_cast<long long>(x.tiles), sh.end - base) - (at - base));
+      int ta, tb;
+      if (!next_piece(sh, item, x.tiles, base, ta, tb)) continue;
+      const int cnt = tb - ta;
       wait(&kfull, piece++);
       for (int i = 0; i < cnt && ok; ++i, ++use) {
         const int s = use % kStages, u = use & 1;
@@ -195,8 +193,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       if (elect_one()) umma_commit(&kempty);
       __syncwarp();
-      base += x.tiles;
-      at = base;
     }
     if (elect_one()) umma_commit(&done);
     __syncwarp();
@@ -210,12 +206,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto wait = [&](uint64_t* bar, int phase) {
       ok = __all_sync(0xffffffffu, ok && mbar_wait(bar, static_cast<uint32_t>(phase & 1), &s_abort, a.wc));
     };
-    long long base = sh.item_base, at = sh.begin;
-    for (int item = sh.item; ok && at < sh.end; ++item) {
+    long long base = sh.item_base;
+    for (int item = sh.item; ok && base < sh.end; ++item) {
       const KeyItem x = item == sh.item ? sh.first : key_item(a, item, per_seg, tok);
-      if (x.tiles == 0) continue;
-      const int ta = static_cast<int>(at - base);
-      const int tb = static_cast<int>(min(static_cast<long long>(x.tiles), sh.end - base));
+      int ta, tb;
+      if (!next_piece(sh, item, x.tiles, base, ta, tb)) continue;
       const int j = x.jb + key;
       // query rows [r0, r1) of the segment see the cached row
       long long r0 = 0, r1 = j < x.n ? static_cast<long long>(x.m) * a.G : 0;
@@ -280,10 +275,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else {
         part[(2ll * blockIdx.x + (first ? 1 : 0)) * kKeys + key] = sum;
         if (first && threadIdx.x == 0)
-          a.rec[blockIdx.x] = make_int2(item, last_cta(sh, base + x.tiles) - static_cast<int>(blockIdx.x));
+          a.rec[blockIdx.x] = make_int2(item, last_cta(sh, base) - static_cast<int>(blockIdx.x));
       }
-      base += x.tiles;
-      at = base;
     }
   }
   __syncwarp();
