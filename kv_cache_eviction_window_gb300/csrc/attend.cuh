@@ -63,7 +63,6 @@ struct AttnArgs {
   // -1, CTAs that follow}
   int2* rec;                      // [grid]
   int by_item;
-  int start;                      // attend_tile_kernel: units for the start of an item
   int grid;                       // CTAs of the kernel that works on the items
   WaitCtl wc;
 };
@@ -259,11 +258,6 @@ __device__ __forceinline__ void rec_first(const AttnArgs& a, int item, int follo
   else if (follow > 0)
     a.rec[blockIdx.x] = make_int2(item, follow);
 }
-
-// What the start of an item costs in attend_tile_kernel, in key tiles, when there are more items than
-// CTAs: results written, Q loaded, an empty pipeline, some 6000 cycles.  (2048 tokens over an empty
-// cache, whose first items have one tile: 75 us without it, 62 at two tiles, 60 at three.)
-constexpr int kStartUnits = 3;
 
 // How far (log2 units) a row's running maximum may rise above the reference that its weights are
 // scaled by before sum and accumulator are rescaled.  Floating point loses nothing by the scale; 16

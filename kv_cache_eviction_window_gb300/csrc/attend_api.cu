@@ -285,7 +285,6 @@ int kvsel_attend(const kvsel_attn_params* p, const void* q, const kvsel_kv* kv, 
   // few rows in all: the join starts a CTA for each (128 items of 256 rows: 119 us, by CTAs 27 us)
   const long long items = static_cast<long long>(p->batch) * p->h_kv * pl.rt;
   a.by_item = items <= pl.grid && items * std::min(pl.tr, p->n_new * p->group) <= 4096;
-  a.start = a.by_item ? 0 : kStartUnits;
   a.wc = WaitCtl{p->wait_cycles ? p->wait_cycles : kDefaultWaitCycles, static_cast<int*>(ws)};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (!pl.tiled) {

@@ -28,6 +28,9 @@ constexpr int kTR = 16;                              // query rows per item
 constexpr int kUnit = 16;                            // cached rows per warp and step
 constexpr int kTK = kUnit * kWarps;                  // cached rows per tile
 constexpr int kStages = 3;
+// what the start of an item costs, in tiles (eight requests, window of 4096: 32.1 us without it, 31.2 at
+// one, 30.6 at two and four; a compacted cache of 4 heads 13.1, 12.3, 12.2)
+constexpr int kStart = 2;
 constexpr int kUnitBytes = kUnit * 256;              // one side (K or V) of a unit
 constexpr int kStageBytes = 2 * kUnitBytes;
 constexpr int kOPad = 132;                           // floats per accumulator row when merging
@@ -70,7 +73,8 @@ __global__ void __launch_bounds__(kThreads, 2) attend_rows_kernel(const AttnArgs
   const int warp = warp_id(), lane = lane_id();
   const int quad = lane >> 2, ql = lane & 3;
   rec_clear(a);
-  const auto sh = share_of<kThreads>(a.B * a.H * a.rt, [&](int i) { return item_range<kTK>(a, i); }, blockIdx.x);
+  const auto sh = share_of<kThreads>(a.B * a.H * a.rt, [&](int i) { return item_range<kTK>(a, i); }, blockIdx.x,
+                                     kStart);
   if (static_cast<int>(blockIdx.x) >= sh.grid) return;
   const uint32_t ring = smem_u32(smem) + warp * (kStages * kStageBytes);
   float* s_o = reinterpret_cast<float*>(smem);

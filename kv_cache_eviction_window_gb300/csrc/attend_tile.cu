@@ -42,6 +42,11 @@ constexpr int kThreads = 512;                        // four warpgroups; warps 1
 constexpr int kSoftRegs = 184, kOtherRegs = 72;
 constexpr int kTile = kTileBytes, kHalf = kHalfBytes;
 constexpr int kStages = 5;                           // of 128 rows; SPLIT: per stream, of 64 rows
+// What the start of an item costs, in tiles: results written, Q loaded, an empty pipeline, some 6000
+// cycles.  (2048 tokens over an empty cache, whose first items have one tile: 75 us without it, 62
+// at two tiles, 60 at three; six tokens of four requests over 4096 rows 25.8 and 22.3 us.  It loses
+// where there is one tile for each CTA: six tokens over 4864 rows 14.1 and 15.7.)
+constexpr int kStart = 3;
 constexpr size_t kSmem = 1024 + 2 * kTile + kStages * kTile;
 
 // A operand in TMEM
@@ -153,7 +158,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&tk);
     tma_prefetch_desc(&tv);
   }
-  const auto& sh = share_of<kThreads>(a.B * a.H * a.rt, [&](int i) { return item_range<kTK>(a, i); }, blockIdx.x, a.start);
+  const auto& sh = share_of<kThreads>(a.B * a.H * a.rt, [&](int i) { return item_range<kTK>(a, i); }, blockIdx.x,
+                                          kStart);
   if (static_cast<int>(blockIdx.x) >= sh.grid) return;   // the whole CTA
   if (warp == kQkWarp) {
     tmem_alloc(&s_tmem, 512);

@@ -16,6 +16,9 @@ namespace kvsel {
 namespace {
 
 constexpr int kKeys = 256;                           // cached rows per item
+// what the start of an item costs, in blocks of query rows (512 tokens over 4096 rows: 80.6 us without it,
+// 79.0 at three to six; 1024 over 8192: 194.6, 189.5; 64 over 1000 rows loses, 32.5 and 33.6)
+constexpr int kStart = 6;
 constexpr int kMmaWarp = 8, kLoadWarp = 9;
 constexpr int kThreads = 320;
 constexpr int kStages = 4;                           // query blocks on their way
@@ -89,7 +92,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (threadIdx.x == 0) a.rec[blockIdx.x] = make_int2(-1, 0);
   const auto sh =
-      share_of<kThreads>(a.B * a.H * per_seg, [&](int i) { return key_item(a, i, per_seg, tok); }, blockIdx.x);
+      share_of<kThreads>(a.B * a.H * per_seg, [&](int i) { return key_item(a, i, per_seg, tok); }, blockIdx.x,
+                         kStart);
   if (static_cast<int>(blockIdx.x) >= sh.grid) return;   // the whole CTA
   if (warp == kMmaWarp) {
     tmem_alloc(&s_tmem, 512);
