@@ -21,8 +21,9 @@ constexpr int kKeys = 256;                           // cached rows per item
 constexpr int kStart = 6;
 constexpr int kMmaWarp = 8, kLoadWarp = 9;
 constexpr int kThreads = 320;
-constexpr int kStages = 4;                           // query blocks on their way
-constexpr size_t kSmem = 1024 + 2 * kTileBytes + kStages * kTileBytes;
+constexpr int kStages = 3;                           // query blocks on their way
+constexpr int kItems = 2;                            // items whose K tiles are there or on their way
+constexpr size_t kSmem = 1024 + (2 * kItems + kStages) * kTileBytes;
 
 struct KeyItem {
   int seg, b, h, jb;              // first cached row
@@ -62,8 +63,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_align1024(smem_raw);
   uint8_t* sK = smem;
-  uint8_t* sQ = smem + 2 * kTileBytes;
-  __shared__ __align__(8) uint64_t kfull, kempty, qfull[kStages], qempty[kStages], lfull[2][2], lempty[2][2], done;
+  uint8_t* sQ = smem + 2 * kItems * kTileBytes;
+  __shared__ __align__(8) uint64_t kfull[kItems], kempty[kItems], qfull[kStages], qempty[kStages], lfull[2][2], lempty[2][2], done;
   __shared__ __align__(16) float s_e[kStages][128];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
@@ -75,8 +76,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     reinterpret_cast<uint4*>(sQ)[i] = make_uint4(0u, 0u, 0u, 0u);
   fence_proxy_async_smem();
   if (threadIdx.x == 0) {
-    mbar_init(&kfull, 2);
-    mbar_init(&kempty, 1);
+    for (int u = 0; u < kItems; ++u) {
+      mbar_init(&kfull[u], 2);
+      mbar_init(&kempty[u], 1);
+    }
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&qfull[s], 2);
       mbar_init(&qempty[s], 9);                      // its products are done, its sums are read
@@ -116,10 +119,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const KeyItem x = item == sh.item ? sh.first : key_item(a, item, per_seg, tok);
       int ta, tb;
       if (!next_piece(sh, item, x.tiles, base, ta, tb)) continue;
-      ok = __all_sync(0xffffffffu, mbar_wait(&kempty, (piece & 1) ^ 1, &s_abort, a.wc));
+      const int kb = piece % kItems;
+      ok = __all_sync(0xffffffffu, mbar_wait(&kempty[kb], ((piece / kItems) & 1) ^ 1, &s_abort, a.wc));
       if (!ok) break;
       for (int w = 0; w < 2; ++w)
-        load_rows<128>(a, x.b, x.h, x.row0, &tk, x.jb + w * 128, x.n, sK + w * kTileBytes, &kfull, [&](int from, int to) {
+        load_rows<128>(a, x.b, x.h, x.row0, &tk, x.jb + w * 128, x.n, sK + (2 * kb + w) * kTileBytes, &kfull[kb],
+                       [&](int from, int to) {
           return a.window <= 0 || !a.causal || from < a.n_sink || to > x.first - a.window;
         });
       ++piece;
@@ -150,10 +155,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (lane == 0) {
       for (int u = max(0, use - kStages); u < use; ++u) mbar_drain(&qfull[u % kStages], (u / kStages) & 1, a.wc.status);
-      if (piece) mbar_drain(&kfull, (piece - 1) & 1, a.wc.status);
+      for (int u = max(0, piece - kItems); u < piece; ++u)
+        mbar_drain(&kfull[u % kItems], (u / kItems) & 1, a.wc.status);
       if (ok) {
         ring_tail(qempty, kStages, use, &s_abort, a.wc);
-        ring_tail(&kempty, 1, piece, &s_abort, a.wc);
+        ring_tail(kempty, kItems, piece, &s_abort, a.wc);
       }
     }
   } else if (warp == kMmaWarp) {
@@ -172,7 +178,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       int ta, tb;
       if (!next_piece(sh, item, x.tiles, base, ta, tb)) continue;
       const int cnt = tb - ta;
-      wait(&kfull, piece++);
+      const int kb = piece % kItems;
+      wait(&kfull[kb], piece / kItems);
+      ++piece;
       for (int i = 0; i < cnt && ok; ++i, ++use) {
         const int s = use % kStages, u = use & 1;
         wait(&qfull[s], use / kStages);
@@ -180,7 +188,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (use >= 2) wait(&lempty[w][u], (use >> 1) - 1);
           if (!ok) break;
           tc_fence_after();
-          const uint64_t qd = qd0 + s * (kTileBytes >> 4), kd = kd0 + w * (kTileBytes >> 4);
+          const uint64_t qd = qd0 + s * (kTileBytes >> 4), kd = kd0 + (2 * kb + w) * (kTileBytes >> 4);
           if (elect_one()) {
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
@@ -195,7 +203,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (!ok) break;
-      if (elect_one()) umma_commit(&kempty);
+      if (elect_one()) umma_commit(&kempty[kb]);
       __syncwarp();
     }
     if (elect_one()) umma_commit(&done);
@@ -216,8 +224,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       int ta, tb;
       if (!next_piece(sh, item, x.tiles, base, ta, tb)) continue;
       const int j = x.jb + key;
-      // query rows [r0, r1) of the segment see the cached row
-      long long r0 = 0, r1 = j < x.n ? static_cast<long long>(x.m) * a.G : 0;
+      // query rows [r0, r1) of the segment see the cached row (the rows behind the last token's are zeros
+      // where no request has more tokens, and their log-sums infinity: they need no mask)
+      const long long all = static_cast<long long>(x.m) * a.G;
+      long long r0 = 0, r1 = j >= x.n ? 0 : x.m == a.m ? all + 128 : all;
       if (a.causal && j < x.n) {
         r0 = static_cast<long long>(max(0, j - x.first)) * a.G;
         if (a.window > 0 && j >= a.n_sink) r1 = min(r1, max(0ll, static_cast<long long>(j) + a.window - x.first) * a.G);
@@ -238,6 +248,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
 #pragma unroll
         for (int c0 = 0; c0 < 128; c0 += 64) {
+          // (a warp skips the query rows that none of its cached rows is seen by)
+          if (rb + c0 >= all || !__any_sync(0xffffffffu, lo < c0 + 64 && hi > c0)) continue;
           float y[64];
           tmem_ld32(tS + u * 128 + c0, y);
           tmem_ld32(tS + u * 128 + c0 + 32, y + 32);
