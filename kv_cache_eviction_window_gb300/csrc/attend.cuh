@@ -30,6 +30,10 @@ struct Div {
 struct AttnArgs {
   int B, H, G, m;                 // requests, KV heads, group, new tokens of a request at most
   Div by_rt, by_H, by_G;          // items per segment, heads, group
+  // weights_tile_kernel: blocks of 256 cached rows of a segment that some query row may see; with a window
+  // that is shorter than a segment, first those of the first rows that stay visible (-1: all blocks)
+  int kb, kb_sink;
+  Div by_kb;
   int page_shift;                 // paged: log2 of the rows of a page
   int max_len;                    // rows of a segment at most
   int causal, window, n_sink;

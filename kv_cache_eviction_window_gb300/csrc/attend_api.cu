@@ -31,6 +31,7 @@ struct AttnPlan {
   int grid = 0, tr = 0, rt = 1;
   bool tiled = false, split = false;
   int block = 0;                 // tiled: query rows per block, whole tokens of the group
+  int kb = 1, kb_sink = -1;      // tiled, with weights: blocks of 256 cached rows (attend.cuh)
   size_t rec = 0, ml = 0, o = 0, lse2 = 0, wpart = 0, logits = 0, total = 0;
   long long logit_stride = 0;
 };
@@ -92,6 +93,13 @@ int plan_attn(const kvsel_attn_params* p, bool with_acc, AttnPlan& pl) {
     const size_t rows = static_cast<size_t>(p->batch) * p->h_kv * R;
     off = align256(off + sizeof(float) * rows);
     if (pl.tiled) {
+      const long long full = (static_cast<long long>(p->max_len) + 255) / 256, sinks = (p->n_sink + 255ll) / 256;
+      const long long part = sinks + (static_cast<long long>(p->window) + p->n_new + 254) / 256 + 1;
+      const bool few = p->causal && p->window > 0 && part < full;
+      const long long kb = few ? part : full;
+      if (kb * p->batch * p->h_kv > (1ll << 31) - 1) return KVSEL_EUNSUPPORTED;
+      pl.kb = static_cast<int>(kb);
+      pl.kb_sink = few ? static_cast<int>(sinks) : -1;
       pl.wpart = off;
       off = align256(off + sizeof(float) * 2 * pl.grid * 256);
     } else {
@@ -275,6 +283,9 @@ int kvsel_attend(const kvsel_attn_params* p, const void* q, const kvsel_kv* kv, 
   a.by_rt = Div::by(pl.rt);
   a.by_H = Div::by(p->h_kv);
   a.by_G = Div::by(p->group);
+  a.kb = pl.kb;
+  a.kb_sink = pl.kb_sink;
+  a.by_kb = Div::by(pl.kb);
   while (a.src.paged && (1 << a.page_shift) < a.src.block_size) ++a.page_shift;
   a.tr = pl.tr;
   a.rt = pl.rt;

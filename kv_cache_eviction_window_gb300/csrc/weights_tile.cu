@@ -31,10 +31,14 @@ struct KeyItem {
   int q0, tiles;                  // first query block, query blocks that see a row of the item
   long long row0;
 };
-__device__ __forceinline__ KeyItem key_item(const AttnArgs& a, int item, int per_seg, int tok) {
+// First row of block i of a segment whose first new token is row `first`.
+__device__ __forceinline__ int key_block(const AttnArgs& a, int i, int first) {
+  if (a.kb_sink < 0 || i < a.kb_sink) return i * kKeys;
+  return max(a.kb_sink * kKeys, max(0, first - a.window + 1) & -kKeys) + (i - a.kb_sink) * kKeys;
+}
+__device__ __forceinline__ KeyItem key_item(const AttnArgs& a, int item, int tok) {
   KeyItem x;
-  x.seg = item / per_seg;
-  x.jb = (item - x.seg * per_seg) * kKeys;
+  x.seg = a.by_kb(item);
   x.b = a.by_H(x.seg);
   x.h = x.seg - x.b * a.H;
   const SegLen s = seg_len(a, x.b, x.h);
@@ -42,6 +46,7 @@ __device__ __forceinline__ KeyItem key_item(const AttnArgs& a, int item, int per
   x.m = s.m;
   x.row0 = s.row0;
   x.first = s.n - s.m;
+  x.jb = key_block(a, item - x.seg * a.kb, x.first);
   x.q0 = x.tiles = 0;
   if (x.jb >= s.n || s.m == 0) return x;
   int t0 = 0, t1 = s.m;           // tokens that see a row of the item
@@ -70,7 +75,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ int s_abort;
 
   const int warp = warp_id(), lane = lane_id();
-  const int tok = block / a.G, per_seg = (a.max_len + kKeys - 1) / kKeys;
+  const int tok = block / a.G;
   // rows of a query stage behind the block's (the group does not divide 128) stay zero
   for (int i = threadIdx.x; i < kStages * kTileBytes / 16; i += kThreads)
     reinterpret_cast<uint4*>(sQ)[i] = make_uint4(0u, 0u, 0u, 0u);
@@ -95,7 +100,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (threadIdx.x == 0) a.rec[blockIdx.x] = make_int2(-1, 0);
   const auto sh =
-      share_of<kThreads>(a.B * a.H * per_seg, [&](int i) { return key_item(a, i, per_seg, tok); }, blockIdx.x,
+      share_of<kThreads>(a.B * a.H * a.kb, [&](int i) { return key_item(a, i, tok); }, blockIdx.x,
                          kStart);
   if (static_cast<int>(blockIdx.x) >= sh.grid) return;   // the whole CTA
   if (warp == kMmaWarp) {
@@ -116,7 +121,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     long long base = sh.item_base;
     for (int item = sh.item; ok && base < sh.end; ++item) {
-      const KeyItem x = item == sh.item ? sh.first : key_item(a, item, per_seg, tok);
+      const KeyItem x = item == sh.item ? sh.first : key_item(a, item, tok);
       int ta, tb;
       if (!next_piece(sh, item, x.tiles, base, ta, tb)) continue;
       const int kb = piece % kItems;
@@ -174,7 +179,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     long long base = sh.item_base;
     for (int item = sh.item; ok && base < sh.end; ++item) {
-      const KeyItem x = item == sh.item ? sh.first : key_item(a, item, per_seg, tok);
+      const KeyItem x = item == sh.item ? sh.first : key_item(a, item, tok);
       int ta, tb;
       if (!next_piece(sh, item, x.tiles, base, ta, tb)) continue;
       const int cnt = tb - ta;
@@ -220,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     long long base = sh.item_base;
     for (int item = sh.item; ok && base < sh.end; ++item) {
-      const KeyItem x = item == sh.item ? sh.first : key_item(a, item, per_seg, tok);
+      const KeyItem x = item == sh.item ? sh.first : key_item(a, item, tok);
       int ta, tb;
       if (!next_piece(sh, item, x.tiles, base, ta, tb)) continue;
       const int j = x.jb + key;
@@ -308,10 +313,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 __global__ void __launch_bounds__(kKeys) weights_join_kernel(const AttnArgs a, const float* part) {
   const int2 rec = a.rec[blockIdx.x];
   if (rec.x < 0) return;
-  const int per_seg = (a.max_len + kKeys - 1) / kKeys;
-  const int seg = rec.x / per_seg, j = (rec.x - seg * per_seg) * kKeys + threadIdx.x;
-  const int b = seg / a.H;
-  if (j >= seg_len(a, b, seg - b * a.H).n) return;
+  const int seg = a.by_kb(rec.x), b = a.by_H(seg);
+  const SegLen s = seg_len(a, b, seg - b * a.H);
+  const int j = key_block(a, rec.x - seg * a.kb, s.n - s.m) + threadIdx.x;
+  if (j >= s.n) return;
   float sum = part[(2ll * blockIdx.x + 1) * kKeys + threadIdx.x];
   for (int c = 1; c <= rec.y; ++c) sum += part[2ll * (blockIdx.x + c) * kKeys + threadIdx.x];
   a.acc[seg * a.acc_stride + j] += sum;

@@ -75,6 +75,14 @@ def test_windows(window, n_sink, m, G, layout, block):
     run(B=2, H=2, G=G, m=m, lens=[1201, m + 7], window=window, n_sink=n_sink, layout=layout, block=block, seed=window)
 
 
+@pytest.mark.parametrize("window,n_sink", [(3, 0), (57, 4), (256, 256), (700, 300)])
+@pytest.mark.parametrize("m,G,layout,block", [(40, 1, "paged", 8), (70, 4, "contiguous", 0), (300, 2, "paged", 64)])
+def test_windows_in_long_caches(window, n_sink, m, G, layout, block):
+    # blocks of cached rows that no token sees lie between the first rows and the window, and before it
+    run(B=3, H=2, G=G, m=m, new=[m, 1, m // 2], lens=[9001, 5 * 1024, 300], window=window, n_sink=n_sink, layout=layout,
+        block=block, seed=window)
+
+
 @pytest.mark.parametrize("m,G", [(1, 4), (5, 3), (90, 4)])
 def test_every_row_visible(m, G):
     # the new tokens are not in the cache: every token sees all rows, an empty cache none
@@ -107,6 +115,9 @@ def test_work_cut_over_many_blocks():
     run(B=64, H=8, G=4, lens=np.arange(64) * 5 + 1, layout="paged", seed=2, acc=False)
     run(B=300, H=2, G=2, lens=np.arange(300) % 7, seed=3)
     run(B=2, H=2, G=4, m=100, lens=[5000, 130], layout="paged", seed=4)
+    # a few tiles each, of more segments than there are blocks: most blocks begin and end within one
+    run(B=40, H=8, G=4, m=70, lens=70 + np.arange(40) * 9, layout="paged", seed=5)
+    run(B=6, H=3, G=8, m=9, lens=[9, 40, 700, 1, 5000, 128], seed=6)
 
 
 def test_weights_add_up_over_calls_and_results_repeat():
