@@ -312,6 +312,18 @@ def test_a_wait_that_runs_out_is_reported(m, G, acc):
     torch.cuda.synchronize()
 
 
+def test_more_blocks_than_can_be_planned_are_refused():
+    from kv_cache_eviction_window_gb300 import binding as L
+
+    p = dict(h_kv=64, group=4, batch=512, n_new=40, acc_stride=1 << 30)
+    with pytest.raises(L.KvselError) as e:
+        L.kvsel_attend_workspace_size(L.make_attn_params(max_len=1 << 30, **p), True)
+    assert e.value.code == L.KVSEL_EUNSUPPORTED
+    # without weights, or with a window, there are few
+    assert L.kvsel_attend_workspace_size(L.make_attn_params(max_len=1 << 30, **p), False) > 0
+    assert L.kvsel_attend_workspace_size(L.make_attn_params(max_len=1 << 30, window=4096, **p), True) > 0
+
+
 @pytest.mark.parametrize("m", [1, 40])
 def test_caches_beyond_2_to_the_32_elements(m):
     """Blocks and rows whose element offset passes 32 bits, in a paged and in a packed cache, and a
