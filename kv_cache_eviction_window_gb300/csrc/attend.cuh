@@ -329,6 +329,14 @@ __device__ __forceinline__ uint64_t sdesc_stage_k(uint32_t saddr, const StageLay
   d |= static_cast<uint64_t>(2u) << 61;
   return d;
 }
+__device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1,
+                                            int c2, int c3, int c4) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6, %7}], "
+      "[%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4)
+      : "memory");
+}
 // ROWS (64 or 128) rows of a segment from row j0 (those below j1) into such a stage, by the lanes of
 // a warp.  seen(first, last): whether any row of a page is seen; other pages are not looked up.
 template <int ROWS, class Seen>

@@ -8,6 +8,7 @@
     python profile_case.py --workload 2 --plain --partition   # + kept/evicted partition
     python profile_case.py --workload 2 --plain --concurrent --sm-budget 76   # two-launch scoring
     python profile_case.py --workload 2 --plain --layers 8 --graph-streams 8 --concurrent --sm-budget 76
+    python profile_case.py --operator chunk-window   # a listed case of perf/operators.py
 
 With --graph-streams S the layers are issued round-robin over S streams (one workspace
 each) and captured as one CUDA graph; after --steps warm-up replays, one more replay runs
@@ -44,7 +45,10 @@ def main():
     ap.add_argument("--sm-budget", type=int, default=0, help="kvsel_params.sm_budget")
     ap.add_argument("--graph-streams", type=int, default=0,
                     help="issue the layers over this many streams as one CUDA graph (see above)")
+    ap.add_argument("--operator", default=None, help="kvsel_attend or kvsel_evict_append on this case of perf/operators.py")
     args = ap.parse_args()
+    if args.operator:
+        return run_operator(args)
     import numpy as np
     import torch
 
@@ -141,6 +145,25 @@ def main():
     for i, name in enumerate(B.STAGES):
         print(f"  {name:9s} {tot[i] / cnt * 1e3:9.2f} us/layer (event-timed, includes launch gaps)")
     return 0 if st == 0 else 1
+
+
+def run_operator(args):
+    """--steps calls on one case, each on inputs of its own."""
+    import torch
+
+    import __graft_entry__
+
+    __graft_entry__.build()
+    from perf import operators
+
+    operators.own = True
+    case = next(c for c in operators.listed() if c["name"] == args.operator)
+    states = [operators.prepare(case, seed) for seed in range(args.steps)]
+    for st in states:
+        operators.run(st)
+    torch.cuda.synchronize()
+    print(f"{args.operator}: {args.steps} calls")
+    return 0
 
 
 def run_graph(args, B, layers, dev):
