@@ -12,8 +12,10 @@
 // shared memory (up to 49,152 slots); a thread owns an odd number of consecutive slots, so that
 // its walk through them meets no bank twice and equal neighbours cost one count.
 // evict_move_kernel: slot keep + i of a segment is handled by one half warp per side: its old
-// row goes to its hole, then new row i takes the slot.  Bound: HBM, 512 B per moved or new row
-// read and written (and 8 B per slot before).
+// row goes to its hole, then new row i takes the slot.  A warp takes two slots at a time (one: 37.2
+// us for the call with 2048 rows of 32 segments of 16384, two 35.7, four 38.3).  Bound: the latency
+// of a slot's chain of loads (its rank, its hole, their pages, its row), then HBM, 512 B per moved
+// or new row read and written (and 8 B per slot before).
 #include <algorithm>
 
 #include "evict.cuh"
@@ -23,7 +25,7 @@ namespace {
 
 constexpr int kSelThreads = 1024;
 constexpr int kMoveThreads = 256;
-constexpr int kMoveSlots = kMoveThreads / 32;        // slots per CTA of the second launch
+constexpr int kMoveWarps = kMoveThreads / 32, kEach = 2;   // of the second launch; slots per warp at a time
 
 // Rank of a weight as an unsigned number: larger weight, larger number; NaN below all.
 __device__ __forceinline__ uint32_t weight_key(float w) {
@@ -184,33 +186,54 @@ __device__ __forceinline__ long long slot_elem(const EvictArgs& a, int b, int h,
   return ((static_cast<long long>(pb) * bs + (i % bs)) * a.H + h) * kHeadDim;
 }
 
-// Slot i of a segment, by one warp: its old row to slot `to` (-1: it does not stay, or stays where it
-// is), then new row `fresh` (-1: none) in its place.
-__device__ __forceinline__ void move_slot(const EvictArgs& a, int b, int h, long long base, int i, int to, int fresh,
-                                          int seen) {
+// Slots i of a segment, by one warp: each slot's old row to slot `to` (-1: it does not stay, or stays where
+// it is), then new row `fresh` (-1: none) in its place.  All loads come before the first store.
+template <int N>
+__device__ __forceinline__ void move_slots(const EvictArgs& a, int b, int h, long long base, const int (&i)[N],
+                                           const int (&to)[N], const int (&fresh)[N], int seen) {
   const int lane = lane_id(), side = lane >> 4, piece = lane & 15;
-  uint16_t* cache = side ? a.v : a.k;
-  const long long e = slot_elem(a, b, h, i);
-  bool bad = e < 0;
-  if (to >= 0) {
-    const long long ed = slot_elem(a, b, h, to);
-    bad |= ed < 0;
-    if (e >= 0 && ed >= 0)
-      *(reinterpret_cast<uint4*>(cache + ed) + piece) = *(reinterpret_cast<const uint4*>(cache + e) + piece);
-    if (lane == 0) {
-      a.pos[base + to] = a.pos[base + i];
-      a.acc[base + to] = a.acc[base + i];
+  uint4* cache = reinterpret_cast<uint4*>(side ? a.v : a.k) + piece;
+  const uint4* rows = reinterpret_cast<const uint4*>(side ? a.v_new : a.k_new) + piece;
+  long long from[N], dst[N];
+  uint4 old[N], add[N];
+  int p[N];
+  float w[N];
+  bool bad = false;
+#pragma unroll
+  for (int u = 0; u < N; ++u) {
+    add[u] = make_uint4(0u, 0u, 0u, 0u);
+    if (fresh[u] >= 0)
+      add[u] = __ldg(rows + (b * a.new_req + h * a.new_head + static_cast<long long>(fresh[u]) * a.new_tok) / 8);
+  }
+#pragma unroll
+  for (int u = 0; u < N; ++u) {
+    from[u] = to[u] >= 0 || fresh[u] >= 0 ? slot_elem(a, b, h, i[u]) : 0;
+    dst[u] = to[u] >= 0 ? slot_elem(a, b, h, to[u]) : 0;
+    bad |= from[u] < 0 || dst[u] < 0;
+    old[u] = make_uint4(0u, 0u, 0u, 0u);
+    if (to[u] >= 0) {
+      if (from[u] >= 0 && dst[u] >= 0) old[u] = cache[from[u] / 8];
+      if (lane == 0) {
+        p[u] = a.pos[base + i[u]];
+        w[u] = a.acc[base + i[u]];
+      }
     }
   }
-  __syncwarp();
-  if (fresh >= 0) {
-    if (e >= 0)
-      *(reinterpret_cast<uint4*>(cache + e) + piece) =
-          __ldg(reinterpret_cast<const uint4*>((side ? a.v_new : a.k_new) + b * a.new_req + h * a.new_head +
-                                               static_cast<long long>(fresh) * a.new_tok) + piece);
-    if (lane == 0) {
-      a.pos[base + i] = seen + fresh;
-      a.acc[base + i] = 0.f;
+#pragma unroll
+  for (int u = 0; u < N; ++u) {
+    if (to[u] >= 0) {
+      if (from[u] >= 0 && dst[u] >= 0) cache[dst[u] / 8] = old[u];
+      if (lane == 0) {
+        a.pos[base + to[u]] = p[u];
+        a.acc[base + to[u]] = w[u];
+      }
+    }
+    if (fresh[u] >= 0) {
+      if (from[u] >= 0) cache[from[u] / 8] = add[u];
+      if (lane == 0) {
+        a.pos[base + i[u]] = seen + fresh[u];
+        a.acc[base + i[u]] = 0.f;
+      }
     }
   }
   if (bad && lane == 0) atomicOr(a.status, DEV_BAD_INDEX);
@@ -288,7 +311,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_few_kernel(const EvictArgs 
     for (int v = 0; v < kFew; ++v)
       if (v == f) to = out[v];                       // holes are the lowest of the slots that leave
   }
-  move_slot(a, b, h, base, s.keep + u, to, u < s.m ? u : -1, s.seen);
+  move_slots<1>(a, b, h, base, {s.keep + u}, {to}, {u < s.m ? u : -1}, s.seen);
 }
 
 __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArgs a) {
@@ -297,9 +320,18 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArg
   const int keep = hd.x, n = hd.y, m = hd.z, seen = hd.w;
   const long long base = static_cast<long long>(seg) * a.capacity, list = static_cast<long long>(seg) * a.most;
   const int slots = max(n - keep, m);
-  for (int u = blockIdx.x * kMoveSlots + warp_id(); u < slots; u += gridDim.x * kMoveSlots) {
-    const int rank = u < n - keep ? a.fills[list + u] : -1;
-    move_slot(a, b, h, base, keep + u, rank >= 0 ? a.holes[list + rank] : -1, u < m ? u : -1, seen);
+  for (int u0 = (blockIdx.x * kMoveWarps + warp_id()) * kEach; u0 < slots; u0 += gridDim.x * kMoveWarps * kEach) {
+    int i[kEach], to[kEach], fresh[kEach];
+#pragma unroll
+    for (int v = 0; v < kEach; ++v) {
+      i[v] = keep + u0 + v;
+      to[v] = u0 + v < n - keep ? a.fills[list + u0 + v] : -1;
+      fresh[v] = u0 + v < m ? u0 + v : -1;
+    }
+#pragma unroll
+    for (int v = 0; v < kEach; ++v)
+      if (to[v] >= 0) to[v] = a.holes[list + to[v]];
+    move_slots<kEach>(a, b, h, base, i, to, fresh, seen);
   }
 }
 
@@ -324,7 +356,7 @@ cudaError_t launch_evict(const EvictArgs& a, cudaStream_t st) {
   }
   note_launch();
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  const int gx = std::min((a.most + kMoveSlots - 1) / kMoveSlots, std::max(1, 16384 / segs));
+  const int gx = std::min((a.most + kMoveWarps * kEach - 1) / (kMoveWarps * kEach), std::max(1, 16384 / segs));
   evict_move_kernel<<<dim3(gx, segs), kMoveThreads, 0, st>>>(a);
   note_launch();
   return cudaGetLastError();
