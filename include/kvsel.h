@@ -19,6 +19,9 @@
  *     Anchor-Residual KV Cache Compression", §3.2).
  *   - Eviction acts on the un-replicated KV heads; the result is a per-head
  *     variable-length cache (KVzip §4.2, §7.1).
+ *   - The cache in use afterwards: attention of new tokens over a contiguous, paged or compacted
+ *     cache, the accumulated weight of every cached row, and eviction by it (kvsel_attend,
+ *     kvsel_evict_append).
  *
  * Conventions (all entry points):
  *   - Every pointer named device is a CUDA device pointer, 16-byte aligned; bf16 data is

@@ -106,6 +106,7 @@ struct ItemRange {
   int rows;                       // valid query rows of the block
   int p0, p1;                     // cache row of the block's first and last token
   int lo, hi, sink, ns, tiles;
+  int skip;                       // the last of the segment's items where this and all behind it are empty, else the item
   long long row0;
 };
 template <int TK>
@@ -123,8 +124,10 @@ __device__ __forceinline__ ItemRange item_range(const AttnArgs& a, int item) {
   const int R = s.m * a.G, r0 = x.rt * TR;
   x.rows = min(TR, R - r0);
   x.lo = x.ns = x.sink = x.hi = x.tiles = x.p0 = x.p1 = 0;
+  x.skip = item;
   if (x.rows <= 0) {
     x.rows = 0;
+    x.skip = item - x.rt + a.rt - 1;
     return x;
   }
   if (a.causal) {
@@ -179,9 +182,11 @@ struct Share {
   long long item_base;            // its first unit
   Item first;                     // and its range
 };
+// SKIP: segments may end in many empty items (64 tokens of four requests of 2000 rows with weights, where
+// max_len is 128000: 190 us without it, 68 with it; one item per segment: 0.3 us more).
 // range(i): the range of item i, with its number of tiles.  The result stays in shared memory; kept in
 // registers through attend_tile_kernel it costs the softmax warps' inner loop 2% (spills).
-template <int THREADS, class Range>
+template <int THREADS, bool SKIP = true, class Range>
 __device__ __forceinline__ auto share_of(int items, Range range, int cta, int start = 0) -> const Share<decltype(range(0))>& {
   using Item = decltype(range(0));
   const auto units = [&](const Item& x) { return x.tiles > 0 ? x.tiles + start : 0; };
@@ -194,6 +199,7 @@ __device__ __forceinline__ auto share_of(int items, Range range, int cta, int st
   for (int i = i0; i < i1; ++i) {
     mine = range(i);
     sum += units(mine);
+    if (SKIP) i = mine.skip;
   }
   long long inc = sum;
 #pragma unroll
@@ -220,6 +226,7 @@ __device__ __forceinline__ auto share_of(int items, Range range, int cta, int st
           mine = range(i);
           if (begin < at + units(mine)) break;
           at += units(mine);
+          if (SKIP) i = mine.skip;
         }
       }
       s_sh.total = total;
@@ -235,13 +242,17 @@ __device__ __forceinline__ auto share_of(int items, Range range, int cta, int st
   return s_sh;
 }
 // The tiles [ta, tb) of an item that this CTA works on; `base`, the item's first unit, moves to the next
-// item's.  False: none.
-template <class Item>
-__device__ __forceinline__ bool next_piece(const Share<Item>& sh, int item, int tiles, long long& base, int& ta, int& tb) {
-  if (tiles == 0) return false;
+// item's, and `item` over empty ones behind it.  False: none.
+template <bool SKIP = true, class Item>
+__device__ __forceinline__ bool next_piece(const Share<Item>& sh, int& item, const Item& x, long long& base, int& ta,
+                                           int& tb) {
+  if (x.tiles == 0) {
+    if (SKIP) item = x.skip;
+    return false;
+  }
   ta = item == sh.item ? max(0, static_cast<int>(sh.begin - base) - sh.start) : 0;
-  tb = static_cast<int>(min(static_cast<long long>(tiles), sh.end - base - sh.start));
-  base += tiles + sh.start;
+  tb = static_cast<int>(min(static_cast<long long>(x.tiles), sh.end - base - sh.start));
+  base += x.tiles + sh.start;
   return ta < tb;
 }
 // The last CTA with a unit of an item that ends before unit `e`.

@@ -14,7 +14,11 @@
 //
 // Items (16 query rows of one segment) are cut along the cache so that every CTA of the grid
 // gets the same number of tiles whatever the lengths are (share_of); the pieces of an item
-// that was cut are joined by attend_join_kernel, in cache order.
+// that was cut are joined by attend_join.cu's kernels, in cache order.
+//
+// Measured, 8 KV heads, one token: 16 requests of 2048 to 65536 rows in pages of 16 340-351 us for
+// 2.31 GB, 0.97 of the copy rate; eight requests, window of 4096 in pages of 64, 30 us for 134 MB
+// (4.4 TB/s: 4 us until the first rows arrive, 4 for the join).
 #include <algorithm>
 
 #include "attend.cuh"
@@ -73,7 +77,7 @@ __global__ void __launch_bounds__(kThreads, 2) attend_rows_kernel(const AttnArgs
   const int warp = warp_id(), lane = lane_id();
   const int quad = lane >> 2, ql = lane & 3;
   rec_clear(a);
-  const auto sh = share_of<kThreads>(a.B * a.H * a.rt, [&](int i) { return item_range<kTK>(a, i); }, blockIdx.x,
+  const auto sh = share_of<kThreads, false>(a.B * a.H * a.rt, [&](int i) { return item_range<kTK>(a, i); }, blockIdx.x,
                                      kStart);
   if (static_cast<int>(blockIdx.x) >= sh.grid) return;
   const uint32_t ring = smem_u32(smem) + warp * (kStages * kStageBytes);
@@ -83,7 +87,7 @@ __global__ void __launch_bounds__(kThreads, 2) attend_rows_kernel(const AttnArgs
   for (int item = sh.item; base < sh.end; ++item) {
     const ItemRange x = item == sh.item ? sh.first : item_range<kTK>(a, item);
     int ta, tb;
-    if (!next_piece(sh, item, x.tiles, base, ta, tb)) continue;
+    if (!next_piece<false>(sh, item, x, base, ta, tb)) continue;
     const int cnt = tb - ta;
 
     // element offset of the cached row that this lane looks up for unit u (rows 0..15: lanes l

@@ -118,6 +118,9 @@ def test_work_cut_over_many_blocks():
     # a few tiles each, of more segments than there are blocks: most blocks begin and end within one
     run(B=40, H=8, G=4, m=70, lens=70 + np.arange(40) * 9, layout="paged", seed=5)
     run(B=6, H=3, G=8, m=9, lens=[9, 40, 700, 1, 5000, 128], seed=6)
+    # room for far more rows, and tokens, than there are: segments that end in many empty items
+    run(B=40, H=4, G=4, m=40, lens=40 + np.arange(40) * 9, pad_rows=20000, layout="paged", block=64, seed=7)
+    run(B=5, H=2, G=4, m=700, new=[0, 3, 700, 1, 90], lens=[0, 3, 900, 5000, 90], seed=8)
 
 
 def test_weights_add_up_over_calls_and_results_repeat():
@@ -310,6 +313,18 @@ def test_a_wait_that_runs_out_is_reported(m, G, acc):
     assert CH.status(ws) == 0
     c.check(acc=acc)
     torch.cuda.synchronize()
+
+
+def test_a_workspace_elsewhere_is_refused():
+    from kv_cache_eviction_window_gb300 import binding as L
+
+    c = CH.Case(lens=50).upload()
+    ws = CH.workspace(L.kvsel_attend_workspace_size(L.make_attn_params(**c.params), True))
+    with pytest.raises(L.KvselError) as e:
+        c.call(acc=True, ws=ws.cpu())
+    assert e.value.code == L.KVSEL_EINVAL
+    c.call(acc=True, ws=ws)
+    c.check(acc=True)
 
 
 def test_more_blocks_than_can_be_planned_are_refused():
