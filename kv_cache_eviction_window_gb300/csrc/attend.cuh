@@ -392,7 +392,8 @@ __device__ __forceinline__ bool elect_one() {
 }
 
 // a few rows per item (a.tr = attend_rows_tile())
-cudaError_t launch_attend_rows(const AttnArgs& a, int grid, cudaStream_t st);
+cudaError_t launch_attend_rows(const AttnArgs& a, int grid, int cluster, cudaStream_t st);
+int attend_rows_cluster(long long items, long long tiles, bool window, int grid);
 int attend_rows_tile();
 int attend_tile_rows(bool split);  // rows of a K/V stage, and of a box of its maps
 int attend_rows_ctas_per_sm();

@@ -31,6 +31,7 @@ struct AttnPlan {
   int grid = 0, tr = 0, rt = 1;
   bool tiled = false, split = false;
   int block = 0;                 // tiled: query rows per block, whole tokens of the group
+  int cluster = 0;               // not tiled: attend_rows_cluster
   int kb = 1, kb_sink = -1;      // tiled, with weights: blocks of 256 cached rows (attend.cuh)
   size_t rec = 0, ml = 0, o = 0, lse2 = 0, wpart = 0, logits = 0, total = 0;
   long long logit_stride = 0;
@@ -72,6 +73,11 @@ int plan_attn(const kvsel_attn_params* p, bool with_acc, AttnPlan& pl) {
     // single tokens and the like: HBM-bound, 16 query rows per item
     pl.tr = attend_rows_tile();
     pl.grid = sms * attend_rows_ctas_per_sm();
+    // tiles of 64 rows that an item may have: with a window some before it and some of the first rows
+    long long tiles = (static_cast<long long>(p->max_len) + 63) / 64;
+    const long long seen = (p->n_sink + 63ll) / 64 + (static_cast<long long>(p->window) + p->n_new + 126) / 64;
+    const bool window = p->window > 0 && seen < tiles;
+    pl.cluster = attend_rows_cluster(static_cast<long long>(p->batch) * p->h_kv, window ? seen : tiles, window, pl.grid);
   } else {
     pl.tiled = true;
     pl.block = 128 / p->group * p->group;
@@ -299,7 +305,7 @@ int kvsel_attend(const kvsel_attn_params* p, const void* q, const kvsel_kv* kv, 
   a.wc = WaitCtl{p->wait_cycles ? p->wait_cycles : kDefaultWaitCycles, static_cast<int*>(ws)};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (!pl.tiled) {
-    rc = launch_rc(launch_attend_rows(a, pl.grid, st));
+    rc = launch_rc(launch_attend_rows(a, pl.grid, pl.cluster, st));
     return rc || !acc ? rc : launch_rc(launch_weights_kept(a, st));
   }
   CUtensorMap tq, tk, tv;

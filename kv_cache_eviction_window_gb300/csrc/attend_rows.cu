@@ -12,16 +12,23 @@
 // four warps are merged once per item.  cp.async writes zeros for rows that no query row
 // sees, so nothing that lies behind a segment's end can reach a product.
 //
-// Items (16 query rows of one segment) are cut along the cache so that every CTA of the grid
+// Where few tiles fall to each CTA (attend_rows_cluster), an item belongs to a cluster, whose CTAs
+// take a share of its tiles each and join them through distributed shared memory.  Otherwise
+// items (16 query rows of one segment) are cut along the cache so that every CTA of the grid
 // gets the same number of tiles whatever the lengths are (share_of); the pieces of an item
 // that was cut are joined by attend_join.cu's kernels, in cache order.
 //
 // Measured, 8 KV heads, one token: 16 requests of 2048 to 65536 rows in pages of 16 340-351 us for
-// 2.31 GB, 0.97 of the copy rate; eight requests, window of 4096 in pages of 64, 30 us for 134 MB
-// (4.4 TB/s: 4 us until the first rows arrive, 4 for the join).
+// 2.31 GB, 0.97 of the copy rate; eight requests, window of 4096 in pages of 64, 26 us for 134 MB
+// (clusters of four; 30 us with plan and join); one request of 1111 rows 6.6 us (7.4).
+#include <cooperative_groups.h>
+
 #include <algorithm>
+#include <atomic>
 
 #include "attend.cuh"
+
+namespace cgx = cooperative_groups;
 
 namespace kvsel {
 namespace {
@@ -32,8 +39,10 @@ constexpr int kTR = 16;                              // query rows per item
 constexpr int kUnit = 16;                            // cached rows per warp and step
 constexpr int kTK = kUnit * kWarps;                  // cached rows per tile
 constexpr int kStages = 3;
-// what the start of an item costs, in tiles (eight requests, window of 4096: 32.1 us without it, 31.2 at
-// one, 30.6 at two and four; a compacted cache of 4 heads 13.1, 12.3, 12.2)
+constexpr int kMaxCluster = 8;
+// what the start of an item costs in the plan, in tiles (eight requests, window of 4096, without
+// clusters: 32.1 us without it, 31.2 at one, 30.6 at two and four; a compacted cache of 4 heads 13.1,
+// 12.3, 12.2)
 constexpr int kStart = 2;
 constexpr int kUnitBytes = kUnit * 256;              // one side (K or V) of a unit
 constexpr int kStageBytes = 2 * kUnitBytes;
@@ -71,23 +80,35 @@ __device__ __forceinline__ void mma16816(float c[4], const uint32_t a[4], uint32
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// CLUSTER: an item's tiles are cut over the CTAs of a cluster instead, which join them.
+template <bool CLUSTER>
 __global__ void __launch_bounds__(kThreads, 2) attend_rows_kernel(const AttnArgs a) {
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ float s_m[kWarps][kTR], s_l[kWarps][kTR];
   const int warp = warp_id(), lane = lane_id();
   const int quad = lane >> 2, ql = lane & 3;
-  rec_clear(a);
-  const auto sh = share_of<kThreads, false>(a.B * a.H * a.rt, [&](int i) { return item_range<kTK>(a, i); }, blockIdx.x,
-                                     kStart);
-  if (static_cast<int>(blockIdx.x) >= sh.grid) return;
+  const int cs = CLUSTER ? static_cast<int>(cgx::this_cluster().num_blocks()) : 1;
+  const int rank = CLUSTER ? static_cast<int>(cgx::this_cluster().block_rank()) : 0;
+  Share<ItemRange> sh{};
+  if (!CLUSTER) {
+    rec_clear(a);
+    sh = share_of<kThreads, false>(a.B * a.H * a.rt, [&](int i) { return item_range<kTK>(a, i); }, blockIdx.x, kStart);
+    if (static_cast<int>(blockIdx.x) >= sh.grid) return;
+  }
   const uint32_t ring = smem_u32(smem) + warp * (kStages * kStageBytes);
   float* s_o = reinterpret_cast<float*>(smem);
 
   long long base = sh.item_base;
-  for (int item = sh.item; base < sh.end; ++item) {
-    const ItemRange x = item == sh.item ? sh.first : item_range<kTK>(a, item);
+  for (int item = CLUSTER ? static_cast<int>(blockIdx.x) / cs : sh.item; CLUSTER || base < sh.end; ++item) {
+    const ItemRange x = !CLUSTER && item == sh.item ? sh.first : item_range<kTK>(a, item);
     int ta, tb;
-    if (!next_piece<false>(sh, item, x, base, ta, tb)) continue;
+    if (CLUSTER) {
+      if (x.tiles == 0) return;                      // the whole cluster
+      ta = static_cast<int>(static_cast<long long>(x.tiles) * rank / cs);
+      tb = static_cast<int>(static_cast<long long>(x.tiles) * (rank + 1) / cs);
+    } else if (!next_piece<false>(sh, item, x, base, ta, tb)) {
+      continue;
+    }
     const int cnt = tb - ta;
 
     // element offset of the cached row that this lane looks up for unit u (rows 0..15: lanes l
@@ -301,7 +322,15 @@ __global__ void __launch_bounds__(kThreads, 2) attend_rows_kernel(const AttnArgs
         y.z += f * z.z;
         y.w += f * z.w;
       }
-      if (first && last) {
+      if (CLUSTER) {
+        // stays here, in the place of the first warp's, for the CTA that joins the row
+        *reinterpret_cast<float4*>(s_o + r * kOPad + lane * 4) = y;
+        __syncwarp();
+        if (lane == 0) {
+          s_m[0][r] = M;
+          s_l[0][r] = L;
+        }
+      } else if (first && last) {
         const float inv = L > 0.f ? 1.f / L : 0.f;
         *reinterpret_cast<uint2*>(out_row(a, x.b, x.h, r0 + r) + lane * 4) =
             make_uint2(pack_bf16(y.x * inv, y.y * inv), pack_bf16(y.z * inv, y.w * inv));
@@ -310,6 +339,40 @@ __global__ void __launch_bounds__(kThreads, 2) attend_rows_kernel(const AttnArgs
         *reinterpret_cast<float4*>(a.part_o + (static_cast<long long>(slot) * kTR + r) * kHeadDim + lane * 4) = y;
         if (lane == 0) a.part_ml[static_cast<long long>(slot) * kTR + r] = make_float2(M, L);
       }
+    }
+    if (CLUSTER) {
+      cgx::cluster_group cl = cgx::this_cluster();
+      cl.sync();
+      for (int r = rank + cs * warp; r < x.rows; r += cs * kWarps) {
+        float m[kMaxCluster], l[kMaxCluster], M = -INFINITY, L = 0.f;
+        float4 z[kMaxCluster], y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int c = 0; c < kMaxCluster; ++c) {
+          m[c] = -INFINITY;
+          if (c < cs) {
+            m[c] = *cl.map_shared_rank(&s_m[0][r], c);
+            l[c] = *cl.map_shared_rank(&s_l[0][r], c);
+            z[c] = *reinterpret_cast<const float4*>(cl.map_shared_rank(s_o + r * kOPad + lane * 4, c));
+          }
+          M = fmaxf(M, m[c]);
+        }
+#pragma unroll
+        for (int c = 0; c < kMaxCluster; ++c) {
+          if (m[c] == -INFINITY) continue;
+          const float f = exp2f(m[c] - M);
+          L += f * l[c];
+          y.x += f * z[c].x;
+          y.y += f * z[c].y;
+          y.z += f * z[c].z;
+          y.w += f * z[c].w;
+        }
+        const float inv = L > 0.f ? 1.f / L : 0.f;
+        *reinterpret_cast<uint2*>(out_row(a, x.b, x.h, r0 + r) + lane * 4) =
+            make_uint2(pack_bf16(y.x * inv, y.y * inv), pack_bf16(y.z * inv, y.w * inv));
+        if (lane == 0) write_lse(a, x.b, x.h, r0 + r, M, L);
+      }
+      cl.sync();                                     // its shared memory has been read
+      return;
     }
     if (first) rec_first(a, item, last ? 0 : last_cta(sh, base) - static_cast<int>(blockIdx.x));
     __syncthreads();   // s_m, s_l and the accumulators are read before the next item
@@ -346,10 +409,82 @@ __global__ void __launch_bounds__(256) weights_kept_kernel(const AttnArgs a) {
 int attend_rows_tile() { return kTR; }
 int attend_rows_ctas_per_sm() { return 2; }
 
-cudaError_t launch_attend_rows(const AttnArgs& a, int grid, cudaStream_t st) {
-  cudaError_t e = ensure_smem(reinterpret_cast<const void*>(attend_rows_kernel), kSmem);
+namespace {
+
+cudaLaunchConfig_t cluster_config(int ctas, int cluster, cudaStream_t st, cudaLaunchAttribute* attr) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas, 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = st;
+  attr->id = cudaLaunchAttributeClusterDimension;
+  attr->val.clusterDim.x = cluster;
+  attr->val.clusterDim.y = 1;
+  attr->val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cfg;
+}
+
+// Clusters of c CTAs that the current device holds at once (a cluster sits inside one GPC, so sizes that
+// do not divide a GPC's CTAs leave some of them empty); asked once per device and size.
+int clusters_at_once(int c) {
+  constexpr int kDevices = 64;
+  static std::atomic<int> known[kDevices][kMaxCluster + 1];   // plus one; 0: not asked yet
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return 0;
+  if (dev < kDevices) {
+    const int n = known[dev][c].load(std::memory_order_relaxed);
+    if (n) return n - 1;
+  }
+  const void* kernel = reinterpret_cast<const void*>(attend_rows_kernel<true>);
+  cudaLaunchAttribute attr[1];
+  const cudaLaunchConfig_t cfg = cluster_config(c, c, nullptr, attr);
+  int n = 0;
+  if (ensure_smem(kernel, kSmem) != cudaSuccess || cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    n = 0;
+  }
+  if (dev < kDevices) known[dev][c].store(n + 1, std::memory_order_relaxed);
+  return n;
+}
+
+}  // namespace
+
+// CTAs of a cluster per item, or 0: a plan of the whole grid and a join.  `items`, of `tiles` tiles at
+// most (with a window: most of them).
+//
+// The plan and the join cost some 3 us, and a tile takes a CTA 0.78 us as long as HBM keeps up, which
+// it does for about 160 CTAs; so clusters win when the tiles of a CTA are less than 4 plus what
+// HBM needs for all of them, items * tiles / 156.  Caches of one batch differ in length, and only a
+// bound is known here: half of that is counted, and one tile less.  Measured, group 4, all caches as
+// long as the bound, plan and cluster: 8 items of 64 rows 5.7 and 4.7 us, of 512 7.5 and 5.2, of 2048
+// 8.1 and 7.7, of 4096 9.1 and 11.0; 40 items of 1111 rows 10.2 and 8.0; 128 items of 128 rows 9.3 and
+// 5.9, of 2048 30.0 and 25.0; 64 items with a window of 4096 29.7 and 25.7.  More clusters than
+// fit at once lose (512 items of 256 rows 17.9 and 35; 40 clusters of seven 12.4 and 16.7).
+int attend_rows_cluster(long long items, long long tiles, bool window, int grid) {
+  long long serial = tiles + 1;
+  int best = 0;
+  for (int c = 1; c <= kMaxCluster && items * c <= grid; ++c)
+    if ((tiles + c - 1) / c < serial && items <= clusters_at_once(c)) {
+      serial = (tiles + c - 1) / c;
+      best = c;
+    }
+  return best && serial <= 3 + items * tiles / (window ? 156 : 312) ? best : 0;
+}
+
+cudaError_t launch_attend_rows(const AttnArgs& a, int grid, int cluster, cudaStream_t st) {
+  const auto kernel = cluster ? attend_rows_kernel<true> : attend_rows_kernel<false>;
+  cudaError_t e = ensure_smem(reinterpret_cast<const void*>(kernel), kSmem);
   if (e != cudaSuccess) return e;
-  attend_rows_kernel<<<grid, kThreads, kSmem, st>>>(a);
+  if (cluster) {
+    cudaLaunchAttribute attr[1];
+    const cudaLaunchConfig_t cfg = cluster_config(a.B * a.H * a.rt * cluster, cluster, st, attr);
+    e = cudaLaunchKernelEx(&cfg, kernel, a);
+    note_launch();
+    return e;
+  }
+  kernel<<<grid, kThreads, kSmem, st>>>(a);
   note_launch();
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   return launch_attend_join(a, grid, st);

@@ -34,6 +34,25 @@ def test_single_tokens(layout, block, n):
     run(layout=layout, block=block, lens=n, H=2, G=4, seed=n)
 
 
+@pytest.mark.parametrize("layout,block", [("contiguous", 0), ("paged", 8), ("paged", 32)])
+@pytest.mark.parametrize("n", [0, 1, 63, 65, 300, 1111, 4000])
+def test_single_tokens_with_room_for_more(layout, block, n):
+    # rows in use far below max_len: the work is cut over the whole grid, whatever the length
+    run(layout=layout, block=block, lens=n, H=2, G=4, pad_rows=4500, seed=n)
+
+
+@pytest.mark.parametrize("pad_rows", [0, 9000])
+def test_few_rows_of_every_kind(pad_rows):
+    # the same calls where an item belongs to one cluster, and where the whole grid shares the work
+    kw = dict(layout="paged", block=16, pad_rows=pad_rows)
+    run(B=5, H=2, G=4, m=1, lens=[0, 1, 64, 513, 700], new=[0, 1, 1, 0, 1], seed=1, **kw)
+    run(B=2, H=3, G=5, m=3, lens=[2, 517], per_head=False, seed=2, **kw)
+    run(B=3, H=2, G=4, m=4, lens=[1, 300, 640], causal=False, seed=3, **kw)
+    run(B=2, H=2, G=8, m=2, lens=[900, 65], window=70, n_sink=3, seed=4, **kw)
+    run(B=7, H=8, G=2, m=8, lens=20 + 97 * np.arange(7), token_major=True, seed=5, **kw)
+    run(B=38, H=8, G=1, m=1, lens=1 + 5 * np.arange(38), seed=6, **kw)
+
+
 @pytest.mark.parametrize("G", [1, 2, 3, 5, 7, 8, 13, 16, 17, 32, 100, 128])
 def test_groups(G):
     run(G=G, H=1, lens=333, seed=G)
