@@ -369,6 +369,7 @@ int kvsel_evict_append(const kvsel_evict_params* p, const kvsel_kv* kv, int32_t*
   a.holes = reinterpret_cast<int32_t*>(wsb + L.holes);
   a.fills = reinterpret_cast<int32_t*>(wsb + L.fills);
   a.most = L.most;
+  if ((rc = device_sms(&a.sms))) return rc;
   a.status = static_cast<int*>(ws);
   return launch_rc(launch_evict(a, static_cast<cudaStream_t>(stream)));
 }

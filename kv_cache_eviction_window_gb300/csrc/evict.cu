@@ -8,12 +8,15 @@
 // evict_few_kernel: up to four rows to evict (a decode step): one CTA per segment finds them by
 // as many block-wide minima and moves the rows itself.  Bound: latency.
 // evict_select_kernel: one CTA per segment ranks the slots: the keep-th largest key by a radix
-// selection in three digits, then ordered scans for ties, holes and fills.  The keys stay in
+// selection in three digits at most (it ends when a whole bin stays: then there are no ties to rank
+// either; 4 to 5 us less for 200 to 16384 slots), then ordered scans for ties, holes and fills.  The keys stay in
 // shared memory (up to 49,152 slots); a thread owns an odd number of consecutive slots, so that
 // its walk through them meets no bank twice and equal neighbours cost one count.
+// With no more segments than SMs and at most 64 rows to move, the same CTA moves them (200 slots, five
+// rows, 8 us with the second launch, 6 without; 256 segments 20.5 and 24, two CTAs an SM no longer).
 // evict_move_kernel: slot keep + i of a segment is handled by one half warp per side: its old
 // row goes to its hole, then new row i takes the slot.  A warp takes two slots at a time (one: 37.2
-// us for the call with 2048 rows of 32 segments of 16384, two 35.7, four 38.3).  Bound: the latency
+// us for the call with 2048 rows of 32 segments of 16384, two 35.7, four 38.3; 30.8 now).  Bound: the latency
 // of a slot's chain of loads (its rank, its hole, their pages, its row), then HBM, 512 B per moved
 // or new row read and written (and 8 B per slot before).
 #include <algorithm>
@@ -79,105 +82,6 @@ __device__ __forceinline__ unsigned long long block_scan(unsigned long long v, u
   return v;
 }
 
-constexpr int kKeptSlots = 49152;                    // slots whose keys fit into shared memory
-
-// KEPT: the keys are in shared memory, else formed again from pos and acc in every pass
-template <bool KEPT>
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictArgs a) {
-  extern __shared__ uint32_t s_key[];
-  __shared__ int s_hist[2048];
-  __shared__ unsigned long long s_w[32];
-  __shared__ uint32_t s_prefix;
-  __shared__ int s_need;
-  const int seg = blockIdx.x, tid = threadIdx.x;
-  const Seg s = seg_of(a, seg);
-  const long long base = static_cast<long long>(seg) * a.capacity;
-  __syncthreads();   // every thread has read lens and seen
-  if (tid == 0) {
-    a.head[seg] = make_int4(s.keep, s.n, s.m, s.seen);
-    a.lens[seg] = s.keep + s.m;
-    a.seen[seg] = s.seen + s.m;
-  }
-  if (s.keep == s.n) return;
-  if (KEPT) {
-#pragma unroll 8
-    for (int i = tid; i < s.n; i += kSelThreads) s_key[i] = slot_key(a, s, base, i);
-  }
-  const int run = ((s.n + kSelThreads - 1) / kSelThreads) | 1;
-  const int i0 = static_cast<int>(min(static_cast<long long>(s.n), static_cast<long long>(tid) * run));
-  const int i1 = static_cast<int>(min(static_cast<long long>(s.n), static_cast<long long>(i0) + run));
-  auto key = [&](int i) { return KEPT ? s_key[i] : slot_key(a, s, base, i); };
-
-  // the keep-th largest key, by digits of 11, 11 and 10 bits from the top
-  uint32_t prefix = 0, mask = 0;
-  int need = s.keep;                                 // rank among the keys that share the prefix
-  if (s.keep == 0) prefix = 0xFFFFFFFFu, mask = 0xFFFFFFFFu, need = 0;
-  for (int pass = 0; pass < 3 && s.keep > 0; ++pass) {
-    const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), bins = pass == 2 ? 1024 : 2048;
-    for (int i = tid; i < bins; i += kSelThreads) s_hist[i] = 0;
-    __syncthreads();
-    int bin = -1, cnt = 0;
-#pragma unroll 4
-    for (int i = i0; i < i1; ++i) {
-      const uint32_t k = key(i);
-      if ((k & mask) != prefix) continue;
-      const int d = static_cast<int>((k >> shift) & (bins - 1));
-      if (d != bin) {
-        if (cnt) atomicAdd(&s_hist[bin], cnt);
-        bin = d;
-        cnt = 0;
-      }
-      ++cnt;
-    }
-    if (cnt) atomicAdd(&s_hist[bin], cnt);
-    __syncthreads();
-    // thread t owns bins 2t and 2t + 1 counted from the top
-    const int per = bins / kSelThreads;
-    int own = 0;
-    for (int u = 0; u < per; ++u) own += s_hist[bins - 1 - (tid * per + u)];
-    unsigned long long total;
-    int before = static_cast<int>(block_scan(own, s_w, total)) - own;
-    for (int u = 0; u < per; ++u) {
-      const int d = bins - 1 - (tid * per + u), c = s_hist[d];
-      if (before < need && need <= before + c) {
-        s_prefix = prefix | (static_cast<uint32_t>(d) << shift);
-        s_need = need - before;
-      }
-      before += c;
-    }
-    __syncthreads();
-    prefix = s_prefix;
-    need = s_need;
-    mask |= static_cast<uint32_t>(bins - 1) << shift;
-  }
-  // keys above `prefix` stay, and the first `need` slots whose key equals it
-  __syncthreads();
-  int ties = 0;
-#pragma unroll 4
-  for (int i = i0; i < i1; ++i) ties += key(i) == prefix;
-  unsigned long long total;
-  const int ties0 = static_cast<int>(block_scan(ties, s_w, total)) - ties;
-  unsigned long long v = 0;                          // holes above, fills below
-  int t = ties0;
-#pragma unroll 4
-  for (int i = i0; i < i1; ++i) {
-    const uint32_t k = key(i);
-    const bool kept = k > prefix || (k == prefix && t++ < need);
-    if (!kept && i < s.keep) v += 1ull << 32;
-    if (kept && i >= s.keep) v += 1;
-  }
-  const unsigned long long sc = block_scan(v, s_w, total) - v;
-  const long long list = static_cast<long long>(seg) * a.most;
-  int hole = static_cast<int>(sc >> 32), fill = static_cast<int>(sc & 0xFFFFFFFFu);
-  t = ties0;
-  for (int i = i0; i < i1; ++i) {
-    const uint32_t k = key(i);
-    const bool kept = k > prefix || (k == prefix && t++ < need);
-    if (!kept && i < s.keep) a.holes[list + hole++] = i;
-    if (i >= s.keep) a.fills[list + i - s.keep] = kept ? fill++ : -1;
-  }
-}
-
 __device__ __forceinline__ long long slot_elem(const EvictArgs& a, int b, int h, int i) {
   if (!a.src.paged) return b * a.stride_req + h * a.stride_head + static_cast<long long>(i) * a.stride_tok;
   const int bs = a.src.block_size;
@@ -237,6 +141,145 @@ __device__ __forceinline__ void move_slots(const EvictArgs& a, int b, int h, lon
     }
   }
   if (bad && lane == 0) atomicOr(a.status, DEV_BAD_INDEX);
+}
+
+// The rows behind the `keep` that stay of n, and m new ones, by warp `warp` of `warps`.
+__device__ __forceinline__ void move_rows(const EvictArgs& a, int seg, int keep, int n, int m, int seen, const int* holes,
+                                          const int* fills, int warp, int warps) {
+  const int b = seg / a.H, h = seg - b * a.H, slots = max(n - keep, m);
+  const long long base = static_cast<long long>(seg) * a.capacity;
+  for (int u0 = warp * kEach; u0 < slots; u0 += warps * kEach) {
+    int i[kEach], to[kEach], fresh[kEach];
+#pragma unroll
+    for (int v = 0; v < kEach; ++v) {
+      i[v] = keep + u0 + v;
+      to[v] = u0 + v < n - keep ? fills[u0 + v] : -1;
+      fresh[v] = u0 + v < m ? u0 + v : -1;
+    }
+#pragma unroll
+    for (int v = 0; v < kEach; ++v)
+      if (to[v] >= 0) to[v] = holes[to[v]];
+    move_slots<kEach>(a, b, h, base, i, to, fresh, seen);
+  }
+}
+
+constexpr int kKeptSlots = 49152;                    // slots whose keys fit into shared memory
+
+constexpr int kHere = 64;                            // rows that the selecting CTA may move itself
+
+// KEPT: the keys are in shared memory, else formed again from pos and acc in every pass.
+// HERE: the CTA moves the rows too (evict_here).
+template <bool KEPT, bool HERE>
+__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictArgs a) {
+  extern __shared__ uint32_t s_key[];
+  __shared__ int s_hist[2048];
+  __shared__ unsigned long long s_w[32];
+  __shared__ uint32_t s_prefix;
+  __shared__ int s_need, s_all;
+  __shared__ int s_holes[HERE ? kHere : 1], s_fills[HERE ? kHere : 1];
+  const int seg = blockIdx.x, tid = threadIdx.x;
+  const Seg s = seg_of(a, seg);
+  const long long base = static_cast<long long>(seg) * a.capacity;
+  __syncthreads();   // every thread has read lens and seen
+  if (tid == 0) {
+    if (!HERE) a.head[seg] = make_int4(s.keep, s.n, s.m, s.seen);
+    a.lens[seg] = s.keep + s.m;
+    a.seen[seg] = s.seen + s.m;
+  }
+  if (s.keep == s.n) {
+    if (HERE) move_rows(a, seg, s.keep, s.n, s.m, s.seen, s_holes, s_fills, warp_id(), kSelThreads / 32);
+    return;
+  }
+  if (KEPT) {
+#pragma unroll 8
+    for (int i = tid; i < s.n; i += kSelThreads) s_key[i] = slot_key(a, s, base, i);
+  }
+  const int run = ((s.n + kSelThreads - 1) / kSelThreads) | 1;
+  const int i0 = static_cast<int>(min(static_cast<long long>(s.n), static_cast<long long>(tid) * run));
+  const int i1 = static_cast<int>(min(static_cast<long long>(s.n), static_cast<long long>(i0) + run));
+  auto key = [&](int i) { return KEPT ? s_key[i] : slot_key(a, s, base, i); };
+
+  // the keep-th largest key, by digits of 11, 11 and 10 bits from the top
+  uint32_t prefix = 0, mask = 0;
+  int need = s.keep;                                 // rank among the keys that share the prefix
+  if (s.keep == 0) prefix = 0xFFFFFFFFu, mask = 0xFFFFFFFFu, need = 0;
+  bool all = false;                                  // every key that shares the prefix stays
+  for (int pass = 0; pass < 3 && s.keep > 0 && !all; ++pass) {
+    const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), bins = pass == 2 ? 1024 : 2048;
+    for (int i = tid; i < bins; i += kSelThreads) s_hist[i] = 0;
+    __syncthreads();
+    int bin = -1, cnt = 0;
+#pragma unroll 4
+    for (int i = i0; i < i1; ++i) {
+      const uint32_t k = key(i);
+      if ((k & mask) != prefix) continue;
+      const int d = static_cast<int>((k >> shift) & (bins - 1));
+      if (d != bin) {
+        if (cnt) atomicAdd(&s_hist[bin], cnt);
+        bin = d;
+        cnt = 0;
+      }
+      ++cnt;
+    }
+    if (cnt) atomicAdd(&s_hist[bin], cnt);
+    __syncthreads();
+    // thread t owns bins 2t and 2t + 1 counted from the top
+    const int per = bins / kSelThreads;
+    int own = 0;
+    for (int u = 0; u < per; ++u) own += s_hist[bins - 1 - (tid * per + u)];
+    unsigned long long total;
+    int before = static_cast<int>(block_scan(own, s_w, total)) - own;
+    for (int u = 0; u < per; ++u) {
+      const int d = bins - 1 - (tid * per + u), c = s_hist[d];
+      if (before < need && need <= before + c) {
+        s_prefix = prefix | (static_cast<uint32_t>(d) << shift);
+        s_need = need - before;
+        s_all = need - before == c;
+      }
+      before += c;
+    }
+    __syncthreads();
+    prefix = s_prefix;
+    need = s_need;
+    all = s_all;
+    mask |= static_cast<uint32_t>(bins - 1) << shift;
+  }
+  // keys above `prefix` stay, and of the slots whose key equals it all, or the first `need`
+  __syncthreads();
+  unsigned long long total;
+  int ties0 = 0;
+  if (!all) {
+    int ties = 0;
+#pragma unroll 4
+    for (int i = i0; i < i1; ++i) ties += key(i) == prefix;
+    ties0 = static_cast<int>(block_scan(ties, s_w, total)) - ties;
+  }
+  auto stays = [&](uint32_t k, int& t) {
+    k &= mask;
+    return k > prefix || (k == prefix && (all || t++ < need));
+  };
+  unsigned long long v = 0;                          // holes above, fills below
+  int t = ties0;
+#pragma unroll 4
+  for (int i = i0; i < i1; ++i) {
+    const bool kept = stays(key(i), t);
+    if (!kept && i < s.keep) v += 1ull << 32;
+    if (kept && i >= s.keep) v += 1;
+  }
+  const unsigned long long sc = block_scan(v, s_w, total) - v;
+  int* holes = HERE ? s_holes : a.holes + static_cast<long long>(seg) * a.most;
+  int* fills = HERE ? s_fills : a.fills + static_cast<long long>(seg) * a.most;
+  int hole = static_cast<int>(sc >> 32), fill = static_cast<int>(sc & 0xFFFFFFFFu);
+  t = ties0;
+  for (int i = i0; i < i1; ++i) {
+    const bool kept = stays(key(i), t);
+    if (!kept && i < s.keep) holes[hole++] = i;
+    if (i >= s.keep) fills[i - s.keep] = kept ? fill++ : -1;
+  }
+  if (HERE) {
+    __syncthreads();
+    move_rows(a, seg, s.keep, s.n, s.m, s.seen, s_holes, s_fills, warp_id(), kSelThreads / 32);
+  }
 }
 
 // At most kFew rows to evict and to append.  A slot ranks by (key, then the later slot first): the
@@ -315,24 +358,11 @@ __global__ void __launch_bounds__(kSelThreads) evict_few_kernel(const EvictArgs 
 }
 
 __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArgs a) {
-  const int seg = blockIdx.y, b = seg / a.H, h = seg - b * a.H;
+  const int seg = blockIdx.y;
   const int4 hd = a.head[seg];
-  const int keep = hd.x, n = hd.y, m = hd.z, seen = hd.w;
-  const long long base = static_cast<long long>(seg) * a.capacity, list = static_cast<long long>(seg) * a.most;
-  const int slots = max(n - keep, m);
-  for (int u0 = (blockIdx.x * kMoveWarps + warp_id()) * kEach; u0 < slots; u0 += gridDim.x * kMoveWarps * kEach) {
-    int i[kEach], to[kEach], fresh[kEach];
-#pragma unroll
-    for (int v = 0; v < kEach; ++v) {
-      i[v] = keep + u0 + v;
-      to[v] = u0 + v < n - keep ? a.fills[list + u0 + v] : -1;
-      fresh[v] = u0 + v < m ? u0 + v : -1;
-    }
-#pragma unroll
-    for (int v = 0; v < kEach; ++v)
-      if (to[v] >= 0) to[v] = a.holes[list + to[v]];
-    move_slots<kEach>(a, b, h, base, i, to, fresh, seen);
-  }
+  const long long list = static_cast<long long>(seg) * a.most;
+  move_rows(a, seg, hd.x, hd.y, hd.z, hd.w, a.holes + list, a.fills + list, blockIdx.x * kMoveWarps + warp_id(),
+            gridDim.x * kMoveWarps);
 }
 
 }  // namespace
@@ -346,16 +376,15 @@ cudaError_t launch_evict(const EvictArgs& a, cudaStream_t st) {
     note_launch();
     return cudaGetLastError();
   }
+  const bool kept = a.capacity <= kKeptSlots, here = a.most <= kHere && segs <= a.sms;
+  const auto select = kept ? (here ? evict_select_kernel<true, true> : evict_select_kernel<true, false>)
+                           : (here ? evict_select_kernel<false, true> : evict_select_kernel<false, false>);
+  const size_t smem = kept ? static_cast<size_t>(a.capacity) * sizeof(uint32_t) : 0;
   cudaError_t e;
-  if (a.capacity <= kKeptSlots) {
-    const size_t smem = static_cast<size_t>(a.capacity) * sizeof(uint32_t);
-    if ((e = ensure_smem(reinterpret_cast<const void*>(evict_select_kernel<true>), smem)) != cudaSuccess) return e;
-    evict_select_kernel<true><<<segs, kSelThreads, smem, st>>>(a);
-  } else {
-    evict_select_kernel<false><<<segs, kSelThreads, 0, st>>>(a);
-  }
+  if (kept && (e = ensure_smem(reinterpret_cast<const void*>(select), smem)) != cudaSuccess) return e;
+  select<<<segs, kSelThreads, smem, st>>>(a);
   note_launch();
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if ((e = cudaGetLastError()) != cudaSuccess || here) return e;
   const int gx = std::min((a.most + kMoveWarps * kEach - 1) / (kMoveWarps * kEach), std::max(1, 16384 / segs));
   evict_move_kernel<<<dim3(gx, segs), kMoveThreads, 0, st>>>(a);
   note_launch();

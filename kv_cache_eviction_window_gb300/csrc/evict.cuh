@@ -22,6 +22,7 @@ struct EvictArgs {
   // workspace: the segment's numbers for the second launch, its holes, and the rank among the
   // kept ones (or -1) of every slot behind the kept range
   int4* head;                     // [B*H]: rows kept, rows before, new rows, tokens seen before
+  int sms;                        // of the device
   int most;                       // rows to evict, and slots behind the kept range, at most
   int32_t* holes;                 // [B*H][most]
   int32_t* fills;                 // [B*H][most]
