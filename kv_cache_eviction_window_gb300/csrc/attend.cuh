@@ -67,6 +67,7 @@ struct AttnArgs {
   // -1, CTAs that follow}
   int2* rec;                      // [grid]
   int by_item;
+  int whole;                      // attend_tile_kernel: a CTA per item, no plan, no join
   int grid;                       // CTAs of the kernel that works on the items
   WaitCtl wc;
 };
@@ -184,14 +185,28 @@ struct Share {
 };
 // SKIP: segments may end in many empty items (64 tokens of four requests of 2000 rows with weights, where
 // max_len is 128000: 190 us without it, 68 with it; one item per segment: 0.3 us more).
+// whole: item `cta` and nothing else.
 // range(i): the range of item i, with its number of tiles.  The result stays in shared memory; kept in
 // registers through attend_tile_kernel it costs the softmax warps' inner loop 2% (spills).
 template <int THREADS, bool SKIP = true, class Range>
-__device__ __forceinline__ auto share_of(int items, Range range, int cta, int start = 0) -> const Share<decltype(range(0))>& {
+__device__ __forceinline__ auto share_of(int items, Range range, int cta, int start = 0, bool whole = false) -> const Share<decltype(range(0))>& {
   using Item = decltype(range(0));
   const auto units = [&](const Item& x) { return x.tiles > 0 ? x.tiles + start : 0; };
   __shared__ long long s_warp[THREADS / 32];
   __shared__ Share<Item> s_sh;
+  if (whole) {
+    if (threadIdx.x == 0) {
+      const Item x = range(cta);
+      s_sh.total = s_sh.end = x.tiles;
+      s_sh.begin = s_sh.item_base = 0;
+      s_sh.grid = gridDim.x;
+      s_sh.start = 0;
+      s_sh.item = cta;
+      s_sh.first = x;
+    }
+    __syncthreads();
+    return s_sh;
+  }
   const int per = (items + THREADS - 1) / THREADS;
   const int i0 = min(items, static_cast<int>(threadIdx.x) * per), i1 = min(items, i0 + per);
   long long sum = 0;
@@ -395,6 +410,7 @@ __device__ __forceinline__ bool elect_one() {
 cudaError_t launch_attend_rows(const AttnArgs& a, int grid, int cluster, cudaStream_t st);
 int attend_rows_cluster(long long items, long long tiles, bool window, int grid);
 int attend_rows_tile();
+bool attend_tile_whole(long long items, long long tiles, bool split, int grid);
 int attend_tile_rows(bool split);  // rows of a K/V stage, and of a box of its maps
 int attend_rows_ctas_per_sm();
 // tcgen05 tiles: two blocks of `block` query rows per item that share the cached rows, or, with

@@ -32,6 +32,7 @@ struct AttnPlan {
   bool tiled = false, split = false;
   int block = 0;                 // tiled: query rows per block, whole tokens of the group
   int cluster = 0;               // not tiled: attend_rows_cluster
+  bool whole = false;            // tiled: attend_tile_whole
   int kb = 1, kb_sink = -1;      // tiled, with weights: blocks of 256 cached rows (attend.cuh)
   size_t rec = 0, ml = 0, o = 0, lse2 = 0, wpart = 0, logits = 0, total = 0;
   long long logit_stride = 0;
@@ -86,6 +87,13 @@ int plan_attn(const kvsel_attn_params* p, bool with_acc, AttnPlan& pl) {
     pl.grid = sms;
   }
   pl.rt = (R + pl.tr - 1) / pl.tr;
+  if (pl.tiled) {
+    // tiles of 128 rows that an item may have
+    long long tiles = (static_cast<long long>(p->max_len) + 127) / 128;
+    if (p->window > 0)
+      tiles = std::min(tiles, (p->n_sink + 127ll) / 128 + (static_cast<long long>(p->window) + pl.tr / p->group + 317) / 128);
+    pl.whole = attend_tile_whole(static_cast<long long>(p->batch) * p->h_kv * pl.rt, tiles, pl.split, pl.grid);
+  }
   // behind the status word and the counters that the scoring calls keep in a shared workspace
   size_t off = kStatusBytes + kCounterBytes;
   pl.rec = off;
@@ -295,6 +303,7 @@ int kvsel_attend(const kvsel_attn_params* p, const void* q, const kvsel_kv* kv, 
   while (a.src.paged && (1 << a.page_shift) < a.src.block_size) ++a.page_shift;
   a.tr = pl.tr;
   a.rt = pl.rt;
+  a.whole = pl.whole;
   a.part_o = reinterpret_cast<float*>(wsb + pl.o);
   a.part_ml = reinterpret_cast<float2*>(wsb + pl.ml);
   a.rec = reinterpret_cast<int2*>(wsb + pl.rec);
