@@ -3,11 +3,11 @@
 // CTA x + c: unnormalised rows, their references (log2 units) and sums.  The loads of a row's
 // pieces do not wait for one another; pieces are added in a fixed order, so results repeat.
 //
-// Bound: latency (the pieces are in L2).  Few items (by_item): a CTA per row, eight warps over its
-// pieces, of which there may be one per CTA of the grid.  Many items, of two or three pieces: a
-// warp per two rows (one row at a time took 2 to 3 us longer), five CTAs for each CTA before; those
-// whose number starts no shared item end at once.
-// (Joining in the CTA that finishes an item's last piece, without a second launch, took 38 us
+// Few rows of many pieces (by_item): a CTA per row, eight warps over its pieces, of which there may
+// be one per CTA of the grid.  Bound: latency.  Otherwise eight rows per warp, and a thread for a
+// row's reference, sum and place: a warp for each row spent 290 instructions on it, nearly all of
+// them the same in every lane, and took 18 us for 38,000 rows; now 8.  Bound: the pieces' bytes, from
+// L2.  (Joining in the CTA that finishes an item's last piece, without a second launch, took 38 us
 // longer for 73 pieces of 7 rows.)
 #include <algorithm>
 
@@ -114,25 +114,61 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_items_kernel(const AttnA
   finish(a, x, r, p);
 }
 
-// grid (CTA of the kernel before, share of its rows): all CTAs resident at once, two rows per warp at a time
-constexpr int kShares = 5;
-__global__ void __launch_bounds__(kJoinWarps * 32, kShares) join_ctas_kernel(const AttnArgs a) {
+// grid (CTA of the kernel before, share of its rows): eight rows per warp.  Lane l looks after row l & 7:
+// its reference, sum and place; the rows themselves are read by the whole warp.
+constexpr int kRows = 8;
+__global__ void __launch_bounds__(kJoinWarps * 32, 3) join_ctas_kernel(const AttnArgs a) {
   const int2 rec = a.rec[blockIdx.x];
   if (rec.x < 0) return;
   const JoinItem x = join_item(a, rec.x, blockIdx.x, rec.y);
-  constexpr int kStep = kShares * kJoinWarps;
-  for (int r = blockIdx.y * kJoinWarps + warp_id(); r < x.rows; r += 2 * kStep) {
-    Joined p = nothing(), p2 = nothing();
-    for (int c = 0; c < x.pieces; c += 2) {
-      float2 ml[4];
-      float4 z[4];
-      fetch<2>(a, x, r, c, 1, ml, z);
-      fetch<2>(a, x, r + kStep, c, 1, ml + 2, z + 2);
-      add_pieces<2>(p, ml, z);
-      add_pieces<2>(p2, ml + 2, z + 2);
+  const int lane = lane_id(), r0 = (blockIdx.y * (blockDim.x >> 5) + warp_id()) * kRows, r = r0 + (lane & 7);
+  if (r0 >= x.rows) return;
+  auto place = [&](int c) { return (c == 0 ? 2ll * x.leader + 1 : 2ll * (x.leader + c)) * a.tr; };
+  auto stats = [&](int c) { return r < x.rows && c < x.pieces ? a.part_ml[place(c) + r] : make_float2(-INFINITY, 0.f); };
+  float M = -INFINITY, L = 0.f;
+  for (int c = 0; c < x.pieces; c += 4) {
+    float2 ml[4];
+    float m2 = M;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) ml[i] = stats(c + i);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m2 = fmaxf(m2, ml[i].x);
+    L *= M == -INFINITY ? 0.f : exp2f(M - m2);
+    M = m2;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) L += ml[i].x == -INFINITY ? 0.f : exp2f(ml[i].x - M) * ml[i].y;
+  }
+  const float inv = L > 0.f ? 1.f / L : 0.f;
+  const int rr = x.rt * a.tr + r;
+  long long dst = 0;
+  if (r < x.rows) {
+    dst = out_row(a, x.b, x.h, rr) - a.out;
+    if (lane < kRows) write_lse(a, x.b, x.h, rr, M, L);
+  }
+  float4 y[kRows];
+#pragma unroll
+  for (int k = 0; k < kRows; ++k) y[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int c = 0; c < x.pieces; ++c) {
+    const float m = stats(c).x;
+    const float w = m == -INFINITY ? 0.f : exp2f(m - M) * inv;
+    const float4* src = reinterpret_cast<const float4*>(a.part_o + (place(c) + r0) * kHeadDim) + lane;
+    float4 z[kRows];
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) z[k] = r0 + k < x.rows ? src[k * (kHeadDim / 4)] : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+      const float f = __shfl_sync(0xffffffffu, w, k);
+      y[k].x += f * z[k].x;
+      y[k].y += f * z[k].y;
+      y[k].z += f * z[k].z;
+      y[k].w += f * z[k].w;
     }
-    finish(a, x, r, p);
-    if (r + kStep < x.rows) finish(a, x, r + kStep, p2);
+  }
+#pragma unroll
+  for (int k = 0; k < kRows; ++k) {
+    const long long d = __shfl_sync(0xffffffffu, dst, k);
+    if (r0 + k < x.rows)
+      *reinterpret_cast<uint2*>(a.out + d + lane * 4) = make_uint2(pack_bf16(y[k].x, y[k].y), pack_bf16(y[k].z, y[k].w));
   }
 }
 
@@ -140,10 +176,12 @@ __global__ void __launch_bounds__(kJoinWarps * 32, kShares) join_ctas_kernel(con
 
 cudaError_t launch_attend_join(const AttnArgs& a, int grid, cudaStream_t st) {
   const int rows = static_cast<int>(std::min<long long>(a.tr, static_cast<long long>(a.m) * a.G));
-  if (a.by_item)
+  if (a.by_item) {
     join_items_kernel<<<dim3(a.B * a.H * a.rt, rows), kJoinWarps * 32, 0, st>>>(a);
-  else
-    join_ctas_kernel<<<dim3(grid, kShares), kJoinWarps * 32, 0, st>>>(a);
+  } else {
+    const int warps = (rows + kRows - 1) / kRows, per = std::min(warps, kJoinWarps);
+    join_ctas_kernel<<<dim3(grid, (warps + per - 1) / per), per * 32, 0, st>>>(a);
+  }
   note_launch();
   return cudaGetLastError();
 }
