@@ -590,17 +590,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 int attend_tile_rows(bool split) { return split ? 64 : 128; }
 
 // Whether every item, of `tiles` tiles at most, goes to one CTA.  The plan, pieces of two kinds and the
-// join cost 5 us with one block of query rows and 16 with two, and the work is cut over all CTAs;
+// join cost 5 us with one block of query rows and 8 with two, and the work is cut over all CTAs;
 // whole items take 2.45 us per two tiles (1.63 per tile), however few there are.  The rule follows
 // these, with three quarters of the items counted (caches of one batch differ in length, and only a
-// bound is known here).  Measured, group 4, plan and whole items, 6 tokens: 8 items of 512 rows 13.2
-// and 12.8 us, of 1024 13.7 and 17.6; 128 items of 512 27.0 and 13.5, of 2048 43.2 and 29.4; 512 tokens:
-// 64 items of 768 rows 32.1 and 19.2, of 2048 39.5 and 35.4, of 4096 50.4 and 61.6.
+// bound is known here).  Measured, group 4, plan and whole items, 6 tokens: 8 items of 256 rows 12.9
+// and 10.4 us, of 1024 13.4 and 17.6; 128 items of 1024 29.2 and 18.2, of 3000 47 and 39.7; 512 tokens:
+// 64 items of 768 rows 22.1 and 19.2, of 1536 26.1 and 29.1; 128 items of 1536 36.6 and 29.5.
 bool attend_tile_whole(long long items, long long tiles, bool split, int grid) {
   if (items > grid) return false;
   const long long serial = split ? (tiles + 1) / 2 : tiles;
   return split ? serial <= 12 && serial * (100 - items * 7 / 10) <= 240
-               : serial <= 32 && serial * (100 - items * 6 / 10) <= 1000;
+               : serial <= 32 && serial * (100 - items * 6 / 10) <= 550;
 }
 
 cudaError_t launch_attend_tile(const AttnArgs& a, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
