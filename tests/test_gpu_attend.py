@@ -140,6 +140,20 @@ def test_work_cut_over_many_blocks():
     # room for far more rows, and tokens, than there are: segments that end in many empty items
     run(B=40, H=4, G=4, m=40, lens=40 + np.arange(40) * 9, pad_rows=20000, layout="paged", block=64, seed=7)
     run(B=5, H=2, G=4, m=700, new=[0, 3, 700, 1, 90], lens=[0, 3, 900, 5000, 90], seed=8)
+    # items of many pieces, few rows and many, and two pieces
+    run(H=2, G=5, m=20, lens=12000, seed=9)
+    run(H=3, G=4, m=130, lens=6000, seed=10)
+    run(B=2, H=8, G=3, m=150, lens=[2500, 2300], layout="paged", block=32, seed=11)
+
+
+@pytest.mark.parametrize("pad_rows", [0, 9000])
+@pytest.mark.parametrize("m,G", [(6, 4), (32, 4), (70, 3), (300, 2)])
+def test_few_rows_under_a_chunk(m, G, pad_rows):
+    # the same calls where an item belongs to one block, and where the whole grid shares the work
+    kw = dict(m=m, G=G, layout="paged", block=16, pad_rows=pad_rows, seed=m)
+    run(B=4, H=2, new=[0, 1, m, m - 1], lens=[0, 1, m + 190, 513], **kw)
+    run(B=2, H=2, lens=[m + 70, m], window=40, n_sink=3, **kw)
+    run(B=2, H=3, lens=[130, m - 3], causal=False, per_head=False, **kw)
 
 
 def test_weights_add_up_over_calls_and_results_repeat():
