@@ -274,12 +274,18 @@ def _current_stream() -> int:
     return raw(torch.cuda.current_device())
 
 
-def _here(ws, where: str) -> None:
-    """The call runs on the current device; a workspace elsewhere (and what belongs to it) is refused."""
+def _place(ws, stream, where: str) -> int:
+    """Handle of the stream of a call with workspace ws.  The call runs on the current device; a workspace
+    elsewhere (and what belongs to it) is refused."""
     import torch
 
-    if ws.get_device() != torch.cuda.current_device():
-        raise KvselError(KVSEL_EINVAL, f"{where}: workspace on {ws.device}, current device cuda:{torch.cuda.current_device()}")
+    dev = torch.cuda.current_device()
+    if ws.get_device() != dev:
+        raise KvselError(KVSEL_EINVAL, f"{where}: workspace on {ws.device}, current device cuda:{dev}")
+    if stream is not None:
+        return stream if isinstance(stream, int) else stream.cuda_stream
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(dev) if raw else torch.cuda.current_stream().cuda_stream
 
 
 def _check(rc: int, where: str) -> None:
@@ -443,9 +449,9 @@ def kvsel_attend_workspace_size(params: kvsel_attn_params, acc: bool = False) ->
 def kvsel_attend(params: kvsel_attn_params, q, kv: kvsel_kv, lens, out, ws, new_lens=None, offsets=None, lse=None,
                  acc=None, stream=None) -> None:
     """Attention of new tokens over the cache; with acc every cached row's weight is added."""
-    _here(ws, "kvsel_attend")
+    st = _place(ws, stream, "kvsel_attend")
     rc = (_lib or load()).kvsel_attend(params, _ptr(q), kv, _ptr(lens), _ptr(new_lens), _ptr(offsets), _ptr(out),
-                                       _ptr(lse), _ptr(acc), ws.data_ptr(), ws.nbytes, _stream(stream))
+                                       _ptr(lse), _ptr(acc), ws.data_ptr(), ws.nbytes, st)
     if rc:
         _check(rc, "kvsel_attend")
 
@@ -460,9 +466,9 @@ def kvsel_evict_append_workspace_size(params: kvsel_evict_params) -> int:
 def kvsel_evict_append(params: kvsel_evict_params, kv: kvsel_kv, lens, seen, pos, acc, k_new, v_new, ws,
                        new_lens=None, stream=None) -> None:
     """Evict by accumulated weight until the new rows fit the budget, then append them."""
-    _here(ws, "kvsel_evict_append")
+    st = _place(ws, stream, "kvsel_evict_append")
     rc = (_lib or load()).kvsel_evict_append(params, kv, _ptr(lens), _ptr(seen), _ptr(pos), _ptr(acc), _ptr(k_new),
-                                             _ptr(v_new), _ptr(new_lens), ws.data_ptr(), ws.nbytes, _stream(stream))
+                                             _ptr(v_new), _ptr(new_lens), ws.data_ptr(), ws.nbytes, st)
     if rc:
         _check(rc, "kvsel_evict_append")
 

@@ -463,14 +463,14 @@ int clusters_at_once(int c) {
 // 5.9, of 2048 30.0 and 25.0; 64 items with a window of 4096 29.7 and 25.7.  More clusters than
 // fit at once lose (512 items of 256 rows 17.9 and 35; 40 clusters of seven 12.4 and 16.7).
 int attend_rows_cluster(long long items, long long tiles, bool window, int grid) {
-  long long serial = tiles + 1;
-  int best = 0;
-  for (int c = 1; c <= kMaxCluster && items * c <= grid; ++c)
-    if ((tiles + c - 1) / c < serial && items <= clusters_at_once(c)) {
-      serial = (tiles + c - 1) / c;
-      best = c;
-    }
-  return best && serial <= 3 + items * tiles / (window ? 156 : 312) ? best : 0;
+  const int bound = static_cast<int>(3 + items * tiles / (window ? 156 : 312)), t = static_cast<int>(tiles);
+  for (int c = static_cast<int>(std::min<long long>(kMaxCluster, grid / items)); c >= 1; --c) {
+    const int serial = (t + c - 1) / c;
+    if (serial > bound) return 0;
+    // (as few CTAs as do it)
+    if ((c == 1 || (t + c - 2) / (c - 1) > serial) && items <= clusters_at_once(c)) return c;
+  }
+  return 0;
 }
 
 cudaError_t launch_attend_rows(const AttnArgs& a, int grid, int cluster, cudaStream_t st) {
