@@ -450,7 +450,7 @@ typedef struct kvsel_attn_params {
  * passes acc).  Tens of MB at most, but with acc and n_new * group <= 16 also
  * 4 * batch * h_kv * n_new * group * max_len bytes (the logits), so keep max_len near the real
  * lengths (with acc and more rows than 16, batch * h_kv * max_len / 256 blocks of cached rows are
- * planned, 2^31 - 1 at most).  Host-only. */
+ * planned, 2^30 at most).  Host-only. */
 int kvsel_attend_workspace_size(const kvsel_attn_params* p, int with_acc, size_t* bytes);
 
 /* out[b][hq][t] = sum_j w_j v_j with w = softmax_j(scale * <q[b][hq][t], k_j>) over the rows that

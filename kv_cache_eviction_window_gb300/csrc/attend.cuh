@@ -189,7 +189,8 @@ struct Share {
 // range(i): the range of item i, with its number of tiles.  The result stays in shared memory; kept in
 // registers through attend_tile_kernel it costs the softmax warps' inner loop 2% (spills).
 template <int THREADS, bool SKIP = true, class Range>
-__device__ __forceinline__ auto share_of(int items, Range range, int cta, int start = 0, bool whole = false) -> const Share<decltype(range(0))>& {
+__device__ __forceinline__ auto share_of(int items, Range range, int cta, int start = 0, bool whole = false)
+    -> const Share<decltype(range(0))>& {
   using Item = decltype(range(0));
   const auto units = [&](const Item& x) { return x.tiles > 0 ? x.tiles + start : 0; };
   __shared__ long long s_warp[THREADS / 32];
@@ -276,7 +277,7 @@ __device__ __forceinline__ int last_cta(const Share<Item>& sh, long long e) {
   return static_cast<int>((e * sh.grid - 1) / sh.total);
 }
 
-// Records for attend_join_kernel: at a kernel's start, and by the CTA that works on an item's first tile
+// Records for the join: at a kernel's start, and by the CTA that works on an item's first tile
 // (`follow` CTAs work on the others).
 __device__ __forceinline__ void rec_clear(const AttnArgs& a) {
   if (threadIdx.x == 0 && !a.by_item) a.rec[blockIdx.x] = make_int2(-1, 0);

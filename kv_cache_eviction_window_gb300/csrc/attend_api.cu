@@ -111,7 +111,7 @@ int plan_attn(const kvsel_attn_params* p, bool with_acc, AttnPlan& pl) {
       const long long part = sinks + (static_cast<long long>(p->window) + p->n_new + 254) / 256 + 1;
       const bool few = p->causal && p->window > 0 && part < full;
       const long long kb = few ? part : full;
-      if (kb * p->batch * p->h_kv > (1ll << 31) - 1) return KVSEL_EUNSUPPORTED;
+      if (kb * p->batch * p->h_kv > 1ll << 30) return KVSEL_EUNSUPPORTED;
       pl.kb = static_cast<int>(kb);
       pl.kb_sink = few ? static_cast<int>(sinks) : -1;
       pl.wpart = off;

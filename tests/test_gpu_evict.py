@@ -186,6 +186,20 @@ def test_caches_beyond_shared_memory(n, m):
     c.check()
 
 
+@pytest.mark.parametrize("ties", [False, True])
+@pytest.mark.parametrize("B,H,n,m,budget", [
+    (1, 1, 60000, 5, 59980), (1, 2, 900, 40, 890), (2, 2, 300, 64, 300), (2, 2, 300, 65, 300), (3, 1, 70, 0, 10),
+    (20, 8, 120, 30, 110), (19, 8, 90, 6, 90)])
+def test_few_rows_to_move(B, H, n, m, budget, ties):
+    # by the block that selects them, or by a second launch; caches that are not full among them
+    c = Cache(B=B, H=H, capacity=n, lens=n - np.arange(B * H).reshape(B, H) % 7, m=m, seed=n + m, ties=ties)
+    g, ws = CH.rng(1), None
+    for _ in range(2):
+        ws = c.step(g, budget=budget, n_sink=2, n_recent=min(60, budget // 3), new=m - np.arange(B) % (m + 1), ws=ws)
+    assert CH.status(ws) == 0
+    c.check()
+
+
 @pytest.mark.parametrize("m", [1, 30])
 def test_a_captured_call_follows_the_lengths(m):
     import torch
