@@ -70,15 +70,24 @@ int plan_attn(const kvsel_attn_params* p, bool with_acc, AttnPlan& pl) {
   int sms = 0;
   if ((rc = device_sms(&sms))) return rc;
   const int R = p->n_new * p->group;
-  if (R <= attend_rows_tile()) {
-    // single tokens and the like: HBM-bound, 16 query rows per item
-    pl.tr = attend_rows_tile();
-    pl.grid = sms * attend_rows_ctas_per_sm();
+  const int tr = attend_rows_tile(), rt = (R + tr - 1) / tr;
+  // up to 32 rows of few tiles go as two items (6 tokens of 8 segments of 512 rows, group 4: 6.5 us, as
+  // chunks 12.7; 20 rows of 32 segments of 4096: 22.5 and 25.4; a CTA per item loses from 256 rows on).
+  // (The weights' logits are kept for one item per segment.)
+  if (rt == 1 || (rt == 2 && !with_acc)) {
     // tiles of 64 rows that an item may have: with a window some before it and some of the first rows
     long long tiles = (static_cast<long long>(p->max_len) + 63) / 64;
     const long long seen = (p->n_sink + 63ll) / 64 + (static_cast<long long>(p->window) + p->n_new + 126) / 64;
     const bool window = p->window > 0 && seen < tiles;
-    pl.cluster = attend_rows_cluster(static_cast<long long>(p->batch) * p->h_kv, window ? seen : tiles, window, pl.grid);
+    if (window) tiles = seen;
+    pl.cluster = attend_rows_cluster(static_cast<long long>(p->batch) * p->h_kv * rt, tiles, window,
+                                     sms * attend_rows_ctas_per_sm());
+    if (rt == 2 && tiles > (pl.cluster == 1 ? 2 : 16 * pl.cluster)) pl.cluster = 0;
+  }
+  if (rt == 1 || pl.cluster) {
+    // single tokens and the like: HBM-bound, 16 query rows per item
+    pl.tr = tr;
+    pl.grid = sms * attend_rows_ctas_per_sm();
   } else {
     pl.tiled = true;
     pl.block = 128 / p->group * p->group;
