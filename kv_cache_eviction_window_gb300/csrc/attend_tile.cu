@@ -2,7 +2,7 @@
 //   S = Q K^T (fp32 in TMEM), P = exp2(s2 * S - ref) rounded to bf16 into TMEM, O += P V.
 // The reference of a row stays within kSlack = 16 of its running maximum (log2 units), so O, which
 // stays in TMEM, is rescaled only when the maximum has grown by more; row sums are fp32 over the
-// unrounded weights.  P is rounded to bf16 (2^-9 relative at most per weight): V is bf16 and
+// unrounded weights.  P is rounded to bf16 (2^-8 relative at most per weight): V is bf16 and
 // both operands of the product need one type.
 //
 // A CTA works on two streams of 128 query rows.  Each has O in TMEM (128 columns) and two S
