@@ -72,6 +72,14 @@ struct AttnArgs {
   WaitCtl wc;
 };
 
+// Whether rows [row0, row0 + n) lie in a packed cache of n_rows rows, whatever the caller's row0 is (the
+// sum row0 + n could pass 64 bits).
+__host__ __device__ constexpr bool segment_fits(long long row0, int n, long long n_rows) {
+  return row0 >= 0 && row0 <= n_rows - n;
+}
+static_assert(segment_fits(0, 8, 8) && segment_fits(8, 0, 8) && !segment_fits(1, 8, 8) && !segment_fits(0, 9, 8));
+static_assert(!segment_fits(-1, 0, 8) && !segment_fits(0x7FFFFFFFFFFFFFFFll, 1, 8));
+
 // Rows of segment (b, h) and new tokens of request b, as the caller's device arrays give them;
 // values out of range are flagged and clamped.
 struct SegLen {
@@ -88,7 +96,7 @@ __device__ __forceinline__ SegLen seg_len(const AttnArgs& a, int b, int h) {
   s.row0 = 0;
   if (a.offsets) {
     s.row0 = __ldg(a.offsets + b * a.H + h);
-    if (s.row0 < 0 || s.row0 + s.n > a.n_rows) {
+    if (!segment_fits(s.row0, s.n, a.n_rows)) {
       bad = true;
       s.n = 0;
       s.row0 = 0;
