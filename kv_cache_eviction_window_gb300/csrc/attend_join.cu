@@ -43,6 +43,13 @@ __device__ __forceinline__ void add_pieces(Joined& p, const float2* ml, const fl
     p.y.w += f * z[i].w;
   }
 }
+// Whether an item's pieces lie in CTAs of the grid, whatever the record holds (the sum of its numbers could
+// pass 32 bits).
+__host__ __device__ constexpr bool pieces_fit(int leader, int follow, int grid) {
+  return leader >= 0 && leader < grid && follow >= 0 && follow < grid - leader;
+}
+static_assert(pieces_fit(0, 0, 1) && pieces_fit(1, 2, 4) && !pieces_fit(1, 3, 4) && !pieces_fit(4, 0, 4));
+static_assert(!pieces_fit(-1, 0, 4) && !pieces_fit(0, -1, 4) && !pieces_fit(3, 0x7FFFFFFF, 4));
 struct JoinItem {
   int b, h, rt, rows, leader, pieces;
 };
@@ -90,7 +97,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_items_kernel(const AttnA
   const int2 rec = a.rec[blockIdx.x];
   // (nor one whose kernel gave up on a wait: what lies there then is not followed)
   const JoinItem x = join_item(a, blockIdx.x, rec.x, rec.y);
-  if (r >= x.rows || rec.x < 0 || rec.y < 0 || rec.x + rec.y >= a.grid || rec.x >= a.grid) return;
+  if (r >= x.rows || !pieces_fit(rec.x, rec.y, a.grid)) return;
   Joined p = nothing();
   for (int c = warp; c < x.pieces; c += 8 * kJoinWarps) {
     float2 ml[8];
