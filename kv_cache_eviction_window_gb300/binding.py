@@ -219,8 +219,38 @@ def make_evict_params(*, h_kv: int, batch: int, capacity: int, budget: int, n_ne
                               *[int(x) for x in new_strides])
 
 
+def _refuse(where: str, why: str) -> None:
+    raise KvselError(KVSEL_EINVAL, f"{where}: {why}")
+
+
+def _is_bf16(t) -> bool:
+    """bf16, or its bit patterns in 16-bit integers."""
+    return t.element_size() == 2 and (not t.is_floating_point() or str(t.dtype) == "torch.bfloat16")
+
+
+def _same_rows(where: str, k, v) -> None:
+    """A view has one set of strides and sizes, taken from k: refuse a v that they do not describe (a v that is
+    absent or a bare address is the caller's own matter)."""
+    if v is None or isinstance(v, int):
+        v = k
+    for t in (k, v):
+        if not _is_bf16(t):
+            _refuse(where, f"rows of {t.dtype}, not bf16")
+        if t.shape[-1] > 1 and t.stride(-1) != 1:
+            _refuse(where, f"columns {t.stride(-1)} elements apart")
+    if v.device != k.device or v.shape[-1] != k.shape[-1]:
+        _refuse(where, f"k {tuple(k.shape)} on {k.device}, v {tuple(v.shape)} on {v.device}")
+    for i in range(1, max(k.dim(), v.dim()) + 1):
+        nk, nv = (t.shape[-i] if i <= t.dim() else 1 for t in (k, v))
+        if nv < nk or (nk > 1 and v.stride(-i) != k.stride(-i)):
+            _refuse(where, f"k {tuple(k.shape)} with strides {k.stride()}, v {tuple(v.shape)} with strides {v.stride()}")
+
+
 def make_kv_contiguous(k, v, *, stride_req: int = 0) -> kvsel_kv:
-    """K/V tensors [H][n][d] (one request) or [B][H][n][d] (bf16, CUDA)."""
+    """K/V tensors [H][n][d] (one request) or [B][H][n][d] (bf16, CUDA), of the same strides."""
+    if k.dim() < 3:
+        _refuse("make_kv_contiguous", f"k {tuple(k.shape)}")
+    _same_rows("make_kv_contiguous", k, v)
     kv = kvsel_kv()
     kv.k, kv.v = _ptr(k), _ptr(v)
     kv.layout = LAYOUT_CONTIGUOUS
@@ -231,7 +261,13 @@ def make_kv_contiguous(k, v, *, stride_req: int = 0) -> kvsel_kv:
 
 
 def make_kv_paged(k_pool, v_pool, block_table) -> kvsel_kv:
-    """Pools [num_blocks][block][H][d] bf16 and block_table [B][max_blocks] int32 (CUDA)."""
+    """Pools [num_blocks][block][H][d] bf16 and block_table [B][max_blocks] int32 (CUDA), all dense."""
+    _same_rows("make_kv_paged", k_pool, v_pool)
+    if not k_pool.is_contiguous():   # (v_pool has its strides)
+        _refuse("make_kv_paged", f"a pool with strides {k_pool.stride()}")
+    t = block_table
+    if t.dim() != 2 or t.element_size() != 4 or t.is_floating_point() or not t.is_contiguous():
+        _refuse("make_kv_paged", f"block table {tuple(t.shape)} of {t.dtype} with strides {t.stride()}")
     kv = kvsel_kv()
     kv.k, kv.v = _ptr(k_pool), _ptr(v_pool)
     kv.layout = LAYOUT_PAGED
@@ -244,7 +280,10 @@ def make_kv_paged(k_pool, v_pool, block_table) -> kvsel_kv:
 
 def make_kv_packed(k, v) -> kvsel_kv:
     """Rows [n_rows][d] bf16 (CUDA) of segments placed by an offsets array, as kvsel_compact
-    writes them (kvsel_attend only)."""
+    writes them (kvsel_attend only), of the same stride."""
+    if k.dim() != 2:
+        _refuse("make_kv_packed", f"k {tuple(k.shape)}")
+    _same_rows("make_kv_packed", k, v)
     kv = kvsel_kv()
     kv.k, kv.v = _ptr(k), _ptr(v)
     kv.layout = LAYOUT_PACKED
