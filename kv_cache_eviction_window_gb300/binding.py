@@ -8,6 +8,7 @@ raises ``KvselUnavailable``.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional, Sequence
 
@@ -78,7 +79,18 @@ class kvsel_kv(ctypes.Structure):
     ]
 
 
-class kvsel_attn_params(ctypes.Structure):
+class _RowParams(ctypes.Structure):
+    """Parameters that describe tensors of bf16 rows.  rows: what those tensors have to be (_rows), worked out
+    by the first call with the present values."""
+    rows = None
+
+    def __setattr__(self, name, value):
+        super().__setattr__(name, value)
+        if name != "rows":
+            self.rows = None
+
+
+class kvsel_attn_params(_RowParams):
     _fields_ = [
         ("h_kv", ctypes.c_int32), ("group", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("batch", ctypes.c_int32),
         ("n_new", ctypes.c_int32), ("max_len", ctypes.c_int32), ("causal", ctypes.c_int32), ("window", ctypes.c_int32),
@@ -89,7 +101,7 @@ class kvsel_attn_params(ctypes.Structure):
     ]
 
 
-class kvsel_evict_params(ctypes.Structure):
+class kvsel_evict_params(_RowParams):
     _fields_ = [
         ("h_kv", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("batch", ctypes.c_int32), ("n_new", ctypes.c_int32),
         ("capacity", ctypes.c_int32), ("budget", ctypes.c_int32), ("n_sink", ctypes.c_int32),
@@ -225,7 +237,9 @@ def _refuse(where: str, why: str) -> None:
 
 def _is_bf16(t) -> bool:
     """bf16, or its bit patterns in 16-bit integers."""
-    return t.element_size() == 2 and (not t.is_floating_point() or str(t.dtype) == "torch.bfloat16")
+    import torch
+
+    return t.dtype is torch.bfloat16 or (t.element_size() == 2 and not t.is_floating_point())
 
 
 def _same_rows(where: str, k, v) -> None:
@@ -295,6 +309,29 @@ def _ptr(t) -> Optional[int]:
     return t if t is None or isinstance(t, int) else t.data_ptr()
 
 
+def _rows(batch: int, heads: int, toks: int, req: int, head: int, tok: int):
+    """Of bf16 rows [batch][heads][toks][128] with these strides (all zero: dense): their type, whether they
+    are dense, and the bytes from the first element to the end of the last."""
+    import torch
+
+    if req or head or tok:
+        return torch.bfloat16, False, 2 * ((batch - 1) * req + (heads - 1) * head + (toks - 1) * tok + 128)
+    return torch.bfloat16, True, 256 * batch * heads * toks
+
+
+def _row_ptr(t, rows, where: str) -> Optional[int]:
+    """Address of a tensor that has to be as `rows` says, else refused (an address is the caller's own matter)."""
+    if t is None or isinstance(t, int):
+        return t
+    dtype, dense, need = rows
+    holds = t.is_contiguous() and t.nbytes >= need
+    if not holds and not dense:
+        holds = t.untyped_storage().nbytes() - 2 * t.storage_offset() >= need and t.stride()[-1] == 1
+    if not holds or (t.dtype is not dtype and not _is_bf16(t)):
+        _refuse(where, f"{tuple(t.shape)} of {t.dtype} with strides {t.stride()} for {need} bytes of {'dense ' * dense}rows")
+    return t.data_ptr()
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
         return _current_stream()
@@ -313,18 +350,27 @@ def _current_stream() -> int:
     return raw(torch.cuda.current_device())
 
 
+@functools.lru_cache(maxsize=None)
+def _cuda():
+    """torch's getters of the current device and of a device's current stream (a handle); the raw ones cost a
+    third of torch.cuda's."""
+    import torch
+
+    torch.cuda.init()
+    return (getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device),
+            getattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: torch.cuda.current_stream(dev).cuda_stream))
+
+
 def _place(ws, stream, where: str) -> int:
     """Handle of the stream of a call with workspace ws.  The call runs on the current device; a workspace
     elsewhere (and what belongs to it) is refused."""
-    import torch
-
-    dev = torch.cuda.current_device()
+    device, current = _cuda()
+    dev = device()
     if ws.get_device() != dev:
         raise KvselError(KVSEL_EINVAL, f"{where}: workspace on {ws.device}, current device cuda:{dev}")
     if stream is not None:
         return stream if isinstance(stream, int) else stream.cuda_stream
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    return raw(dev) if raw else torch.cuda.current_stream().cuda_stream
+    return current(dev)
 
 
 def _check(rc: int, where: str) -> None:
@@ -488,9 +534,15 @@ def kvsel_attend_workspace_size(params: kvsel_attn_params, acc: bool = False) ->
 def kvsel_attend(params: kvsel_attn_params, q, kv: kvsel_kv, lens, out, ws, new_lens=None, offsets=None, lse=None,
                  acc=None, stream=None) -> None:
     """Attention of new tokens over the cache; with acc every cached row's weight is added."""
+    if params.rows is None:
+        p, B, H = params, params.batch, params.h_kv * params.group
+        p.rows = (_rows(B, H, p.n_new, p.q_stride_req, p.q_stride_head, p.q_stride_tok),
+                  _rows(B, H, p.n_new, p.o_stride_req, p.o_stride_head, p.o_stride_tok))
+    q_rows, o_rows = params.rows
+    q, out = _row_ptr(q, q_rows, "kvsel_attend: q"), _row_ptr(out, o_rows, "kvsel_attend: out")
     st = _place(ws, stream, "kvsel_attend")
-    rc = (_lib or load()).kvsel_attend(params, _ptr(q), kv, _ptr(lens), _ptr(new_lens), _ptr(offsets), _ptr(out),
-                                       _ptr(lse), _ptr(acc), ws.data_ptr(), ws.nbytes, st)
+    rc = (_lib or load()).kvsel_attend(params, q, kv, _ptr(lens), _ptr(new_lens), _ptr(offsets), out, _ptr(lse),
+                                       _ptr(acc), ws.data_ptr(), ws.nbytes, st)
     if rc:
         _check(rc, "kvsel_attend")
 
@@ -505,9 +557,14 @@ def kvsel_evict_append_workspace_size(params: kvsel_evict_params) -> int:
 def kvsel_evict_append(params: kvsel_evict_params, kv: kvsel_kv, lens, seen, pos, acc, k_new, v_new, ws,
                        new_lens=None, stream=None) -> None:
     """Evict by accumulated weight until the new rows fit the budget, then append them."""
+    if params.rows is None:
+        p = params
+        p.rows = _rows(p.batch, p.h_kv, p.n_new, p.new_stride_req, p.new_stride_head, p.new_stride_tok)
+    k_new = _row_ptr(k_new, params.rows, "kvsel_evict_append: k_new")
+    v_new = _row_ptr(v_new, params.rows, "kvsel_evict_append: v_new")
     st = _place(ws, stream, "kvsel_evict_append")
-    rc = (_lib or load()).kvsel_evict_append(params, kv, _ptr(lens), _ptr(seen), _ptr(pos), _ptr(acc), _ptr(k_new),
-                                             _ptr(v_new), _ptr(new_lens), ws.data_ptr(), ws.nbytes, st)
+    rc = (_lib or load()).kvsel_evict_append(params, kv, _ptr(lens), _ptr(seen), _ptr(pos), _ptr(acc), k_new, v_new,
+                                             _ptr(new_lens), ws.data_ptr(), ws.nbytes, st)
     if rc:
         _check(rc, "kvsel_evict_append")
 
