@@ -182,6 +182,54 @@ class Case:
                     assert np.all(got[b, h, n:] == 0.0)
 
 
+def token_tolerance(o, n):
+    """How far a row of the kernel of few rows may be from the oracle's o (n cached rows).
+
+    A logit is off by e = (D + 4) 2^-23 max sum |q||k| scale as above; in the exponent's argument it is rounded
+    twice, |argument| <= 3 abs_logit in log2 units, and ex2.approx is off by 2^-22: weights are off by 2 e'
+    (over their sum).  They enter the second product as a bf16 part and a bf16 remainder, each off by at most
+    half a step, 2^-8: 2^-16 in all.  A warp adds two products for each of its at most n / 4 + 16 rows, and as
+    many weights into the sum; rescaling and joining parts add less than a hundred roundings more: (n + 128)
+    2^-23.  The result is rounded once to bf16, 2^-8."""
+    e = (D + 4) * 2.0 ** -23 * o["abs_logit"] + (3 * o["abs_logit"] + 4) * 2.0 ** -22
+    w = 2 * e[..., None] + 2.0 ** -16 + (n + 128) * 2.0 ** -23
+    return w * (1 + 2.0 ** -8) * o["mean_abs"] + 2.0 ** -8 * np.abs(o["out"]) + 1e-30
+
+
+def paired(c):
+    """Values in pairs of opposite rows, so that results are small next to what they are summed from: a rounding
+    of the weights shows, the rounding of the result does not."""
+    for r in c.v:
+        for v in r:
+            v[1::2] = -v[:v.shape[0] // 2 * 2:2]
+    return c
+
+
+def marked(c):
+    """Values that name their rows: column u of 64 is non-zero in every 64th unit of 16 rows, the others in
+    every 64th row, so with even weights a unit that is lost, read twice or misplaced moves its column by a
+    few per cent at 20,000 rows, and by more at fewer."""
+    for r in c.v:
+        for v in r:
+            j = np.arange(v.shape[0])
+            v[:] = 0.0
+            v[j, j // 16 % 64] = 1.0 + j // 1024 % 4
+            v[j, 64 + j % 64] = 1.0 + j // 64 % 4
+    return c
+
+
+def check_tokens(c, ora=None):
+    """Results of the kernel of few rows under its own bound (rows of every token of a request)."""
+    ora = ora or c.oracle()
+    out = to_f64(c.t["out"]).reshape(c.B, c.H, c.G, c.m, D)
+    for b in range(c.B):
+        for h in range(c.H):
+            o, mb = ora[b][h], c.new[b]
+            tol = token_tolerance(o, c.lens[b][h])
+            err = np.abs(out[b, h, :, :mb] - o["out"])
+            assert np.all(err <= tol), (b, h, float(np.nanmax(err / tol)), np.isnan(err).sum())
+
+
 def workspace(nbytes):
     import torch
 
