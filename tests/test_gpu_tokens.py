@@ -69,3 +69,44 @@ def test_every_row_counts_once_for_tokens(kw, acc):
     dict(H=2, G=3, m=50, lens=4099, causal=False)])
 def test_every_row_counts_once_for_chunks(kw):
     run(CH.marked(CH.Case(scale=1e-3, seed=1, **kw)), acc=True, tokens=False)
+
+
+# ------------------------------------------------------------------------------ 17 to 32 query rows
+TWO = [(3, 7), (4, 7), (1, 17), (1, 32), (6, 4), (8, 4), (17, 1), (2, 13)]
+
+
+@pytest.mark.parametrize("m,G", TWO)
+@pytest.mark.parametrize("layout,block", [("contiguous", 0), ("packed", 0), ("paged", 8), ("paged", 32)])
+def test_two_items(m, G, layout, block):
+    # clusters of one and of several, requests without tokens, with one, with all: an item that is empty, or
+    # begins within a token's group
+    for n in (1, 40, 100, 129, 500, 1111):
+        for new in (None, [0, 1, m], [m, max(1, m - 1), 0]):
+            lens = np.array([n, max(0, n - 9), n]) + (np.array([m] * 3) if new is None else np.array(new))
+            run(CH.Case(B=3, H=2, G=G, m=m, lens=lens if layout != "packed" else np.repeat(lens[:, None], 2, 1), new=new,
+                        layout=layout, block=block, token_major=n == 100, seed=n))
+
+
+@pytest.mark.parametrize("m,G", TWO)
+@pytest.mark.parametrize("layout,block", [("contiguous", 0), ("packed", 0), ("paged", 16)])
+def test_two_items_with_windows(m, G, layout, block):
+    for window, n_sink in ((1, 0), (2, 1), (40, 3), (130, 70), (700, 64)):
+        for new in (None, [1, m]):
+            lens = np.array([1201, m + 7])
+            run(CH.Case(B=2, H=2, G=G, m=m, lens=lens if layout != "packed" else np.repeat(lens[:, None], 2, 1), new=new,
+                        window=window, n_sink=n_sink, layout=layout, block=block, seed=window))
+
+
+@pytest.mark.parametrize("m,G", TWO)
+def test_two_items_of_every_kind(m, G):
+    g = CH.rng(m)
+    # every row visible; an empty cache; fewer rows than tokens; a length per head
+    run(CH.Case(B=3, G=G, m=m, lens=[0, 77, 300], causal=False, new=[m, 1, m], seed=1))
+    run(CH.Case(B=4, G=G, m=m, lens=[0, 1, m - 1, m], layout="paged", block=8, seed=2))
+    run(CH.Case(B=2, H=4, G=G, m=m, lens=g.integers(m, 900, (2, 4)), per_head=True, layout="paged", block=16, seed=3))
+    # as many segments as there are places for: clusters of one; and logits that make the maximum move
+    run(CH.Case(B=9, H=8, G=G, m=m, lens=m + np.arange(9) * 12, seed=4))
+    run(CH.Case(B=2, G=G, m=m, lens=[900, 321], scale=0.6, logit=3.0, seed=5))
+    run(CH.paired(CH.Case(B=2, G=G, m=m, lens=[m + 5, 64], logit=0.1, seed=6)))
+    run(CH.marked(CH.Case(H=1, G=G, m=m, lens=1500, scale=1e-3, seed=7)))
+    run(CH.Case(B=2, G=G, m=m, lens=[m + 5, 640], seed=8), lse=False)
