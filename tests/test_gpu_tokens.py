@@ -110,3 +110,32 @@ def test_two_items_of_every_kind(m, G):
     run(CH.paired(CH.Case(B=2, G=G, m=m, lens=[m + 5, 64], logit=0.1, seed=6)))
     run(CH.marked(CH.Case(H=1, G=G, m=m, lens=1500, scale=1e-3, seed=7)))
     run(CH.Case(B=2, G=G, m=m, lens=[m + 5, 640], seed=8), lse=False)
+
+
+# ------------------------------------------------------------------------------ kept logits
+@pytest.mark.parametrize("m,G", [(1, 4), (1, 3), (2, 2), (4, 1), (1, 1), (1, 8), (2, 4), (1, 5), (3, 2), (7, 1)])
+@pytest.mark.parametrize("window,n_sink", [(0, 0), (300, 5), (700, 300), (1, 0)])
+def test_weights_of_many_rows(m, G, window, n_sink):
+    """More than 1200 blocks of 256 rows: a thread adds up four cached rows (m G <= 4) or two (<= 8)."""
+    lens = np.array([[255, 256, 257, 511, 513, 1023, 1025, 1], [0, 769, 767, 1279, 1281, 2047, 2100, 64],
+                     [1536, 2049, 300, 900, 1793, 512, 768, 1024], [100, 1400, 1700, 2000, 258, 260, 514, 31]])
+    for new in (None, [0, 1, m, m]):
+        at = lens if new is None else np.maximum(lens, np.array(new)[:, None])
+        c = CH.Case(B=4, H=8, G=G, m=m, lens=at, layout="packed", new=new, window=window, n_sink=n_sink, pad_rows=9000, seed=m)
+        assert -(-c.max_len // 256) * 32 > 1200
+        run(c, acc=True)
+
+
+@pytest.mark.parametrize("m,G", [(1, 4), (2, 4)])
+def test_weights_of_many_rows_from_pages(m, G):
+    lens = 1200 - 37 * np.arange(20)
+    for window, n_sink in ((0, 0), (333, 4)):
+        run(CH.Case(B=20, H=8, G=G, m=m, lens=lens, layout="paged", block=16, window=window, n_sink=n_sink, pad_rows=849,
+                    seed=window), acc=True)
+    for calls in (1, 2):       # and they add up
+        c = CH.Case(B=4, H=8, G=G, m=m, lens=[[2100, 900, 1025, 257, 1, 256, 0, 1999]] * 4, causal=False, layout="packed", pad_rows=9000, seed=3).upload()
+        ws = None
+        for _ in range(calls):
+            ws = c.call(acc=True, ws=ws)
+        assert CH.status(ws) == 0
+        c.check(acc=True, calls=calls)
