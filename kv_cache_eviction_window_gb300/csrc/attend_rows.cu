@@ -505,10 +505,18 @@ cudaError_t launch_attend_rows(const AttnArgs& a, int grid, int cluster, cudaStr
   return launch_attend_join(a, grid, st);
 }
 
-// With more CTAs of 256 rows than the device holds at once, about, a thread takes EACH rows, so that with few
-// query rows as many loads are on their way (128 segments of 3500 to 8192 rows, 4 query rows: the call 82.2
-// us with one row each, 77.5 with four).
-constexpr int kWave = 1200;
+// With more CTAs of 256 rows than the device holds at once, about, and few query rows, a thread takes four
+// cached rows, so that as many loads are on their way.  The whole call, with one row each and with four (best
+// of three, us; blocks: of 256 cached rows, over all segments):
+//   query rows        4               5               7               8
+//   1024 blocks  27.7 and 27.9   28.3 and 28.4   30.0 and 29.8   28.8 and 31.1
+//   1280         34.2     34.0   35.3     35.1   36.7     36.7   36.2     38.7
+//   1536         38.6     37.9   39.7     38.9   41.2     40.5   40.3     42.8
+//   2048         48.8     47.2   50.3     48.7   52.6     50.5   51.7     53.3
+//   4096         84.2     80.1   86.2     81.8   90.3     84.8   89.1     87.9
+// (512 blocks lose 0.4 with four query rows, 2.7 with eight; 16 query rows lose everywhere, 3 to 9; two cached
+// rows each mostly lie between the two.)
+constexpr int kWave = 1200, kFewRows = 7;
 
 template <int EACH>
 void launch_weights_kept_of(const AttnArgs& a, cudaStream_t st) {
@@ -516,12 +524,9 @@ void launch_weights_kept_of(const AttnArgs& a, cudaStream_t st) {
   weights_kept_kernel<EACH><<<dim3(std::min((a.max_len + rows - 1) / rows, std::max(1, 16384 / segs)), segs), 256, 0, st>>>(a);
 }
 cudaError_t launch_weights_kept(const AttnArgs& a, cudaStream_t st) {
-  const int R = a.m * a.G;
   const bool many = static_cast<long long>((a.max_len + 255) / 256) * a.B * a.H > kWave;
-  if (many && R <= 4)
+  if (many && a.m * a.G <= kFewRows)
     launch_weights_kept_of<4>(a, st);
-  else if (many && R <= 8)
-    launch_weights_kept_of<2>(a, st);
   else
     launch_weights_kept_of<1>(a, st);
   note_launch();

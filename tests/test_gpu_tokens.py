@@ -116,7 +116,7 @@ def test_two_items_of_every_kind(m, G):
 @pytest.mark.parametrize("m,G", [(1, 4), (1, 3), (2, 2), (4, 1), (1, 1), (1, 8), (2, 4), (1, 5), (3, 2), (7, 1)])
 @pytest.mark.parametrize("window,n_sink", [(0, 0), (300, 5), (700, 300), (1, 0)])
 def test_weights_of_many_rows(m, G, window, n_sink):
-    """More than 1200 blocks of 256 rows: a thread adds up four cached rows (m G <= 4) or two (<= 8)."""
+    """More than 1200 blocks of 256 rows: a thread adds up four cached rows (m G <= 7), or one."""
     lens = np.array([[255, 256, 257, 511, 513, 1023, 1025, 1], [0, 769, 767, 1279, 1281, 2047, 2100, 64],
                      [1536, 2049, 300, 900, 1793, 512, 768, 1024], [100, 1400, 1700, 2000, 258, 260, 514, 31]])
     for new in (None, [0, 1, m, m]):
