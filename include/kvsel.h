@@ -91,7 +91,10 @@ enum { KVSEL_WO_GROUP_SUM = 0, KVSEL_WO_PER_HEAD = 1 };
  * W_h^T W_h (32x fewer flops at D = 4096); group-sum W_O reading only. */
 enum { KVSEL_NORM_L1 = 0, KVSEL_NORM_L2 = 1 };
 /* PACKED (kvsel_attend only): rows [n_rows][head_dim], stride_tok apart, the segments placed by
- * an offsets array: what kvsel_compact and kvsel_run_layer write. */
+ * an offsets array: what kvsel_compact and kvsel_run_layer write.  Such rows are read in place and
+ * not grown: kvsel_evict_append refuses them.  As kvsel_compact leaves them they have no room for
+ * a new token's own row, and kvsel_attend with causal = 0 attends to the kept rows alone; to go on
+ * decoding, the caller moves the segments into a contiguous or paged cache. */
 enum { KVSEL_LAYOUT_CONTIGUOUS = 0, KVSEL_LAYOUT_PAGED = 1, KVSEL_LAYOUT_PACKED = 2 };
 
 #define KVSEL_MAX_BATCH 128
@@ -447,10 +450,11 @@ typedef struct kvsel_attn_params {
 } kvsel_attn_params;
 
 /* Bytes of device workspace that kvsel_attend needs on the current device (with_acc: the call
- * passes acc).  Tens of MB at most, but with acc and n_new * group <= 16 also
- * 4 * batch * h_kv * n_new * group * max_len bytes (the logits), so keep max_len near the real
- * lengths (with acc and more rows than 16, batch * h_kv * max_len / 256 blocks of cached rows are
- * planned, 2^30 at most).  Host-only. */
+ * passes acc).  Tens of MB at most without acc.  With acc 4 * batch * h_kv * n_new * group bytes more
+ * (the log-sums), and with n_new * group <= 16 max_len times as many (the logits, at their rows'
+ * own places: with a window too, although it fills few of them), so keep max_len near the real
+ * lengths (with more rows than 16, batch * h_kv * max_len / 256 blocks of cached rows are planned,
+ * 2^30 at most).  Host-only. */
 int kvsel_attend_workspace_size(const kvsel_attn_params* p, int with_acc, size_t* bytes);
 
 /* out[b][hq][t] = sum_j w_j v_j with w = softmax_j(scale * <q[b][hq][t], k_j>) over the rows that
@@ -471,8 +475,11 @@ int kvsel_attend_workspace_size(const kvsel_attn_params* p, int with_acc, size_t
  *   ws       workspace of kvsel_attend_workspace_size bytes, 256-byte aligned, its status word
  *            zeroed by kvsel_workspace_init; one per call that may run at the same time (two
  *            graphs that replay at the same time included)
- * Softmax statistics and sums are fp32; out is rounded once to bf16.  Two calls with the same
- * inputs give the same bits on the same kind of device.  K/V rows that no new token sees may
+ * Softmax statistics and sums are fp32, lse and acc take the weights unrounded, and out is rounded
+ * to bf16 at the end.  In the sum with v the weights are kept to 2^-16 relative where n_new * group
+ * <= 16; with more query rows they may be rounded to bf16 first (2^-8 relative at most per weight:
+ * the chunk kernel's second product takes both operands in one type, and v is bf16).  Two calls
+ * with the same inputs give the same bits on the same kind of device.  K/V rows that no new token sees may
  * hold anything and pages without a visible row are not looked up; rows that some token of
  * the request sees must be finite.  A length, offset or block-table entry out of range is
  * recorded in the status word (KVSEL_EDEVICE through kvsel_get_device_status): lengths are
