@@ -18,8 +18,8 @@
 // gets the same number of tiles whatever the lengths are (share_of); the pieces of an item
 // that was cut are joined by attend_join.cu's kernels, in cache order.
 //
-// Measured, 8 KV heads, one token: 16 requests of 2048 to 65536 rows in pages of 16 340-351 us for
-// 2.31 GB, 0.97 of the copy rate; eight requests, window of 4096 in pages of 64, 26 us for 134 MB
+// Measured, 8 KV heads, one token: 16 requests of 2048 to 65536 rows in pages of 16 342-345 us for
+// 2.30 GB, the copy rate; eight requests, window of 4096 in pages of 64, 26 us for 134 MB
 // (clusters of four; 30 us with plan and join); one request of 1111 rows 6.6 us (7.4).
 #include <cooperative_groups.h>
 

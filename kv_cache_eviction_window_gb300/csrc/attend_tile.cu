@@ -29,9 +29,10 @@
 //
 // Bound: the latency of a softmax step (about 1500 cycles for 128 x 64: wait, TMEM load and maximum,
 // exponentials, TMEM store), two streams at a time; then the tensor cores.  Measured, 8 KV heads:
-// 2048 tokens of 4 query heads each over 32768 contiguous rows 722 us, 1475 TFLOP/s, 0.78 of
-// cuBLAS; from pages of 16 rows 733 us; over an empty cache 54 us; 2048 tokens of 8 query heads over
-// 16384 rows, window of 4096, 254 us (tensor pipe 51% active, issue 47%).
+// 2048 tokens of 4 query heads each over 32768 contiguous rows 714 us, 1492 TFLOP/s, 0.75 of
+// cuBLAS in a burst; from pages of 16 rows 725 us (761-772 in a long run, under the power cap); over an
+// empty cache 54 us; 2048 tokens of 8 query heads over 16384 rows, window of 4096, 254 us (tensor pipe
+// 51% active, issue 47%).
 #include "attend.cuh"
 
 namespace kvsel {

@@ -16,7 +16,7 @@
 // rows, 8 us with the second launch, 6 without; 256 segments 20.5 and 24, two CTAs an SM no longer).
 // evict_move_kernel: slot keep + i of a segment is handled by one half warp per side: its old
 // row goes to its hole, then new row i takes the slot.  A warp takes two slots at a time (one: 37.2
-// us for the call with 2048 rows of 32 segments of 16384, two 35.7, four 38.3; 30.8 now).  Bound: the latency
+// us for the call with 2048 rows of 32 segments of 16384, two 35.7, four 38.3; 31.6 now, 17 of them the selection).  Bound: the latency
 // of a slot's chain of loads (its rank, its hole, their pages, its row), then HBM, 512 B per moved
 // or new row read and written (and 8 B per slot before).
 #include <algorithm>
