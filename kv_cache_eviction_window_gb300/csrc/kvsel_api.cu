@@ -373,10 +373,18 @@ bool encode(CUtensorMap* m, const void* ptr, int rank, const cuuint64_t* dims, c
   cuuint32_t es[5] = {1, 1, 1, 1, 1};
   PFN_cuTensorMapEncodeTiled_v12000 enc = encoder();
   if (!enc) return false;
-  const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(ptr), dims,
-                                            strides_bytes, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                                            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  auto once = [&] {
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(ptr), dims, strides_bytes, box, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  };
+  CUresult r = once();
+  // The driver's encoder wants a current context, and a host thread whose first CUDA call this is has none
+  // yet: the runtime makes its device's current there.
+  int dev = 0;
+  if ((r == CUDA_ERROR_INVALID_CONTEXT || r == CUDA_ERROR_NOT_INITIALIZED) && cudaGetDevice(&dev) == cudaSuccess &&
+      cudaSetDevice(dev) == cudaSuccess)
+    r = once();
   return r == CUDA_SUCCESS;
 }
 
