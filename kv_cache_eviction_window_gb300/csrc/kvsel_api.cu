@@ -379,7 +379,7 @@ bool encode(CUtensorMap* m, const void* ptr, int rank, const cuuint64_t* dims, c
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   };
   CUresult r = once();
-  // The driver's encoder wants a current context, and a host thread whose first CUDA call this is has none
+  // cuTensorMapEncodeTiled wants a current context, and a host thread whose first CUDA call this is has none
   // yet: the runtime makes its device's current there.
   int dev = 0;
   if ((r == CUDA_ERROR_INVALID_CONTEXT || r == CUDA_ERROR_NOT_INITIALIZED) && cudaGetDevice(&dev) == cudaSuccess &&
