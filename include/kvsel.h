@@ -21,7 +21,10 @@
  *     variable-length cache (KVzip §4.2, §7.1).
  *   - The cache in use afterwards: attention of new tokens over a contiguous, paged or compacted
  *     cache, the accumulated weight of every cached row, and eviction by it (kvsel_attend,
- *     kvsel_evict_append).
+ *     kvsel_evict_append); kept rows left in their cache (kvsel_compact_in_place).
+ *   - A step of drafted tokens over it: attention of a tree (kvsel_attend_tree), which of its nodes
+ *     are accepted (kvsel_verify), the pages that requests share (kvsel_pages_*), and rotary
+ *     positions (kvsel_rope, kvsel_rope_cache).
  *
  * Conventions (all entry points):
  *   - Every pointer named device is a CUDA device pointer, 16-byte aligned; bf16 data is
@@ -100,6 +103,8 @@ enum { KVSEL_LAYOUT_CONTIGUOUS = 0, KVSEL_LAYOUT_PAGED = 1, KVSEL_LAYOUT_PACKED 
 #define KVSEL_MAX_BATCH 128
 #define KVSEL_MAX_ATTN_BATCH 1024  /* kvsel_attend, kvsel_evict_append */
 #define KVSEL_MAX_ATTN_GROUP 128   /* kvsel_attend */
+#define KVSEL_MAX_TREE 1024        /* kvsel_attend_tree, kvsel_tree_masks, kvsel_verify: nodes of a request */
+#define KVSEL_MAX_VOCAB 262144     /* kvsel_verify */
 
 /* ---- parameters --------------------------------------------------------------------- */
 typedef struct kvsel_params {
@@ -327,7 +332,7 @@ enum {
 };
 
 /* Diagnostics: while `events` is non-NULL, each kernel launched by this thread's
- * subsequent calls (kvsel_attend and kvsel_evict_append excepted) is bracketed by cudaEventRecord(events[2*stage]) and
+ * subsequent calls (those of the cache in use excepted, kvsel_attend and what follows it here) is bracketed by cudaEventRecord(events[2*stage]) and
  * cudaEventRecord(events[2*stage + 1]) on the launch stream (NULL entries skipped).
  * `events` is a host array of 2*KVSEL_STAGE_COUNT cudaEvent_t created by the caller and
  * must stay valid until the hook is cleared with NULL.  No effect on results. */
@@ -534,6 +539,259 @@ int kvsel_evict_append_workspace_size(const kvsel_evict_params* p, size_t* bytes
 int kvsel_evict_append(const kvsel_evict_params* p, const kvsel_kv* kv, int32_t* lens, int32_t* seen, int32_t* pos,
                        float* acc, const void* k_new, const void* v_new, const int32_t* new_lens, void* ws,
                        size_t ws_bytes, void* stream);
+
+/* ---- the cache in use: kept rows left in their cache ----------------------------------- */
+
+/* What kvsel_compact writes into buffers of its own, done in the cache itself: the kept rows of every
+ * segment become its first counts rows.  Rows that lie there already stay where they are, and the
+ * kept rows behind fill the holes, both in ascending order, so that at most min(counts, n - counts)
+ * rows move.  The call also sets up what kvsel_evict_append and kvsel_attend go on with: lens =
+ * counts, seen = n, pos = the token position of each row, acc = its score.  Pages behind the rows can be
+ * freed then (kvsel_pages_trim with lens_per_head).
+ *   p, idx, counts, offsets   as kvsel_compact takes them: the kept set as kvsel_select writes it
+ *   kv       contiguous or paged, written in place; no two segments may share memory
+ *   scores   device fp32, packed as kvsel_score writes them, or NULL (then acc = 0)
+ *   lens, seen  device int32 [batch*h_kv], written; seen may be NULL
+ *   pos      device int32 [batch*h_kv][capacity]; acc device fp32 likewise, or NULL: entries 0..counts-1
+ *            of a segment are written, the others left as they are
+ *   capacity entries between segments of pos and acc, at least the longest n
+ *   ws       NULL, or a workspace of at least 256 bytes whose status word records entries found out of
+ *            range
+ * Nothing outside the cache and the outputs is touched whatever idx holds.  A segment whose count or
+ * offset does not fit is left as it is, with lens 0; an index outside [0, n) or a block-table entry out of
+ * range moves no row; a list that is not strictly ascending leaves the segment's rows, pos and acc
+ * undefined.  All of these are recorded in the status word. */
+int kvsel_compact_in_place(const kvsel_params* p, const kvsel_kv* kv, const int32_t* idx, const int32_t* counts,
+                           const int64_t* offsets, const float* scores, int32_t* lens, int32_t* seen, int32_t* pos,
+                           float* acc, int64_t capacity, void* ws, size_t ws_bytes, void* stream);
+
+/* ---- drafted tokens: attention of a tree ------------------------------------------------ */
+
+/* A tree of drafted tokens has m nodes per request: node 0 the token decided last (its row is not in
+ * the cache yet), the others drafted, parents before children: parents[b][t] in [0, t), and -1 for node
+ * 0.  A chain is a tree in which each node's parent is the node before.
+ *
+ * Masks: bit t % 32 of word t / 32 of a node's mask is set for itself and its ancestors; a mask has
+ * ceil(n_new / 32) words.
+ *   parents  device int32 [batch][n_new]; a parent outside [0, t) counts as none
+ *   new_lens device int32 [batch], nodes m of every request (0..n_new, clamped), or NULL = n_new for all
+ *   first    device int32 [batch], position of node 0 of every request (pos only)
+ *   tree     device uint32 [batch][n_new][ceil(n_new / 32)], written for nodes 0..m-1
+ *   pos      device int32 [batch][n_new] or NULL: first + depth of each of these nodes, what kvsel_rope takes
+ * batch 1..KVSEL_MAX_ATTN_BATCH, n_new 1..KVSEL_MAX_TREE.  Asynchronous on `stream`; no workspace. */
+int kvsel_tree_masks(const int32_t* parents, const int32_t* new_lens, const int32_t* first, int32_t batch, int32_t n_new,
+                     uint32_t* tree, int32_t* pos, void* stream);
+
+/* Bytes of device workspace that kvsel_attend_tree needs on the current device.  Host-only. */
+int kvsel_attend_tree_workspace_size(const kvsel_attn_params* p, size_t* bytes);
+
+/* kvsel_attend for the nodes of a tree, whose rows are the last m of every segment (append them first):
+ * node t sees row j when
+ *     j < n - m  and  (window == 0  or  j > r - window  or  j < n_sink),  r = n - m + set bits of its mask - 1
+ *     j = n - m + u  and  bit u of its mask is set
+ * (r is the row that the node would have in a chain of what it sees; a node with an empty mask counts as
+ * n - m.)  Any mask will do: a node that sees nothing (an empty mask over an empty cache) gets zeros and -inf.
+ *   p        causal = 1, n_new <= KVSEL_MAX_TREE; acc_stride is not read
+ *   tree     device uint32 [batch][n_new][ceil(n_new / 32)] as kvsel_tree_masks writes it; bits of rows at or
+ *            behind m and the masks of nodes at or behind m are not used
+ *   the other arguments, results, workspace and errors as kvsel_attend's
+ * The rows of the tree, and the cached rows that a token at row n - m sees, must be finite; the others
+ * may hold anything.  (No accumulated weights: rows of nodes that are not accepted leave the cache.) */
+int kvsel_attend_tree(const kvsel_attn_params* p, const void* q, const kvsel_kv* kv, const int32_t* lens,
+                      const int32_t* new_lens, const int64_t* offsets, const uint32_t* tree, void* out, float* lse,
+                      void* ws, size_t ws_bytes, void* stream);
+
+/* ---- drafted tokens: verification ------------------------------------------------------- */
+
+/* SAMPLED: every node but 0 was drawn from its parent's draft distribution, siblings independently.
+ * POINT: drafted without probabilities (the draft distribution is 1 at the drafted token).
+ * GREEDY: the target's largest value decides (ties: the lowest token). */
+enum { KVSEL_VERIFY_SAMPLED = 0, KVSEL_VERIFY_POINT = 1, KVSEL_VERIFY_GREEDY = 2 };
+enum { KVSEL_DTYPE_FP32 = 0, KVSEL_DTYPE_BF16 = 1 };
+
+typedef struct kvsel_verify_params {
+  int32_t batch;         /* requests, 1..KVSEL_MAX_ATTN_BATCH                                */
+  int32_t n_new;         /* nodes of a request at most, 1..KVSEL_MAX_TREE                    */
+  int32_t vocab;         /* tokens V, 1..KVSEL_MAX_VOCAB                                     */
+  int32_t mode;          /* KVSEL_VERIFY_*                                                   */
+  int32_t dtype;         /* KVSEL_DTYPE_* of target and draft                                */
+  int64_t stride_req, stride_node;   /* target and draft element (b, t, x) at b*stride_req +
+                            t*stride_node + x; both 0 = [batch][n_new][vocab]                */
+} kvsel_verify_params;
+
+/* Bytes of device workspace that kvsel_verify needs (its status word).  Host-only. */
+int kvsel_verify_workspace_size(const kvsel_verify_params* p, size_t* bytes);
+
+/* Which drafted tokens stay, and the token after them, such that the tokens follow the target's
+ * distribution.  p_t, q_t: target's and draft's probabilities of the token after node t.  From node
+ * c = 0, with rest r = p_0 and mass Z = 1, over its children t in ascending order, x = tokens[t]:
+ *     accepted when u_t q_c(x) Z < r(x): then c = t, r = p_t, Z = 1
+ *     else r = max(r - Z q_c, 0), Z = sum of r      (POINT: q_c = 1 at x: r(x) = 0, Z = Z - r(x))
+ * until no child is left; next = the smallest x with r(0) + ... + r(x) > u_0 (sum of r) (where r has no
+ * mass, of p_c; -1 where that has none either).  GREEDY: a child is accepted when its token is the
+ * lowest x with the largest p_c(x) (any values, logits will do; NaN is below all), and next is that x.
+ *   tokens   device int32 [batch][n_new], parents likewise (as kvsel_tree_masks takes them)
+ *   target   device, strides above, 4-byte (fp32) or 2-byte (bf16) aligned: rows of probabilities that sum to 1
+ *            (a value counts as what it is in [0, 1], to 2^-47; NaN as 0)
+ *   draft    device, as target (SAMPLED), else NULL
+ *   u        device fp32 [batch][n_new], uniform in [0, 1): u_t of node t's test, u_0 of the last draw
+ *            (NULL when GREEDY)
+ *   new_lens device int32 [batch], nodes of every request (0..n_new), or NULL = n_new for all
+ *   path     device int32 [batch][n_new]: node 0 and the accepted nodes, ascending, then -1
+ *   counts   device int32 [batch]: entries of path (0 for a request without nodes, whose next is -1)
+ *   next     device int32 [batch]
+ *   ws       workspace of kvsel_verify_workspace_size bytes, 256-byte aligned
+ * Sums are exact (64-bit integers in units of 2^-46), so results do not depend on their order.  A token
+ * outside [0, vocab) is never accepted, takes nothing from the rest, and is recorded in the status
+ * word with a node count out of range (clamped) and a parent outside [0, t) (the node is ignored). */
+int kvsel_verify(const kvsel_verify_params* p, const int32_t* tokens, const int32_t* parents, const void* target,
+                 const void* draft, const float* u, const int32_t* new_lens, int32_t* path, int32_t* counts,
+                 int32_t* next, void* ws, size_t ws_bytes, void* stream);
+
+/* ---- pages that requests share ----------------------------------------------------------- */
+
+/* A pool of pages for every layer ([layers][num_blocks][block_size][h_kv][head_dim], K and V) under one
+ * block table, and the uses of every page.  Between calls:
+ *     table  device int32 [batch][max_blocks]: pages of a request in order, then -1
+ *     ref    device int32 [num_blocks]: entries of the table that name the page; 0 = free
+ * Several requests may name a page (a prompt in common).  Rows are written only to pages with one use:
+ * kvsel_pages_reserve sees to that for the rows of new tokens; a request that is to be evicted from
+ * (kvsel_evict_append with a budget below its rows, kvsel_compact_in_place) must share none. */
+typedef struct kvsel_pages_params {
+  int32_t h_kv;          /* KV heads, 1..64                                                  */
+  int32_t head_dim;      /* must be 128                                                      */
+  int32_t batch;         /* rows of the table, 1..KVSEL_MAX_ATTN_BATCH                       */
+  int32_t block_size;    /* rows of a page: 8, 16, 32 or 64                                  */
+  int32_t max_blocks;    /* entries of a table row, 1..2^20                                  */
+  int32_t num_blocks;    /* pages of a layer's pool, 1..2^28                                 */
+  int32_t layers;        /* pools under the table, 1..1024                                   */
+  int32_t n_new;         /* new rows of a request at most, 0..2^20;
+                            batch * (n_new / block_size + 2) <= 2^20                         */
+  int32_t lens_per_head; /* 0: lens [batch]; 1: lens [batch*h_kv], heads of a request may differ */
+  int64_t stride_layer;  /* elements between the pools of layers; 0 = dense                  */
+} kvsel_pages_params;
+
+/* Bytes of device workspace that the calls below need (one size serves all).  Host-only. */
+int kvsel_pages_workspace_size(const kvsel_pages_params* p, size_t* bytes);
+
+/* New rows of the table from old ones: row b takes the pages and lens of old row src[b] (-1: none, its
+ * lens 0).  Several rows may take the same one (beams, samples of one prompt); an old row that none
+ * takes gives its pages back.  ref follows.
+ *   table_in, lens_in   device, read;  table_out, lens_out  device, written; they must not overlap
+ *   src      device int32 [batch]
+ * A src or page out of range is recorded in the status word and counts as -1. */
+int kvsel_pages_fork(const kvsel_pages_params* p, const int32_t* table_in, const int32_t* lens_in, const int32_t* src,
+                     int32_t* table_out, int32_t* lens_out, int32_t* ref, void* ws, size_t ws_bytes, void* stream);
+
+/* Makes rows lens .. lens + m - 1 of every request its own to write: entries without a page get a free
+ * one, and a page that others use too is copied (its rows below lens, in every layer) unless, of the
+ * requests in order, only this one is left to use it.  Pages are the lowest free ones, in order of requests and
+ * rows.  Where those run out, requests are served in order: one whose pages, together with all before
+ * it, exceed the free ones gets none (one that needs none is served).
+ *   k, v     device bf16, the pools of layer 0, 16-byte aligned
+ *   lens     device int32 [batch] or [batch*h_kv], not changed (with lens_per_head the pages from the shortest
+ *            head's rows to the longest's are made the request's own, with the rows of its longest)
+ *   new_lens device int32 [batch], m of every request (0..n_new), or NULL = n_new for all
+ *   granted  device int32 [batch], written: m, or 0 where the request was not served
+ * A length, table entry or row count out of range is recorded in the status word; such a request is not
+ * served. */
+int kvsel_pages_reserve(const kvsel_pages_params* p, void* k, void* v, int32_t* table, int32_t* ref, const int32_t* lens,
+                        const int32_t* new_lens, int32_t* granted, void* ws, size_t ws_bytes, void* stream);
+
+/* Gives back the pages of every request behind its rows (lens = 0: all of them): their entries become
+ * -1 and lose a use each. */
+int kvsel_pages_trim(const kvsel_pages_params* p, int32_t* table, int32_t* ref, const int32_t* lens, void* ws,
+                     size_t ws_bytes, void* stream);
+
+/* Moves the rows of the accepted nodes of a tree to its front, in every layer: with n = lens[b] rows, the
+ * last m of them the tree's, row n - m + path[b][i] goes to row n - m + i for i < counts[b], and
+ * lens_out[b] = n - m + counts[b].  (Then kvsel_pages_trim frees what lies behind.)
+ *   k, v, table  as above, the rows n - m .. n - 1 reserved by kvsel_pages_reserve
+ *   lens     device int32 [batch] or [batch*h_kv]: rows with the tree's; lens_out likewise, written (may be lens)
+ *   new_lens device int32 [batch], m of every request (0..n_new), or NULL = n_new for all
+ *   path     device int32 [batch][n_new], counts device int32 [batch], as kvsel_verify writes them
+ * A count or length out of range is clamped, a path entry that is below its place, not above the
+ * one before, or not below m moves nothing; each is recorded in the status word. */
+int kvsel_pages_accept(const kvsel_pages_params* p, void* k, void* v, const int32_t* table, const int32_t* lens,
+                       const int32_t* new_lens, const int32_t* path, const int32_t* counts, int32_t* lens_out, void* ws,
+                       size_t ws_bytes, void* stream);
+
+/* ---- rotary positions --------------------------------------------------------------------- */
+
+/* Layout of the pairs in the first rot_dim columns: (2i, 2i + 1), or (i, i + rot_dim / 2). */
+enum { KVSEL_ROPE_HALF = 0, KVSEL_ROPE_INTERLEAVED = 1 };
+/* TRANSPOSE turns back with the same factor: the gradient of FORWARD.  INVERSE undoes it. */
+enum { KVSEL_ROPE_FORWARD = 0, KVSEL_ROPE_TRANSPOSE = 1, KVSEL_ROPE_INVERSE = 2 };
+/* How the frequencies f_i = theta^(-2i / rot_dim) follow a context that is `factor` times orig_len:
+ *   LINEAR  f_i / factor
+ *   NTK     theta * factor^(rot_dim / (rot_dim - 2)) in place of theta
+ *   YARN    f_i (g / factor + 1 - g), g rising from 0 to 1 between the pairs that turn beta_fast and
+ *           beta_slow times in orig_len (rounded outwards), and values times 0.1 ln(factor) + 1
+ *   BANDS   f_i (s + (1 - s) / factor), s rising from 0 to 1 between low_freq and high_freq turns in
+ *           orig_len */
+enum { KVSEL_ROPE_NONE = 0, KVSEL_ROPE_LINEAR = 1, KVSEL_ROPE_NTK = 2, KVSEL_ROPE_YARN = 3, KVSEL_ROPE_BANDS = 4 };
+
+typedef struct kvsel_rope_params {
+  int32_t rot_dim;       /* columns that are turned, a multiple of 16 up to 128 (at least 32 for NTK) */
+  int32_t layout;        /* KVSEL_ROPE_HALF, KVSEL_ROPE_INTERLEAVED                          */
+  int32_t direction;     /* KVSEL_ROPE_FORWARD, ...                                          */
+  int32_t scaling;       /* KVSEL_ROPE_NONE, ...                                             */
+  int32_t orig_len;      /* YARN, BANDS                                                      */
+  double theta;          /* > 1                                                              */
+  double factor;         /* >= 1 (scaling other than NONE)                                   */
+  double beta_fast, beta_slow;   /* YARN: 32 and 1 as a rule; beta_fast > beta_slow > 0      */
+  double low_freq, high_freq;    /* BANDS: 1 and 4 as a rule; high_freq > low_freq > 0       */
+  double value_scale;    /* factor of the turned values; 0 = as the scaling says             */
+} kvsel_rope_params;
+
+/* What the calls below take, made once per model: turns per position of every pair in units of 2^-64
+ * (so that an angle is exact at any position: an integer product that wraps at a whole turn). */
+typedef struct kvsel_rope_angles {
+  uint64_t turns[64];
+  int32_t rot_dim, layout;
+  float scale;           /* of the turned values, direction included                         */
+  int32_t back;          /* 1: turned back                                                   */
+} kvsel_rope_angles;
+int kvsel_rope_table(const kvsel_rope_params* p, kvsel_rope_angles* table);
+
+/* Rows of one or two tensors (queries and keys) that share their positions. */
+typedef struct kvsel_rope_rows {
+  int32_t batch;         /* requests, 1..65535                                               */
+  int32_t n_tok;         /* tokens of a request at most, 1..2^20                             */
+  int32_t heads, k_heads;   /* heads of q (>= 1) and of k (0: none), 8192 at most together   */
+  int64_t q_req, q_head, q_tok;          /* strides of q in elements, multiples of 8; columns contiguous */
+  int64_t qo_req, qo_head, qo_tok;       /* of q_out                                         */
+  int64_t k_req, k_head, k_tok;
+  int64_t ko_req, ko_head, ko_tok;
+  int64_t pos_req;       /* entries of pos between requests (0: the same for all)            */
+} kvsel_rope_rows;
+
+/* q_out[b][h][t] = q[b][h][t] turned by position pos[b][t], columns behind rot_dim unchanged, and k_out
+ * likewise.  q, q_out, k, k_out: device bf16, 16-byte aligned; an output may be its input (the same
+ * strides), otherwise they must not overlap.  pos: device int32, any values.  new_lens: device int32
+ * [batch], tokens of every request (clamped to 0..n_tok), or NULL = n_tok for all; the rows of the
+ * others are left as they are.  Computed in fp32, rounded to bf16 once. */
+int kvsel_rope(const kvsel_rope_angles* table, const kvsel_rope_rows* p, const void* q, void* q_out, const void* k,
+               void* k_out, const int32_t* pos, const int32_t* new_lens, void* stream);
+
+typedef struct kvsel_rope_cache_params {
+  int32_t h_kv, batch;   /* KV heads 1..64; requests, 1..KVSEL_MAX_ATTN_BATCH                */
+  int32_t max_len;       /* rows of a segment at most, 1..2^30                               */
+  int32_t lens_per_head; /* 0: lens [batch]; 1: lens [batch*h_kv]                            */
+  int64_t pos_stride;    /* entries of pos between segments, >= max_len; 0 = position j for row j */
+  int64_t o_req, o_head, o_tok;   /* strides of k_out in elements, multiples of 8            */
+} kvsel_rope_cache_params;
+
+/* Every cached key turned by pos[seg][j]: in place (k_out NULL), e.g. by the difference to its new position
+ * after an eviction, or into k_out [b][h][j], e.g. INVERSE: the keys before their rotation, which
+ * kvsel_anchor_project wants.
+ *   kv       contiguous or paged; only k is read (or written)
+ *   lens     device int32, rows of every segment (clamped to max_len); rows behind are left as they are
+ *   pos      device int32 [batch*h_kv][pos_stride], NULL with pos_stride 0
+ *   ws       NULL, or a workspace of at least 256 bytes whose status word records a length or block-table
+ *            entry out of range (whose rows are not turned) */
+int kvsel_rope_cache(const kvsel_rope_angles* table, const kvsel_rope_cache_params* p, const kvsel_kv* kv,
+                     const int32_t* lens, const int32_t* pos, void* k_out, void* ws, size_t ws_bytes, void* stream);
 
 /* Static description of an error code. */
 const char* kvsel_strerror(int code);

@@ -29,6 +29,11 @@ POOL = {"none": 0, "max": 1, "avg": 2}
 BUDGET = {"head": 0, "layer": 1, "anchor": 2}
 WO_MODE = {"group_sum": 0, "per_head": 1}
 VALUE_NORM = {"l1": 0, "l2": 1}
+VERIFY = {"sampled": 0, "point": 1, "greedy": 2}
+DTYPE = {"fp32": 0, "bf16": 1}
+ROPE_LAYOUT = {"half": 0, "interleaved": 1}
+ROPE_DIRECTION = {"forward": 0, "transpose": 1, "inverse": 2}
+ROPE_SCALING = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3, "bands": 4}
 LAYOUT_CONTIGUOUS, LAYOUT_PAGED, LAYOUT_PACKED = 0, 1, 2
 MAX_BATCH = 128
 
@@ -39,7 +44,10 @@ EXPORTS = ("kvsel_workspace_size", "kvsel_output_size", "kvsel_workspace_init", 
            "kvsel_run_anchors", "kvsel_perturbation_workspace_size", "kvsel_perturbation",
            "kvsel_query_agnostic_split", "kvsel_prepared_w_o_size", "kvsel_prepare_w_o",
            "kvsel_attend_workspace_size", "kvsel_attend", "kvsel_evict_append_workspace_size",
-           "kvsel_evict_append")
+           "kvsel_evict_append", "kvsel_compact_in_place", "kvsel_tree_masks", "kvsel_attend_tree_workspace_size",
+           "kvsel_attend_tree", "kvsel_verify_workspace_size", "kvsel_verify", "kvsel_pages_workspace_size",
+           "kvsel_pages_fork", "kvsel_pages_reserve", "kvsel_pages_trim", "kvsel_pages_accept", "kvsel_rope_table",
+           "kvsel_rope", "kvsel_rope_cache")
 NOALLOC_SCRATCH_BYTES = 16 << 20
 STAGES = ("rowstats", "keysum", "wbar", "vnorm", "finalize", "select", "compact", "project", "perturb")
 
@@ -110,6 +118,50 @@ class kvsel_evict_params(_RowParams):
     ]
 
 
+class kvsel_verify_params(ctypes.Structure):
+    _fields_ = [
+        ("batch", ctypes.c_int32), ("n_new", ctypes.c_int32), ("vocab", ctypes.c_int32), ("mode", ctypes.c_int32),
+        ("dtype", ctypes.c_int32), ("stride_req", ctypes.c_int64), ("stride_node", ctypes.c_int64),
+    ]
+
+
+class kvsel_pages_params(ctypes.Structure):
+    _fields_ = [
+        ("h_kv", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("batch", ctypes.c_int32), ("block_size", ctypes.c_int32),
+        ("max_blocks", ctypes.c_int32), ("num_blocks", ctypes.c_int32), ("layers", ctypes.c_int32),
+        ("n_new", ctypes.c_int32), ("lens_per_head", ctypes.c_int32), ("stride_layer", ctypes.c_int64),
+    ]
+
+
+class kvsel_rope_params(ctypes.Structure):
+    _fields_ = [
+        ("rot_dim", ctypes.c_int32), ("layout", ctypes.c_int32), ("direction", ctypes.c_int32), ("scaling", ctypes.c_int32),
+        ("orig_len", ctypes.c_int32), ("theta", ctypes.c_double), ("factor", ctypes.c_double),
+        ("beta_fast", ctypes.c_double), ("beta_slow", ctypes.c_double), ("low_freq", ctypes.c_double),
+        ("high_freq", ctypes.c_double), ("value_scale", ctypes.c_double),
+    ]
+
+
+class kvsel_rope_angles(ctypes.Structure):
+    _fields_ = [
+        ("turns", ctypes.c_uint64 * 64), ("rot_dim", ctypes.c_int32), ("layout", ctypes.c_int32), ("scale", ctypes.c_float),
+        ("back", ctypes.c_int32),
+    ]
+
+
+class kvsel_rope_rows(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("n_tok", ctypes.c_int32), ("heads", ctypes.c_int32), ("k_heads", ctypes.c_int32)] + [
+        (f"{t}_{s}", ctypes.c_int64) for t in ("q", "qo", "k", "ko") for s in ("req", "head", "tok")] + [
+        ("pos_req", ctypes.c_int64)]
+
+
+class kvsel_rope_cache_params(ctypes.Structure):
+    _fields_ = [
+        ("h_kv", ctypes.c_int32), ("batch", ctypes.c_int32), ("max_len", ctypes.c_int32), ("lens_per_head", ctypes.c_int32),
+        ("pos_stride", ctypes.c_int64), ("o_req", ctypes.c_int64), ("o_head", ctypes.c_int64), ("o_tok", ctypes.c_int64),
+    ]
+
+
 _lib = None
 
 
@@ -127,6 +179,8 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
         raise KvselUnavailable(f"cannot load {p}: {e}") from e
     P, K = ctypes.POINTER(kvsel_params), ctypes.POINTER(kvsel_kv)
     PA, PE = ctypes.POINTER(kvsel_attn_params), ctypes.POINTER(kvsel_evict_params)
+    PV, PP = ctypes.POINTER(kvsel_verify_params), ctypes.POINTER(kvsel_pages_params)
+    PR, RA, i32 = ctypes.POINTER(kvsel_rope_params), ctypes.POINTER(kvsel_rope_angles), ctypes.c_int32
     vp, sz, i64p = ctypes.c_void_p, ctypes.c_size_t, ctypes.POINTER(ctypes.c_int64)
     sig = {
         "kvsel_workspace_size": ([P, ctypes.POINTER(sz)], ctypes.c_int),
@@ -154,6 +208,20 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
         "kvsel_attend": ([PA, vp, K] + [vp] * 7 + [sz, vp], ctypes.c_int),
         "kvsel_evict_append_workspace_size": ([PE, ctypes.POINTER(sz)], ctypes.c_int),
         "kvsel_evict_append": ([PE, K] + [vp] * 8 + [sz, vp], ctypes.c_int),
+        "kvsel_compact_in_place": ([P, K] + [vp] * 8 + [ctypes.c_int64, vp, sz, vp], ctypes.c_int),
+        "kvsel_tree_masks": ([vp, vp, vp, i32, i32, vp, vp, vp], ctypes.c_int),
+        "kvsel_attend_tree_workspace_size": ([PA, ctypes.POINTER(sz)], ctypes.c_int),
+        "kvsel_attend_tree": ([PA, vp, K] + [vp] * 7 + [sz, vp], ctypes.c_int),
+        "kvsel_verify_workspace_size": ([PV, ctypes.POINTER(sz)], ctypes.c_int),
+        "kvsel_verify": ([PV] + [vp] * 10 + [sz, vp], ctypes.c_int),
+        "kvsel_pages_workspace_size": ([PP, ctypes.POINTER(sz)], ctypes.c_int),
+        "kvsel_pages_fork": ([PP] + [vp] * 7 + [sz, vp], ctypes.c_int),
+        "kvsel_pages_reserve": ([PP] + [vp] * 8 + [sz, vp], ctypes.c_int),
+        "kvsel_pages_trim": ([PP] + [vp] * 4 + [sz, vp], ctypes.c_int),
+        "kvsel_pages_accept": ([PP] + [vp] * 9 + [sz, vp], ctypes.c_int),
+        "kvsel_rope_table": ([PR, RA], ctypes.c_int),
+        "kvsel_rope": ([RA, ctypes.POINTER(kvsel_rope_rows)] + [vp] * 7, ctypes.c_int),
+        "kvsel_rope_cache": ([RA, ctypes.POINTER(kvsel_rope_cache_params), K] + [vp] * 4 + [sz, vp], ctypes.c_int),
         "kvsel_perturbation_workspace_size": ([P, ctypes.POINTER(sz)], ctypes.c_int),
         "kvsel_perturbation": ([P, vp, K, vp, vp, vp, vp, vp, vp, sz, vp], ctypes.c_int),
     }
@@ -229,6 +297,19 @@ def make_evict_params(*, h_kv: int, batch: int, capacity: int, budget: int, n_ne
     [batch][h_kv][n_new][head_dim]."""
     return kvsel_evict_params(h_kv, head_dim, batch, n_new, capacity, budget, n_sink, n_recent,
                               *[int(x) for x in new_strides])
+
+
+def make_verify_params(*, batch: int, n_new: int, vocab: int, mode: str = "sampled", dtype: str = "fp32",
+                       stride_req: int = 0, stride_node: int = 0) -> kvsel_verify_params:
+    """Strides of target and draft in elements; zeros = dense [batch][n_new][vocab]."""
+    return kvsel_verify_params(batch, n_new, vocab, VERIFY[mode], DTYPE[dtype], stride_req, stride_node)
+
+
+def make_pages_params(*, batch: int, max_blocks: int, num_blocks: int, block_size: int, h_kv: int, layers: int = 1,
+                      n_new: int = 1, head_dim: int = 128, lens_per_head: bool = False) -> kvsel_pages_params:
+    """Pools [layers][num_blocks][block_size][h_kv][head_dim] under a table [batch][max_blocks]."""
+    return kvsel_pages_params(h_kv, head_dim, batch, block_size, max_blocks, num_blocks, layers, n_new,
+                              int(bool(lens_per_head)), 0)
 
 
 def _refuse(where: str, why: str) -> None:
@@ -567,6 +648,249 @@ def kvsel_evict_append(params: kvsel_evict_params, kv: kvsel_kv, lens, seen, pos
                                              _ptr(new_lens), ws.data_ptr(), ws.nbytes, st)
     if rc:
         _check(rc, "kvsel_evict_append")
+
+
+def _int32(t, count: int, where: str) -> Optional[int]:
+    """Address of a dense tensor of at least `count` 32-bit integers, else refused (an address is the caller's
+    own matter)."""
+    if t is None or isinstance(t, int):
+        return t
+    if t.element_size() != 4 or t.is_floating_point() or not t.is_contiguous() or t.numel() < count:
+        _refuse(where, f"{tuple(t.shape)} of {t.dtype} with strides {t.stride()} for {count} dense 32-bit integers")
+    return t.data_ptr()
+
+
+def _fp32(t, count: int, where: str) -> Optional[int]:
+    if t is None or isinstance(t, int):
+        return t
+    if t.element_size() != 4 or not t.is_floating_point() or not t.is_contiguous() or t.numel() < count:
+        _refuse(where, f"{tuple(t.shape)} of {t.dtype} with strides {t.stride()} for {count} dense fp32 numbers")
+    return t.data_ptr()
+
+
+def kvsel_compact_in_place(params, kv: kvsel_kv, idx, counts, offsets, lens, seen, pos, ws=None, scores=None, acc=None,
+                           stream=None) -> None:
+    """The kept rows of every segment become its first ones, in the cache itself; lens, seen, pos and acc as
+    kvsel_evict_append goes on with them.  pos (and acc): [batch][h_kv][capacity]."""
+    where, segs = "kvsel_compact_in_place", params.batch * params.h_kv
+    capacity = pos.shape[-1]
+    if acc is not None and acc.shape[-1] != capacity:
+        _refuse(where, f"pos {tuple(pos.shape)}, acc {tuple(acc.shape)}")
+    n_scores, n_kept, _ = kvsel_output_size(params)
+    if offsets.element_size() != 8 or not offsets.is_contiguous() or offsets.numel() < segs:
+        _refuse(where, f"offsets {tuple(offsets.shape)} of {offsets.dtype}")
+    st = _place(pos, stream, where)
+    _check(load().kvsel_compact_in_place(
+        params, kv, _int32(idx, n_kept, where), _int32(counts, segs, where), _ptr(offsets), _fp32(scores, n_scores, where),
+        _int32(lens, segs, where), _int32(seen, segs, where), _int32(pos, segs * capacity, where),
+        _fp32(acc, segs * capacity, where), capacity, _ptr(ws), 0 if ws is None else ws.nbytes, st), where)
+
+
+def kvsel_tree_masks(parents, tree, pos=None, first=None, new_lens=None, stream=None) -> None:
+    """Masks (and positions first + depth) of trees: parents [batch][n_new] -> tree [batch][n_new][words]."""
+    where = "kvsel_tree_masks"
+    B, m = parents.shape
+    st = _place(parents, stream, where)
+    _check((_lib or load()).kvsel_tree_masks(
+        _int32(parents, B * m, where), _int32(new_lens, B, where), _int32(first, B, where), B, m,
+        _int32(tree, B * m * ((m + 31) // 32), where), _int32(pos, B * m, where), st), where)
+
+
+def kvsel_attend_tree_workspace_size(params: kvsel_attn_params) -> int:
+    out = ctypes.c_size_t()
+    _check(load().kvsel_attend_tree_workspace_size(ctypes.byref(params), ctypes.byref(out)),
+           "kvsel_attend_tree_workspace_size")
+    return out.value
+
+
+def kvsel_attend_tree(params: kvsel_attn_params, q, kv: kvsel_kv, lens, tree, out, ws, new_lens=None, offsets=None,
+                      lse=None, stream=None) -> None:
+    """Attention of the nodes of a tree over the cache; tree: the masks [batch][n_new][words]."""
+    if params.rows is None:
+        p, B, H = params, params.batch, params.h_kv * params.group
+        p.rows = (_rows(B, H, p.n_new, p.q_stride_req, p.q_stride_head, p.q_stride_tok),
+                  _rows(B, H, p.n_new, p.o_stride_req, p.o_stride_head, p.o_stride_tok))
+    q_rows, o_rows = params.rows
+    q, out = _row_ptr(q, q_rows, "kvsel_attend_tree: q"), _row_ptr(out, o_rows, "kvsel_attend_tree: out")
+    m = params.n_new
+    tree = _int32(tree, params.batch * m * ((m + 31) // 32), "kvsel_attend_tree: tree")
+    st = _place(ws, stream, "kvsel_attend_tree")
+    rc = (_lib or load()).kvsel_attend_tree(params, q, kv, _ptr(lens), _ptr(new_lens), _ptr(offsets), tree, out, _ptr(lse),
+                                            ws.data_ptr(), ws.nbytes, st)
+    if rc:
+        _check(rc, "kvsel_attend_tree")
+
+
+def kvsel_verify_workspace_size(params: kvsel_verify_params) -> int:
+    out = ctypes.c_size_t()
+    _check(load().kvsel_verify_workspace_size(ctypes.byref(params), ctypes.byref(out)), "kvsel_verify_workspace_size")
+    return out.value
+
+
+def _values(t, params: kvsel_verify_params, where: str) -> Optional[int]:
+    """Address of target or draft, whose type and strides have to be as the parameters say."""
+    if t is None or isinstance(t, int):
+        return t
+    p = params
+    req, node = (p.stride_req, p.stride_node) if p.stride_req or p.stride_node else (p.n_new * p.vocab, p.vocab)
+    size = 2 if p.dtype else 4
+    typed = _is_bf16(t) if p.dtype else t.element_size() == 4 and t.is_floating_point()
+    need = size * ((p.batch - 1) * req + (p.n_new - 1) * node + p.vocab)
+    if not typed or t.stride()[-1] != 1 or t.untyped_storage().nbytes() - size * t.storage_offset() < need or (
+            t.dim() == 3 and (t.shape[0] < p.batch or t.shape[1] < p.n_new or t.shape[2] < p.vocab
+                              or (p.batch > 1 and t.stride(0) != req) or (p.n_new > 1 and t.stride(1) != node))):
+        _refuse(where, f"{tuple(t.shape)} of {t.dtype} with strides {t.stride()}")
+    return t.data_ptr()
+
+
+def kvsel_verify(params: kvsel_verify_params, tokens, parents, target, path, counts, next, ws, draft=None, u=None,
+                 new_lens=None, stream=None) -> None:
+    """Which drafted tokens stay (path, counts) and the token after them (next)."""
+    where, B, n = "kvsel_verify", params.batch, params.batch * params.n_new
+    st = _place(ws, stream, where)
+    rc = (_lib or load()).kvsel_verify(
+        params, _int32(tokens, n, where), _int32(parents, n, where), _values(target, params, where), _values(draft, params, where),
+        _fp32(u, n, where), _int32(new_lens, B, where), _int32(path, n, where), _int32(counts, B, where), _int32(next, B, where),
+        ws.data_ptr(), ws.nbytes, st)
+    if rc:
+        _check(rc, where)
+
+
+def kvsel_pages_workspace_size(params: kvsel_pages_params) -> int:
+    out = ctypes.c_size_t()
+    _check(load().kvsel_pages_workspace_size(ctypes.byref(params), ctypes.byref(out)), "kvsel_pages_workspace_size")
+    return out.value
+
+
+def _pool(t, params: kvsel_pages_params, where: str) -> Optional[int]:
+    if isinstance(t, int):
+        return t
+    p = params
+    if not _is_bf16(t) or not t.is_contiguous() or t.numel() < p.layers * p.num_blocks * p.block_size * p.h_kv * p.head_dim:
+        _refuse(where, f"{tuple(t.shape)} of {t.dtype} with strides {t.stride()} for {p.layers} pools")
+    return t.data_ptr()
+
+
+def _segments(params: kvsel_pages_params) -> int:
+    return params.batch * params.h_kv if params.lens_per_head else params.batch
+
+
+def kvsel_pages_fork(params: kvsel_pages_params, table_in, lens_in, src, table_out, lens_out, ref, ws, stream=None) -> None:
+    """Row b of table_out is row src[b] of table_in (-1: none); the uses of the pages follow."""
+    where, n, segs = "kvsel_pages_fork", params.batch * params.max_blocks, _segments(params)
+    st = _place(ws, stream, where)
+    rc = (_lib or load()).kvsel_pages_fork(
+        params, _int32(table_in, n, where), _int32(lens_in, segs, where), _int32(src, params.batch, where),
+        _int32(table_out, n, where), _int32(lens_out, segs, where), _int32(ref, params.num_blocks, where), ws.data_ptr(),
+        ws.nbytes, st)
+    if rc:
+        _check(rc, where)
+
+
+def kvsel_pages_reserve(params: kvsel_pages_params, k, v, table, ref, lens, granted, ws, new_lens=None, stream=None) -> None:
+    """Pages for the new rows of every request; a shared page that they go to is copied, in every layer."""
+    where, B = "kvsel_pages_reserve", params.batch
+    st = _place(ws, stream, where)
+    rc = (_lib or load()).kvsel_pages_reserve(
+        params, _pool(k, params, where), _pool(v, params, where), _int32(table, B * params.max_blocks, where),
+        _int32(ref, params.num_blocks, where), _int32(lens, _segments(params), where), _int32(new_lens, B, where),
+        _int32(granted, B, where), ws.data_ptr(), ws.nbytes, st)
+    if rc:
+        _check(rc, where)
+
+
+def kvsel_pages_trim(params: kvsel_pages_params, table, ref, lens, ws, stream=None) -> None:
+    """Pages behind a request's rows are given back."""
+    where = "kvsel_pages_trim"
+    st = _place(ws, stream, where)
+    rc = (_lib or load()).kvsel_pages_trim(
+        params, _int32(table, params.batch * params.max_blocks, where), _int32(ref, params.num_blocks, where),
+        _int32(lens, _segments(params), where), ws.data_ptr(), ws.nbytes, st)
+    if rc:
+        _check(rc, where)
+
+
+def kvsel_pages_accept(params: kvsel_pages_params, k, v, table, lens, path, counts, lens_out, ws, new_lens=None,
+                       stream=None) -> None:
+    """The rows of the accepted nodes move to the front of the tree's, in every layer."""
+    where, B, segs = "kvsel_pages_accept", params.batch, _segments(params)
+    st = _place(ws, stream, where)
+    rc = (_lib or load()).kvsel_pages_accept(
+        params, _pool(k, params, where), _pool(v, params, where), _int32(table, B * params.max_blocks, where),
+        _int32(lens, segs, where), _int32(new_lens, B, where), _int32(path, B * params.n_new, where), _int32(counts, B, where),
+        _int32(lens_out, segs, where), ws.data_ptr(), ws.nbytes, st)
+    if rc:
+        _check(rc, where)
+
+
+def kvsel_rope_table(*, rot_dim: int = 128, layout: str = "half", theta: float = 10000.0, scaling: str = "none",
+                     factor: float = 1.0, orig_len: int = 0, direction: str = "forward", beta_fast: float = 32.0,
+                     beta_slow: float = 1.0, low_freq: float = 1.0, high_freq: float = 4.0,
+                     value_scale: float = 0.0) -> kvsel_rope_angles:
+    """The angles that kvsel_rope and kvsel_rope_cache take, made once per model and direction."""
+    p = kvsel_rope_params(rot_dim, ROPE_LAYOUT[layout], ROPE_DIRECTION[direction], ROPE_SCALING[scaling], orig_len, theta,
+                          factor, beta_fast, beta_slow, low_freq, high_freq, value_scale)
+    t = kvsel_rope_angles()
+    _check(load().kvsel_rope_table(p, t), "kvsel_rope_table")
+    return t
+
+
+@functools.lru_cache(maxsize=256)
+def _rope_rows(q_shape, q, qo, k_shape, k, ko, pos_shape, pos) -> kvsel_rope_rows:
+    """What kvsel_rope is told of tensors with these shapes and strides."""
+    where, (B, h, n, d) = "kvsel_rope", q_shape
+    hk = k_shape[1] if k_shape else 0
+    if d != 128 or (k_shape and (k_shape[0], *k_shape[2:]) != (B, n, d)) or any(s[3] != 1 for s in (q, qo, k, ko) if s):
+        _refuse(where, f"q {q_shape} with strides {q} and {qo}, k {k_shape} with strides {k} and {ko}")
+    if tuple(pos_shape) not in ((B, n), (n,)) or (n > 1 and pos[-1] != 1):
+        _refuse(where, f"pos {pos_shape} with strides {pos}")
+    zero = (0, 0, 0, 0)
+    return kvsel_rope_rows(B, n, h, hk, *q[:3], *qo[:3], *(k or zero)[:3], *(ko or zero)[:3], pos[0] if len(pos_shape) == 2 else 0)
+
+
+def kvsel_rope(table: kvsel_rope_angles, q, pos, q_out=None, k=None, k_out=None, new_lens=None, stream=None) -> None:
+    """Rows q [batch][heads][tokens][128] (and k, with other heads) turned by pos [batch][tokens] or [tokens];
+    without an output in place."""
+    where = "kvsel_rope"
+    q_out = q if q_out is None else q_out
+    if k is not None and k_out is None:
+        k_out = k
+    for t, like in ((q, q), (q_out, q), (k, k), (k_out, k)):
+        if t is not None and (not _is_bf16(t) or t.shape != like.shape):
+            _refuse(where, f"{tuple(t.shape)} of {t.dtype}")
+    if pos.element_size() != 4 or pos.is_floating_point():
+        _refuse(where, f"pos of {pos.dtype}")
+    p = _rope_rows(q.shape, q.stride(), q_out.stride(), *((k.shape, k.stride(), k_out.stride()) if k is not None else (None,) * 3),
+                   pos.shape, pos.stride())
+    st = _place(q, stream, where)
+    rc = (_lib or load()).kvsel_rope(table, p, q.data_ptr(), q_out.data_ptr(), _ptr(k), _ptr(k_out), pos.data_ptr(),
+                                     _int32(new_lens, p.batch, where), st)
+    if rc:
+        _check(rc, where)
+
+
+def kvsel_rope_cache(table: kvsel_rope_angles, kv: kvsel_kv, lens, pos=None, ws=None, out=None, batch: int = 0,
+                     h_kv: int = 0, max_len: int = 0, stream=None) -> None:
+    """Cached keys turned by pos [batch][h_kv][rows] (None: row j's position is j, with batch, h_kv and max_len
+    given), in place or into out [batch][h_kv][rows][128].  lens: [batch] or [batch][h_kv]."""
+    where = "kvsel_rope_cache"
+    if pos is not None:
+        B, H, n = pos.shape
+    else:
+        B, H, n = batch, h_kv, max_len
+    per_head = lens.numel() != B
+    o = (0, 0, 0)
+    if out is not None:
+        o = out.stride()[:3]
+        if not _is_bf16(out) or out.dim() != 4 or out.stride()[3] != 1 or out.shape[3] != 128 or out.shape[0] < B or (
+                out.shape[1] < H or out.shape[2] < n):
+            _refuse(where, f"out {tuple(out.shape)} of {out.dtype} with strides {out.stride()}")
+    p = kvsel_rope_cache_params(H, B, n, int(per_head), n if pos is not None else 0, *o)
+    st = _place(lens, stream, where)
+    rc = (_lib or load()).kvsel_rope_cache(table, p, kv, _int32(lens, B * H if per_head else B, where), _int32(pos, B * H * n, where),
+                                           _ptr(out), _ptr(ws), 0 if ws is None else ws.nbytes, st)
+    if rc:
+        _check(rc, where)
 
 
 def kvsel_get_device_status(ws, stream=None) -> int:

@@ -67,6 +67,8 @@ struct AttnArgs {
   // -1, CTAs that follow}
   int2* rec;                      // [grid]
   int by_item;
+  const uint32_t* tree;           // [B][m][tree_words]: which of the new tokens' rows a new token sees (TREE)
+  int tree_words;
   int whole;                      // attend_tile_kernel: a CTA per item, no plan, no join
   int grid;                       // CTAs of the kernel that works on the items
   WaitCtl wc;
@@ -118,7 +120,8 @@ struct ItemRange {
   int skip;                       // the last of the segment's items where this and all behind it are empty, else the item
   long long row0;
 };
-template <int TK>
+// TREE: which of the new rows a token sees is in a.tree, and its position is anywhere from n - m to n - 1.
+template <int TK, bool TREE = false>
 __device__ __forceinline__ ItemRange item_range(const AttnArgs& a, int item) {
   ItemRange x;
   const int TR = a.tr;
@@ -139,7 +142,11 @@ __device__ __forceinline__ ItemRange item_range(const AttnArgs& a, int item) {
     x.skip = item - x.rt + a.rt - 1;
     return x;
   }
-  if (a.causal) {
+  if (TREE) {
+    x.p0 = s.n - s.m;
+    x.p1 = s.n - 1;
+    x.hi = s.n;
+  } else if (a.causal) {
     x.p0 = s.n - s.m + a.by_G(r0);
     x.p1 = s.n - s.m + a.by_G(r0 + x.rows - 1);
     x.hi = max(0, x.p1 + 1);
@@ -309,6 +316,39 @@ __device__ __forceinline__ bool sees(const AttnArgs& a, int p, int j) {
   if (!a.causal) return true;
   return j <= p && (a.window <= 0 || j > p - a.window || j < a.n_sink);
 }
+// Node t of request b's tree: the words of its mask, and its position in a segment whose first row of the tree
+// is `base`: it follows the nodes that it sees, itself among them.
+__device__ __forceinline__ const uint32_t* tree_mask(const AttnArgs& a, int b, int t) {
+  return a.tree + (static_cast<long long>(b) * a.m + t) * a.tree_words;
+}
+__device__ __forceinline__ int tree_position(const AttnArgs& a, const uint32_t* mask, int m, int base) {
+  int set = 0;
+  for (int w = 0; w * 32 < m; ++w) {
+    const int left = m - w * 32;
+    set += __popc(__ldg(mask + w) & (left < 32 ? (1u << left) - 1u : ~0u));
+  }
+  return base + max(set, 1) - 1;
+}
+// whether the node with this mask and position p sees cached row j (j < hi of its tile)
+__device__ __forceinline__ bool tree_sees(const AttnArgs& a, const uint32_t* mask, int p, int base, int j) {
+  if (j >= base) return __ldg(mask + ((j - base) >> 5)) >> ((j - base) & 31) & 1u;
+  return a.window <= 0 || j > p - a.window || j < a.n_sink;
+}
+// 64 bits of a mask of m nodes from bit `at` on (at > -64); bit i of the result: node at + i
+__device__ __forceinline__ uint64_t tree_bits(const uint32_t* mask, int m, int at) {
+  uint64_t y = 0;
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    const int w = (at >> 5) + i, s = w * 32 - at;    // the word's place in the result: -31 to 95
+    if (w < 0 || w * 32 >= m || s >= 64) continue;
+    const int left = m - w * 32;
+    const uint64_t x = __ldg(mask + w) & (left < 32 ? (1u << left) - 1u : ~0u);
+    y |= s < 0 ? x >> -s : x << s;
+  }
+  return y;
+}
+// the lowest n bits (n may be negative or more than 64)
+__device__ __forceinline__ uint64_t low_bits(int n) { return n <= 0 ? 0 : n >= 64 ? ~0ull : (1ull << n) - 1; }
 // element offset of cached row j, or -1 (a block-table entry out of range)
 __device__ __forceinline__ long long row_elem(const AttnArgs& a, int b, int h, long long row0, int j) {
   if (!a.src.paged)

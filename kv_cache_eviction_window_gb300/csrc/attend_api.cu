@@ -64,6 +64,12 @@ int check_attn(const kvsel_attn_params* p) {
   return KVSEL_OK;
 }
 
+int check_tree(const kvsel_attn_params* p) {
+  const int rc = check_attn(p);
+  if (rc) return rc;
+  return !p->causal || p->n_new > KVSEL_MAX_TREE ? KVSEL_EUNSUPPORTED : KVSEL_OK;
+}
+
 int plan_attn(const kvsel_attn_params* p, bool with_acc, AttnPlan& pl) {
   int rc = check_attn(p);
   if (rc) return rc;
@@ -238,20 +244,10 @@ EvictLayout evict_layout(const kvsel_evict_params* p) {
 
 }  // namespace
 
-extern "C" {
-
-int kvsel_attend_workspace_size(const kvsel_attn_params* p, int with_acc, size_t* bytes) {
-  if (!bytes) return KVSEL_EINVAL;
-  AttnPlan pl;
-  const int rc = plan_attn(p, with_acc != 0, pl);
-  if (rc) return rc;
-  *bytes = pl.total;
-  return KVSEL_OK;
-}
-
-int kvsel_attend(const kvsel_attn_params* p, const void* q, const kvsel_kv* kv, const int32_t* lens,
-                 const int32_t* new_lens, const int64_t* offsets, void* out, float* lse, float* acc, void* ws,
-                 size_t ws_bytes, void* stream) {
+// kvsel_attend, and with `tree` kvsel_attend_tree
+static int attend(const kvsel_attn_params* p, const void* q, const kvsel_kv* kv, const int32_t* lens,
+                  const int32_t* new_lens, const int64_t* offsets, const uint32_t* tree, void* out, float* lse, float* acc,
+                  void* ws, size_t ws_bytes, void* stream) {
   int rc = check_attn(p);
   if (rc) return rc;
   if (!q || !aligned(q, 16) || !lens || !aligned(lens, 4) || !out || !aligned(out, 16)) return KVSEL_EINVAL;
@@ -303,6 +299,8 @@ int kvsel_attend(const kvsel_attn_params* p, const void* q, const kvsel_kv* kv, 
     a.stride_req = kv->stride_req;
     a.stride_head = kv->stride_head;
   }
+  a.tree = tree;
+  a.tree_words = (p->n_new + 31) / 32;
   a.by_rt = Div::by(pl.rt);
   a.by_H = Div::by(p->h_kv);
   a.by_G = Div::by(p->group);
@@ -336,6 +334,42 @@ int kvsel_attend(const kvsel_attn_params* p, const void* q, const kvsel_kv* kv, 
   if (rc || !acc) return rc;
   if (pl.split && !cache_map(&tk, kv->k, kv, p, attend_tile_rows(false))) return KVSEL_EINVAL;
   return launch_rc(launch_weights_tile(a, tq, tk, pl.block, reinterpret_cast<float*>(wsb + pl.wpart), pl.grid, st));
+}
+
+extern "C" {
+
+int kvsel_attend_workspace_size(const kvsel_attn_params* p, int with_acc, size_t* bytes) {
+  if (!bytes) return KVSEL_EINVAL;
+  AttnPlan pl;
+  const int rc = plan_attn(p, with_acc != 0, pl);
+  if (rc) return rc;
+  *bytes = pl.total;
+  return KVSEL_OK;
+}
+
+int kvsel_attend(const kvsel_attn_params* p, const void* q, const kvsel_kv* kv, const int32_t* lens,
+                 const int32_t* new_lens, const int64_t* offsets, void* out, float* lse, float* acc, void* ws,
+                 size_t ws_bytes, void* stream) {
+  return attend(p, q, kv, lens, new_lens, offsets, nullptr, out, lse, acc, ws, ws_bytes, stream);
+}
+
+int kvsel_attend_tree_workspace_size(const kvsel_attn_params* p, size_t* bytes) {
+  if (!bytes) return KVSEL_EINVAL;
+  int rc = check_tree(p);
+  if (rc) return rc;
+  AttnPlan pl;
+  if ((rc = plan_attn(p, false, pl))) return rc;
+  *bytes = pl.total;
+  return KVSEL_OK;
+}
+
+int kvsel_attend_tree(const kvsel_attn_params* p, const void* q, const kvsel_kv* kv, const int32_t* lens,
+                      const int32_t* new_lens, const int64_t* offsets, const uint32_t* tree, void* out, float* lse,
+                      void* ws, size_t ws_bytes, void* stream) {
+  const int rc = check_tree(p);
+  if (rc) return rc;
+  if (!tree || !aligned(tree, 4)) return KVSEL_EINVAL;
+  return attend(p, q, kv, lens, new_lens, offsets, tree, out, lse, nullptr, ws, ws_bytes, stream);
 }
 
 int kvsel_evict_append_workspace_size(const kvsel_evict_params* p, size_t* bytes) {

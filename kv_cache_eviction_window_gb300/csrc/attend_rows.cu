@@ -81,7 +81,8 @@ __device__ __forceinline__ void mma16816(float c[4], const uint32_t a[4], uint32
 }
 
 // CLUSTER: an item's tiles are cut over the CTAs of a cluster instead, which join them.
-template <bool CLUSTER>
+// TREE: the visibility of the new tokens' rows is in a.tree.
+template <bool CLUSTER, bool TREE>
 __global__ void __launch_bounds__(kThreads, 2) attend_rows_kernel(const AttnArgs a) {
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ float s_m[kWarps][kTR], s_l[kWarps][kTR];
@@ -92,7 +93,7 @@ __global__ void __launch_bounds__(kThreads, 2) attend_rows_kernel(const AttnArgs
   Share<ItemRange> sh{};
   if (!CLUSTER) {
     rec_clear(a);
-    sh = share_of<kThreads, false>(a.B * a.H * a.rt, [&](int i) { return item_range<kTK>(a, i); }, blockIdx.x, kStart);
+    sh = share_of<kThreads, false>(a.B * a.H * a.rt, [&](int i) { return item_range<kTK, TREE>(a, i); }, blockIdx.x, kStart);
     if (static_cast<int>(blockIdx.x) >= sh.grid) return;
   }
   const uint32_t ring = smem_u32(smem) + warp * (kStages * kStageBytes);
@@ -100,7 +101,7 @@ __global__ void __launch_bounds__(kThreads, 2) attend_rows_kernel(const AttnArgs
 
   long long base = sh.item_base;
   for (int item = CLUSTER ? static_cast<int>(blockIdx.x) / cs : sh.item; CLUSTER || base < sh.end; ++item) {
-    const ItemRange x = !CLUSTER && item == sh.item ? sh.first : item_range<kTK>(a, item);
+    const ItemRange x = !CLUSTER && item == sh.item ? sh.first : item_range<kTK, TREE>(a, item);
     int ta, tb;
     if (CLUSTER) {
       if (x.tiles == 0) return;                      // the whole cluster
@@ -150,12 +151,17 @@ __global__ void __launch_bounds__(kThreads, 2) attend_rows_kernel(const AttnArgs
     uint32_t qf[8][4];
     const int r0 = x.rt * kTR;
     int pos[2];
+    const uint32_t* mask[2] = {a.tree, a.tree};
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const int r = r0 + quad + 8 * u;
       const int t = a.by_G(r), g = r - t * a.G;
       const bool live = quad + 8 * u < x.rows;
       pos[u] = live ? (a.causal ? x.n - x.m + t : x.n - 1) : -1;
+      if (TREE && live) {
+        mask[u] = tree_mask(a, x.b, t);
+        pos[u] = tree_position(a, mask[u], x.m, x.n - x.m);
+      }
       const uint16_t* src = a.q + x.b * a.q_req + static_cast<long long>(x.h * a.G + g) * a.q_head +
                             static_cast<long long>(t) * a.q_tok;
 #pragma unroll
@@ -198,7 +204,7 @@ __global__ void __launch_bounds__(kThreads, 2) attend_rows_kernel(const AttnArgs
       // every row of the block sees all 16 cached rows: no element masks
       const bool whole =
           j0 + kUnit <= j1 &&
-          (!a.causal || (j0 + kUnit <= x.p0 + 1 && (a.window <= 0 || j0 > x.p1 - a.window || j0 + kUnit <= a.n_sink)));
+          (!a.causal || (j0 + kUnit <= x.p0 + (TREE ? 0 : 1) && (a.window <= 0 || j0 > x.p1 - a.window || j0 + kUnit <= a.n_sink)));
       float p[2][4];
       float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
@@ -208,7 +214,9 @@ __global__ void __launch_bounds__(kThreads, 2) attend_rows_kernel(const AttnArgs
           float y = c[nt][i] * a.s2;
           if (!whole) {
             const int j = j0 + nt * 8 + ql * 2 + (i & 1);
-            if (j >= j1 || !sees(a, pos[i >> 1], j)) y = -INFINITY;
+            if (j >= j1 ||
+                !(TREE ? tree_sees(a, mask[i >> 1], pos[i >> 1], x.n - x.m, j) : sees(a, pos[i >> 1], j)))
+              y = -INFINITY;
           }
           p[nt][i] = y;
           top[i >> 1] = fmaxf(top[i >> 1], y);
@@ -218,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, 2) attend_rows_kernel(const AttnArgs
         top[u2] = fmaxf(top[u2], __shfl_xor_sync(0xffffffffu, top[u2], 1));
         top[u2] = fmaxf(top[u2], __shfl_xor_sync(0xffffffffu, top[u2], 2));
       }
-      if (a.logits) {
+      if (!TREE && a.logits) {
         // kept for the weights, which need the whole row's sum first (4 B per row and query row
         // instead of reading K again)
 #pragma unroll
@@ -452,7 +460,7 @@ int clusters_at_once(int c) {
     const int n = known[dev][c].load(std::memory_order_relaxed);
     if (n) return n - 1;
   }
-  const void* kernel = reinterpret_cast<const void*>(attend_rows_kernel<true>);
+  const void* kernel = reinterpret_cast<const void*>(attend_rows_kernel<true, false>);
   cudaLaunchAttribute attr[1];
   const cudaLaunchConfig_t cfg = cluster_config(c, c, nullptr, attr);
   int n = 0;
@@ -489,7 +497,8 @@ int attend_rows_cluster(long long items, long long tiles, bool window, int grid)
 }
 
 cudaError_t launch_attend_rows(const AttnArgs& a, int grid, int cluster, cudaStream_t st) {
-  const auto kernel = cluster ? attend_rows_kernel<true> : attend_rows_kernel<false>;
+  const auto kernel = a.tree ? (cluster ? attend_rows_kernel<true, true> : attend_rows_kernel<false, true>)
+                             : (cluster ? attend_rows_kernel<true, false> : attend_rows_kernel<false, false>);
   cudaError_t e = ensure_smem(reinterpret_cast<const void*>(kernel), kSmem);
   if (e != cudaSuccess) return e;
   if (cluster) {

@@ -119,7 +119,8 @@ __device__ __forceinline__ void regs_down() {
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-template <bool SPLIT>
+// TREE: the visibility of the new tokens' rows is in a.tree
+template <bool SPLIT, bool TREE>
 __global__ void __launch_bounds__(kThreads, 1)
     attend_tile_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                        const __grid_constant__ CUtensorMap tv, const AttnArgs a, const int block) {
@@ -162,7 +163,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&tk);
     tma_prefetch_desc(&tv);
   }
-  const auto& sh = share_of<kThreads>(a.B * a.H * a.rt, [&](int i) { return item_range<kTK>(a, i); }, blockIdx.x, kStart,
+  const auto& sh = share_of<kThreads>(a.B * a.H * a.rt, [&](int i) { return item_range<kTK, TREE>(a, i); }, blockIdx.x, kStart,
                                       a.whole);
   if (static_cast<int>(blockIdx.x) >= sh.grid) return;   // the whole CTA
   if (warp == kQkWarp) {
@@ -185,7 +186,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;                                  // the same in every lane
     long long base = sh.item_base;
     for (int item = sh.item; ok && base < sh.end; ++item) {
-      const ItemRange x = item == sh.item ? sh.first : item_range<kTK>(a, item);
+      const ItemRange x = item == sh.item ? sh.first : item_range<kTK, TREE>(a, item);
       int ta, tb;
       if (!next_piece(sh, item, x, base, ta, tb)) continue;
       const int cnt = tb - ta;
@@ -267,7 +268,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tS = tbase + w * 128, tO = tbase + 256 + w * 128;
     long long base = sh.item_base;
     for (int item = sh.item; ok && base < sh.end; ++item) {
-      const ItemRange x = item == sh.item ? sh.first : item_range<kTK>(a, item);
+      const ItemRange x = item == sh.item ? sh.first : item_range<kTK, TREE>(a, item);
       int ta, tb;
       if (!next_piece(sh, item, x, base, ta, tb)) continue;
       const int cnt = tb - ta;
@@ -333,17 +334,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     long long base = sh.item_base;
     for (int item = sh.item; ok && base < sh.end; ++item) {
-      const ItemRange x = item == sh.item ? sh.first : item_range<kTK>(a, item);
+      const ItemRange x = item == sh.item ? sh.first : item_range<kTK, TREE>(a, item);
       int ta, tb;
       if (!next_piece(sh, item, x, base, ta, tb)) continue;
       const int cnt = tb - ta;
       const int first_row = SPLIT ? 0 : w * block;   // of the item
       const int rows = min(block, x.rows - first_row);
       const int rr = x.rt * a.tr + first_row + row;  // row of the segment
-      const int p = a.causal ? x.n - x.m + a.by_G(rr) : x.n - 1;
-      // cache rows of the block's first and last token
-      const int pa = a.causal ? x.n - x.m + a.by_G(x.rt * a.tr + first_row) : x.n - 1;
-      const int pb = a.causal ? x.n - x.m + a.by_G(x.rt * a.tr + first_row + max(rows, 1) - 1) : x.n - 1;
+      const int tree0 = x.n - x.m;                   // TREE: the first row of the tree
+      const uint32_t* mask = TREE ? tree_mask(a, x.b, row < rows ? a.by_G(rr) : 0) : nullptr;
+      const int p = TREE ? tree_position(a, mask, x.m, tree0) : a.causal ? x.n - x.m + a.by_G(rr) : x.n - 1;
+      // cache rows of the block's first and last token (TREE: all see the rows up to pa; none is behind pb)
+      const int pa = TREE ? tree0 - 1 : a.causal ? x.n - x.m + a.by_G(x.rt * a.tr + first_row) : x.n - 1;
+      const int pb = TREE ? x.p1 : a.causal ? x.n - x.m + a.by_G(x.rt * a.tr + first_row + max(rows, 1) - 1) : x.n - 1;
       float ref = -INFINITY, sum = 0.f;
       int mine = 0;                                  // steps of this piece so far
       const int steps = 2 * (SPLIT ? (cnt + 1 - w) / 2 : cnt);
@@ -363,7 +366,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld_wait();
         const bool whole = js + 64 <= j1 && (!a.causal || (js + 64 <= pa + 1 &&
                                                            (a.window <= 0 || js > pb - a.window || js + 64 <= a.n_sink)));
-        if (!whole) {
+        if (TREE && !whole) {
+          // columns before the tree: below `hi`, and not in [first, lo); the others by the node's mask
+          const int hi = min(j1, tree0) - js;
+          const int lo = a.window > 0 ? p - a.window + 1 - js : 0, first = a.window > 0 ? a.n_sink - js : 0;
+          const uint64_t see = (low_bits(hi) & ~(low_bits(lo) & ~low_bits(first))) |
+                               (js + 64 > tree0 ? tree_bits(mask, x.m, js - tree0) & low_bits(j1 - js) : 0);
+          const uint32_t see0 = static_cast<uint32_t>(see), see1 = static_cast<uint32_t>(see >> 32);
+#pragma unroll
+          for (int c = 0; c < 64; ++c)
+            if (!((c < 32 ? see0 : see1) >> (c & 31) & 1u)) s[c] = -INFINITY;
+        } else if (!whole) {
           // a row sees columns [0, hi) and, with a window, of these [lo, hi) and those below `first`
           const int hi = min(j1, a.causal ? p + 1 : j1) - js;
           const int lo = a.window > 0 ? p - a.window + 1 - js : -1, first = a.window > 0 ? a.n_sink - js : 0;
@@ -606,7 +619,8 @@ bool attend_tile_whole(long long items, long long tiles, bool split, int grid) {
 
 cudaError_t launch_attend_tile(const AttnArgs& a, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                                int block, bool split, int grid, cudaStream_t st) {
-  const auto kernel = split ? attend_tile_kernel<true> : attend_tile_kernel<false>;
+  const auto kernel = a.tree ? (split ? attend_tile_kernel<true, true> : attend_tile_kernel<false, true>)
+                             : (split ? attend_tile_kernel<true, false> : attend_tile_kernel<false, false>);
   cudaError_t e = ensure_smem(reinterpret_cast<const void*>(kernel), kSmem);
   if (e != cudaSuccess) return e;
   kernel<<<a.whole ? a.B * a.H * a.rt : grid, kThreads, kSmem, st>>>(tq, tk, tv, a, block);

@@ -13,6 +13,7 @@
 
 #include "../../include/kvsel.h"
 #include "internal.cuh"
+#include "step.cuh"
 
 using namespace kvsel;
 
@@ -1074,6 +1075,41 @@ int kvsel_compact(const kvsel_params* p, const kvsel_kv* kv, const int32_t* idx,
   if (ws && ws_bytes < kStatusBytes) return KVSEL_EWORKSPACE;
   if (pl.n_kept == 0) return KVSEL_OK;
   return do_compact(pl, kv, idx, counts, offsets, k_out, v_out, ws, static_cast<cudaStream_t>(stream));
+}
+
+int kvsel_compact_in_place(const kvsel_params* p, const kvsel_kv* kv, const int32_t* idx, const int32_t* counts,
+                           const int64_t* offsets, const float* scores, int32_t* lens, int32_t* seen, int32_t* pos,
+                           float* acc, int64_t capacity, void* ws, size_t ws_bytes, void* stream) {
+  Plan pl;
+  int rc = make_plan(p, pl, false);
+  if (rc) return rc;
+  if (!idx || !counts || !offsets || !lens || !pos || capacity < pl.n_max) return KVSEL_EINVAL;
+  const uintptr_t words = reinterpret_cast<uintptr_t>(idx) | reinterpret_cast<uintptr_t>(counts) |
+                          reinterpret_cast<uintptr_t>(scores) | reinterpret_cast<uintptr_t>(lens) |
+                          reinterpret_cast<uintptr_t>(seen) | reinterpret_cast<uintptr_t>(pos) | reinterpret_cast<uintptr_t>(acc);
+  if ((words & 3) || (reinterpret_cast<uintptr_t>(offsets) & 7)) return KVSEL_EINVAL;
+  if ((rc = check_kv(kv, pl, true))) return rc;
+  if (ws && (ws_bytes < kStatusBytes || !aligned16(ws))) return KVSEL_EWORKSPACE;
+  KeepArgs a{};
+  a.rq = pl.rq;
+  a.src = kv_source(kv);
+  a.k = static_cast<uint16_t*>(const_cast<void*>(kv->k));
+  a.v = static_cast<uint16_t*>(const_cast<void*>(kv->v));
+  a.stride_req = kv->stride_req;
+  a.stride_head = kv->stride_head;
+  a.stride_tok = kv->stride_tok;
+  a.idx = idx;
+  a.counts = counts;
+  a.offsets = offsets;
+  a.n_kept = pl.n_kept;
+  a.scores = scores;
+  a.lens = lens;
+  a.seen = seen;
+  a.pos = pos;
+  a.acc = acc;
+  a.capacity = capacity;
+  a.status = static_cast<int*>(ws);
+  return launch_keep(a, pl.max_count, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KVSEL_OK : KVSEL_ECUDA;
 }
 
 int kvsel_partition(const kvsel_params* p, const kvsel_kv* kv, const int32_t* idx, const int32_t* counts,
