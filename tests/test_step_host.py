@@ -293,12 +293,12 @@ def test_oracle_follows_the_target(kids):
 
     def walk(t, tokens, us, weight):
         if t > kids:
-            for cell in range(32):
-                path, nxt = SO.verify([0] + tokens, [-1] + [0] * kids, rows, drafts, [(cell + 0.5) / 32] + us, "sampled")
-                total[tokens[path[1] - 1] if len(path) > 1 else nxt] += weight / 32
+            for cell in range(48):
+                path, nxt = SO.verify([0] + tokens, [-1] + [0] * kids, rows, drafts, [(cell + 0.5) / 48] + us, "sampled")
+                total[tokens[path[1] - 1] if len(path) > 1 else nxt] += weight / 48
             return
         for x in range(3):
-            # with u in the middle of 16 cells: every border that these numbers have lies between cells
+            # u in the middle of 16 cells (and u_0 of 48): the borders, 1/4 and 2/3, lie between cells
             for cell in range(16):
                 walk(t + 1, tokens + [x], us + [(cell + 0.5) / 16], weight * q[x] / 16)
 
