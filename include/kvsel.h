@@ -632,7 +632,7 @@ int kvsel_verify_workspace_size(const kvsel_verify_params* p, size_t* bytes);
  * lowest x with the largest p_c(x) (any values, logits will do; NaN is below all), and next is that x.
  *   tokens   device int32 [batch][n_new], parents likewise (as kvsel_tree_masks takes them)
  *   target   device, strides above, 4-byte (fp32) or 2-byte (bf16) aligned: rows of probabilities that sum to 1
- *            (a value counts as what it is in [0, 1], to 2^-47; NaN as 0)
+ *            (a value counts as what it is in [0, 1], to 2^-46; NaN as 0)
  *   draft    device, as target (SAMPLED), else NULL
  *   u        device fp32 [batch][n_new], uniform in [0, 1): u_t of node t's test, u_0 of the last draw
  *            (NULL when GREEDY)
@@ -641,7 +641,7 @@ int kvsel_verify_workspace_size(const kvsel_verify_params* p, size_t* bytes);
  *   counts   device int32 [batch]: entries of path (0 for a request without nodes, whose next is -1)
  *   next     device int32 [batch]
  *   ws       workspace of kvsel_verify_workspace_size bytes, 256-byte aligned
- * Sums are exact (64-bit integers in units of 2^-46), so results do not depend on their order.  A token
+ * Sums are exact (64-bit integers in units of 2^-45), so results do not depend on their order.  A token
  * outside [0, vocab) is never accepted, takes nothing from the rest, and is recorded in the status
  * word with a node count out of range (clamped) and a parent outside [0, t) (the node is ignored). */
 int kvsel_verify(const kvsel_verify_params* p, const int32_t* tokens, const int32_t* parents, const void* target,
@@ -757,7 +757,7 @@ int kvsel_rope_table(const kvsel_rope_params* p, kvsel_rope_angles* table);
 /* Rows of one or two tensors (queries and keys) that share their positions. */
 typedef struct kvsel_rope_rows {
   int32_t batch;         /* requests, 1..65535                                               */
-  int32_t n_tok;         /* tokens of a request at most, 1..2^20                             */
+  int32_t n_tok;         /* tokens of a request at most, 1..2^20; batch * n_tok <= 2^31 - 64 */
   int32_t heads, k_heads;   /* heads of q (>= 1) and of k (0: none), 8192 at most together   */
   int64_t q_req, q_head, q_tok;          /* strides of q in elements, multiples of 8; columns contiguous */
   int64_t qo_req, qo_head, qo_tok;       /* of q_out                                         */

@@ -22,7 +22,7 @@ struct VerifyArgs {
   int32_t* next;
   int* status;
 };
-cudaError_t launch_verify(const VerifyArgs& a, int batch, bool bf16, cudaStream_t st);
+cudaError_t launch_verify(const VerifyArgs& a, int batch, bool bf16, int sms, cudaStream_t st);
 
 struct PagesArgs {
   int H, B, block_size, shift, max_blocks, num_blocks, layers;
@@ -55,8 +55,8 @@ cudaError_t launch_pages_trim(const PagesArgs& a, cudaStream_t st);
 cudaError_t launch_pages_accept(const PagesArgs& a, cudaStream_t st);
 
 struct RopeTable {
-  unsigned long long turns[64];
-  int rot, interleaved, back;
+  unsigned long long turns[64];   // of one position, in units of 2^-64 turns; turned back: their negatives
+  int rot, interleaved;
   float scale;
 };
 struct RopeArgs {
@@ -85,7 +85,7 @@ struct RopeCacheArgs {
   long long o_req, o_head, o_tok;
   int* status;                    // may be null
 };
-cudaError_t launch_rope_cache(const RopeCacheArgs& a, int sms, cudaStream_t st);
+cudaError_t launch_rope_cache(const RopeCacheArgs& a, cudaStream_t st);
 
 struct KeepArgs {
   ReqTable rq;

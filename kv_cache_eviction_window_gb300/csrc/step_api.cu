@@ -91,10 +91,9 @@ bool words(std::initializer_list<const void*> list) {
 
 RopeTable rope_table(const kvsel_rope_angles* t) {
   RopeTable r;
-  std::memcpy(r.turns, t->turns, sizeof(r.turns));
+  for (int i = 0; i < 64; ++i) r.turns[i] = t->back ? 0 - t->turns[i] : t->turns[i];
   r.rot = t->rot_dim;
   r.interleaved = t->layout == KVSEL_ROPE_INTERLEAVED;
-  r.back = t->back;
   r.scale = t->scale;
   return r;
 }
@@ -151,7 +150,9 @@ int kvsel_verify(const kvsel_verify_params* p, const int32_t* tokens, const int3
   a.counts = counts;
   a.next = next;
   a.status = static_cast<int*>(ws);
-  return launch_rc(launch_verify(a, p->batch, p->dtype == KVSEL_DTYPE_BF16, static_cast<cudaStream_t>(stream)));
+  int sms = 0;
+  if ((rc = device_sms(&sms))) return rc;
+  return launch_rc(launch_verify(a, p->batch, p->dtype == KVSEL_DTYPE_BF16, sms, static_cast<cudaStream_t>(stream)));
 }
 
 int kvsel_pages_workspace_size(const kvsel_pages_params* p, size_t* bytes) {
@@ -288,7 +289,7 @@ int kvsel_rope(const kvsel_rope_angles* table, const kvsel_rope_rows* p, const v
                void* k_out, const int32_t* pos, const int32_t* new_lens, void* stream) {
   if (bad_table(table) || !p) return KVSEL_EINVAL;
   if (p->batch < 1 || p->n_tok < 1 || p->heads < 1 || p->k_heads < 0 || p->pos_req < 0) return KVSEL_EINVAL;
-  if (p->batch > 65535 || p->n_tok > (1 << 20) || p->heads > 8192 || p->k_heads > 8192 || p->heads + p->k_heads > 8192)
+  if (p->batch > 65535 || p->n_tok > (1 << 20) || static_cast<long long>(p->batch) * p->n_tok > (1ll << 31) - 64 || p->heads > 8192 || p->k_heads > 8192 || p->heads + p->k_heads > 8192)
     return KVSEL_EUNSUPPORTED;
   if (!q || !q_out || !aligned(q, 16) || !aligned(q_out, 16) || !pos || !aligned(pos, 4) || !aligned(new_lens, 4)) return KVSEL_EINVAL;
   if (p->k_heads && (!k || !k_out || !aligned(k, 16) || !aligned(k_out, 16))) return KVSEL_EINVAL;
@@ -375,9 +376,7 @@ int kvsel_rope_cache(const kvsel_rope_angles* table, const kvsel_rope_cache_para
   a.o_head = p->o_head;
   a.o_tok = p->o_tok;
   a.status = static_cast<int*>(ws);
-  int sms = 0;
-  const int rc = device_sms(&sms);
-  return rc ? rc : launch_rc(launch_rope_cache(a, sms, static_cast<cudaStream_t>(stream)));
+  return launch_rc(launch_rope_cache(a, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

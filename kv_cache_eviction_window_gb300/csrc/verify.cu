@@ -8,7 +8,7 @@
 // of them walk down the tree alike.  The rest of a node c after k rejections is r = max(p_c - A q_c, 0),
 // A the masses before each of them (q is positive: taking it off twice or as a sum is the same), so only a
 // sum over the vocabulary is needed where a sibling follows, and one for the last draw.  Probabilities
-// count as integers in units of 2^-46 there: sums are exact and do not depend on their order, 2^18 of them
+// count as integers in units of 2^-45 there: sums are exact and do not depend on their order, 2^18 of them
 // fit 64 bits, and the draw is the comparison of integers.
 // Bound: latency; a row of p and q is read for each rejection that a sibling follows and for the last draw.
 #include <cooperative_groups.h>
@@ -53,9 +53,10 @@ __global__ void __launch_bounds__(1024) tree_masks_kernel(const int32_t* __restr
   if (pos) pos[row + t] = __ldg(first + b) + depth;
 }
 
-constexpr int kThreads = 512, kWarps = kThreads / 32;
-constexpr int kCluster = 8;
-constexpr int kUnitBits = 46;                        // probabilities in units of 2^-46
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kMaxCluster = 16;
+constexpr int kUnitBits = 45;                        // probabilities in units of 2^-45
+constexpr unsigned long long kOne = 1ull << kUnitBits;
 
 template <class T>
 __device__ __forceinline__ float value_of(T x);
@@ -64,92 +65,153 @@ __device__ __forceinline__ float value_of<float>(float x) { return x; }
 template <>
 __device__ __forceinline__ float value_of<uint16_t>(uint16_t x) { return __uint_as_float(static_cast<uint32_t>(x) << 16); }
 
-// a probability in [0, 1] (NaN: 0), and in units of 2^-46, rounded
-__device__ __forceinline__ float prob(float x) { return fminf(fmaxf(x, 0.f), 1.f); }
-__device__ __forceinline__ unsigned long long units(float x) {
-  return __float2ull_rn(prob(x) * 70368744177664.f);
+// a probability in [0, 1] (NaN: 0)
+__device__ __forceinline__ float prob(float x) { return __saturatef(x); }
+// x in [0, 1] as hi 2^-22 + lo 2^-45, rounded to that: adding 2^23 leaves an integer in the last bits of a number.
+// (A conversion to 64 bits takes a quarter of a cycle per SM: 25 us for 64 rows of 131072.)
+struct Parts {
+  int hi, lo;
+};
+__device__ __forceinline__ Parts parts(float x) {
+  const float y = fmaf(x, 4194304.f, 8388608.f);
+  const float r = fmaf(x, 4194304.f, 8388608.f - y);           // exact, in [-1/2, 1/2]
+  return Parts{__float_as_int(y) - 0x4B000000, __float_as_int(fmaf(r, 8388608.f, 12582912.f)) - 0x4B400000};
 }
-// max(p - A q, 0) in units; A in units, below 2^56
+__device__ __forceinline__ long long whole(long long hi, int lo) { return hi * 8388608 + lo; }
+__device__ __forceinline__ unsigned long long units(float x) {
+  const Parts a = parts(prob(x));
+  return whole(a.hi, a.lo);
+}
+// max(p - A q, 0) in units; A in units, below 2^55
 __device__ __forceinline__ unsigned long long rest_units(float p, float q, unsigned long long A) {
   const unsigned long long P = units(p), Q = units(q);
-  const unsigned long long AQ = __umul64hi(A << 8, Q << 10);
+  const unsigned long long AQ = A == kOne ? Q : __umul64hi(A << 9, Q << 10);
   return P > AQ ? P - AQ : 0;
 }
-// larger value, larger key; ties: the lower token; NaN below all
-__device__ __forceinline__ unsigned long long arg_key(float x, int i) {
-  uint32_t k = 0;
-  if (x == x) {
-    const uint32_t u = __float_as_uint(x == 0.f ? 0.f : x);
-    k = (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-  }
-  return (static_cast<unsigned long long>(k) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(i));
-}
 
-// Vectors of 16 bytes of a row: elements [i0, i1) of it, by the threads of a group; f(i, x...) for each.
-template <class T, class F>
-__device__ __forceinline__ void each_of(const T* p, int i0, int i1, int at, int step, F f) {
+// Elements [i0, i1) of a row (or of two at the same places) by the lanes of a warp, 16 bytes at a time and kAhead
+// of these loaded before the first is used: f(i, x, y) for each, in ascending order within a lane; g() after as many.
+constexpr int kAhead = 4;
+template <bool TWO, class T, class F, class G>
+__device__ __forceinline__ void each_of(const T* p, const T* q, int i0, int i1, F f, G g) {
   constexpr int N = 16 / sizeof(T);
+  const int lane = lane_id();
   // the first element on a 16-byte boundary
   const int lead = static_cast<int>(((16 - (reinterpret_cast<uintptr_t>(p + i0) & 15)) & 15) / sizeof(T));
   const int v0 = min(i1, i0 + lead), nv = (i1 - v0) / N, v1 = v0 + nv * N;
-  if (at < v0 - i0) f(i0 + at, p[i0 + at]);
-  if (at < i1 - v1) f(v1 + at, p[v1 + at]);
-#pragma unroll 2
-  for (int u = at; u < nv; u += step) {
-    const uint4 raw = __ldg(reinterpret_cast<const uint4*>(p + v0) + u);
-    T x[N];
-    memcpy(x, &raw, 16);
-#pragma unroll
-    for (int c = 0; c < N; ++c) f(v0 + u * N + c, x[c]);
-  }
-}
-template <class T, class F>
-__device__ __forceinline__ void each_of(const T* p, const T* q, int i0, int i1, int at, int step, F f) {
-  constexpr int N = 16 / sizeof(T);
-  const int lead = static_cast<int>(((16 - (reinterpret_cast<uintptr_t>(p + i0) & 15)) & 15) / sizeof(T));
-  const int v0 = min(i1, i0 + lead), nv = (i1 - v0) / N, v1 = v0 + nv * N;
-  const bool alike = ((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(q)) & 15) == 0;
-  if (at < v0 - i0) f(i0 + at, p[i0 + at], q[i0 + at]);
-  if (at < i1 - v1) f(v1 + at, p[v1 + at], q[v1 + at]);
-  if (alike) {
-#pragma unroll 2
-    for (int u = at; u < nv; u += step) {
-      const uint4 rp = __ldg(reinterpret_cast<const uint4*>(p + v0) + u), rq = __ldg(reinterpret_cast<const uint4*>(q + v0) + u);
-      T x[N], y[N];
-      memcpy(x, &rp, 16);
-      memcpy(y, &rq, 16);
-#pragma unroll
-      for (int c = 0; c < N; ++c) f(v0 + u * N + c, x[c], y[c]);
+  if (TWO && ((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(q)) & 15)) {
+    for (int i = i0 + lane; i < i1; i += 32) {
+      f(i, p[i], q[i]);
+      g();
     }
-  } else {
-    for (int i = v0 + at; i < v1; i += step) f(i, p[i], q[i]);
+    return;
   }
+  if (lane < v0 - i0) f(i0 + lane, p[i0 + lane], TWO ? q[i0 + lane] : T());
+  for (int u0 = lane; u0 < nv; u0 += 32 * kAhead) {
+    uint4 rp[kAhead], rq[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+      if (u0 + 32 * k < nv) {
+        rp[k] = __ldg(reinterpret_cast<const uint4*>(p + v0) + u0 + 32 * k);
+        if (TWO) rq[k] = __ldg(reinterpret_cast<const uint4*>(q + v0) + u0 + 32 * k);
+      }
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+      if (u0 + 32 * k < nv) {
+        T x[N], y[N];
+        memcpy(x, &rp[k], 16);
+        if (TWO) memcpy(y, &rq[k], 16);
+#pragma unroll
+        for (int c = 0; c < N; ++c) f(v0 + (u0 + 32 * k) * N + c, x[c], TWO ? y[c] : T());
+      }
+    g();
+  }
+  if (lane < i1 - v1) f(v1 + lane, p[v1 + lane], TWO ? q[v1 + lane] : T());
+  g();
 }
 
-__device__ __forceinline__ unsigned long long warp_sum(unsigned long long v) {
+// The largest value of elements [i0, i1) of a row and the lowest place that has it, by the lanes of a warp (each
+// its own; at = -1: none but NaN): vectors first, then the place in the vector that has it.
+__device__ __forceinline__ float vector_max(const uint4& v, float) {
+  return fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)), fmaxf(__uint_as_float(v.z), __uint_as_float(v.w)));
+}
+__device__ __forceinline__ float vector_max(const uint4& v, uint16_t) {
+  __nv_bfloat162 x[4];
+  memcpy(x, &v, 16);
+  const float2 y = __bfloat1622float2(__hmax2(__hmax2(x[0], x[1]), __hmax2(x[2], x[3])));
+  return fmaxf(y.x, y.y);
+}
+template <class T>
+__device__ __forceinline__ void largest_of(const T* p, int i0, int i1, float& top, int& at) {
+  constexpr int N = 16 / sizeof(T), kLoads = 8;
+  const int lane = lane_id();
+  const int lead = static_cast<int>(((16 - (reinterpret_cast<uintptr_t>(p + i0) & 15)) & 15) / sizeof(T));
+  const int v0 = min(i1, i0 + lead), nv = (i1 - v0) / N, v1 = v0 + nv * N;
+  top = -INFINITY;
+  at = -1;
+  auto look = [&](float y, int i) {
+    if (y > top || (at < 0 && y == y)) {
+      top = y;
+      at = i;
+    }
+  };
+  // what lies before and behind the vectors: at most one element per lane
+  float edge[2] = {__int_as_float(0x7FC00000), __int_as_float(0x7FC00000)};
+  if (lane < v0 - i0) edge[0] = value_of<T>(p[i0 + lane]);
+  if (lane < i1 - v1) edge[1] = value_of<T>(p[v1 + lane]);
+  for (int u0 = lane; u0 < nv; u0 += 32 * kLoads) {
+    uint4 r[kLoads];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
+    for (int k = 0; k < kLoads; ++k)
+      if (u0 + 32 * k < nv) r[k] = __ldg(reinterpret_cast<const uint4*>(p + v0) + u0 + 32 * k);
+    if (u0 == lane) look(edge[0], i0 + lane);
+#pragma unroll
+    for (int k = 0; k < kLoads; ++k)
+      if (u0 + 32 * k < nv) look(vector_max(r[k], T()), v0 + (u0 + 32 * k) * N);
+  }
+  if (lane >= nv) look(edge[0], i0 + lane);          // (no vector of this lane's)
+  if (at >= v0) {
+    const uint4 r = __ldg(reinterpret_cast<const uint4*>(p + at));
+    T x[N];
+    memcpy(x, &r, 16);
+    int c = 0;
+#pragma unroll
+    for (int i = N - 1; i >= 0; --i)
+      if (value_of<T>(x[i]) == top) c = i;
+    at += c;
+  }
+  look(edge[1], v1 + lane);
+}
+
+// sums and maxima over a warp by its integer reductions: 27 bits at a time (a sum of 32 fits 32 bits), or a key's
+// high word and then, of those that have it, the low word
+__device__ __forceinline__ unsigned long long warp_sum(unsigned long long v) {
+  const uint32_t a = __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(v) & 0x7FFFFFFu);
+  const uint32_t b = __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(v >> 27) & 0x7FFFFFFu);
+  const uint32_t c = __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(v >> 54));
+  return a + (static_cast<unsigned long long>(b) << 27) + (static_cast<unsigned long long>(c) << 54);
 }
 __device__ __forceinline__ unsigned long long warp_max(unsigned long long v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
-  return v;
+  const uint32_t hi = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(v >> 32));
+  const uint32_t lo = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(v >> 32) == hi ? static_cast<uint32_t>(v) : 0u);
+  return static_cast<unsigned long long>(hi) << 32 | lo;
 }
 
 enum Want : int { kMass, kDraw, kLargest, kDone };
+// of a node: its token is one, its first test (A = 0, Z = 1) passes, an earlier sibling has its token (POINT)
+enum Flag : int { kValid = 1, kPasses = 2, kAgain = 4 };
 struct Shared {
-  int par[KVSEL_MAX_TREE], tok[KVSEL_MAX_TREE];
+  int par[KVSEL_MAX_TREE], tok[KVSEL_MAX_TREE], flag[KVSEL_MAX_TREE];
   float p[KVSEL_MAX_TREE], q[KVSEL_MAX_TREE], u[KVSEL_MAX_TREE];
-  int out[KVSEL_MAX_TREE];                           // POINT: tokens rejected at the present node
-  unsigned long long warp[kWarps];                   // sums of the warps' shares
-  unsigned long long part[2][kWarps + 1];            // of this CTA, for the cluster: total, then by warp
-  int cur, nout, want;
+  int out[KVSEL_MAX_TREE], nout;                     // POINT: nodes whose tokens have no weight in the draw
+  // what every warp of the cluster found in its share of the vocabulary, written by that warp to all CTAs
+  unsigned long long part[2][kMaxCluster * kWarps];
+  int cur, want;
   unsigned long long A;
 };
 
-template <class T>
-__global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs a) {
+template <class T, int MODE>
+__global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a) {
   __shared__ Shared s;
   cgx::cluster_group cl = cgx::this_cluster();
   const int cs = static_cast<int>(cl.num_blocks()), rank = static_cast<int>(cl.block_rank());
@@ -157,27 +219,35 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs a) {
   const T* target = static_cast<const T*>(a.target) + b * a.stride_req;
   const T* draft = a.draft ? static_cast<const T*>(a.draft) + b * a.stride_req : nullptr;
   const long long row = static_cast<long long>(b) * a.m;
+  constexpr bool greedy = MODE == KVSEL_VERIFY_GREEDY, point = MODE == KVSEL_VERIFY_POINT, sampled = MODE == KVSEL_VERIFY_SAMPLED;
   const int raw = a.new_lens ? __ldg(a.new_lens + b) : a.m, m = min(max(raw, 0), a.m);
   bool bad = raw != m;
   for (int t = tid; t < m; t += kThreads) {
     int p = t ? a.parents[row + t] : -1;
     const int x = a.tokens[row + t];
+    const float u = a.u ? a.u[row + t] : 0.f;
+    float pv = 0.f, qv = 1.f;
+    int flag = 0;
     if (t && (p < 0 || p >= t)) {
       bad = true;
       p = -1;
     }
-    float pv = 0.f, qv = 1.f;
     if (t && (x < 0 || x >= a.vocab)) {
       bad = true;
-    } else if (t && p >= 0 && a.mode != KVSEL_VERIFY_GREEDY) {
-      pv = prob(value_of<T>(target[p * a.stride_node + x]));
-      if (draft) qv = prob(value_of<T>(draft[p * a.stride_node + x]));
+    } else if (t && p >= 0) {
+      flag = kValid;
+      if (!greedy) {
+        pv = prob(value_of<T>(target[p * a.stride_node + x]));
+        if (sampled) qv = prob(value_of<T>(draft[p * a.stride_node + x]));
+        if (static_cast<double>(u) * qv < static_cast<double>(pv)) flag |= kPasses;
+      }
     }
     s.par[t] = p;
     s.tok[t] = x;
+    s.flag[t] = flag;
     s.p[t] = pv;
     s.q[t] = qv;
-    s.u[t] = a.u ? a.u[row + t] : 0.f;
+    s.u[t] = u;
   }
   for (int t = tid + (rank ? a.m : 0); t < a.m; t += kThreads) a.path[row + t] = t ? -1 : (m ? 0 : -1);
   if (bad && rank == 0) atomicOr(a.status, DEV_BAD_INDEX);
@@ -189,18 +259,37 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs a) {
     return;
   }
   __syncthreads();
+  if (point) {
+    for (int t = tid; t < m; t += kThreads)
+      for (int c = 1; c < t; ++c)
+        if (s.par[c] == s.par[t] && s.tok[c] == s.tok[t]) {
+          s.flag[t] |= kAgain;
+          break;
+        }
+    __syncthreads();
+  }
+  if (cs > 1) cl.sync();                             // every CTA of the cluster runs: its shared memory may be written
 
-  // this CTA's share of the vocabulary, and this warp's of that
-  const int per_cta = (a.vocab + cs - 1) / cs, per_warp = ((per_cta + kWarps - 1) / kWarps + 31) & ~31;
-  const int c0 = min(a.vocab, rank * per_cta), c1 = min(a.vocab, c0 + per_cta);
-  const int w0 = min(c1, c0 + warp * per_warp), w1 = min(c1, w0 + per_warp);
-  // Of warp 0, the same in every lane: the node, the last node that was looked at, accepted ones, and the
-  // mass of the rest (units, and as a number), what A q_c has been taken off
+  // this warp's share of the vocabulary
+  const int per_warp = ((a.vocab + cs * kWarps - 1) / (cs * kWarps) + 7) & ~7;
+  const int mine = rank * kWarps + warp;
+  const int w0 = min(a.vocab, mine * per_warp), w1 = min(a.vocab, w0 + per_warp);
+  // Of warp 0, the same in every lane: the node, the last child that was looked at, accepted nodes, and the
+  // mass of the rest, which A q has been taken off
   int cur = 0, last = 0, count = 1;
-  unsigned long long A = 0, Z = 1ull << kUnitBits;
-  int best = -1, nout = 0;
+  unsigned long long A = 0, Z = kOne;
+  int best = -1;
   int phase = 0;
-  bool stale = a.mode == KVSEL_VERIFY_GREEDY;        // the largest value of the node is not known
+  int held = 0, my_par = -2, my_flag = 0, my_tok = 0;
+  auto hold = [&](int t0) {
+    held = t0;
+    const int t = t0 + lane;
+    my_par = t < m ? s.par[t] : -2;
+    my_flag = t < m ? s.flag[t] : 0;
+    my_tok = t < m ? s.tok[t] : 0;
+  };
+  if (warp == 0) hold(0);
+  bool stale = greedy;                               // the largest value of the node is not known
   bool lean = false;                                 // Z is not known
   while (true) {
     if (warp == 0) {
@@ -210,15 +299,26 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs a) {
           want = kLargest;
           break;
         }
-        // the next child
-        int child = -1;
-        for (int t0 = (last + 1) & ~31; t0 < m && child < 0; t0 += 32) {
-          const int t = t0 + lane;
-          const unsigned hit = __ballot_sync(0xffffffffu, t > last && t < m && s.par[t] == cur);
-          if (hit) child = t0 + __ffs(hit) - 1;
+        // the next child: children come after their parents and are looked at in order, so the 32 nodes that the
+        // lanes hold only move on
+        unsigned hit = __ballot_sync(0xffffffffu, my_par == cur && held + lane > last);
+        while (!hit && held + 32 < m) {
+          hold(held + 32);
+          hit = __ballot_sync(0xffffffffu, my_par == cur && held + lane > last);
         }
+        const int child = hit ? held + __ffs(hit) - 1 : -1;
         if (child < 0) {
-          want = a.mode == KVSEL_VERIFY_GREEDY ? kDone : kDraw;
+          want = greedy ? kDone : kDraw;
+          int n = 0;
+          if (point)          // all its children were rejected
+            for (int t0 = 0; t0 < m; t0 += 32) {
+              const int t = t0 + lane;
+              const bool out = t < m && s.par[t] == cur && (s.flag[t] & (kValid | kAgain)) == kValid;
+              const unsigned hit = __ballot_sync(0xffffffffu, out);
+              if (out) s.out[n + __popc(hit & ((1u << lane) - 1u))] = t;
+              n += __popc(hit);
+            }
+          if (lane == 0) s.nout = n;
           break;
         }
         if (lean) {
@@ -226,94 +326,122 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs a) {
           break;
         }
         last = child;
-        const int x = s.tok[child];
+        const int flag = __shfl_sync(0xffffffffu, my_flag, child - held);
+        if (!(flag & kValid)) continue;              // takes nothing from the rest
         bool take;
-        if (a.mode == KVSEL_VERIFY_GREEDY) {
-          take = x == best;
+        if (greedy) {
+          take = __shfl_sync(0xffffffffu, my_tok, child - held) == best;
+        } else if (A == 0 && Z == kOne) {
+          take = flag & kPasses;
         } else {
-          const double unit = 1.0 / 70368744177664.0, z = static_cast<double>(Z) * unit;
+          const double unit = 1.0 / 35184372088832.0;
           double r = s.p[child];
-          if (a.mode == KVSEL_VERIFY_SAMPLED) {
+          if (sampled)
             r = fmax(r - static_cast<double>(A) * unit * s.q[child], 0.0);
-          } else {
-            bool out = false;
-            for (int i = lane; i < nout; i += 32) out |= s.out[i] == x;
-            if (__any_sync(0xffffffffu, out)) r = 0.0;
-          }
-          take = static_cast<double>(s.u[child]) * s.q[child] * z < r && x >= 0 && x < a.vocab;
+          else if (flag & kAgain)
+            r = 0.0;
+          take = static_cast<double>(s.u[child]) * s.q[child] * (static_cast<double>(Z) * unit) < r;
         }
         if (take) {
           cur = child;
           if (lane == 0 && rank == 0) a.path[row + count] = child;
           ++count;
           A = 0;
-          Z = 1ull << kUnitBits;
-          nout = 0;
-          stale = a.mode == KVSEL_VERIFY_GREEDY;
-        } else if (x < 0 || x >= a.vocab) {
-          // takes nothing from the rest
-        } else if (a.mode == KVSEL_VERIFY_SAMPLED) {
+          Z = kOne;
+          stale = greedy;
+        } else if (sampled) {
           A += Z;
           lean = true;
-        } else if (a.mode == KVSEL_VERIFY_POINT) {
-          bool out = false;
-          for (int i = lane; i < nout; i += 32) out |= s.out[i] == x;
-          if (!__any_sync(0xffffffffu, out)) {
-            const unsigned long long gone = units(s.p[child]);
-            Z = Z > gone ? Z - gone : 0;
-            if (lane == 0) s.out[nout] = x;
-            ++nout;
-            __syncwarp();
-          }
+        } else if (point && !(flag & kAgain)) {
+          const unsigned long long gone = units(s.p[child]);
+          Z = Z > gone ? Z - gone : 0;
         }
       }
       if (lane == 0) {
         s.want = want;
         s.cur = cur;
         s.A = A;
-        s.nout = nout;
       }
       lean = false;                                  // (the pass to come finds it)
     }
     __syncthreads();
     const int want = s.want;
     if (want == kDone) break;
-    const T* p = target + s.cur * a.stride_node;
-    const T* q = draft + s.cur * a.stride_node;
+    const int node = s.cur;
+    const T* p = target + node * a.stride_node;
+    const T* q = draft + node * a.stride_node;
     const unsigned long long off = s.A;
-    unsigned long long v = 0;
-    if (want == kLargest) {
-      each_of(p, w0, w1, lane, 32, [&](int i, T x) { v = max(v, arg_key(value_of<T>(x), i)); });
-      v = warp_max(v);
-    } else if (off) {
-      each_of(p, q, w0, w1, lane, 32, [&](int, T x, T y) { v += rest_units(value_of<T>(x), value_of<T>(y), off); });
-      v = warp_sum(v);
-    } else {
-      each_of(p, w0, w1, lane, 32, [&](int, T x) { v += units(value_of<T>(x)); });
-      v = warp_sum(v);
-      // POINT: what was rejected here has no weight any more
-      for (int i = 0; i < s.nout; ++i)
-        if (s.out[i] >= w0 && s.out[i] < w1) v -= units(value_of<T>(p[s.out[i]]));
+    bool first = true;                               // the draw is from the rest, not from p itself
+    unsigned long long v, all, before;
+    while (true) {
+      v = 0;
+      int hi = 0, lo = 0;
+      auto flush = [&] {
+        v += static_cast<unsigned long long>(whole(hi, lo));
+        hi = lo = 0;
+      };
+      if (greedy) {
+        float top;
+        int at;
+        largest_of(p, w0, w1, top, at);
+        // larger value, larger key; ties: the lower token; NaN below all
+        if (at >= 0) {
+          const uint32_t k = __float_as_uint(top == 0.f ? 0.f : top);
+          v = static_cast<unsigned long long>((k & 0x80000000u) ? ~k : (k | 0x80000000u)) << 32 | (0xFFFFFFFFu - static_cast<uint32_t>(at));
+        }
+        v = warp_max(v);
+      } else if (sampled && off == kOne && first) {
+        // the first rejection: p - q where that is positive
+        each_of<true>(p, q, w0, w1, [&](int, T x, T y) {
+          const float xp = prob(value_of<T>(x)), xq = prob(value_of<T>(y));
+          const Parts P = parts(xp), Q = parts(xq);
+          hi += xp > xq ? P.hi - Q.hi : 0;
+          lo += xp > xq ? P.lo - Q.lo : 0;
+        }, flush);
+        v = warp_sum(v);
+      } else if (sampled && off && first) {
+        each_of<true>(p, q, w0, w1, [&](int, T x, T y) { v += rest_units(value_of<T>(x), value_of<T>(y), off); }, [] {});
+        v = warp_sum(v);
+      } else {
+        each_of<false>(p, p, w0, w1, [&](int, T x, T) {
+          const Parts P = parts(prob(value_of<T>(x)));
+          hi += P.hi;
+          lo += P.lo;
+        }, flush);
+        if (point && first)                          // POINT: what was rejected here has no weight any more
+          for (int k = lane; k < s.nout; k += 32) {
+            const int x = s.tok[s.out[k]];
+            if (x >= w0 && x < w1) v -= units(s.p[s.out[k]]);
+          }
+        v = warp_sum(v);
+      }
+      if (cs == 1) {
+        if (lane == 0) s.part[phase][warp] = v;
+        __syncthreads();
+      } else {
+        if (lane < cs) *cl.map_shared_rank(&s.part[phase][mine], lane) = v;
+        cl.sync();
+      }
+      const unsigned long long* part = s.part[phase];
+      phase ^= 1;
+      all = before = 0;
+      if (want == kDraw || warp == 0) {
+#pragma unroll
+        for (int k = 0; k < kMaxCluster * kWarps / 32; ++k) {
+          const int i = lane + 32 * k;
+          if (i >= cs * kWarps) continue;
+          const unsigned long long y = part[i];
+          all = greedy ? max(all, y) : all + y;
+          if (i < mine) before += y;
+        }
+        all = greedy ? warp_max(all) : warp_sum(all);
+        if (!greedy && want == kDraw) before = warp_sum(before);
+      }
+      if (want != kDraw || all || !first) break;
+      first = false;                                 // nothing is left of the rest
     }
-    unsigned long long* part = s.part[phase];
-    if (lane == 0) part[1 + warp] = v;
-    __syncthreads();
-    if (warp == 0) {
-      unsigned long long y = lane < kWarps ? part[1 + lane] : 0;
-      y = want == kLargest ? warp_max(y) : warp_sum(y);
-      if (lane == 0) part[0] = y;
-    }
-    cl.sync();
-    unsigned long long mine = 0, all = 0, before = 0;
-    for (int c = 0; c < cs; ++c) {
-      const unsigned long long y = *cl.map_shared_rank(part, c);
-      if (c == rank) mine = y;
-      if (c < rank) before += y;
-      all = want == kLargest ? max(all, y) : all + y;
-    }
-    phase ^= 1;
-    if (want == kLargest) {
-      best = static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(all));
+    if (greedy) {
+      best = all ? static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(all)) : 0;
       stale = false;
       continue;
     }
@@ -322,55 +450,51 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs a) {
       continue;
     }
     // the last draw: the smallest token whose sum passes u_0 of all
-    if (all == 0 && (off || s.nout)) {               // nothing is left of the rest: from p_c itself
-      __syncthreads();
-      A = 0;
-      nout = 0;
-      continue;
-    }
-    if (all == 0) {
-      best = -1;
-      break;
-    }
+    best = all ? -2 : -1;                            // -2: written here
     const float u = fminf(fmaxf(s.u[0], 0.f), 0.99999994f);
     const unsigned long long goal = __umul64hi(all, __float2ull_rz(u * 18446744073709551616.f));
-    if (before <= goal && goal < before + mine) {
-      // in this CTA: the warp's share, then its elements 32 at a time
-      if (warp == 0) {
-        unsigned long long sum = before;
-        int w = 0;
-        while (w < kWarps - 1 && sum + part[1 + w] <= goal) sum += part[1 + w++];
-        const int e0 = min(c1, c0 + w * per_warp), e1 = min(c1, e0 + per_warp);
-        for (int i0 = e0; i0 < e1; i0 += 32) {
-          const int i = i0 + lane;
-          unsigned long long y = 0;
-          if (i < e1) {
-            y = off ? rest_units(value_of<T>(p[i]), value_of<T>(q[i]), off) : units(value_of<T>(p[i]));
-            for (int k = 0; k < s.nout; ++k)
-              if (s.out[k] == i) y = 0;
-          }
+    if (all && before <= goal && goal < before + v) {
+      // in this warp's share: a vector of tokens per lane at a time
+      constexpr int N = 16 / sizeof(T);
+      auto weight = [&](int i) -> unsigned long long {
+        if (i >= w1) return 0;
+        if (sampled && off && first) return rest_units(value_of<T>(p[i]), value_of<T>(q[i]), off);
+        unsigned long long y = units(value_of<T>(p[i]));
+        for (int k = 0; point && first && k < s.nout; ++k)
+          if (s.tok[s.out[k]] == i) y = 0;
+        return y;
+      };
+      unsigned long long at = before;
+      for (int i0 = w0; i0 < w1; i0 += 32 * N) {
+        const int e = i0 + lane * N;
+        unsigned long long y = 0;
 #pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const unsigned long long z = __shfl_up_sync(0xffffffffu, y, o);
-            if (lane >= o) y += z;
-          }
-          const unsigned hit = __ballot_sync(0xffffffffu, sum + y > goal);
-          if (hit) {
-            if (lane == 0) a.next[b] = i0 + __ffs(hit) - 1;
-            break;
-          }
-          sum += __shfl_sync(0xffffffffu, y, 31);
+        for (int c = 0; c < N; ++c) y += weight(e + c);
+        unsigned long long sum = y;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const unsigned long long z = __shfl_up_sync(0xffffffffu, sum, o);
+          if (lane >= o) sum += z;
         }
+        const unsigned hit = __ballot_sync(0xffffffffu, at + sum > goal);
+        if (hit) {
+          if (lane == __ffs(hit) - 1) {
+            unsigned long long z = at + sum - y;
+            int c = 0;
+            while (c < N - 1 && (z += weight(e + c)) <= goal) ++c;
+            a.next[b] = e + c;
+          }
+          break;
+        }
+        at += __shfl_sync(0xffffffffu, sum, 31);
       }
     }
-    best = -2;                                       // written
     break;
   }
   if (rank == 0 && tid == 0) {
     a.counts[b] = count;
     if (best != -2) a.next[b] = best;
   }
-  cl.sync();                                         // its shared memory has been read
 }
 
 }  // namespace
@@ -382,19 +506,41 @@ cudaError_t launch_tree_masks(const int32_t* parents, const int32_t* new_lens, c
   return cudaGetLastError();
 }
 
-cudaError_t launch_verify(const VerifyArgs& a, int batch, bool bf16, cudaStream_t st) {
+namespace {
+
+template <class T>
+auto kernel_of(int mode) {
+  return mode == KVSEL_VERIFY_SAMPLED ? verify_kernel<T, KVSEL_VERIFY_SAMPLED>
+         : mode == KVSEL_VERIFY_POINT ? verify_kernel<T, KVSEL_VERIFY_POINT>
+                                      : verify_kernel<T, KVSEL_VERIFY_GREEDY>;
+}
+
+// CTAs of a request: no more than three per SM over all requests, with at least a thousand tokens each
+int cluster_of(int batch, int vocab, int sms) {
+  int c = 1;
+  while (c < kMaxCluster && 2 * c * batch <= 3 * sms && 2 * c * 1024 <= vocab) c *= 2;
+  return c;
+}
+
+}  // namespace
+
+cudaError_t launch_verify(const VerifyArgs& a, int batch, bool bf16, int sms, cudaStream_t st) {
+  const auto kernel = bf16 ? kernel_of<uint16_t>(a.mode) : kernel_of<float>(a.mode);
+  cudaError_t e = ensure_smem(reinterpret_cast<const void*>(kernel), 1);   // (allows clusters of 16)
+  if (e != cudaSuccess) return e;
+  const int cluster = cluster_of(batch, a.vocab, sms);
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
-  cfg.gridDim = dim3(batch * kCluster, 1, 1);
+  cfg.gridDim = dim3(batch * cluster, 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.stream = st;
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = kCluster;
+  attr[0].val.clusterDim.x = cluster;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = bf16 ? cudaLaunchKernelEx(&cfg, verify_kernel<uint16_t>, a) : cudaLaunchKernelEx(&cfg, verify_kernel<float>, a);
+  e = cudaLaunchKernelEx(&cfg, kernel, a);
   note_launch();
   return e;
 }
