@@ -650,22 +650,28 @@ def kvsel_evict_append(params: kvsel_evict_params, kv: kvsel_kv, lens, seen, pos
         _check(rc, "kvsel_evict_append")
 
 
-def _int32(t, count: int, where: str) -> Optional[int]:
-    """Address of a dense tensor of at least `count` 32-bit integers, else refused (an address is the caller's
-    own matter)."""
+@functools.lru_cache(maxsize=None)
+def _word_types():
+    import torch
+
+    return (torch.int32, torch.uint32), (torch.float32,)
+
+
+def _words(t, count: int, where: str, real: bool = False) -> Optional[int]:
+    """Address of a dense tensor of at least `count` 32-bit integers (or fp32 numbers), else refused (an address is
+    the caller's own matter)."""
     if t is None or isinstance(t, int):
         return t
-    if t.element_size() != 4 or t.is_floating_point() or not t.is_contiguous() or t.numel() < count:
-        _refuse(where, f"{tuple(t.shape)} of {t.dtype} with strides {t.stride()} for {count} dense 32-bit integers")
+    if t.dtype not in _word_types()[real] or t.numel() < count or not t.is_contiguous():
+        _refuse(where, f"{tuple(t.shape)} of {t.dtype} with strides {t.stride()} for {count} dense {'fp32 numbers' if real else '32-bit integers'}")
     return t.data_ptr()
+
+
+_int32 = _words
 
 
 def _fp32(t, count: int, where: str) -> Optional[int]:
-    if t is None or isinstance(t, int):
-        return t
-    if t.element_size() != 4 or not t.is_floating_point() or not t.is_contiguous() or t.numel() < count:
-        _refuse(where, f"{tuple(t.shape)} of {t.dtype} with strides {t.stride()} for {count} dense fp32 numbers")
-    return t.data_ptr()
+    return _words(t, count, where, True)
 
 
 def kvsel_compact_in_place(params, kv: kvsel_kv, idx, counts, offsets, lens, seen, pos, ws=None, scores=None, acc=None,

@@ -130,43 +130,66 @@ __device__ __forceinline__ Reserve reserve_of(const PagesArgs& a, int b) {
 }
 
 enum Need : int { kNothing, kPage, kCopy };
+constexpr int kShared = 4096;                        // entries with a shared page that are kept in shared memory
 
 __global__ void __launch_bounds__(kThreads) pages_plan_kernel(const PagesArgs a) {
   __shared__ int s_w[32];
   __shared__ int s_copies;
   __shared__ int s_end[KVSEL_MAX_ATTN_BATCH + 1];    // pages wanted up to request b, at b + 1
   __shared__ unsigned s_bad[KVSEL_MAX_ATTN_BATCH / 32];
+  __shared__ int s_shared[kShared];
   const int tid = threadIdx.x, items = a.B * a.per;
   if (tid == 0) s_copies = s_end[0] = 0;
   if (tid < KVSEL_MAX_ATTN_BATCH / 32) s_bad[tid] = 0;
   __syncthreads();
+  // a thread has `each` entries in a row, as a rule one or none
   const int each = (items + kThreads - 1) / kThreads;
   const int i0 = min(items, tid * each), i1 = min(items, i0 + each);
-  int mine = 0;
+  Reserve r{};
+  int of = -1;                                       // whose r is
+  auto range = [&](int b) -> const Reserve& {
+    if (b != of) r = reserve_of(a, b);
+    of = b;
+    return r;
+  };
+  int mine = 0, shared = 0;
   for (int it = i0; it < i1; ++it) {
     const int b = it / a.per, u = it - b * a.per;
-    const Reserve r = reserve_of(a, b);
+    range(b);
     int need = kNothing;
     const int i = r.page0 + u;
     if (!r.ok && u == 0) atomicOr(&s_bad[b >> 5], 1u << (b & 31));
-    if (r.ok && r.m > 0 && (static_cast<long long>(i) << a.shift) < r.end) {
+    if ((static_cast<long long>(i) << a.shift) < r.end) {
       const int page = a.table[static_cast<long long>(b) * a.max_blocks + i];
       if (page < 0) {
         need = kPage;
       } else if (page >= a.num_blocks) {
         atomicOr(&s_bad[b >> 5], 1u << (b & 31));
-      } else {
-        int left = a.ref[page] - 1;
-        // of those who share it, the requests before this one leave first
-        for (int c = 0; c < b && left > 0; ++c) {
-          if (a.table[static_cast<long long>(c) * a.max_blocks + i] != page) continue;
-          const Reserve o = reserve_of(a, c);
-          left -= o.ok && o.m > 0 && i >= o.page0 && (static_cast<long long>(i) << a.shift) < o.end;
-        }
-        if (left > 0) need = kCopy;
+      } else if (a.ref[page] > 1) {
+        need = kCopy;                                // to be seen
+        ++shared;
       }
     }
     a.need[it] = need;
+  }
+  int sharers;
+  int at = block_scan(shared, s_w, sharers) - shared;
+  if (sharers) {
+    // Of the requests that write to a shared page the last keeps it where no other uses it: as many of them before it
+    // as the page has other uses.  The pages in order of entries: here, or where the free ones go later.
+    int* list = sharers <= kShared ? s_shared : a.pages;
+    int k = at;
+    for (int it = i0; it < i1; ++it)
+      if (a.need[it] == kCopy) list[k++] = a.table[static_cast<long long>(it / a.per) * a.max_blocks + range(it / a.per).page0 + it % a.per];
+    __syncthreads();
+    for (int it = i0; it < i1; ++it) {
+      if (a.need[it] != kCopy) continue;
+      const int page = list[at];
+      int before = 0;
+      for (int c = 0; c < at; ++c) before += list[c] == page;
+      if (before >= a.ref[page] - 1) a.need[it] = kNothing;
+      ++at;
+    }
   }
   __syncthreads();
   for (int it = i0; it < i1; ++it) {
@@ -207,11 +230,11 @@ __global__ void __launch_bounds__(kThreads) pages_plan_kernel(const PagesArgs a)
     const int need = a.need[it];
     if (u == 0) {
       const bool bad = s_bad[b >> 5] >> (b & 31) & 1u;
-      a.granted[b] = served && !bad ? reserve_of(a, b).m : 0;
+      a.granted[b] = served && !bad ? range(b).m : 0;
     }
     if (need != kNothing) {
       if (served) {
-        const Reserve r = reserve_of(a, b);
+        range(b);
         const int i = r.page0 + u, page = a.pages[before];
         int32_t* entry = a.table + static_cast<long long>(b) * a.max_blocks + i;
         if (need == kCopy) {
@@ -229,6 +252,7 @@ __global__ void __launch_bounds__(kThreads) pages_plan_kernel(const PagesArgs a)
   if (tid == 0) a.copies[0].x = s_copies;
 }
 
+constexpr int kAtOnce = 4;
 // grid (copies, layer): rows of all heads of a page lie together
 __global__ void __launch_bounds__(256) pages_copy_kernel(const PagesArgs a) {
   const int n = a.copies[0].x;
@@ -239,10 +263,21 @@ __global__ void __launch_bounds__(256) pages_copy_kernel(const PagesArgs a) {
     for (int layer = blockIdx.y; layer < a.layers; layer += gridDim.y) {
       uint4* k = reinterpret_cast<uint4*>(a.k + layer * a.stride_layer);
       uint4* v = reinterpret_cast<uint4*>(a.v + layer * a.stride_layer);
-#pragma unroll 4
-      for (int i = threadIdx.x; i < pieces; i += 256) {
-        k[x.y * page + i] = k[x.x * page + i];
-        v[x.y * page + i] = v[x.x * page + i];
+      // (all loads of a batch come before its first store)
+      for (int i0 = threadIdx.x; i0 < pieces; i0 += 256 * kAtOnce) {
+        uint4 y[kAtOnce], z[kAtOnce];
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u)
+          if (i0 + u * 256 < pieces) {
+            y[u] = k[x.x * page + i0 + u * 256];
+            z[u] = v[x.x * page + i0 + u * 256];
+          }
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u)
+          if (i0 + u * 256 < pieces) {
+            k[x.y * page + i0 + u * 256] = y[u];
+            v[x.y * page + i0 + u * 256] = z[u];
+          }
       }
     }
   }
@@ -258,6 +293,7 @@ __global__ void __launch_bounds__(256) pages_accept_kernel(const PagesArgs a) {
   const int n = static_cast<int>(min(static_cast<long long>(max(raw_n, 0)), static_cast<long long>(a.max_blocks) << a.shift));
   const int base = max(0, n - m), count = min(max(raw_c, 0), n - base);
   bool bad = raw_m != m || raw_n != n || raw_c != count || n < m;
+  if (a.lens_out && layer == 0 && (a.per_head || h == 0) && lane == 0) a.lens_out[a.per_head ? bh : b] = base + count;
   const int32_t* row = a.table + static_cast<long long>(b) * a.max_blocks;
   const int32_t* path = a.path + static_cast<long long>(b) * a.m;
   uint4* cache = reinterpret_cast<uint4*>((lane >> 4 ? a.v : a.k) + layer * a.stride_layer) + (lane & 15);
@@ -299,7 +335,7 @@ __global__ void __launch_bounds__(256) pages_accept_kernel(const PagesArgs a) {
   if (bad && layer == 0) atomicOr(a.status, DEV_BAD_INDEX);
 }
 
-// after the rows have moved: lens_out may be lens
+// after the rows have moved, where lens_out is lens
 __global__ void __launch_bounds__(256) pages_lens_kernel(const PagesArgs a) {
   const int i = blockIdx.x * 256 + threadIdx.x, b = a.per_head ? i / a.H : i;
   if (b >= a.B) return;
@@ -335,14 +371,17 @@ cudaError_t launch_pages_reserve(const PagesArgs& a, int sms, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-cudaError_t launch_pages_accept(const PagesArgs& a, cudaStream_t st) {
+cudaError_t launch_pages_accept(const PagesArgs& args, cudaStream_t st) {
+  PagesArgs a = args;
+  const bool apart = args.lens_out != args.lens;     // otherwise after all rows have moved
+  if (!apart) a.lens_out = nullptr;
   const long long items = static_cast<long long>(a.B) * a.H * a.layers;
   pages_accept_kernel<<<static_cast<unsigned>((items + 7) / 8), 256, 0, st>>>(a);
   note_launch();
   const cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || apart) return e;
   const int n = a.per_head ? a.B * a.H : a.B;
-  pages_lens_kernel<<<(n + 255) / 256, 256, 0, st>>>(a);
+  pages_lens_kernel<<<(n + 255) / 256, 256, 0, st>>>(args);
   note_launch();
   return cudaGetLastError();
 }

@@ -15,16 +15,43 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// sines and cosines of the eight pairs 8 * unit .. of position pos
-__device__ __forceinline__ void sincos8(const RopeTable& t, int unit, int pos, float (&c)[8], float (&s)[8]) {
-  const float scale = t.scale, back = t.back ? -scale : scale;
+// The eight pairs 8 * unit .. that a thread looks after: turns per position as hi 2^-32 + lo 2^-64, lo signed.  (Read
+// by its own index from the kernel's parameters in the inner loop, eight units of a warp in turn, they cost as much
+// as the rows.)
+struct Turns {
+  int hi[8], lo[8];
+};
+constexpr int kUnit = 9;                             // entries between units: the banks of eight units differ
+__device__ __forceinline__ void load_turns(const RopeTable& t, int2* s_turns, int unit, Turns& w) {
+  if (threadIdx.x < 64) {
+    const unsigned long long y = t.turns[threadIdx.x];
+    s_turns[threadIdx.x / 8 * kUnit + threadIdx.x % 8] = make_int2(static_cast<int>((y + 0x80000000ull) >> 32), static_cast<int>(y));
+  }
+  __syncthreads();
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const unsigned long long turn = static_cast<unsigned long long>(static_cast<long long>(pos)) * t.turns[unit * 8 + i];
-    // signed turns in units of 2^-32
-    const float x = static_cast<float>(static_cast<int>(turn >> 32)) * 1.4629180792671596e-9f;   // 2 pi 2^-32
-    c[i] = __cosf(x) * scale;
-    s[i] = __sinf(x) * back;
+    const int2 y = s_turns[unit * kUnit + i];
+    w.hi[i] = y.x;
+    w.lo[i] = y.y;
+  }
+}
+// Their sines and cosines at position pos.  Bits 32 to 63 of pos * turns are the angle in units of 2^-32 turns; the
+// upper 23 of them make a number in [1, 2) (the sign's bit flipped: half a turn more), and so the angle in [-pi, pi].
+// (A conversion from integer would go to the unit of the sine and cosine, which is the busier one.)
+__device__ __forceinline__ void sincos8(const Turns& w, int pos, float (&c)[8], float (&s)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t x = static_cast<uint32_t>(pos) * static_cast<uint32_t>(w.hi[i]) + static_cast<uint32_t>(__mulhi(pos, w.lo[i]));
+    const float y = fmaf(__uint_as_float((x >> 9) ^ 0x3FC00000u), 6.2831853f, -9.4247780f);
+    c[i] = __cosf(y);
+    s[i] = __sinf(y);
+  }
+}
+__device__ __forceinline__ void scale8(float scale, float (&c)[8], float (&s)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    c[i] *= scale;
+    s[i] *= scale;
   }
 }
 __device__ __forceinline__ void unpack8(const uint4& a, float (&x)[8]) {
@@ -79,64 +106,121 @@ __device__ __forceinline__ void turn(const RopeTable& t, const float (&c)[8], co
   b = pack8(q);
 }
 
-// A group of eight lanes per (token, share of the heads): grid (tokens, share), `each` heads per group.
-__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeArgs a, const int each) {
-  const long long tok = static_cast<long long>(blockIdx.x) * (kThreads / 8) + (threadIdx.x >> 3);
-  const int u = threadIdx.x & 7, b = static_cast<int>(tok / a.n_tok), i = static_cast<int>(tok - static_cast<long long>(b) * a.n_tok);
+// Rows in flight per thread: all loads of a batch come before its first use.
+constexpr int kBatch = 4;
+
+// A group of eight lanes per (token, share of the heads): grid (tokens, shares of q's heads, then of k's), `each` heads
+// per group.
+__global__ void __launch_bounds__(kThreads, 3) rope_kernel(const __grid_constant__ RopeArgs a, const int each, const int q_shares) {
+  __shared__ int2 s_turns[8 * kUnit];
+  Turns w;
+  const int u = threadIdx.x & 7;
+  load_turns(a.t, s_turns, u, w);
+  const unsigned tok = blockIdx.x * (kThreads / 8) + (threadIdx.x >> 3);
+  const int b = tok / static_cast<unsigned>(a.n_tok), i = tok - b * static_cast<unsigned>(a.n_tok);
   if (b >= a.B) return;
   if (a.new_lens && i >= __ldg(a.new_lens + b)) return;
   const bool turns = u < (a.t.rot >> 4);
-  float c[8], s[8];
-  if (turns) sincos8(a.t, u, __ldg(a.pos + b * a.pos_req + i), c, s);
+  const int pos = __ldg(a.pos + b * a.pos_req + i);
   int pa, pb;
   places(a.t, u, pa, pb);
-  const int h0 = blockIdx.y * each, h1 = min(h0 + each, a.heads + a.k_heads);
-#pragma unroll 4
-  for (int h = h0; h < h1; ++h) {
-    const bool is_k = h >= a.heads;
-    const int hh = is_k ? h - a.heads : h;
-    const uint16_t* src = is_k ? a.k + b * a.k_req + hh * a.k_head + i * a.k_tok : a.q + b * a.q_req + hh * a.q_head + i * a.q_tok;
-    uint16_t* dst = is_k ? a.k_out + b * a.ko_req + hh * a.ko_head + i * a.ko_tok
-                         : a.q_out + b * a.qo_req + hh * a.qo_head + i * a.qo_tok;
-    if (!turns && src == dst) continue;
-    uint4 x = reinterpret_cast<const uint4*>(src)[pa], y = reinterpret_cast<const uint4*>(src)[pb];
-    if (turns) turn(a.t, c, s, x, y);
-    reinterpret_cast<uint4*>(dst)[pa] = x;
-    reinterpret_cast<uint4*>(dst)[pb] = y;
+  const bool is_k = static_cast<int>(blockIdx.y) >= q_shares;
+  const int h0 = (blockIdx.y - (is_k ? q_shares : 0)) * each, h1 = min(h0 + each, is_k ? a.k_heads : a.heads);
+  const long long in = is_k ? a.k_head : a.q_head, out = is_k ? a.ko_head : a.qo_head;
+  const uint16_t* src = (is_k ? a.k + b * a.k_req + i * a.k_tok : a.q + b * a.q_req + i * a.q_tok) + h0 * in;
+  uint16_t* dst = (is_k ? a.k_out + b * a.ko_req + i * a.ko_tok : a.q_out + b * a.qo_req + i * a.qo_tok) + h0 * out;
+  if (!turns && src == dst) return;                  // (in place: the strides are the same)
+  float c[8], s[8];
+  for (int h = h0; h < h1; h += kBatch) {
+    uint4 x[kBatch], y[kBatch];
+#pragma unroll
+    for (int r = 0; r < kBatch; ++r)
+      if (h + r < h1) {
+        x[r] = reinterpret_cast<const uint4*>(src)[pa];
+        y[r] = reinterpret_cast<const uint4*>(src)[pb];
+        src += in;
+      }
+    if (turns && h == h0) {
+      sincos8(w, pos, c, s);
+      scale8(a.t.scale, c, s);
+    }
+#pragma unroll
+    for (int r = 0; r < kBatch; ++r)
+      if (h + r < h1) {
+        if (turns) turn(a.t, c, s, x[r], y[r]);
+        reinterpret_cast<uint4*>(dst)[pa] = x[r];
+        reinterpret_cast<uint4*>(dst)[pb] = y[r];
+        dst += out;
+      }
   }
 }
 
-// grid (rows, segment): eight lanes per row
-__global__ void __launch_bounds__(kThreads) rope_cache_kernel(const __grid_constant__ RopeCacheArgs a) {
-  const int seg = blockIdx.y, b = seg / a.H, h = seg - b * a.H, u = threadIdx.x & 7;
+// grid (segment, blocks of kRows rows), so that the heads of a page are read at about the same time: eight lanes per
+// row.  A thread works out a row's places for the eight that turn it.
+// SCALED: the turned values have a factor
+constexpr int kRows = kThreads / 8 * kBatch;
+struct Row {
+  long long src, dst;                                // elements; src < 0: nothing to do
+  int pos;
+};
+template <bool SCALED>
+__global__ void __launch_bounds__(kThreads, 3) rope_cache_kernel(const __grid_constant__ RopeCacheArgs a) {
+  __shared__ int2 s_turns[8 * kUnit];
+  __shared__ Row s_row[kRows];
+  const int seg = blockIdx.x, b = seg / a.H, h = seg - b * a.H, u = threadIdx.x & 7;
   const int raw = __ldg(a.lens + (a.per_head ? seg : b)), n = min(max(raw, 0), a.max_len);
   bool bad = raw != n;
+  Turns w;
+  load_turns(a.t, s_turns, u, w);
   const bool turns = u < (a.t.rot >> 4);
   int pa, pb;
   places(a.t, u, pa, pb);
-  for (int j = blockIdx.x * (kThreads / 8) + (threadIdx.x >> 3); j < n; j += gridDim.x * (kThreads / 8)) {
-    long long e;
-    if (a.src.paged) {
-      const int page = __ldg(a.src.block_table + static_cast<size_t>(b) * a.src.max_blocks + (j >> a.page_shift));
-      if (page < 0 || page >= a.src.num_blocks) {
-        bad = true;
-        continue;
+  uint16_t* to = a.out ? a.out : a.k;
+  for (long long j0 = static_cast<long long>(blockIdx.y) * kRows; j0 < n; j0 += static_cast<long long>(gridDim.y) * kRows) {
+    if (threadIdx.x < kRows) {
+      Row x{-1, 0, 0};
+      const int j = static_cast<int>(j0) + threadIdx.x;
+      if (j < n) {
+        x.pos = a.pos ? __ldg(a.pos + seg * a.pos_stride + j) : j;
+        if (a.src.paged) {
+          const int page = __ldg(a.src.block_table + static_cast<size_t>(b) * a.src.max_blocks + (j >> a.page_shift));
+          if (page < 0 || page >= a.src.num_blocks)
+            bad = true;
+          else
+            x.src = (((static_cast<long long>(page) << a.page_shift) + (j & (a.src.block_size - 1))) * a.H + h) * kHeadDim;
+        } else {
+          x.src = b * a.stride_req + h * a.stride_head + j * a.stride_tok;
+        }
+        x.dst = a.out ? b * a.o_req + h * a.o_head + j * a.o_tok : x.src;
       }
-      e = (((static_cast<long long>(page) << a.page_shift) + (j & (a.src.block_size - 1))) * a.H + h) * kHeadDim;
-    } else {
-      e = b * a.stride_req + h * a.stride_head + j * a.stride_tok;
+      s_row[threadIdx.x] = x;
     }
-    uint16_t* src = a.k + e;
-    uint16_t* dst = a.out ? a.out + b * a.o_req + h * a.o_head + j * a.o_tok : src;
-    if (!turns && src == dst) continue;
-    uint4 x = reinterpret_cast<const uint4*>(src)[pa], y = reinterpret_cast<const uint4*>(src)[pb];
-    if (turns) {
-      float c[8], s[8];
-      sincos8(a.t, u, a.pos ? __ldg(a.pos + seg * a.pos_stride + j) : j, c, s);
-      turn(a.t, c, s, x, y);
+    __syncthreads();
+    if (turns || a.out) {
+      const Row* rows = s_row + (threadIdx.x >> 3);
+      uint4 x[kBatch], y[kBatch];
+#pragma unroll
+      for (int r = 0; r < kBatch; ++r) {
+        const long long e = rows[r * (kThreads / 8)].src;
+        if (e < 0) continue;
+        x[r] = reinterpret_cast<const uint4*>(a.k + e)[pa];
+        y[r] = reinterpret_cast<const uint4*>(a.k + e)[pb];
+      }
+#pragma unroll
+      for (int r = 0; r < kBatch; ++r) {
+        const Row& at = rows[r * (kThreads / 8)];
+        if (at.src < 0) continue;
+        if (turns) {
+          float c[8], s[8];
+          sincos8(w, at.pos, c, s);
+          if (SCALED) scale8(a.t.scale, c, s);
+          turn(a.t, c, s, x[r], y[r]);
+        }
+        reinterpret_cast<uint4*>(to + at.dst)[pa] = x[r];
+        reinterpret_cast<uint4*>(to + at.dst)[pb] = y[r];
+      }
     }
-    reinterpret_cast<uint4*>(dst)[pa] = x;
-    reinterpret_cast<uint4*>(dst)[pb] = y;
+    __syncthreads();
   }
   if (bad && a.status) atomicOr(a.status, DEV_BAD_INDEX);
 }
@@ -147,18 +231,18 @@ cudaError_t launch_rope(const RopeArgs& a, int sms, cudaStream_t st) {
   const long long toks = static_cast<long long>(a.B) * a.n_tok;
   const unsigned gx = static_cast<unsigned>((toks + kThreads / 8 - 1) / (kThreads / 8));
   // heads per group: as many as leave every SM some blocks
-  const int heads = a.heads + a.k_heads;
   int each = 8;
-  while (each > 1 && static_cast<long long>(gx) * ((heads + each - 1) / each) < 8 * sms) each /= 2;
-  rope_kernel<<<dim3(gx, (heads + each - 1) / each), kThreads, 0, st>>>(a, each);
+  auto shares = [&](int heads) { return (heads + each - 1) / each; };
+  while (each > 1 && static_cast<long long>(gx) * (shares(a.heads) + shares(a.k_heads)) < 8 * sms) each /= 2;
+  rope_kernel<<<dim3(gx, shares(a.heads) + shares(a.k_heads)), kThreads, 0, st>>>(a, each, shares(a.heads));
   note_launch();
   return cudaGetLastError();
 }
 
-cudaError_t launch_rope_cache(const RopeCacheArgs& a, int sms, cudaStream_t st) {
-  const int segs = a.B * a.H;
-  const int rows = (a.max_len + kThreads / 8 - 1) / (kThreads / 8);
-  rope_cache_kernel<<<dim3(std::min(rows, std::max(1, 64 * sms / segs)), segs), kThreads, 0, st>>>(a);
+cudaError_t launch_rope_cache(const RopeCacheArgs& a, cudaStream_t st) {
+  const int segs = a.B * a.H, blocks = (a.max_len + kRows - 1) / kRows;
+  const auto kernel = a.t.scale != 1.f ? rope_cache_kernel<true> : rope_cache_kernel<false>;
+  kernel<<<dim3(segs, std::min(blocks, 65535)), kThreads, 0, st>>>(a);
   note_launch();
   return cudaGetLastError();
 }
