@@ -319,7 +319,8 @@ static int attend(const kvsel_attn_params* p, const void* q, const kvsel_kv* kv,
   // which there are grid / items.  (16 items of 256 rows: 31 and 22 us for the whole call; 2 of 100, 76
   // pieces each: 20 and 43.)
   const long long items = static_cast<long long>(p->batch) * p->h_kv * pl.rt;
-  a.by_item = items <= pl.grid && items * items * std::min(pl.tr, p->n_new * p->group) <= 83ll * pl.grid;
+  const int rows = std::min(pl.tr, p->n_new * p->group);
+  a.by_item = tree ? items * 5 <= pl.grid : items <= pl.grid && items * items * rows <= 83ll * pl.grid;
   a.wc = WaitCtl{p->wait_cycles ? p->wait_cycles : kDefaultWaitCycles, static_cast<int*>(ws)};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (!pl.tiled) {

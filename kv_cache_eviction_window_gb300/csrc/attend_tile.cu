@@ -117,10 +117,87 @@ template <int N>
 __device__ __forceinline__ void regs_down() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
+// Pages of a 128-row tile of a piece of `cnt`: lane i gets the block of page i (rows of the pool in all, and a note, where
+// the table's entry is out of range; -1: a page that no row is seen of).
+__device__ __forceinline__ int page_of(const AttnArgs& a, const ItemRange& x, int ta, int ti, int cnt, bool note) {
+  if (ti >= cnt) return -1;
+  int j0, j1;
+  tile_rows<kTK>(x, ta + ti, j0, j1);
+  const int lane = lane_id(), bs = a.src.block_size, at = j0 + lane * bs;
+  if (lane >= (kTK >> a.page_shift) || at >= j1 || (a.window > 0 && at >= a.n_sink && at + bs - 1 <= x.p0 - a.window)) return -1;
+  int pb = __ldg(a.src.block_table + static_cast<size_t>(x.b) * a.src.max_blocks + (at >> a.page_shift));
+  if (pb < 0 || pb >= a.src.num_blocks) {
+    if (note) atomicOr(a.wc.status, DEV_BAD_INDEX);
+    pb = a.src.num_blocks;                           // outside the pool: zeros
+  }
+  return pb;
+}
+// ROWS rows of it, half `sub` where that is 64, into a stage
+template <int ROWS>
+__device__ __forceinline__ void load_pages(const AttnArgs& a, const CUtensorMap* map, int h, int pb, int sub, uint8_t* dst,
+                                           uint64_t* bar) {
+  const int lane = lane_id(), bs = a.src.block_size, page = lane - (sub * 64 >> a.page_shift);
+  const bool live = pb >= 0 && page >= 0 && page < (ROWS >> a.page_shift);
+  const unsigned pages = __popc(__ballot_sync(0xffffffffu, live));
+  if (lane == 0) mbar_arrive_expect_tx(bar, pages * bs * 256);
+  __syncwarp();
+  if (live) tma_load_5d(dst + page * bs * 256, map, bar, 0, 0, 0, 0, pb * (bs * a.H) + h);
+  __syncwarp();
+}
+
+// V tiles of a paged cache by a warp of its own, in the order in which warp 12 loads K.  Warp 12, which sees every use of
+// a stage, says where there is room: kvempty's phases pass for K's uses too, two of them look alike, and a warp that sees
+// every other use would take one for the other.  (It is never four V tiles of a ring ahead: the stage of the fourth needs
+// the first of them landed.)
+template <bool SPLIT, bool TREE, class Sh>
+__device__ __forceinline__ void load_values(const AttnArgs& a, const Sh& sh, const CUtensorMap* tv, uint8_t* sKV,
+                                            uint64_t (&kvfull)[2][kStages], uint64_t (&vroom)[2][4], int* s_abort) {
+  constexpr int kRows = SPLIT ? 64 : 128;
+  int use[2] = {1, 1};
+  bool ok = true;                                    // the same in every lane
+  long long base = sh.item_base;
+  for (int item = sh.item; ok && base < sh.end; ++item) {
+    const ItemRange x = item == sh.item ? sh.first : item_range<kTK, TREE>(a, item);
+    int ta, tb;
+    if (!next_piece(sh, item, x, base, ta, tb)) continue;
+    const int cnt = tb - ta;
+    auto load = [&](int ring, int sub, int page) {
+      const int u = use[ring], s = u % kStages;
+      ok = __all_sync(0xffffffffu, ok && mbar_wait(&vroom[ring][u >> 1 & 3], u >> 3 & 1, s_abort, a.wc));
+      if (!ok) return;
+      use[ring] += 2;
+      load_pages<kRows>(a, tv, x.h, page, sub, sKV + (ring * kStages + s) * (kRows * 256), &kvfull[ring][s]);
+    };
+    // (looked up two tiles ahead of their use)
+    int next0 = page_of(a, x, ta, 0, cnt, false), next1 = page_of(a, x, ta, 1, cnt, false);
+    for (int i = 0; i < cnt && ok; i += 2) {
+      const int page0 = next0, page1 = next1;
+      next0 = page_of(a, x, ta, i + 2, cnt, false);
+      next1 = page_of(a, x, ta, i + 3, cnt, false);
+      if (SPLIT) {
+        load(0, 0, page0);
+        if (i + 1 < cnt && ok) load(1, 0, page1);
+        if (ok) load(0, 1, page0);
+        if (i + 1 < cnt && ok) load(1, 1, page1);
+      } else {
+        load(0, 0, page0);
+        if (i + 1 < cnt && ok) load(0, 0, page1);
+      }
+    }
+  }
+  // copies in flight land before the CTA ends
+  if (lane_id() == 0)
+#pragma unroll
+    for (int r = 0; r < (SPLIT ? 2 : 1); ++r)
+      for (int u = max(1, use[r] - 6); u < use[r]; u += 2) mbar_drain(&kvfull[r][u % kStages], (u / kStages) & 1, a.wc.status);
+}
+
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // TREE: the visibility of the new tokens' rows is in a.tree
-template <bool SPLIT, bool TREE>
+// BOTH: warp 12 loads K alone, by boxes, and warps 13 to 15 load V by 16-byte copies (attend_tile_both).  Each stage's
+// barrier then counts an arrival of each lane of these: all by warp 12 for K.
+template <bool SPLIT, bool TREE, bool BOTH>
 __global__ void __launch_bounds__(kThreads, 1)
     attend_tile_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                        const __grid_constant__ CUtensorMap tv, const AttnArgs a, const int block) {
@@ -129,7 +206,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* sQ = smem;                                // two blocks (SPLIT: one, then the exchange buffer)
   uint8_t* sKV = smem + 2 * kTile;
   __shared__ __align__(8) uint64_t qfull, qempty, kvfull[2][kStages], kvempty[2][kStages], sfull[2][2], pfull[2][2], pv[2][2], done;
-  __shared__ __align__(8) uint64_t xfull, xempty, vfix[4];
+  __shared__ __align__(8) uint64_t xfull, xempty, vfix[4], vroom[2][4];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   __shared__ float2 s_ml[128];
@@ -145,7 +222,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&kvempty[w][s], SPLIT ? 1 : 2);    // both streams read a tile, or one
       }
     }
-    for (int u = 0; u < 4; ++u) mbar_init(&vfix[u], 4);
+    for (int u = 0; u < 4; ++u) {
+      mbar_init(&vfix[u], 4);
+      if (BOTH) {
+        mbar_init(&vroom[0][u], 1);
+        mbar_init(&vroom[1][u], 1);
+      }
+    }
     for (int w = 0; w < 2; ++w)
       for (int u = 0; u < 2; ++u) {
         mbar_init(&sfull[w][u], 1);
@@ -203,30 +286,45 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       ++piece;
       __syncwarp();
-      auto load = [&](int ring, int ti, int sub, bool is_v) {
+      auto load = [&](int ring, int ti, int sub, bool is_v, int page = 0) {
         const int u = use[ring], s = u % kStages;
         ok = __all_sync(0xffffffffu, ok && mbar_wait(&kvempty[ring][s], ((u / kStages) & 1) ^ 1, &s_abort, a.wc));
         if (!ok) return;
+        ++use[ring];
+        if (BOTH && is_v) {
+          if (lane == 0) mbar_arrive(&vroom[ring][u >> 1 & 3]);
+          __syncwarp();
+          return;
+        }
+        if (BOTH) {
+          load_pages<kStageRows>(a, &tk, x.h, page, sub, stage(ring, u), &kvfull[ring][s]);
+          return;
+        }
         int j0, j1;
         tile_rows<kTK>(x, ta + ti, j0, j1);
         load_rows<kStageRows>(a, x.b, x.h, x.row0, is_v ? &tv : &tk, j0 + sub * 64, j1, stage(ring, u), &kvfull[ring][s],
                               [&](int from, int to) { return a.window <= 0 || from < a.n_sink || to > x.p0 - a.window; });
-        ++use[ring];
       };
       // K, then V, in the order in which the UMMA warps take them
-      if (SPLIT) {
-        for (int i = 0; i < cnt && ok; i += 2)
-          for (int sub = 0; sub < 2; ++sub)
-#pragma unroll
-            for (int w = 0; w < 2; ++w) {
-              if (i + w >= cnt) break;
-              load(w, i + w, sub, false);
-              if (ok) load(w, i + w, sub, true);
-            }
-      } else {
-        for (int i = 0; i < cnt && ok; ++i) {
-          load(0, i, 0, false);
-          if (ok) load(0, i, 0, true);
+      auto both = [&](int ring, int ti, int sub, int page) {
+        load(ring, ti, sub, false, page);
+        if (ok) load(ring, ti, sub, true);
+      };
+      int next0 = BOTH ? page_of(a, x, ta, 0, cnt, true) : 0, next1 = BOTH ? page_of(a, x, ta, 1, cnt, true) : 0;
+      for (int i = 0; i < cnt && ok; i += 2) {
+        const int page0 = next0, page1 = next1;
+        if (BOTH) {
+          next0 = page_of(a, x, ta, i + 2, cnt, true);
+          next1 = page_of(a, x, ta, i + 3, cnt, true);
+        }
+        if (SPLIT) {
+          both(0, i, 0, page0);
+          if (i + 1 < cnt && ok) both(1, i + 1, 0, page1);
+          if (ok) both(0, i, 1, page0);
+          if (i + 1 < cnt && ok) both(1, i + 1, 1, page1);
+        } else {
+          both(0, i, 0, page0);
+          if (i + 1 < cnt && ok) both(0, i + 1, 0, page1);
         }
       }
     }
@@ -235,7 +333,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int r = 0; r < nring; ++r)
         for (int u = max(0, use[r] - kStages); u < use[r]; ++u)
-          mbar_drain(&kvfull[r][u % kStages], (u / kStages) & 1, a.wc.status);
+          if (!BOTH || (u & 1) == 0)                 // (V's are not this warp's)
+            mbar_drain(&kvfull[r][u % kStages], (u / kStages) & 1, a.wc.status);
       if (piece) mbar_drain(&qfull, (piece - 1) & 1, a.wc.status);
       if (ok) {
 #pragma unroll
@@ -243,6 +342,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         ring_tail(&qempty, 1, piece, &s_abort, a.wc);
       }
     }
+  } else if (BOTH && warp == kLoadWarp + 1) {
+    load_values<SPLIT, TREE>(a, sh, &tv, sKV, kvfull, vroom, &s_abort);
   } else if (warp >= kQkWarp && warp < kLoadWarp) {
     // the whole warp follows the loop and one elected lane issues, so that descriptors stay in
     // uniform registers
@@ -617,10 +718,14 @@ bool attend_tile_whole(long long items, long long tiles, bool split, int grid) {
                : serial <= 32 && serial * (100 - items * 6 / 10) <= 550;
 }
 
+// Whether V comes by 16-byte copies while K comes by boxes: from pages of up to 16 rows, whose boxes are small.
+static bool attend_tile_both(const AttnArgs& a) { return a.src.paged; }
+
 cudaError_t launch_attend_tile(const AttnArgs& a, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                                int block, bool split, int grid, cudaStream_t st) {
-  const auto kernel = a.tree ? (split ? attend_tile_kernel<true, true> : attend_tile_kernel<false, true>)
-                             : (split ? attend_tile_kernel<true, false> : attend_tile_kernel<false, false>);
+  const auto kernel = !a.tree ? (split ? attend_tile_kernel<true, false, false> : attend_tile_kernel<false, false, false>)
+                      : attend_tile_both(a) ? (split ? attend_tile_kernel<true, true, true> : attend_tile_kernel<false, true, true>)
+                                            : (split ? attend_tile_kernel<true, true, false> : attend_tile_kernel<false, true, false>);
   cudaError_t e = ensure_smem(reinterpret_cast<const void*>(kernel), kSmem);
   if (e != cudaSuccess) return e;
   kernel<<<a.whole ? a.B * a.H * a.rt : grid, kThreads, kSmem, st>>>(tq, tk, tv, a, block);
