@@ -458,6 +458,7 @@ __device__ __forceinline__ bool elect_one() {
 // a few rows per item (a.tr = attend_rows_tile())
 cudaError_t launch_attend_rows(const AttnArgs& a, int grid, int cluster, cudaStream_t st);
 int attend_rows_cluster(long long items, long long tiles, bool window, int grid);
+int attend_rows_clusters(int c);   // clusters of c CTAs that the current device holds at once
 int attend_rows_tile();
 bool attend_tile_whole(long long items, long long tiles, bool split, int grid);
 int attend_tile_rows(bool split);  // rows of a K/V stage, and of a box of its maps

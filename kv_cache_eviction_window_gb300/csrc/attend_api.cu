@@ -70,7 +70,46 @@ int check_tree(const kvsel_attn_params* p) {
   return !p->causal || p->n_new > KVSEL_MAX_TREE ? KVSEL_EUNSUPPORTED : KVSEL_OK;
 }
 
-int plan_attn(const kvsel_attn_params* p, bool with_acc, AttnPlan& pl) {
+// How the nodes of a tree go: in items of 16 rows by clusters of c CTAs (pl.cluster), each item of which reads the cache
+// again, from L2; in items of 128 rows or two such blocks, whole ones to CTAs (pl.whole); or these cut over the grid and
+// joined.  The estimate, in tenths of a microsecond, follows what was measured (8 to 512 rows per segment, 1 to 128
+// segments of 128 to 4096 rows, pages of 16, masks included, us):
+//   clusters  6.3 and 0.97 per tile of 64 rows, 7.8 and 1.06 where CTAs share an SM: 32 items of 1024 rows by clusters of
+//             eight 10.0, of four 10.2, of two 14.6; 96 items by clusters of two 16.6; more clusters than fit at once lose
+//   whole     8.4 and 2.45 per two tiles of 128 rows (one block), 8.6 and 1.7 per tile: 32 segments of 1024 rows 18.2
+//   cut       15.5 and the cache at 4.2 TB/s or the products at 1.3 PFLOP/s: 8 segments of 1024 rows 15.5, 64 of 4096 43
+// (Over those 210 shapes the calls take 1.11 times less than by the rules of kvsel_attend, and at most 15% more than by the
+// best of the three.)
+void plan_tree(const kvsel_attn_params* p, int sms, AttnPlan& pl) {
+  const long long segs = static_cast<long long>(p->batch) * p->h_kv, R = static_cast<long long>(p->n_new) * p->group;
+  // rows that a node may see, first ones and a window's apart
+  long long rows = p->max_len;
+  if (p->window > 0) rows = std::min(rows, p->n_sink + static_cast<long long>(p->window) + p->n_new + 128);
+  const int block = 128 / p->group * p->group;
+  const bool split = R <= block;
+  const long long tiles = (rows + 127) / 128, items = segs * ((R + 2 * block - 1) / (2 * block));
+  double best = 155.0 + std::max(segs * rows * 512.0 / 4.2e5, segs * rows * R * 512.0 / 1.3e8);
+  if (items <= sms) {
+    const double t = split ? 84.0 + 24.5 * ((tiles + 1) / 2) : 86.0 + 17.0 * tiles;
+    if (t < best) {
+      best = t;
+      pl.whole = true;
+    }
+  }
+  const long long small = segs * ((R + attend_rows_tile() - 1) / attend_rows_tile()), steps = (rows + 63) / 64;
+  for (int c = 8; c >= 1; c /= 2) {
+    if (small * c > static_cast<long long>(sms) * attend_rows_ctas_per_sm() || small > attend_rows_clusters(c)) continue;
+    const bool shared = small * c > sms;
+    const double t = (shared ? 78.0 : 63.0) + (shared ? 10.6 : 9.7) * ((steps + c - 1) / c);
+    if (t < best) {
+      best = t;
+      pl.cluster = c;
+    }
+  }
+  if (pl.cluster) pl.whole = false;
+}
+
+int plan_attn(const kvsel_attn_params* p, bool with_acc, bool tree, AttnPlan& pl) {
   int rc = check_attn(p);
   if (rc) return rc;
   int sms = 0;
@@ -80,7 +119,9 @@ int plan_attn(const kvsel_attn_params* p, bool with_acc, AttnPlan& pl) {
   // up to 32 rows of few tiles go as two items (6 tokens of 8 segments of 512 rows, group 4: 6.5 us, as
   // chunks 12.7; 20 rows of 32 segments of 4096: 22.5 and 25.4; a CTA per item loses from 256 rows on).
   // (The weights' logits are kept for one item per segment.)
-  if (rt == 1 || (rt == 2 && !with_acc)) {
+  if (tree) {
+    plan_tree(p, sms, pl);
+  } else if (rt == 1 || (rt == 2 && !with_acc)) {
     // tiles of 64 rows that an item may have: with a window some before it and some of the first rows
     long long tiles = (static_cast<long long>(p->max_len) + 63) / 64;
     const long long seen = (p->n_sink + 63ll) / 64 + (static_cast<long long>(p->window) + p->n_new + 126) / 64;
@@ -90,7 +131,7 @@ int plan_attn(const kvsel_attn_params* p, bool with_acc, AttnPlan& pl) {
                                      sms * attend_rows_ctas_per_sm());
     if (rt == 2 && tiles > (pl.cluster == 1 ? 2 : 16 * pl.cluster)) pl.cluster = 0;
   }
-  if (rt == 1 || pl.cluster) {
+  if (tree ? pl.cluster != 0 : rt == 1 || pl.cluster) {
     // single tokens and the like: HBM-bound, 16 query rows per item
     pl.tr = tr;
     pl.grid = sms * attend_rows_ctas_per_sm();
@@ -107,7 +148,7 @@ int plan_attn(const kvsel_attn_params* p, bool with_acc, AttnPlan& pl) {
     long long tiles = (static_cast<long long>(p->max_len) + 127) / 128;
     if (p->window > 0)
       tiles = std::min(tiles, (p->n_sink + 127ll) / 128 + (static_cast<long long>(p->window) + pl.tr / p->group + 317) / 128);
-    pl.whole = attend_tile_whole(static_cast<long long>(p->batch) * p->h_kv * pl.rt, tiles, pl.split, pl.grid);
+    if (!tree) pl.whole = attend_tile_whole(static_cast<long long>(p->batch) * p->h_kv * pl.rt, tiles, pl.split, pl.grid);
   }
   // behind the status word and the counters that the scoring calls keep in a shared workspace
   size_t off = kStatusBytes + kCounterBytes;
@@ -255,7 +296,7 @@ static int attend(const kvsel_attn_params* p, const void* q, const kvsel_kv* kv,
   if ((rc = check_cache(kv, p->batch, p->h_kv, p->max_len, offsets, p->n_rows))) return rc;
   if (acc && p->acc_stride < p->max_len) return KVSEL_EINVAL;
   AttnPlan pl;
-  if ((rc = plan_attn(p, acc != nullptr, pl))) return rc;
+  if ((rc = plan_attn(p, acc != nullptr, tree != nullptr, pl))) return rc;
   if ((rc = check_ws(ws, ws_bytes, pl.total))) return rc;
   uint8_t* wsb = static_cast<uint8_t*>(ws);
   AttnArgs a{};
@@ -342,7 +383,7 @@ extern "C" {
 int kvsel_attend_workspace_size(const kvsel_attn_params* p, int with_acc, size_t* bytes) {
   if (!bytes) return KVSEL_EINVAL;
   AttnPlan pl;
-  const int rc = plan_attn(p, with_acc != 0, pl);
+  const int rc = plan_attn(p, with_acc != 0, false, pl);
   if (rc) return rc;
   *bytes = pl.total;
   return KVSEL_OK;
@@ -359,7 +400,7 @@ int kvsel_attend_tree_workspace_size(const kvsel_attn_params* p, size_t* bytes) 
   int rc = check_tree(p);
   if (rc) return rc;
   AttnPlan pl;
-  if ((rc = plan_attn(p, false, pl))) return rc;
+  if ((rc = plan_attn(p, false, true, pl))) return rc;
   *bytes = pl.total;
   return KVSEL_OK;
 }

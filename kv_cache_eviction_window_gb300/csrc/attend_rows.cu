@@ -474,6 +474,8 @@ int clusters_at_once(int c) {
 
 }  // namespace
 
+int attend_rows_clusters(int c) { return clusters_at_once(c); }
+
 // CTAs of a cluster per item, or 0: a plan of the whole grid and a join.  `items`, of `tiles` tiles at
 // most (with a window: most of them).
 //
