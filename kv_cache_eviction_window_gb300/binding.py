@@ -118,7 +118,7 @@ class kvsel_evict_params(_RowParams):
     ]
 
 
-class kvsel_verify_params(ctypes.Structure):
+class kvsel_verify_params(_RowParams):
     _fields_ = [
         ("batch", ctypes.c_int32), ("n_new", ctypes.c_int32), ("vocab", ctypes.c_int32), ("mode", ctypes.c_int32),
         ("dtype", ctypes.c_int32), ("stride_req", ctypes.c_int64), ("stride_node", ctypes.c_int64),
@@ -733,18 +733,33 @@ def kvsel_verify_workspace_size(params: kvsel_verify_params) -> int:
     return out.value
 
 
+def _values_of(p: kvsel_verify_params):
+    """What target and draft have to be: types, elements between requests and nodes, and bytes (dense: of all)."""
+    import torch
+
+    dense = not (p.stride_req or p.stride_node)
+    req, node = (p.n_new * p.vocab, p.vocab) if dense else (p.stride_req, p.stride_node)
+    size = 2 if p.dtype else 4
+    types = (torch.bfloat16, torch.int16, torch.uint16) if p.dtype else (torch.float32,)
+    return types, dense, req, node, size * ((p.batch - 1) * req + (p.n_new - 1) * node + p.vocab), (p.batch, p.n_new, p.vocab)
+
+
 def _values(t, params: kvsel_verify_params, where: str) -> Optional[int]:
     """Address of target or draft, whose type and strides have to be as the parameters say."""
     if t is None or isinstance(t, int):
         return t
-    p = params
-    req, node = (p.stride_req, p.stride_node) if p.stride_req or p.stride_node else (p.n_new * p.vocab, p.vocab)
-    size = 2 if p.dtype else 4
-    typed = _is_bf16(t) if p.dtype else t.element_size() == 4 and t.is_floating_point()
-    need = size * ((p.batch - 1) * req + (p.n_new - 1) * node + p.vocab)
-    if not typed or t.stride()[-1] != 1 or t.untyped_storage().nbytes() - size * t.storage_offset() < need or (
-            t.dim() == 3 and (t.shape[0] < p.batch or t.shape[1] < p.n_new or t.shape[2] < p.vocab
-                              or (p.batch > 1 and t.stride(0) != req) or (p.n_new > 1 and t.stride(1) != node))):
+    if params.rows is None:
+        params.rows = _values_of(params)
+    types, dense, req, node, need, shape = params.rows
+    holds = t.dtype in types
+    if holds and not (dense and t.is_contiguous() and t.nbytes >= need):
+        holds = t.stride()[-1] == 1 and t.untyped_storage().nbytes() - t.element_size() * t.storage_offset() >= need
+        if holds and t.dim() == 3:
+            holds = all(a >= b for a, b in zip(t.shape, shape)) and (shape[0] == 1 or t.stride(0) == req) and (
+                shape[1] == 1 or t.stride(1) == node)
+        elif holds and not t.is_contiguous():
+            holds = False
+    if not holds:
         _refuse(where, f"{tuple(t.shape)} of {t.dtype} with strides {t.stride()}")
     return t.data_ptr()
 

@@ -2,9 +2,10 @@
 //
 // fork     out rows are copies of in rows; uses go up for one and down for the other (atomic additions, whose
 //          order does not matter).  Bound: latency, an entry and an addition.
-// reserve  one CTA looks at the entries that new rows touch, counts what they need, finds that many free
-//          pages (the lowest, by ordered scans over the uses) and hands them out in order; a second launch copies
-//          the shared pages' rows in every layer.  Bound: latency, then HBM for the copies.
+// reserve  a CTA looks at the entries that new rows touch, counts what they need, finds that many free
+//          pages (the lowest, by ordered scans over the uses) and hands them out in order; the shared pages' rows
+//          are copied in every layer.  Bound: the latency of lengths, table, uses and free pages one after another, then HBM
+//          for the copies.
 // trim     entries behind a request's rows lose their pages.
 // accept   a warp per request, head and layer moves the rows of the accepted nodes to the tree's front, K by
 //          one half and V by the other.  A row's place is never above where it comes from, so with all loads of eight
@@ -130,17 +131,37 @@ __device__ __forceinline__ Reserve reserve_of(const PagesArgs& a, int b) {
 }
 
 enum Need : int { kNothing, kPage, kCopy };
-constexpr int kShared = 4096;                        // entries with a shared page that are kept in shared memory
 
-__global__ void __launch_bounds__(kThreads) pages_plan_kernel(const PagesArgs a) {
-  __shared__ int s_w[32];
-  __shared__ int s_copies;
-  __shared__ int s_end[KVSEL_MAX_ATTN_BATCH + 1];    // pages wanted up to request b, at b + 1
-  __shared__ unsigned s_bad[KVSEL_MAX_ATTN_BATCH / 32];
-  __shared__ int s_shared[kShared];
+// What a reservation of up to ITEMS touched entries keeps in shared memory (larger ones: `need`, `pages`, `copies` and the
+// list of shared pages are in the workspace).
+constexpr int kItems = 1024;
+struct PlanShared {
+  int w[32];
+  int end[KVSEL_MAX_ATTN_BATCH + 1];                 // pages wanted up to request b, at b + 1
+  unsigned bad[KVSEL_MAX_ATTN_BATCH / 32];
+  int have;                                          // free pages found, as many as are wanted at most
+  int copies;
+};
+
+// The plan of a reservation, by one CTA: needs, pages and copies {from, to, rows} of all entries, in their order.  It
+// writes nothing but these.  Returns the number of copies.
+// SMALL: up to kItems entries (two numbers of them in one scan).
+template <bool SMALL>
+__device__ __forceinline__ int plan_pages(const PagesArgs& a, PlanShared& s, int* need, int* pages, int4* copies, int* list) {
+  constexpr int kMany = 1 << 15;                     // (kItems is less)
   const int tid = threadIdx.x, items = a.B * a.per;
-  if (tid == 0) s_copies = s_end[0] = 0;
-  if (tid < KVSEL_MAX_ATTN_BATCH / 32) s_bad[tid] = 0;
+  // the first uses are on their way before anything else is looked at
+  int uses[4];
+  auto fetch = [&](int p0) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int p = p0 + tid * 4 + u;
+      uses[u] = p < a.num_blocks ? a.ref[p] : 1;
+    }
+  };
+  fetch(0);
+  if (tid == 0) s.end[0] = s.copies = 0;
+  if (tid < KVSEL_MAX_ATTN_BATCH / 32) s.bad[tid] = 0;
   __syncthreads();
   // a thread has `each` entries in a row, as a rule one or none
   const int each = (items + kThreads - 1) / kThreads;
@@ -156,131 +177,183 @@ __global__ void __launch_bounds__(kThreads) pages_plan_kernel(const PagesArgs a)
   for (int it = i0; it < i1; ++it) {
     const int b = it / a.per, u = it - b * a.per;
     range(b);
-    int need = kNothing;
+    int n = kNothing;
     const int i = r.page0 + u;
-    if (!r.ok && u == 0) atomicOr(&s_bad[b >> 5], 1u << (b & 31));
+    if (!r.ok && u == 0) atomicOr(&s.bad[b >> 5], 1u << (b & 31));
     if ((static_cast<long long>(i) << a.shift) < r.end) {
       const int page = a.table[static_cast<long long>(b) * a.max_blocks + i];
       if (page < 0) {
-        need = kPage;
+        n = kPage;
       } else if (page >= a.num_blocks) {
-        atomicOr(&s_bad[b >> 5], 1u << (b & 31));
+        atomicOr(&s.bad[b >> 5], 1u << (b & 31));
       } else if (a.ref[page] > 1) {
-        need = kCopy;                                // to be seen
+        n = kCopy;                                   // to be seen
         ++shared;
       }
     }
-    a.need[it] = need;
+    need[it] = n;
   }
   int sharers;
-  int at = block_scan(shared, s_w, sharers) - shared;
+  int at = block_scan(shared, s.w, sharers) - shared;
   if (sharers) {
     // Of the requests that write to a shared page the last keeps it where no other uses it: as many of them before it
-    // as the page has other uses.  The pages in order of entries: here, or where the free ones go later.
-    int* list = sharers <= kShared ? s_shared : a.pages;
+    // as the page has other uses.  The pages in order of entries:
     int k = at;
     for (int it = i0; it < i1; ++it)
-      if (a.need[it] == kCopy) list[k++] = a.table[static_cast<long long>(it / a.per) * a.max_blocks + range(it / a.per).page0 + it % a.per];
+      if (need[it] == kCopy) list[k++] = a.table[static_cast<long long>(it / a.per) * a.max_blocks + range(it / a.per).page0 + it % a.per];
     __syncthreads();
     for (int it = i0; it < i1; ++it) {
-      if (a.need[it] != kCopy) continue;
+      if (need[it] != kCopy) continue;
       const int page = list[at];
       int before = 0;
+#pragma unroll 8
       for (int c = 0; c < at; ++c) before += list[c] == page;
-      if (before >= a.ref[page] - 1) a.need[it] = kNothing;
+      if (before >= a.ref[page] - 1) need[it] = kNothing;
       ++at;
     }
   }
   __syncthreads();
   for (int it = i0; it < i1; ++it) {
     const int b = it / a.per;
-    if (s_bad[b >> 5] >> (b & 31) & 1u) a.need[it] = kNothing;
-    mine += a.need[it] != kNothing;
+    if (s.bad[b >> 5] >> (b & 31) & 1u) need[it] = kNothing;
+    mine += (need[it] != kNothing) + (SMALL && need[it] == kCopy ? kMany : 0);
   }
-  if (tid < KVSEL_MAX_ATTN_BATCH / 32 && s_bad[tid]) atomicOr(a.status, DEV_BAD_INDEX);
-  int total;
-  int before = block_scan(mine, s_w, total) - mine;
+  // pages wanted before this thread's entries, and copies among them
+  int total, before, c;
+  if (SMALL) {
+    const int sum = block_scan(mine, s.w, total) - mine;
+    before = sum & (kMany - 1);
+    c = sum / kMany;
+    total &= kMany - 1;
+  } else {
+    before = block_scan(mine, s.w, total) - mine;
+    int copied = 0;
+    for (int it = i0; it < i1; ++it) copied += need[it] == kCopy;
+    int all;
+    c = block_scan(copied, s.w, all) - copied;
+  }
   for (int it = i0, upto = before; it < i1; ++it) {
-    upto += a.need[it] != kNothing;
-    if ((it + 1) % a.per == 0) s_end[(it + 1) / a.per] = upto;
+    upto += need[it] != kNothing;
+    if ((it + 1) % a.per == 0) s.end[(it + 1) / a.per] = upto;
   }
   // the lowest free pages, as many as are wanted
   int have = 0;
   for (int p0 = 0; p0 < a.num_blocks && have < total; p0 += kThreads * 4) {
-    const int p = p0 + tid * 4;
     int free = 0;
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
-      if (p + u < a.num_blocks && a.ref[p + u] == 0) free |= 1 << u;
+    for (int u = 0; u < 4; ++u) free |= (uses[u] == 0) << u;
+    fetch(p0 + kThreads * 4);
     int got;
-    int at = have + block_scan(__popc(free), s_w, got) - __popc(free);
+    int k = have + block_scan(__popc(free), s.w, got) - __popc(free);
 #pragma unroll
     for (int u = 0; u < 4; ++u)
       if (free >> u & 1) {
-        if (at < total) a.pages[at] = p + u;
-        ++at;
+        if (k < total) pages[k] = p0 + tid * 4 + u;
+        ++k;
       }
     have += got;
   }
+  if (tid == 0) s.have = have;
   __syncthreads();
-  // requests in order while the pages last
-  for (int it = i0; it < i1; ++it) {
-    const int b = it / a.per, u = it - b * a.per;
-    const bool served = s_end[b + 1] == s_end[b] || s_end[b + 1] <= have;
-    const int need = a.need[it];
-    if (u == 0) {
-      const bool bad = s_bad[b >> 5] >> (b & 31) & 1u;
-      a.granted[b] = served && !bad ? range(b).m : 0;
-    }
-    if (need != kNothing) {
-      if (served) {
+  // requests in order while the pages last (the copies of those that are not served come behind all others)
+  for (int it = i0, k = before; it < i1; ++it) {
+    const int b = it / a.per, u = it - b * a.per, n = need[it];
+    if (n == kCopy) {
+      if (s.end[b + 1] <= have) {
         range(b);
-        const int i = r.page0 + u, page = a.pages[before];
-        int32_t* entry = a.table + static_cast<long long>(b) * a.max_blocks + i;
-        if (need == kCopy) {
-          const int old = *entry, at = atomicAdd(&s_copies, 1);
-          a.copies[1 + at] = make_int4(old, page, min(a.block_size, r.end - r.m - (i << a.shift)), 0);
-          atomicSub(a.ref + old, 1);
-        }
-        *entry = page;
-        a.ref[page] = 1;
+        const int i = r.page0 + u;
+        copies[c] = make_int4(a.table[static_cast<long long>(b) * a.max_blocks + i], pages[k],
+                              min(a.block_size, r.end - r.m - (i << a.shift)), 0);
+        atomicMax(&s.copies, c + 1);
       }
-      ++before;
+      ++c;
     }
+    k += n != kNothing;
   }
   __syncthreads();
-  if (tid == 0) a.copies[0].x = s_copies;
+  return s.copies;
 }
 
-constexpr int kAtOnce = 4;
-// grid (copies, layer): rows of all heads of a page lie together
+// The plan's table entries, uses and what was granted, by one CTA.
+__device__ __forceinline__ void apply_pages(const PagesArgs& a, const PlanShared& s, const int* need, const int* pages) {
+  const int tid = threadIdx.x, items = a.B * a.per, each = (items + kThreads - 1) / kThreads;
+  const int i0 = min(items, tid * each), i1 = min(items, i0 + each);
+  if (tid < KVSEL_MAX_ATTN_BATCH / 32 && s.bad[tid]) atomicOr(a.status, DEV_BAD_INDEX);
+  int k = 0;                                         // the entry's place among the pages, if it wants one
+  for (int it = i0; it < i1; ++it) {
+    const int b = it / a.per, u = it - b * a.per;
+    const bool served = s.end[b + 1] == s.end[b] || s.end[b + 1] <= s.have;
+    const Reserve r = reserve_of(a, b);
+    if (u == 0) a.granted[b] = served && !(s.bad[b >> 5] >> (b & 31) & 1u) ? r.m : 0;
+    if (u == 0 || it == i0) {
+      k = s.end[b];
+      for (int v = 0; v < u; ++v) k += need[b * a.per + v] != kNothing;
+    }
+    if (need[it] == kNothing) continue;
+    ++k;
+    if (!served) continue;
+    const int page = pages[k - 1];
+    int32_t* entry = a.table + static_cast<long long>(b) * a.max_blocks + r.page0 + u;
+    if (need[it] == kCopy) atomicSub(a.ref + *entry, 1);
+    *entry = page;
+    a.ref[page] = 1;
+  }
+}
+
+// Rows of all heads of a page lie together: one side (K, V) of a copy in a layer by a group of 256 threads, all loads of a
+// batch before its first store.
+constexpr int kAtOnce = 8;
+__device__ __forceinline__ void copy_page(const PagesArgs& a, const int4& x, int layer, int side, int tid) {
+  const long long page = static_cast<long long>(a.block_size) * a.H * (kHeadDim / 8);   // in 16-byte pieces
+  const int pieces = x.z * a.H * (kHeadDim / 8);
+  uint4* rows = reinterpret_cast<uint4*>((side ? a.v : a.k) + layer * a.stride_layer);
+  for (int i0 = tid; i0 < pieces; i0 += 256 * kAtOnce) {
+    uint4 y[kAtOnce];
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u)
+      if (i0 + u * 256 < pieces) y[u] = rows[x.x * page + i0 + u * 256];
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u)
+      if (i0 + u * 256 < pieces) rows[x.y * page + i0 + u * 256] = y[u];
+  }
+}
+
+// A reservation of up to kItems entries in one launch: every CTA makes the same plan for itself and copies its share of
+// the pages; the last of them to have made it (`ticket`; none waits for another) writes the table and the uses, which
+// all have read by then.  (Two launches: 1.9 us more on the GPU and 2.3 on the host.)
+__global__ void __launch_bounds__(kThreads, 1) pages_reserve_kernel(const PagesArgs a) {
+  __shared__ PlanShared s;
+  __shared__ int s_need[kItems], s_pages[kItems], s_list[kItems];
+  __shared__ int4 s_copies[kItems];
+  __shared__ bool s_last;
+  const int copies = plan_pages<true>(a, s, s_need, s_pages, s_copies, s_list);
+  if (threadIdx.x == 0) {
+    __threadfence();
+    s_last = atomicAdd(a.ticket, 1) == static_cast<int>(gridDim.x) - 1;
+  }
+  __syncthreads();
+  if (s_last) {
+    __threadfence();
+    apply_pages(a, s, s_need, s_pages);
+    if (threadIdx.x == 0) *a.ticket = 0;
+  }
+  const int groups = gridDim.x * (kThreads / 256), units = copies * a.layers * 2;
+  for (int i = blockIdx.x + gridDim.x * (threadIdx.x >> 8); i < units; i += groups)
+    copy_page(a, s_copies[(i >> 1) / a.layers], (i >> 1) % a.layers, i & 1, threadIdx.x & 255);
+}
+
+// Larger ones: a launch of one CTA for the plan, and one for the copies.
+__global__ void __launch_bounds__(kThreads) pages_plan_kernel(const PagesArgs a) {
+  __shared__ PlanShared s;
+  const int copies = plan_pages<false>(a, s, a.need, a.pages, a.copies + 1, a.list);
+  apply_pages(a, s, a.need, a.pages);
+  if (threadIdx.x == 0) a.copies[0].x = copies;
+}
 __global__ void __launch_bounds__(256) pages_copy_kernel(const PagesArgs a) {
   const int n = a.copies[0].x;
-  const long long page = static_cast<long long>(a.block_size) * a.H * (kHeadDim / 8);   // in 16-byte pieces
-  for (int c = blockIdx.x; c < n; c += gridDim.x) {
-    const int4 x = a.copies[1 + c];
-    const int pieces = x.z * a.H * (kHeadDim / 8);
-    for (int layer = blockIdx.y; layer < a.layers; layer += gridDim.y) {
-      uint4* k = reinterpret_cast<uint4*>(a.k + layer * a.stride_layer);
-      uint4* v = reinterpret_cast<uint4*>(a.v + layer * a.stride_layer);
-      // (all loads of a batch come before its first store)
-      for (int i0 = threadIdx.x; i0 < pieces; i0 += 256 * kAtOnce) {
-        uint4 y[kAtOnce], z[kAtOnce];
-#pragma unroll
-        for (int u = 0; u < kAtOnce; ++u)
-          if (i0 + u * 256 < pieces) {
-            y[u] = k[x.x * page + i0 + u * 256];
-            z[u] = v[x.x * page + i0 + u * 256];
-          }
-#pragma unroll
-        for (int u = 0; u < kAtOnce; ++u)
-          if (i0 + u * 256 < pieces) {
-            k[x.y * page + i0 + u * 256] = y[u];
-            v[x.y * page + i0 + u * 256] = z[u];
-          }
-      }
-    }
-  }
+  for (int c = blockIdx.x; c < n; c += gridDim.x)
+    for (int layer = blockIdx.y; layer < a.layers; layer += gridDim.y)
+      for (int side = 0; side < 2; ++side) copy_page(a, a.copies[1 + c], layer, side, threadIdx.x);
 }
 
 constexpr int kRows = 8;                             // of a path at a time
@@ -360,6 +433,13 @@ cudaError_t launch_pages_trim(const PagesArgs& a, cudaStream_t st) {
 }
 
 cudaError_t launch_pages_reserve(const PagesArgs& a, int sms, cudaStream_t st) {
+  if (a.B * a.per <= kItems) {
+    // a CTA per SM, or one for every four sides of copies that there may be
+    const long long units = 2ll * a.B * a.layers;
+    pages_reserve_kernel<<<static_cast<unsigned>(std::min<long long>(sms, (units + 3) / 4)), kThreads, 0, st>>>(a);
+    note_launch();
+    return cudaGetLastError();
+  }
   pages_plan_kernel<<<1, kThreads, 0, st>>>(a);
   note_launch();
   cudaError_t e = cudaGetLastError();

@@ -46,7 +46,9 @@ struct PagesArgs {
   // {from, to, rows, 0}, their number in copies[0].x
   int32_t* need;                  // [B*per]
   int32_t* pages;                 // [B*per]
+  int32_t* list;                  // [B*per]
   int4* copies;                   // [1 + B*per]
+  int* ticket;                    // zero between calls
   int* status;
 };
 cudaError_t launch_pages_fork(const PagesArgs& a, cudaStream_t st);

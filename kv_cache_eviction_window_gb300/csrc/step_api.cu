@@ -53,7 +53,7 @@ int check_pages(const kvsel_pages_params* p) {
 }
 
 struct PagesLayout {
-  size_t need = 0, pages = 0, copies = 0, total = 0;
+  size_t need = 0, pages = 0, list = 0, copies = 0, total = 0;
 };
 PagesLayout pages_layout(const kvsel_pages_params* p) {
   PagesLayout L;
@@ -61,7 +61,8 @@ PagesLayout pages_layout(const kvsel_pages_params* p) {
   // behind the status word and the counters that other calls keep in a shared workspace
   L.need = kStatusBytes + kCounterBytes;
   L.pages = align256(L.need + items * sizeof(int32_t));
-  L.copies = align256(L.pages + items * sizeof(int32_t));
+  L.list = align256(L.pages + items * sizeof(int32_t));
+  L.copies = align256(L.list + items * sizeof(int32_t));
   L.total = align256(L.copies + (items + 1) * sizeof(int4));
   return L;
 }
@@ -200,7 +201,9 @@ int kvsel_pages_reserve(const kvsel_pages_params* p, void* k, void* v, int32_t* 
   a.granted = granted;
   a.need = reinterpret_cast<int32_t*>(wsb + L.need);
   a.pages = reinterpret_cast<int32_t*>(wsb + L.pages);
+  a.list = reinterpret_cast<int32_t*>(wsb + L.list);
   a.copies = reinterpret_cast<int4*>(wsb + L.copies);
+  a.ticket = reinterpret_cast<int*>(wsb + kStatusBytes);   // one of the counters that kvsel_workspace_init zeroes
   int sms = 0;
   if ((rc = device_sms(&sms))) return rc;
   return launch_rc(launch_pages_reserve(a, sms, static_cast<cudaStream_t>(stream)));
