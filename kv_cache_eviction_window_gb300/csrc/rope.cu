@@ -155,10 +155,10 @@ __global__ void __launch_bounds__(kThreads, 3) rope_kernel(const __grid_constant
   }
 }
 
-// grid (segment, blocks of kRows rows), so that the heads of a page are read at about the same time: eight lanes per
-// row.  A thread works out a row's places for the eight that turn it.
+// grid (segment, CTAs that share its blocks of kRows rows), so that the heads of a page are read at about the same time:
+// eight lanes per row.  A thread works out a row's places for the eight that turn it, a block of rows ahead.
 // SCALED: the turned values have a factor
-constexpr int kRows = kThreads / 8 * kBatch;
+constexpr int kEach = 4, kRows = kThreads / 8 * kEach;
 struct Row {
   long long src, dst;                                // elements; src < 0: nothing to do
   int pos;
@@ -166,60 +166,64 @@ struct Row {
 template <bool SCALED>
 __global__ void __launch_bounds__(kThreads, 3) rope_cache_kernel(const __grid_constant__ RopeCacheArgs a) {
   __shared__ int2 s_turns[8 * kUnit];
-  __shared__ Row s_row[kRows];
+  __shared__ Row s_row[2][kRows];
   const int seg = blockIdx.x, b = seg / a.H, h = seg - b * a.H, u = threadIdx.x & 7;
   const int raw = __ldg(a.lens + (a.per_head ? seg : b)), n = min(max(raw, 0), a.max_len);
   bool bad = raw != n;
+  const int step = gridDim.y * kRows;
+  auto place = [&](long long j0) {
+    Row x{-1, 0, 0};
+    const long long jl = j0 + threadIdx.x;
+    if (threadIdx.x < kRows && jl < n) {
+      const int j = static_cast<int>(jl);
+      x.pos = a.pos ? __ldg(a.pos + seg * a.pos_stride + j) : j;
+      if (a.src.paged) {
+        const int page = __ldg(a.src.block_table + static_cast<size_t>(b) * a.src.max_blocks + (j >> a.page_shift));
+        if (page < 0 || page >= a.src.num_blocks)
+          bad = true;
+        else
+          x.src = (((static_cast<long long>(page) << a.page_shift) + (j & (a.src.block_size - 1))) * a.H + h) * kHeadDim;
+      } else {
+        x.src = b * a.stride_req + h * a.stride_head + j * a.stride_tok;
+      }
+      x.dst = a.out ? b * a.o_req + h * a.o_head + j * a.o_tok : x.src;
+    }
+    return x;
+  };
+  long long j0 = static_cast<long long>(blockIdx.y) * kRows;
+  if (threadIdx.x < kRows) s_row[0][threadIdx.x] = place(j0);
   Turns w;
-  load_turns(a.t, s_turns, u, w);
+  load_turns(a.t, s_turns, u, w);                    // (a barrier)
   const bool turns = u < (a.t.rot >> 4);
   int pa, pb;
   places(a.t, u, pa, pb);
   uint16_t* to = a.out ? a.out : a.k;
-  for (long long j0 = static_cast<long long>(blockIdx.y) * kRows; j0 < n; j0 += static_cast<long long>(gridDim.y) * kRows) {
-    if (threadIdx.x < kRows) {
-      Row x{-1, 0, 0};
-      const int j = static_cast<int>(j0) + threadIdx.x;
-      if (j < n) {
-        x.pos = a.pos ? __ldg(a.pos + seg * a.pos_stride + j) : j;
-        if (a.src.paged) {
-          const int page = __ldg(a.src.block_table + static_cast<size_t>(b) * a.src.max_blocks + (j >> a.page_shift));
-          if (page < 0 || page >= a.src.num_blocks)
-            bad = true;
-          else
-            x.src = (((static_cast<long long>(page) << a.page_shift) + (j & (a.src.block_size - 1))) * a.H + h) * kHeadDim;
-        } else {
-          x.src = b * a.stride_req + h * a.stride_head + j * a.stride_tok;
-        }
-        x.dst = a.out ? b * a.o_req + h * a.o_head + j * a.o_tok : x.src;
-      }
-      s_row[threadIdx.x] = x;
-    }
-    __syncthreads();
-    if (turns || a.out) {
-      const Row* rows = s_row + (threadIdx.x >> 3);
-      uint4 x[kBatch], y[kBatch];
+  for (int side = 0; j0 < n; j0 += step, side ^= 1) {
+    const Row* rows = s_row[side] + (threadIdx.x >> 3);
+    uint4 x[kEach], y[kEach];
+    const bool mine = turns || a.out;
 #pragma unroll
-      for (int r = 0; r < kBatch; ++r) {
-        const long long e = rows[r * (kThreads / 8)].src;
-        if (e < 0) continue;
-        x[r] = reinterpret_cast<const uint4*>(a.k + e)[pa];
-        y[r] = reinterpret_cast<const uint4*>(a.k + e)[pb];
-      }
-#pragma unroll
-      for (int r = 0; r < kBatch; ++r) {
-        const Row& at = rows[r * (kThreads / 8)];
-        if (at.src < 0) continue;
-        if (turns) {
-          float c[8], s[8];
-          sincos8(w, at.pos, c, s);
-          if (SCALED) scale8(a.t.scale, c, s);
-          turn(a.t, c, s, x[r], y[r]);
-        }
-        reinterpret_cast<uint4*>(to + at.dst)[pa] = x[r];
-        reinterpret_cast<uint4*>(to + at.dst)[pb] = y[r];
-      }
+    for (int r = 0; r < kEach; ++r) {
+      const long long e = rows[r * (kThreads / 8)].src;
+      if (e < 0 || !mine) continue;
+      x[r] = reinterpret_cast<const uint4*>(a.k + e)[pa];
+      y[r] = reinterpret_cast<const uint4*>(a.k + e)[pb];
     }
+    const Row next = place(j0 + step);
+#pragma unroll
+    for (int r = 0; r < kEach; ++r) {
+      const Row& at = rows[r * (kThreads / 8)];
+      if (at.src < 0 || !mine) continue;
+      if (turns) {
+        float c[8], s[8];
+        sincos8(w, at.pos, c, s);
+        if (SCALED) scale8(a.t.scale, c, s);
+        turn(a.t, c, s, x[r], y[r]);
+      }
+      reinterpret_cast<uint4*>(to + at.dst)[pa] = x[r];
+      reinterpret_cast<uint4*>(to + at.dst)[pb] = y[r];
+    }
+    if (threadIdx.x < kRows) s_row[side ^ 1][threadIdx.x] = next;
     __syncthreads();
   }
   if (bad && a.status) atomicOr(a.status, DEV_BAD_INDEX);
@@ -239,10 +243,12 @@ cudaError_t launch_rope(const RopeArgs& a, int sms, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-cudaError_t launch_rope_cache(const RopeCacheArgs& a, cudaStream_t st) {
+cudaError_t launch_rope_cache(const RopeCacheArgs& a, int sms, cudaStream_t st) {
+  constexpr int kCtas = 3;
   const int segs = a.B * a.H, blocks = (a.max_len + kRows - 1) / kRows;
   const auto kernel = a.t.scale != 1.f ? rope_cache_kernel<true> : rope_cache_kernel<false>;
-  kernel<<<dim3(segs, std::min(blocks, 65535)), kThreads, 0, st>>>(a);
+  // CTAs for every SM to hold kCtas, or as many blocks as there are
+  kernel<<<dim3(segs, std::min({blocks, 65535, std::max(1, kCtas * sms / segs)})), kThreads, 0, st>>>(a);
   note_launch();
   return cudaGetLastError();
 }

@@ -87,7 +87,7 @@ struct RopeCacheArgs {
   long long o_req, o_head, o_tok;
   int* status;                    // may be null
 };
-cudaError_t launch_rope_cache(const RopeCacheArgs& a, cudaStream_t st);
+cudaError_t launch_rope_cache(const RopeCacheArgs& a, int sms, cudaStream_t st);
 
 struct KeepArgs {
   ReqTable rq;

@@ -379,7 +379,9 @@ int kvsel_rope_cache(const kvsel_rope_angles* table, const kvsel_rope_cache_para
   a.o_head = p->o_head;
   a.o_tok = p->o_tok;
   a.status = static_cast<int*>(ws);
-  return launch_rc(launch_rope_cache(a, static_cast<cudaStream_t>(stream)));
+  int sms = 0;
+  const int rc = device_sms(&sms);
+  return rc ? rc : launch_rc(launch_rope_cache(a, sms, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"
