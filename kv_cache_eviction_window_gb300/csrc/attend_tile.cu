@@ -290,13 +290,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int u = use[ring], s = u % kStages;
         ok = __all_sync(0xffffffffu, ok && mbar_wait(&kvempty[ring][s], ((u / kStages) & 1) ^ 1, &s_abort, a.wc));
         if (!ok) return;
-        ++use[ring];
         if (BOTH && is_v) {
+          ++use[ring];
           if (lane == 0) mbar_arrive(&vroom[ring][u >> 1 & 3]);
           __syncwarp();
           return;
         }
         if (BOTH) {
+          ++use[ring];
           load_pages<kStageRows>(a, &tk, x.h, page, sub, stage(ring, u), &kvfull[ring][s]);
           return;
         }
@@ -304,27 +305,42 @@ __global__ void __launch_bounds__(kThreads, 1)
         tile_rows<kTK>(x, ta + ti, j0, j1);
         load_rows<kStageRows>(a, x.b, x.h, x.row0, is_v ? &tv : &tk, j0 + sub * 64, j1, stage(ring, u), &kvfull[ring][s],
                               [&](int from, int to) { return a.window <= 0 || from < a.n_sink || to > x.p0 - a.window; });
+        ++use[ring];
       };
       // K, then V, in the order in which the UMMA warps take them
-      auto both = [&](int ring, int ti, int sub, int page) {
-        load(ring, ti, sub, false, page);
-        if (ok) load(ring, ti, sub, true);
-      };
-      int next0 = BOTH ? page_of(a, x, ta, 0, cnt, true) : 0, next1 = BOTH ? page_of(a, x, ta, 1, cnt, true) : 0;
-      for (int i = 0; i < cnt && ok; i += 2) {
-        const int page0 = next0, page1 = next1;
-        if (BOTH) {
+      if constexpr (BOTH) {
+        auto both = [&](int ring, int ti, int sub, int page) {
+          load(ring, ti, sub, false, page);
+          if (ok) load(ring, ti, sub, true);
+        };
+        int next0 = page_of(a, x, ta, 0, cnt, true), next1 = page_of(a, x, ta, 1, cnt, true);
+        for (int i = 0; i < cnt && ok; i += 2) {
+          const int page0 = next0, page1 = next1;
           next0 = page_of(a, x, ta, i + 2, cnt, true);
           next1 = page_of(a, x, ta, i + 3, cnt, true);
+          if (SPLIT) {
+            both(0, i, 0, page0);
+            if (i + 1 < cnt && ok) both(1, i + 1, 0, page1);
+            if (ok) both(0, i, 1, page0);
+            if (i + 1 < cnt && ok) both(1, i + 1, 1, page1);
+          } else {
+            both(0, i, 0, page0);
+            if (i + 1 < cnt && ok) both(0, i + 1, 0, page1);
+          }
         }
-        if (SPLIT) {
-          both(0, i, 0, page0);
-          if (i + 1 < cnt && ok) both(1, i + 1, 0, page1);
-          if (ok) both(0, i, 1, page0);
-          if (i + 1 < cnt && ok) both(1, i + 1, 1, page1);
-        } else {
-          both(0, i, 0, page0);
-          if (i + 1 < cnt && ok) both(0, i + 1, 0, page1);
+      } else if (SPLIT) {
+        for (int i = 0; i < cnt && ok; i += 2)
+          for (int sub = 0; sub < 2; ++sub)
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+              if (i + w >= cnt) break;
+              load(w, i + w, sub, false);
+              if (ok) load(w, i + w, sub, true);
+            }
+      } else {
+        for (int i = 0; i < cnt && ok; ++i) {
+          load(0, i, 0, false);
+          if (ok) load(0, i, 0, true);
         }
       }
     }
