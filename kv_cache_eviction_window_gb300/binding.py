@@ -876,8 +876,10 @@ def kvsel_rope(table: kvsel_rope_angles, q, pos, q_out=None, k=None, k_out=None,
     q_out = q if q_out is None else q_out
     if k is not None and k_out is None:
         k_out = k
+    if (k_out is not None) and k is None:
+        _refuse(where, "k_out without k")
     for t, like in ((q, q), (q_out, q), (k, k), (k_out, k)):
-        if t is not None and (not _is_bf16(t) or t.shape != like.shape):
+        if t is not None and (t.dim() != 4 or not _is_bf16(t) or t.shape != like.shape):
             _refuse(where, f"{tuple(t.shape)} of {t.dtype}")
     if pos.element_size() != 4 or pos.is_floating_point():
         _refuse(where, f"pos of {pos.dtype}")

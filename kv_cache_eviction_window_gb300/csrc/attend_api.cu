@@ -30,6 +30,7 @@ int device_sms(int* sms) {
 struct AttnPlan {
   int grid = 0, tr = 0, rt = 1;
   bool tiled = false, split = false;
+  bool few = false;              // a tree: up to 16 query rows, cut over the grid
   int block = 0;                 // tiled: query rows per block, whole tokens of the group
   int cluster = 0;               // not tiled: attend_rows_cluster
   bool whole = false;            // tiled: attend_tile_whole
@@ -71,13 +72,15 @@ int check_tree(const kvsel_attn_params* p) {
 }
 
 // How the nodes of a tree go: in items of 16 rows by clusters of c CTAs (pl.cluster), each item of which reads the cache
-// again, from L2; in items of 128 rows or two such blocks, whole ones to CTAs (pl.whole); or these cut over the grid and
-// joined.  The estimate, in tenths of a microsecond, follows what was measured (8 to 512 rows per segment, 1 to 128
+// again, from L2; up to 16 rows cut over the grid and joined (pl.few); in items of 128 rows or two such blocks, whole ones
+// to CTAs (pl.whole); or these cut over the grid and joined.  The estimate, in tenths of a microsecond, follows what was measured (8 to 512 rows per segment, 1 to 128
 // segments of 128 to 4096 rows, pages of 16, masks included, us):
 //   clusters  6.3 and 0.97 per tile of 64 rows, 7.8 and 1.06 where CTAs share an SM: 32 items of 1024 rows by clusters of
 //             eight 10.0, of four 10.2, of two 14.6; 96 items by clusters of two 16.6; more clusters than fit at once lose
 //   whole     8.4 and 2.45 per two tiles of 128 rows (one block), 8.6 and 1.7 per tile: 32 segments of 1024 rows 18.2
-//   cut       15.5 and the cache at 4.2 TB/s or the products at 1.3 PFLOP/s: 8 segments of 1024 rows 15.5, 64 of 4096 43
+//   few       8.0 and the cache at 6.2 TB/s: 32 segments of 65536 rows 164.8
+//   cut       17.0 and the cache at 6.3 TB/s or the products at 1.3 PFLOP/s: 8 segments of 1024 rows 15.5, 64 of 4096 43,
+//             32 of 65536 182
 // (Over those 210 shapes the calls take 1.11 times less than by the rules of kvsel_attend, and at most 15% more than by the
 // best of the three.)
 void plan_tree(const kvsel_attn_params* p, int sms, AttnPlan& pl) {
@@ -88,7 +91,7 @@ void plan_tree(const kvsel_attn_params* p, int sms, AttnPlan& pl) {
   const int block = 128 / p->group * p->group;
   const bool split = R <= block;
   const long long tiles = (rows + 127) / 128, items = segs * ((R + 2 * block - 1) / (2 * block));
-  double best = 155.0 + std::max(segs * rows * 512.0 / 4.2e5, segs * rows * R * 512.0 / 1.3e8);
+  double best = 170.0 + std::max(segs * rows * 512.0 / 6.3e5, segs * rows * R * 512.0 / 1.3e8);
   if (items <= sms) {
     const double t = split ? 84.0 + 24.5 * ((tiles + 1) / 2) : 86.0 + 17.0 * tiles;
     if (t < best) {
@@ -106,7 +109,11 @@ void plan_tree(const kvsel_attn_params* p, int sms, AttnPlan& pl) {
       pl.cluster = c;
     }
   }
-  if (pl.cluster) pl.whole = false;
+  if (small == segs && 80.0 + segs * rows * 512.0 / 6.2e5 < best) {
+    pl.few = true;
+    pl.cluster = 0;
+  }
+  if (pl.cluster || pl.few) pl.whole = false;
 }
 
 int plan_attn(const kvsel_attn_params* p, bool with_acc, bool tree, AttnPlan& pl) {
@@ -131,7 +138,7 @@ int plan_attn(const kvsel_attn_params* p, bool with_acc, bool tree, AttnPlan& pl
                                      sms * attend_rows_ctas_per_sm());
     if (rt == 2 && tiles > (pl.cluster == 1 ? 2 : 16 * pl.cluster)) pl.cluster = 0;
   }
-  if (tree ? pl.cluster != 0 : rt == 1 || pl.cluster) {
+  if (tree ? pl.cluster || pl.few : rt == 1 || pl.cluster) {
     // single tokens and the like: HBM-bound, 16 query rows per item
     pl.tr = tr;
     pl.grid = sms * attend_rows_ctas_per_sm();
