@@ -632,6 +632,7 @@ int kvsel_verify_workspace_size(const kvsel_verify_params* p, size_t* bytes);
  * lowest x with the largest p_c(x) (any values, logits will do; NaN is below all), and next is that x.
  *   tokens   device int32 [batch][n_new], parents likewise (as kvsel_tree_masks takes them)
  *   target   device, strides above, 4-byte (fp32) or 2-byte (bf16) aligned: rows of probabilities that sum to 1
+ *            as far as their type can (by a sixteenth more at most)
  *            (a value counts as what it is in [0, 1], to 2^-46; NaN as 0)
  *   draft    device, as target (SAMPLED), else NULL
  *   u        device fp32 [batch][n_new], uniform in [0, 1): u_t of node t's test, u_0 of the last draw

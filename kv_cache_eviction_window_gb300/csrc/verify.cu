@@ -321,13 +321,11 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a)
           if (lane == 0) s.nout = n;
           break;
         }
-        if (lean) {
-          want = kMass;
-          break;
-        }
-        last = child;
         const int flag = __shfl_sync(0xffffffffu, my_flag, child - held);
-        if (!(flag & kValid)) continue;              // takes nothing from the rest
+        if (!(flag & kValid)) {                      // takes nothing from the rest
+          last = child;
+          continue;
+        }
         bool take;
         if (greedy) {
           take = __shfl_sync(0xffffffffu, my_tok, child - held) == best;
@@ -340,8 +338,17 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a)
             r = fmax(r - static_cast<double>(A) * unit * s.q[child], 0.0);
           else if (flag & kAgain)
             r = 0.0;
-          take = static_cast<double>(s.u[child]) * s.q[child] * (static_cast<double>(Z) * unit) < r;
+          // the mass that is not known yet is at most the one before; the first, taken as 1, is what p sums to
+          const double z = lean && A == kOne ? 1.0625 : static_cast<double>(Z) * unit;
+          take = static_cast<double>(s.u[child]) * s.q[child] * z < r;
         }
+        // (what passes with a larger mass is accepted, without a sum)
+        if (lean && !take) {
+          want = kMass;
+          break;
+        }
+        last = child;
+        lean = false;
         if (take) {
           cur = child;
           if (lane == 0 && rank == 0) a.path[row + count] = child;
