@@ -125,7 +125,7 @@ class kvsel_verify_params(_RowParams):
     ]
 
 
-class kvsel_pages_params(ctypes.Structure):
+class kvsel_pages_params(_RowParams):
     _fields_ = [
         ("h_kv", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("batch", ctypes.c_int32), ("block_size", ctypes.c_int32),
         ("max_blocks", ctypes.c_int32), ("num_blocks", ctypes.c_int32), ("layers", ctypes.c_int32),
@@ -650,28 +650,36 @@ def kvsel_evict_append(params: kvsel_evict_params, kv: kvsel_kv, lens, seen, pos
         _check(rc, "kvsel_evict_append")
 
 
-@functools.lru_cache(maxsize=None)
-def _word_types():
-    import torch
-
-    return (torch.int32, torch.uint32), (torch.float32,)
+_INT32 = _FP32 = None   # torch's types, once it is loaded
 
 
-def _words(t, count: int, where: str, real: bool = False) -> Optional[int]:
-    """Address of a dense tensor of at least `count` 32-bit integers (or fp32 numbers), else refused (an address is
-    the caller's own matter)."""
-    if t is None or isinstance(t, int):
+def _int32(t, count: int, where: str) -> Optional[int]:
+    """Address of a dense tensor of at least `count` 32-bit integers, else refused (an address is the caller's own
+    matter)."""
+    if t is None or t.__class__ is int:
         return t
-    if t.dtype not in _word_types()[real] or t.numel() < count or not t.is_contiguous():
-        _refuse(where, f"{tuple(t.shape)} of {t.dtype} with strides {t.stride()} for {count} dense {'fp32 numbers' if real else '32-bit integers'}")
-    return t.data_ptr()
-
-
-_int32 = _words
+    if t.dtype is _INT32 and t.numel() >= count and t.is_contiguous():
+        return t.data_ptr()
+    return _other_words(t, count, where, False)
 
 
 def _fp32(t, count: int, where: str) -> Optional[int]:
-    return _words(t, count, where, True)
+    if t is None or t.__class__ is int:
+        return t
+    if t.dtype is _FP32 and t.numel() >= count and t.is_contiguous():
+        return t.data_ptr()
+    return _other_words(t, count, where, True)
+
+
+def _other_words(t, count: int, where: str, real: bool) -> int:
+    """The first tensor of its type, one of unsigned integers, or one that is refused."""
+    global _INT32, _FP32
+    import torch
+
+    _INT32, _FP32 = torch.int32, torch.float32
+    if t.dtype not in ((_FP32,) if real else (_INT32, torch.uint32)) or t.numel() < count or not t.is_contiguous():
+        _refuse(where, f"{tuple(t.shape)} of {t.dtype} with strides {t.stride()} for {count} dense {'fp32 numbers' if real else '32-bit integers'}")
+    return t.data_ptr()
 
 
 def kvsel_compact_in_place(params, kv: kvsel_kv, idx, counts, offsets, lens, seen, pos, ws=None, scores=None, acc=None,
@@ -784,11 +792,14 @@ def kvsel_pages_workspace_size(params: kvsel_pages_params) -> int:
 
 
 def _pool(t, params: kvsel_pages_params, where: str) -> Optional[int]:
-    if isinstance(t, int):
+    if t.__class__ is int:
         return t
-    p = params
-    if not _is_bf16(t) or not t.is_contiguous() or t.numel() < p.layers * p.num_blocks * p.block_size * p.h_kv * p.head_dim:
-        _refuse(where, f"{tuple(t.shape)} of {t.dtype} with strides {t.stride()} for {p.layers} pools")
+    need = params.rows
+    if need is None:
+        p = params
+        need = params.rows = 2 * p.layers * p.num_blocks * p.block_size * p.h_kv * p.head_dim
+    if t.nbytes < need or not t.is_contiguous() or not _is_bf16(t):
+        _refuse(where, f"{tuple(t.shape)} of {t.dtype} with strides {t.stride()} for pools of {need} bytes")
     return t.data_ptr()
 
 
