@@ -365,7 +365,8 @@ static int attend(const kvsel_attn_params* p, const void* q, const kvsel_kv* kv,
   a.grid = pl.grid;
   // A CTA for each row takes 2.2 us per 456 rows, eight rows per warp 0.4 us per piece of an item, of
   // which there are grid / items.  (16 items of 256 rows: 31 and 22 us for the whole call; 2 of 100, 76
-  // pieces each: 20 and 43.)
+  // pieces each: 20 and 43.)  A tree's rows go to a warp by eights, or to eight warps by eights from five
+  // pieces an item on (join_trees_kernel: 19 pieces of 256 rows 16.6 and 5.2 us, two or three of 128 rows 6.6 and 9.6).
   const long long items = static_cast<long long>(p->batch) * p->h_kv * pl.rt;
   const int rows = std::min(pl.tr, p->n_new * p->group);
   a.by_item = tree ? items * 5 <= pl.grid : items <= pl.grid && items * items * rows <= 83ll * pl.grid;

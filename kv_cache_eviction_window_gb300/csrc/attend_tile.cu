@@ -195,8 +195,9 @@ __device__ __forceinline__ void load_values(const AttnArgs& a, const Sh& sh, con
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // TREE: the visibility of the new tokens' rows is in a.tree
-// BOTH: warp 12 loads K alone, by boxes, and warps 13 to 15 load V by 16-byte copies (attend_tile_both).  Each stage's
-// barrier then counts an arrival of each lane of these: all by warp 12 for K.
+// BOTH: small pages by two warps, 12 for K and 13 for V, with the table looked up two tiles ahead.  A box takes its warp
+// some 50 cycles beside its bytes.  8 segments of 8 requests of 2048 to 32768 rows, 32 nodes of 4 heads, pages of 16: one
+// warp for both, which looks a page up when it loads it, 150 us; two 125; V by 16-byte copies of three warps 136 to 264.
 template <bool SPLIT, bool TREE, bool BOTH>
 __global__ void __launch_bounds__(kThreads, 1)
     attend_tile_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
@@ -734,8 +735,10 @@ bool attend_tile_whole(long long items, long long tiles, bool split, int grid) {
                : serial <= 32 && serial * (100 - items * 6 / 10) <= 550;
 }
 
-// Whether V comes by 16-byte copies while K comes by boxes: from pages of up to 16 rows, whose boxes are small.
-static bool attend_tile_both(const AttnArgs& a) { return a.src.paged; }
+// Whether K and V come by a warp each: from pages of less than a stage's 64 rows.  The sizes above, two warps and one: pages
+// of 8 133 and 151 us, of 16 125 and 150, of 32 126 and 127 (16 nodes 119 and 127), of 64 125 and 121 (contiguous rows, one
+// warp, 115).
+static bool attend_tile_both(const AttnArgs& a) { return a.src.paged && a.src.block_size < 64; }
 
 cudaError_t launch_attend_tile(const AttnArgs& a, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                                int block, bool split, int grid, cudaStream_t st) {

@@ -3,7 +3,9 @@
 // With k0 kept positions below count, the moves are idx[k0 + j] -> hole j, and a row p that is not kept is hole
 // p minus the kept rows before it: a search for a block's first row, then a count over its rows.  Rows
 // that move lie at or behind count, holes below it: nothing that is read is written.
-// Bound: HBM, 512 B per moved row read and written, and 12 B per kept row.
+// Bound: HBM, 512 B per moved row read and written, and 12 B per kept row.  Measured: 13107 of 32768 rows of 32 segments in
+// pages of 16 49 us for 263 MB (38.7 at the copy rate); rows of 64 to 512 per CTA, two to eight rows per warp at a time and
+// other numbers of CTAs per SM were no faster.  (A search for every hole: 92 us.)
 #include <algorithm>
 
 #include "step.cuh"

@@ -1,15 +1,16 @@
 // Pages that requests share: a block table, the uses of every page, and a pool for each layer.
 //
 // fork     out rows are copies of in rows; uses go up for one and down for the other (atomic additions, whose
-//          order does not matter).  Bound: latency, an entry and an addition.
+//          order does not matter).  Bound: latency, an entry and an addition; 64 rows of 127 entries 2.0 us.
 // reserve  a CTA looks at the entries that new rows touch, counts what they need, finds that many free
 //          pages (the lowest, by ordered scans over the uses) and hands them out in order; the shared pages' rows
 //          are copied in every layer.  Bound: the latency of lengths, table, uses and free pages one after another, then HBM
-//          for the copies.
-// trim     entries behind a request's rows lose their pages.
+//          for the copies.  64 beams in fours, 8 layers of 8 heads: 9 us, 5 of them the plan; without copies 6.2.
+// trim     entries behind a request's rows lose their pages: 1.9 us.
 // accept   a warp per request, head and layer moves the rows of the accepted nodes to the tree's front, K by
 //          one half and V by the other.  A row's place is never above where it comes from, so with all loads of eight
-//          rows before their stores, in ascending order, nothing is overwritten before it is read.
+//          rows before their stores, in ascending order, nothing is overwritten before it is read.  Bound: latency, path,
+//          entry, row and store one after another: 4.2 us for 32 requests of 8 heads and 8 layers.
 #include <algorithm>
 
 #include "../../include/kvsel.h"

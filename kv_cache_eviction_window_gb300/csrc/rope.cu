@@ -5,7 +5,9 @@
 // approximate ones, off by 2^-21 of the pair's length; the result's rounding to bf16 is 2^-9 of the value.
 //
 // A thread turns eight pairs (32 bytes of a row) by the same sines for all heads of a token that fall
-// to it.  Bound: HBM, a row read and written.
+// to it; cached keys have a position each.  Bound: HBM, a row read and written.  Measured: 8192 tokens of 32 + 8 heads
+// 27.5 us for 168 MB (24.7 at the copy rate); 32 segments of 13107 cached keys 42 us for 216 MB (31.9), of which the
+// launch, the first places and the last stores are some 5; half the columns turned take as long.
 #include <algorithm>
 
 #include "step.cuh"
@@ -36,7 +38,8 @@ __device__ __forceinline__ void load_turns(const RopeTable& t, int2* s_turns, in
   }
 }
 // Their sines and cosines at position pos.  Bits 32 to 63 of pos * turns are the angle in units of 2^-32 turns; the
-// upper 23 of them make a number in [1, 2) (the sign's bit flipped: half a turn more), and so the angle in [-pi, pi].
+// upper 23 of them make a number in [1, 2) (the sign's bit flipped: half a turn more), and so the angle in [-pi, pi], off by
+// at most 2^-23 turns (little beside a bf16 value's 2^-8).
 // (A conversion from integer would go to the unit of the sine and cosine, which is the busier one.)
 __device__ __forceinline__ void sincos8(const Turns& w, int pos, float (&c)[8], float (&s)[8]) {
 #pragma unroll

@@ -34,10 +34,10 @@ def table(**kw):
 
 
 def close(got, x, pos, o):
-    """A turned value is x1 c - x2 s.  The angle, at most pi, is rounded to fp32, multiplied by a rounded constant
-    and rounded again: off by pi (2^-24 + 2^-25 + 2^-24) < 2^-21 (and by 2^-32 turns and 2^31 * 2^-53, which is
-    little); the approximate sine and cosine by 2^-21 within [-pi, pi]; factor, product and sum round three times, 2^-24
-    each.  Together below 2^-19 of |x1| + |x2| times the factor.  One rounding to bf16: 2^-8 of the value."""
+    """A turned value is x1 c - x2 s.  The angle, at most pi, is cut to 23 bits of a turn (2 pi 2^-23 < 7.5e-7), multiplied
+    by a rounded constant and rounded again (pi (2^-25 + 2^-24) < 2.9e-7; 2^-32 turns are little); the approximate sine and
+    cosine are off by 2^-21 < 4.8e-7 within [-pi, pi]; factor, product and sum round three times, 2^-24 each, 1.8e-7.
+    Together below 2^-19 = 1.9e-6 of |x1| + |x2| times the factor.  One rounding to bf16: 2^-8 of the value."""
     want = SO.rope(x, pos, **o)
     rot = 2 * len(o["f"])
     half = rot // 2
