@@ -8,7 +8,7 @@
     python profile_case.py --workload 2 --plain --partition   # + kept/evicted partition
     python profile_case.py --workload 2 --plain --concurrent --sm-budget 76   # two-launch scoring
     python profile_case.py --workload 2 --plain --layers 8 --graph-streams 8 --concurrent --sm-budget 76
-    python profile_case.py --operator chunk-window   # a listed case of perf/operators.py
+    python profile_case.py --operator chunk-window   # a listed case of perf/operators.py or perf/more_operators.py
 
 With --graph-streams S the layers are issued round-robin over S streams (one workspace
 each) and captured as one CUDA graph; after --steps warm-up replays, one more replay runs
@@ -45,7 +45,7 @@ def main():
     ap.add_argument("--sm-budget", type=int, default=0, help="kvsel_params.sm_budget")
     ap.add_argument("--graph-streams", type=int, default=0,
                     help="issue the layers over this many streams as one CUDA graph (see above)")
-    ap.add_argument("--operator", default=None, help="kvsel_attend or kvsel_evict_append on this case of perf/operators.py")
+    ap.add_argument("--operator", default=None, help="the calls of this case of perf/operators.py or perf/more_operators.py")
     args = ap.parse_args()
     if args.operator:
         return run_operator(args)
@@ -154,10 +154,10 @@ def run_operator(args):
     import __graft_entry__
 
     __graft_entry__.build()
-    from perf import operators
+    from perf import more_operators, operators as cache_operators
 
+    operators, case = next((o, c) for o in (cache_operators, more_operators) for c in o.listed() if c["name"] == args.operator)
     operators.own = True
-    case = next(c for c in operators.listed() if c["name"] == args.operator)
     states = [operators.prepare(case, seed) for seed in range(args.steps)]
     for st in states:
         operators.run(st)
