@@ -688,7 +688,9 @@ int kvsel_pages_fork(const kvsel_pages_params* p, const int32_t* table_in, const
  * one, and a page that others use too is copied (its rows below lens, in every layer) unless, of the
  * requests in order, only this one is left to use it.  Pages are the lowest free ones, in order of requests and
  * rows.  Where those run out, requests are served in order: one whose pages, together with all before
- * it, exceed the free ones gets none (one that needs none is served).
+ * it, exceed the free ones gets none, nor does one that is to be left with a page by those before it (one
+ * that needs neither is served).  Shared pages that new rows go to are ranked, in time with their number squared:
+ * the last page of each request, as a rule.
  *   k, v     device bf16, the pools of layer 0, 16-byte aligned
  *   lens     device int32 [batch] or [batch*h_kv], not changed (with lens_per_head the pages from the shortest
  *            head's rows to the longest's are made the request's own, with the rows of its longest)
@@ -785,7 +787,8 @@ typedef struct kvsel_rope_cache_params {
 
 /* Every cached key turned by pos[seg][j]: in place (k_out NULL), e.g. by the difference to its new position
  * after an eviction, or into k_out [b][h][j], e.g. INVERSE: the keys before their rotation, which
- * kvsel_anchor_project wants.
+ * kvsel_anchor_project wants.  In place no two segments may share memory (a page that two requests name
+ * would be turned by both).
  *   kv       contiguous or paged; only k is read (or written)
  *   lens     device int32, rows of every segment (clamped to max_len); rows behind are left as they are
  *   pos      device int32 [batch*h_kv][pos_stride], NULL with pos_stride 0

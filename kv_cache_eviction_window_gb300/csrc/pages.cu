@@ -131,7 +131,9 @@ __device__ __forceinline__ Reserve reserve_of(const PagesArgs& a, int b) {
   return r;
 }
 
-enum Need : int { kNothing, kPage, kCopy };
+// kKeep: a shared page that its last writer takes over, without a page from the pool
+enum Need : int { kNothing, kKeep, kPage, kCopy };
+__device__ __forceinline__ bool wants(int need) { return need >= kPage; }
 
 // What a reservation of up to ITEMS touched entries keeps in shared memory (larger ones: `need`, `pages`, `copies` and the
 // list of shared pages are in the workspace).
@@ -139,9 +141,14 @@ constexpr int kItems = 1024;
 struct PlanShared {
   int w[32];
   int end[KVSEL_MAX_ATTN_BATCH + 1];                 // pages wanted up to request b, at b + 1
-  unsigned bad[KVSEL_MAX_ATTN_BATCH / 32];
+  unsigned bad[KVSEL_MAX_ATTN_BATCH / 32], keeps[KVSEL_MAX_ATTN_BATCH / 32];
   int have;                                          // free pages found, as many as are wanted at most
   int copies;
+  __device__ __forceinline__ static bool has(const unsigned* bits, int b) { return bits[b >> 5] >> (b & 31) & 1u; }
+  // a request that takes a page over needs those before it to leave it: all that is asked for up to it
+  __device__ __forceinline__ bool served(int b) const {
+    return !has(bad, b) && ((end[b + 1] == end[b] && !has(keeps, b)) || end[b + 1] <= have);
+  }
 };
 
 // The plan of a reservation, by one CTA: needs, pages and copies {from, to, rows} of all entries, in their order.  It
@@ -162,7 +169,7 @@ __device__ __forceinline__ int plan_pages(const PagesArgs& a, PlanShared& s, int
   };
   fetch(0);
   if (tid == 0) s.end[0] = s.copies = 0;
-  if (tid < KVSEL_MAX_ATTN_BATCH / 32) s.bad[tid] = 0;
+  if (tid < KVSEL_MAX_ATTN_BATCH / 32) s.bad[tid] = s.keeps[tid] = 0;
   __syncthreads();
   // a thread has `each` entries in a row, as a rule one or none
   const int each = (items + kThreads - 1) / kThreads;
@@ -198,10 +205,12 @@ __device__ __forceinline__ int plan_pages(const PagesArgs& a, PlanShared& s, int
   int at = block_scan(shared, s.w, sharers) - shared;
   if (sharers) {
     // Of the requests that write to a shared page the last keeps it where no other uses it: as many of them before it
-    // as the page has other uses.  The pages in order of entries:
+    // as the page has other uses (requests that are not served for what their entries hold do not count).  The pages in
+    // order of entries:
     int k = at;
     for (int it = i0; it < i1; ++it)
-      if (need[it] == kCopy) list[k++] = a.table[static_cast<long long>(it / a.per) * a.max_blocks + range(it / a.per).page0 + it % a.per];
+      if (need[it] == kCopy)
+        list[k++] = s.has(s.bad, it / a.per) ? -1 : a.table[static_cast<long long>(it / a.per) * a.max_blocks + range(it / a.per).page0 + it % a.per];
     __syncthreads();
     for (int it = i0; it < i1; ++it) {
       if (need[it] != kCopy) continue;
@@ -209,15 +218,17 @@ __device__ __forceinline__ int plan_pages(const PagesArgs& a, PlanShared& s, int
       int before = 0;
 #pragma unroll 8
       for (int c = 0; c < at; ++c) before += list[c] == page;
-      if (before >= a.ref[page] - 1) need[it] = kNothing;
       ++at;
+      if (page < 0 || before < a.ref[page] - 1) continue;
+      need[it] = kKeep;
+      atomicOr(&s.keeps[it / a.per >> 5], 1u << (it / a.per & 31));
     }
   }
   __syncthreads();
   for (int it = i0; it < i1; ++it) {
     const int b = it / a.per;
-    if (s.bad[b >> 5] >> (b & 31) & 1u) need[it] = kNothing;
-    mine += (need[it] != kNothing) + (SMALL && need[it] == kCopy ? kMany : 0);
+    if (s.has(s.bad, b)) need[it] = kNothing;
+    mine += wants(need[it]) + (SMALL && need[it] == kCopy ? kMany : 0);
   }
   // pages wanted before this thread's entries, and copies among them
   int total, before, c;
@@ -234,7 +245,7 @@ __device__ __forceinline__ int plan_pages(const PagesArgs& a, PlanShared& s, int
     c = block_scan(copied, s.w, all) - copied;
   }
   for (int it = i0, upto = before; it < i1; ++it) {
-    upto += need[it] != kNothing;
+    upto += wants(need[it]);
     if ((it + 1) % a.per == 0) s.end[(it + 1) / a.per] = upto;
   }
   // the lowest free pages, as many as are wanted
@@ -269,7 +280,7 @@ __device__ __forceinline__ int plan_pages(const PagesArgs& a, PlanShared& s, int
       }
       ++c;
     }
-    k += n != kNothing;
+    k += wants(n);
   }
   __syncthreads();
   return s.copies;
@@ -283,14 +294,14 @@ __device__ __forceinline__ void apply_pages(const PagesArgs& a, const PlanShared
   int k = 0;                                         // the entry's place among the pages, if it wants one
   for (int it = i0; it < i1; ++it) {
     const int b = it / a.per, u = it - b * a.per;
-    const bool served = s.end[b + 1] == s.end[b] || s.end[b + 1] <= s.have;
+    const bool served = s.served(b);
     const Reserve r = reserve_of(a, b);
-    if (u == 0) a.granted[b] = served && !(s.bad[b >> 5] >> (b & 31) & 1u) ? r.m : 0;
+    if (u == 0) a.granted[b] = served ? r.m : 0;
     if (u == 0 || it == i0) {
       k = s.end[b];
-      for (int v = 0; v < u; ++v) k += need[b * a.per + v] != kNothing;
+      for (int v = 0; v < u; ++v) k += wants(need[b * a.per + v]);
     }
-    if (need[it] == kNothing) continue;
+    if (!wants(need[it])) continue;
     ++k;
     if (!served) continue;
     const int page = pages[k - 1];

@@ -139,7 +139,7 @@ class Pages:
         lens = np.asarray(lens).reshape(len(self.table), -1)
         for b, m in enumerate(new):
             lo, hi = int(lens[b].min()), int(lens[b].max())
-            job = []
+            job, keep = [], False
             if hi + m > cap:
                 jobs.append(None)
                 continue
@@ -151,15 +151,18 @@ class Pages:
                     elif uses[page] > 1:
                         job.append((i, page, min(self.bs, max(0, hi - i * self.bs))))
                         uses[page] -= 1
-            jobs.append(job)
+                    elif self.ref[page] > 1:          # those before it leave it
+                        keep = True
+            jobs.append((job, keep))
         free, asked = list(np.flatnonzero(self.ref == 0)), 0
         have = len(free)
-        for b, job in enumerate(jobs):
-            if job is None:
+        for b, x in enumerate(jobs):
+            if x is None:
                 granted.append(0)
                 continue
+            job, keep = x
             asked += len(job)
-            if job and asked > have:
+            if (job or keep) and asked > have:
                 granted.append(0)
                 continue
             for i, page, rows in job:

@@ -59,6 +59,40 @@ def test_when_pages_run_out(spare):
     c.check()
 
 
+@pytest.mark.parametrize("n_new", [64, 8192])
+@pytest.mark.parametrize("spare", [0, 1, 2, 3])
+def test_a_page_is_taken_over_only_from_those_that_leave_it(n_new, spare):
+    # request 0 has more rows on the shared page than request 1: left with it, 1 would write over them
+    def case(**kw):                                   # of the free pages `spare` are left (those not needed twice are free, too)
+        c = SH.PageCase(cap=8, seed=spare, **kw)
+        c.o.ref[np.flatnonzero(c.o.ref == 0)[spare:]] = 1
+        return c.upload()
+
+    c = case(B=4, rows=[23, 18, 23, 7], share=[None, 0, 0, None])
+    granted, st = reserve(c, [3, 2, 0, 1], n_new=n_new)
+    assert st == 0 and granted.tolist() == [3 * (spare > 0), 2 * (spare > 1), 0, 1]
+    c.check()
+    c = case(B=2, rows=[23, 18], share=[None, 0])
+    granted, st = reserve(c, [3, 2], n_new=n_new)
+    assert st == 0 and granted.tolist() == ([3, 2] if spare else [0, 0])
+    c.check()
+
+
+@pytest.mark.parametrize("n_new", [64, 8192])
+def test_a_page_of_a_request_that_is_refused_stays_its_own(n_new):
+    c = SH.PageCase(B=2, rows=[23, 18], share=[None, 0], cap=8, spare=5, seed=3).upload()
+    page = int(c.table[0, 1])
+    c.table[0, 2] = 10 ** 6
+    granted = SH.ints([7, 7])
+    lib().kvsel_pages_reserve(c.params(n_new), c.k, c.v, c.table, c.ref, c.d_lens, granted, c.ws, new_lens=SH.ints([20, 2]))
+    assert CH.status(c.ws) == -7 and granted.tolist() == [0, 2]
+    to = int(np.flatnonzero(c.o.ref == 0)[0])
+    assert c.table[:, 1].tolist() == [page, to] and c.ref[page] == 1 and c.ref[to] == 1
+    want = c.o.k.copy()
+    want[:, to, :2] = want[:, page, :2]               # (its rows 16 and 17)
+    assert np.array_equal(c.k.cpu().numpy().view(np.uint16), want)
+
+
 def test_heads_of_different_lengths():
     rows = [[5, 20, 33], [16, 16, 0], [0, 0, 0], [64, 1, 30]]
     for share in (None, [None, None, None, 0]):

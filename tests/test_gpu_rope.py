@@ -34,10 +34,12 @@ def table(**kw):
 
 
 def close(got, x, pos, o):
-    """A turned value is x1 c - x2 s.  The angle, at most pi, is cut to 23 bits of a turn (2 pi 2^-23 < 7.5e-7), multiplied
-    by a rounded constant and rounded again (pi (2^-25 + 2^-24) < 2.9e-7; 2^-32 turns are little); the approximate sine and
-    cosine are off by 2^-21 < 4.8e-7 within [-pi, pi]; factor, product and sum round three times, 2^-24 each, 1.8e-7.
-    Together below 2^-19 = 1.9e-6 of |x1| + |x2| times the factor.  One rounding to bf16: 2^-8 of the value."""
+    """A turned value is x1 c - x2 s.  The angle, at most pi, is cut to 23 bits of a turn (2 pi 2^-23 < 7.5e-7) and made of
+    them by one product and sum of rounded constants (4.5e-7 at most, over all of them); the approximate sine and cosine are
+    off by 2^-21.19 < 4.2e-7 within [-pi, pi]; factor, product and sum round three times, 2^-24 each, 1.8e-7.  Together
+    1.8e-6, below 2^-19 = 1.9e-6 of |x1| + |x2| times the factor.  (At positions near 2^31 the angles here, pos f rounded to
+    64 bits, are off by 2^-22 themselves, what is left of the bound and as much again, if all of these met.)  One rounding
+    to bf16: 2^-8 of the value."""
     want = SO.rope(x, pos, **o)
     rot = 2 * len(o["f"])
     half = rot // 2

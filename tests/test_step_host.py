@@ -329,6 +329,9 @@ def test_oracle_pages_by_hand():
     assert o.table.tolist() == [[4, -1, -1]] * 2 and o.ref.tolist() == [0, 1, 0, 0, 2, 0]
     o.trim([0, 8])
     assert o.ref.tolist() == [0, 1, 0, 0, 1, 0]
+    # no page is left: request 0 stays on the page, so request 1 cannot have it for itself
+    o = SO.Pages(np.array([[0, -1], [0, -1]]), np.array([2]), k[:, :1], k[:, :1])
+    assert o.reserve([5, 3], [1, 1]).tolist() == [0, 0] and o.table.tolist() == [[0, -1]] * 2 and o.ref.tolist() == [2]
     assert SO.keep_rows(6, [0, 3, 5]) == [0, 3, 5] and SO.keep_rows(6, [1, 2, 4]) == [4, 1, 2]
 
 
