@@ -15,6 +15,7 @@ size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 bool aligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 int launch_rc(cudaError_t e) { return e == cudaSuccess ? KVSEL_OK : KVSEL_ECUDA; }
 bool bad_stride(long long s, long long extent) { return extent > 1 && (s <= 0 || s % 8 != 0); }
+bool other(long long a, long long b, long long extent) { return extent > 1 && a != b; }
 int check_ws(const void* ws, size_t have, size_t need) {
   return !ws || !aligned(ws, 256) || have < need ? KVSEL_EWORKSPACE : KVSEL_OK;
 }
@@ -302,6 +303,12 @@ int kvsel_rope(const kvsel_rope_angles* table, const kvsel_rope_rows* p, const v
     return KVSEL_EINVAL;
   if (p->k_heads && (bad_stride(p->k_req, B) || bad_stride(p->k_head, p->k_heads) || bad_stride(p->k_tok, n) ||
                      bad_stride(p->ko_req, B) || bad_stride(p->ko_head, p->k_heads) || bad_stride(p->ko_tok, n)))
+    return KVSEL_EINVAL;
+  // in place: a row goes where it came from
+  if (q == q_out && (other(p->q_req, p->qo_req, B) || other(p->q_head, p->qo_head, p->heads) || other(p->q_tok, p->qo_tok, n)))
+    return KVSEL_EINVAL;
+  if (p->k_heads && k == k_out &&
+      (other(p->k_req, p->ko_req, B) || other(p->k_head, p->ko_head, p->k_heads) || other(p->k_tok, p->ko_tok, n)))
     return KVSEL_EINVAL;
   RopeArgs a{};
   a.t = rope_table(table);

@@ -192,6 +192,9 @@ def test_rope_refuses(B):
                      (dict(n_tok=0), -1), (dict(n_tok=(1 << 20) + 1), -3), (dict(heads=0), -1), (dict(heads=8192), -3), (dict(k_heads=-1), -1),
                      (dict(q_tok=100), -1), (dict(qo_head=0), -1), (dict(ko_req=-8), -1), (dict(pos_req=-1), -1)):
         assert call(**kw) == code, kw
+    # in place, but not to the same rows
+    for kw in (dict(qo_req=4608), dict(qo_tok=512, qo_head=128), dict(ko_tok=256), dict(ko_req=768)):
+        assert call(**kw) == -1, kw
     bad = B.kvsel_rope_table()
     bad.rot_dim = 130
     assert call(table=bad) == -1
