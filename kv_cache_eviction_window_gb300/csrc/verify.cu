@@ -19,6 +19,7 @@
 #include <cooperative_groups.h>
 
 #include "../../include/kvsel.h"
+#include "ptx.cuh"
 #include "step.cuh"
 
 namespace cgx = cooperative_groups;
@@ -60,6 +61,7 @@ __global__ void __launch_bounds__(1024) tree_masks_kernel(const int32_t* __restr
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kMaxCluster = 16;
+constexpr unsigned long long kWaitCycles = 2000000000ull;   // ~1 s at the boost clock
 constexpr int kUnitBits = 45;                        // probabilities in units of 2^-45
 constexpr unsigned long long kOne = 1ull << kUnitBits;
 
@@ -202,6 +204,25 @@ __device__ __forceinline__ unsigned long long warp_max(unsigned long long v) {
   return static_cast<unsigned long long>(hi) << 32 | lo;
 }
 
+// One number to a place of the cluster's CTA `rank`, counted by the barrier there.
+__device__ __forceinline__ void send(unsigned long long* to, unsigned long long v, uint64_t* bar, int rank) {
+  uint32_t at, there;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(to)), "r"(rank));
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(smem_u32(bar)), "r"(rank));
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.u64 [%0], %1, [%2];" ::"r"(at), "l"(v), "r"(there) : "memory");
+}
+__device__ __forceinline__ bool came(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok;
+}
+
 enum Want : int { kMass, kDraw, kLargest, kDone };
 // of a node: its token is one, its first test (A = 0, Z = 1) passes, an earlier sibling has its token (POINT)
 enum Flag : int { kValid = 1, kPasses = 2, kAgain = 4 };
@@ -211,7 +232,8 @@ struct Shared {
   int out[KVSEL_MAX_TREE], nout;                     // POINT: nodes whose tokens have no weight in the draw
   // what every warp of the cluster found in its share of the vocabulary, written by that warp to all CTAs
   unsigned long long part[2][kMaxCluster * kWarps];
-  int cur, want;
+  uint64_t came[2];                                  // bytes of `part` that have come
+  int cur, want, lost;
   unsigned long long A;
 };
 
@@ -227,6 +249,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a)
   constexpr bool greedy = MODE == KVSEL_VERIFY_GREEDY, point = MODE == KVSEL_VERIFY_POINT, sampled = MODE == KVSEL_VERIFY_SAMPLED;
   const int raw = a.new_lens ? __ldg(a.new_lens + b) : a.m, m = min(max(raw, 0), a.m);
   bool bad = raw != m;
+  if (tid == 0) s.lost = 0;
   for (int t = tid; t < m; t += kThreads) {
     int p = t ? a.parents[row + t] : -1;
     const int x = a.tokens[row + t];
@@ -273,7 +296,14 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a)
         }
     __syncthreads();
   }
-  if (cs > 1) cl.sync();                             // every CTA of the cluster runs: its shared memory may be written
+  if (cs > 1) {
+    if (tid == 0) {
+      mbar_init(&s.came[0], 1);
+      mbar_init(&s.came[1], 1);
+      fence_mbar_init();
+    }
+    cl.sync();                                       // every CTA of the cluster runs: its shared memory may be written
+  }
 
   // this warp's share of the vocabulary
   const int per_warp = ((a.vocab + cs * kWarps - 1) / (cs * kWarps) + 7) & ~7;
@@ -284,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a)
   int cur = 0, last = 0, count = 1;
   unsigned long long A = 0, Z = kOne;
   int best = -1;
-  int phase = 0;
+  int pass = 0;
   int held = 0, my_par = -2, my_flag = 0, my_tok = 0;
   auto hold = [&](int t0) {
     held = t0;
@@ -299,7 +329,8 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a)
   while (true) {
     if (warp == 0) {
       int want = kDone;
-      while (true) {
+      const bool lost = s.lost;
+      while (!lost) {
         if (stale) {
           want = kLargest;
           break;
@@ -427,15 +458,27 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a)
           }
         v = warp_sum(v);
       }
+      // All CTAs get all numbers.  A warp sends those of the next pass when this CTA has got all of this one, so those of
+      // the pass after that, which go to the same places, find these read.
+      const int side = pass & 1;
       if (cs == 1) {
-        if (lane == 0) s.part[phase][warp] = v;
+        if (lane == 0) s.part[side][warp] = v;
         __syncthreads();
       } else {
-        if (lane < cs) *cl.map_shared_rank(&s.part[phase][mine], lane) = v;
-        cl.sync();
+        if (tid == 0) mbar_arrive_expect_tx(&s.came[side], cs * kWarps * 8);
+        if (lane < cs) send(&s.part[side][mine], v, &s.came[side], lane);
+        if (want == kDraw || warp == 0) {
+          const long long t0 = clock64();
+          while (!came(&s.came[side], pass >> 1 & 1) && !*static_cast<volatile int*>(&s.lost))
+            if (static_cast<unsigned long long>(clock64() - t0) > kWaitCycles) {
+              s.lost = 1;
+              atomicOr(a.status, DEV_TIMEOUT_PIPE);
+            }
+          __syncwarp();
+        }
       }
-      const unsigned long long* part = s.part[phase];
-      phase ^= 1;
+      const unsigned long long* part = s.part[side];
+      ++pass;
       all = before = 0;
       if (want == kDraw || warp == 0) {
 #pragma unroll
@@ -479,9 +522,9 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a)
       unsigned long long at = before;
       for (int i0 = w0; i0 < w1; i0 += 32 * N) {
         const int e = i0 + lane * N;
-        unsigned long long y = 0;
+        unsigned long long y = 0, w[N];
 #pragma unroll
-        for (int c = 0; c < N; ++c) y += weight(e + c);
+        for (int c = 0; c < N; ++c) y += w[c] = weight(e + c);
         unsigned long long sum = y;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -492,8 +535,12 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a)
         if (hit) {
           if (lane == __ffs(hit) - 1) {
             unsigned long long z = at + sum - y;
-            int c = 0;
-            while (c < N - 1 && (z += weight(e + c)) <= goal) ++c;
+            int c = 0;                               // of these tokens the sum up to c passes the goal
+#pragma unroll
+            for (int k = 0; k < N - 1; ++k) {
+              z += w[k];
+              c += z <= goal;
+            }
             a.next[b] = e + c;
           }
           break;
@@ -503,6 +550,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a)
     }
     break;
   }
+  if (__any_sync(0xffffffffu, s.lost)) cl.sync();                   // (nothing may still be on its way here)
   if (rank == 0 && tid == 0) {
     a.counts[b] = count;
     if (best != -2) a.next[b] = best;
