@@ -122,15 +122,20 @@ __device__ __forceinline__ void each_of(const T* p, const T* q, int i0, int i1, 
         rp[k] = __ldg(reinterpret_cast<const uint4*>(p + v0) + u0 + 32 * k);
         if (TWO) rq[k] = __ldg(reinterpret_cast<const uint4*>(q + v0) + u0 + 32 * k);
       }
+    // (a loop, not unrolled: code that runs once or twice costs more to fetch than these moves)
+#pragma unroll 1
+    for (int u = u0; u < min(nv, u0 + 32 * kAhead); u += 32) {
+      T x[N], y[N];
+      memcpy(x, &rp[0], 16);
+      if (TWO) memcpy(y, &rq[0], 16);
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k)
-      if (u0 + 32 * k < nv) {
-        T x[N], y[N];
-        memcpy(x, &rp[k], 16);
-        if (TWO) memcpy(y, &rq[k], 16);
+      for (int c = 0; c < N; ++c) f(v0 + u * N + c, x[c], TWO ? y[c] : T());
 #pragma unroll
-        for (int c = 0; c < N; ++c) f(v0 + (u0 + 32 * k) * N + c, x[c], TWO ? y[c] : T());
+      for (int k = 0; k + 1 < kAhead; ++k) {
+        rp[k] = rp[k + 1];
+        if (TWO) rq[k] = rq[k + 1];
       }
+    }
     g();
   }
   if (lane < i1 - v1) f(v1 + lane, p[v1 + lane], TWO ? q[v1 + lane] : T());
@@ -202,6 +207,28 @@ __device__ __forceinline__ unsigned long long warp_max(unsigned long long v) {
   const uint32_t hi = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(v >> 32));
   const uint32_t lo = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(v >> 32) == hi ? static_cast<uint32_t>(v) : 0u);
   return static_cast<unsigned long long>(hi) << 32 | lo;
+}
+
+// inclusive
+__device__ __forceinline__ unsigned long long warp_scan(unsigned long long v) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned long long z = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane_id() >= o) v += z;
+  }
+  return v;
+}
+// elements e .. of a row, as many as 16 bytes hold; zeros outside [i0, i1)
+template <class T>
+__device__ __forceinline__ void some_of(const T* p, int e, int i0, int i1, T (&x)[16 / sizeof(T)]) {
+  constexpr int N = 16 / sizeof(T);
+  if (e >= i0 && e + N <= i1 && !(reinterpret_cast<uintptr_t>(p + e) & 15)) {
+    const uint4 r = __ldg(reinterpret_cast<const uint4*>(p + e));
+    memcpy(x, &r, 16);
+    return;
+  }
+#pragma unroll
+  for (int c = 0; c < N; ++c) x[c] = e + c >= i0 && e + c < i1 ? p[e + c] : T();
 }
 
 // One number to a place of the cluster's CTA `rank`, counted by the barrier there.
@@ -509,48 +536,49 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a)
     const float u = fminf(fmaxf(s.u[0], 0.f), 0.99999994f);
     const unsigned long long goal = __umul64hi(all, __float2ull_rz(u * 18446744073709551616.f));
     if (all && before <= goal && goal < before + v) {
-      // in this warp's share: a vector of tokens per lane at a time
+      // In this warp's share: each lane sums a run of tokens, and the run that passes the goal is looked at again by all
+      // lanes.  (A vector per lane at a time, with a scan each, took 1 us per 256 tokens.)
       constexpr int N = 16 / sizeof(T);
-      auto weight = [&](int i) -> unsigned long long {
-        if (i >= w1) return 0;
-        if (sampled && off && first) return rest_units(value_of<T>(p[i]), value_of<T>(q[i]), off);
-        unsigned long long y = units(value_of<T>(p[i]));
+      const bool rest = sampled && off && first;
+      const int lead = static_cast<int>((reinterpret_cast<uintptr_t>(p + w0) & 15) / sizeof(T));
+      const int per = ((w1 - w0 + lead + 31) / 32 + N - 1) / N * N, run = w0 - lead + lane * per;
+      const int l0 = max(run, w0), l1 = min(run + per, w1);
+      unsigned long long y = 0;
+#pragma unroll 1
+      for (int e = run; e < l1; e += N) {
+        T x[N], z[N] = {};
+        some_of(p, e, l0, l1, x);
+        if (rest) some_of(q, e, l0, l1, z);
+#pragma unroll
+        for (int c = 0; c < N; ++c) y += rest_units(value_of<T>(x[c]), value_of<T>(z[c]), off);
+      }
+      for (int k = 0; point && first && k < s.nout; ++k) {
+        const int t = s.out[k], x = s.tok[t];
+        if (x >= l0 && x < l1) y -= units(s.p[t]);
+      }
+      unsigned long long at = before + warp_scan(y) - y;
+      unsigned hit = __ballot_sync(0xffffffffu, at + y > goal);
+      const int who = __ffs(hit) - 1, r0 = __shfl_sync(0xffffffffu, l0, who), r1 = __shfl_sync(0xffffffffu, l1, who);
+      at = __shfl_sync(0xffffffffu, at, who);
+#pragma unroll 1
+      for (int i0 = r0; i0 < r1; i0 += 32) {
+        const int i = i0 + lane;
+        const float x = i < r1 ? value_of<T>(p[i]) : 0.f, z = rest && i < r1 ? value_of<T>(q[i]) : 0.f;
+        unsigned long long w = rest_units(x, z, off);
         for (int k = 0; point && first && k < s.nout; ++k)
-          if (s.tok[s.out[k]] == i) y = 0;
-        return y;
-      };
-      unsigned long long at = before;
-      for (int i0 = w0; i0 < w1; i0 += 32 * N) {
-        const int e = i0 + lane * N;
-        unsigned long long y = 0, w[N];
-#pragma unroll
-        for (int c = 0; c < N; ++c) y += w[c] = weight(e + c);
-        unsigned long long sum = y;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const unsigned long long z = __shfl_up_sync(0xffffffffu, sum, o);
-          if (lane >= o) sum += z;
-        }
-        const unsigned hit = __ballot_sync(0xffffffffu, at + sum > goal);
+          if (s.tok[s.out[k]] == i) w = 0;
+        const unsigned long long sum = at + warp_scan(w);
+        hit = __ballot_sync(0xffffffffu, sum > goal);
         if (hit) {
-          if (lane == __ffs(hit) - 1) {
-            unsigned long long z = at + sum - y;
-            int c = 0;                               // of these tokens the sum up to c passes the goal
-#pragma unroll
-            for (int k = 0; k < N - 1; ++k) {
-              z += w[k];
-              c += z <= goal;
-            }
-            a.next[b] = e + c;
-          }
+          if (lane == 0) a.next[b] = i0 + __ffs(hit) - 1;
           break;
         }
-        at += __shfl_sync(0xffffffffu, sum, 31);
+        at = __shfl_sync(0xffffffffu, sum, 31);
       }
     }
     break;
   }
-  if (__any_sync(0xffffffffu, s.lost)) cl.sync();                   // (nothing may still be on its way here)
+  if (__any_sync(0xffffffffu, s.lost)) cl.sync();    // (nothing may still be on its way here)
   if (rank == 0 && tid == 0) {
     a.counts[b] = count;
     if (best != -2) a.next[b] = best;
