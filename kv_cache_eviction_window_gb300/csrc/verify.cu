@@ -96,50 +96,60 @@ __device__ __forceinline__ unsigned long long rest_units(float p, float q, unsig
   return P > AQ ? P - AQ : 0;
 }
 
-// Elements [i0, i1) of a row (or of two at the same places) by the lanes of a warp, 16 bytes at a time and kAhead
-// of these loaded before the first is used: f(i, x, y) for each, in ascending order within a lane; g() after as many.
+// Elements [i0, i1) of a row (or, with q, of two at the same places) by the lanes of a warp, 16 bytes at a time and kAhead
+// of these loaded before the first is used: f(x, y) for each (y = 0 without q); g() after as many.
+// Loops are not unrolled where that only saves moves: code that runs once or twice costs more to fetch.
 constexpr int kAhead = 4;
-template <bool TWO, class T, class F, class G>
+template <class T, class F, class G>
 __device__ __forceinline__ void each_of(const T* p, const T* q, int i0, int i1, F f, G g) {
   constexpr int N = 16 / sizeof(T);
   const int lane = lane_id();
-  // the first element on a 16-byte boundary
+  // the first element on a 16-byte boundary; rows that do not share one go element by element
+  const bool apart = q && ((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(q)) & 15);
   const int lead = static_cast<int>(((16 - (reinterpret_cast<uintptr_t>(p + i0) & 15)) & 15) / sizeof(T));
-  const int v0 = min(i1, i0 + lead), nv = (i1 - v0) / N, v1 = v0 + nv * N;
-  if (TWO && ((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(q)) & 15)) {
-    for (int i = i0 + lane; i < i1; i += 32) {
-      f(i, p[i], q[i]);
-      g();
-    }
-    return;
-  }
-  if (lane < v0 - i0) f(i0 + lane, p[i0 + lane], TWO ? q[i0 + lane] : T());
+  const int v0 = apart ? i1 : min(i1, i0 + lead), nv = (i1 - v0) / N, v1 = v0 + nv * N;
+  // what lies before the vectors by the lower lanes, what lies behind by the upper ones: at most one element each
+  int i = apart || lane < 16 ? i0 + lane : v1 + lane - 16;
+  const int end = apart || lane >= 16 ? i1 : v0;
+  T ex = T(), ey = T();
+  auto edge = [&] {
+    if (i >= end) return;
+    ex = p[i];
+    if (q) ey = q[i];
+  };
+  edge();
   for (int u0 = lane; u0 < nv; u0 += 32 * kAhead) {
     uint4 rp[kAhead], rq[kAhead];
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k)
+    for (int k = 0; k < kAhead; ++k) {
+      rq[k] = make_uint4(0u, 0u, 0u, 0u);
       if (u0 + 32 * k < nv) {
         rp[k] = __ldg(reinterpret_cast<const uint4*>(p + v0) + u0 + 32 * k);
-        if (TWO) rq[k] = __ldg(reinterpret_cast<const uint4*>(q + v0) + u0 + 32 * k);
+        if (q) rq[k] = __ldg(reinterpret_cast<const uint4*>(q + v0) + u0 + 32 * k);
       }
-    // (a loop, not unrolled: code that runs once or twice costs more to fetch than these moves)
+    }
 #pragma unroll 1
     for (int u = u0; u < min(nv, u0 + 32 * kAhead); u += 32) {
       T x[N], y[N];
       memcpy(x, &rp[0], 16);
-      if (TWO) memcpy(y, &rq[0], 16);
+      memcpy(y, &rq[0], 16);
 #pragma unroll
-      for (int c = 0; c < N; ++c) f(v0 + u * N + c, x[c], TWO ? y[c] : T());
+      for (int c = 0; c < N; ++c) f(x[c], y[c]);
 #pragma unroll
       for (int k = 0; k + 1 < kAhead; ++k) {
         rp[k] = rp[k + 1];
-        if (TWO) rq[k] = rq[k + 1];
+        rq[k] = rq[k + 1];
       }
     }
     g();
   }
-  if (lane < i1 - v1) f(v1 + lane, p[v1 + lane], TWO ? q[v1 + lane] : T());
-  g();
+#pragma unroll 1
+  while (i < end) {
+    f(ex, ey);
+    g();
+    i += 32;
+    edge();
+  }
 }
 
 // The largest value of elements [i0, i1) of a row and the lowest place that has it, by the lanes of a warp (each
@@ -460,23 +470,16 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a)
           v = static_cast<unsigned long long>((k & 0x80000000u) ? ~k : (k | 0x80000000u)) << 32 | (0xFFFFFFFFu - static_cast<uint32_t>(at));
         }
         v = warp_max(v);
-      } else if (sampled && off == kOne && first) {
-        // the first rejection: p - q where that is positive
-        each_of<true>(p, q, w0, w1, [&](int, T x, T y) {
+      } else if (sampled && off && off != kOne && first) {
+        each_of(p, q, w0, w1, [&](T x, T y) { v += rest_units(value_of<T>(x), value_of<T>(y), off); }, [] {});
+        v = warp_sum(v);
+      } else {
+        // p itself, or after the first rejection p - q where that is positive
+        each_of(p, sampled && off && first ? q : nullptr, w0, w1, [&](T x, T y) {
           const float xp = prob(value_of<T>(x)), xq = prob(value_of<T>(y));
           const Parts P = parts(xp), Q = parts(xq);
           hi += xp > xq ? P.hi - Q.hi : 0;
           lo += xp > xq ? P.lo - Q.lo : 0;
-        }, flush);
-        v = warp_sum(v);
-      } else if (sampled && off && first) {
-        each_of<true>(p, q, w0, w1, [&](int, T x, T y) { v += rest_units(value_of<T>(x), value_of<T>(y), off); }, [] {});
-        v = warp_sum(v);
-      } else {
-        each_of<false>(p, p, w0, w1, [&](int, T x, T) {
-          const Parts P = parts(prob(value_of<T>(x)));
-          hi += P.hi;
-          lo += P.lo;
         }, flush);
         if (point && first)                          // POINT: what was rejected here has no weight any more
           for (int k = lane; k < s.nout; k += 32) {
