@@ -10,12 +10,13 @@
 // sum over the vocabulary is needed where a sibling follows, and one for the last draw.  Probabilities
 // count as integers in units of 2^-45 there: sums are exact and do not depend on their order, 2^18 of them
 // fit 64 bits, and the draw is the comparison of integers.
-// Bound: latency.  Launch, the nodes' values and the first walk take some 5 us; a sum or maximum over a row of 131072
-// tokens 4500 cycles: 2000 for the row (2 KB a warp), 1500 until the cluster has met (every warp writes its number to all
-// of its CTAs before, so nothing is fetched behind it), 600 for the walk, 400 for the numbers.  One is made for each
-// rejection that a sibling follows, unless the sibling passes with the mass before, and one for the last draw; GREEDY
-// makes one per accepted node.  Measured on one GB300: 32 chains of five drafted tokens over 50257 tokens, fp32, 12.3 us;
-// 8 trees of 64 nodes over 131072, bf16, 15 to 25 us by what is rejected; 32 requests of 26 nodes, GREEDY, 16.2 us.
+// Bound: latency, of loads and of instructions: code that runs once per launch is fetched from L2, so loops are kept
+// small.  One request of one node, GREEDY, 131072 tokens, takes 4.6 us, each round over the vocabulary more 2.1: the row's
+// loads 1, the numbers to all CTAs of the cluster (which a barrier there counts; a barrier of the cluster took 0.35 longer)
+// and the walk.  A round is made for each rejection that a sibling follows, unless the sibling passes with the mass before,
+// and one for the last draw; GREEDY makes one per accepted node.  Measured on one GB300: 32 chains of five drafted tokens
+// over 50257 tokens, fp32, 10.7 us; 8 trees of 64 nodes over 131072, bf16, 13 to 27 us by what is rejected; 32 requests of
+// 26 nodes, GREEDY, 14.4 us.  (512 threads per CTA: 1 to 4 us less for 64 requests, 1 to 5 more for small vocabularies.)
 #include <cooperative_groups.h>
 
 #include "../../include/kvsel.h"
