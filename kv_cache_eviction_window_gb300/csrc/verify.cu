@@ -15,8 +15,9 @@
 // loads 1, the numbers to all CTAs of the cluster (which a barrier there counts; a barrier of the cluster took 0.35 longer)
 // and the walk.  A round is made for each rejection that a sibling follows, unless the sibling passes with the mass before,
 // and one for the last draw; GREEDY makes one per accepted node.  Measured on one GB300: 32 chains of five drafted tokens
-// over 50257 tokens, fp32, 10.7 us; 8 trees of 64 nodes over 131072, bf16, 13 to 27 us by what is rejected; 32 requests of
-// 26 nodes, GREEDY, 14.4 us.  (512 threads per CTA: 1 to 4 us less for 64 requests, 1 to 5 more for small vocabularies.)
+// over 50257 tokens, fp32, 9.9 us; 8 trees of 64 nodes over 131072, bf16, 13 to 28 us by what is rejected; 32 requests of
+// 26 nodes, GREEDY, 14.4 us; 512 requests of one node, bf16, 87 us for 134 MB (the sums' instructions).  (512 threads per
+// CTA: a tenth to a quarter less for hundreds of requests, 1 to 5 us more for small vocabularies.)
 #include <cooperative_groups.h>
 
 #include "../../include/kvsel.h"
@@ -97,60 +98,75 @@ __device__ __forceinline__ unsigned long long rest_units(float p, float q, unsig
   return P > AQ ? P - AQ : 0;
 }
 
-// Elements [i0, i1) of a row (or, with q, of two at the same places) by the lanes of a warp, 16 bytes at a time and kAhead
-// of these loaded before the first is used: f(x, y) for each (y = 0 without q); g() after as many.
-// Loops are not unrolled where that only saves moves: code that runs once or twice costs more to fetch.
+// The 16-byte vectors in elements [i0, i1) of a row (or, with q, of two at the same places): nv from v0 on, which end at v1.
+// Rows that do not share a boundary have none.
 constexpr int kAhead = 4;
-template <class T, class F, class G>
-__device__ __forceinline__ void each_of(const T* p, const T* q, int i0, int i1, F f, G g) {
-  constexpr int N = 16 / sizeof(T);
+template <class T>
+struct Span {
+  static constexpr int N = 16 / sizeof(T), kChunk = 32 * kAhead * N;
+  int i0, i1, v0, nv, v1;
+  bool apart;
+  // the last draw looks for a chunk first
+  __device__ __forceinline__ bool wide() const { return nv > 32 * kAhead; }
+  __device__ __forceinline__ Span(const T* p, const T* q, int from, int to) : i0(from), i1(to) {
+    apart = q && ((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(q)) & 15);
+    const int lead = static_cast<int>(((16 - (reinterpret_cast<uintptr_t>(p + i0) & 15)) & 15) / sizeof(T));
+    v0 = apart ? i1 : min(i1, i0 + lead);
+    nv = (i1 - v0) / N;
+    v1 = v0 + nv * N;
+  }
+};
+// f(x, y) for each element (y = 0 without q), by the lanes of a warp: kChunk elements at a time, a vector of each lane after
+// another and all loaded before the first is used, with chunk() after them; then what lies before the vectors by the lower
+// lanes and what lies behind by the upper ones, with edge() after one element of each.
+// Loops are not unrolled where that only saves moves: code that runs once or twice costs more to fetch.
+template <class T, class F, class G, class E>
+__device__ __forceinline__ void each_of(const Span<T>& x, const T* p, const T* q, F f, G chunk, E edge) {
+  constexpr int N = Span<T>::N;
   const int lane = lane_id();
-  // the first element on a 16-byte boundary; rows that do not share one go element by element
-  const bool apart = q && ((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(q)) & 15);
-  const int lead = static_cast<int>(((16 - (reinterpret_cast<uintptr_t>(p + i0) & 15)) & 15) / sizeof(T));
-  const int v0 = apart ? i1 : min(i1, i0 + lead), nv = (i1 - v0) / N, v1 = v0 + nv * N;
-  // what lies before the vectors by the lower lanes, what lies behind by the upper ones: at most one element each
-  int i = apart || lane < 16 ? i0 + lane : v1 + lane - 16;
-  const int end = apart || lane >= 16 ? i1 : v0;
+  int i = x.apart || lane < 16 ? x.i0 + lane : x.v1 + lane - 16;
+  const int end = x.apart || lane >= 16 ? x.i1 : x.v0;
   T ex = T(), ey = T();
-  auto edge = [&] {
+  auto next = [&] {
     if (i >= end) return;
     ex = p[i];
     if (q) ey = q[i];
   };
-  edge();
-  for (int u0 = lane; u0 < nv; u0 += 32 * kAhead) {
+  next();
+  for (int c0 = 0; c0 < x.nv; c0 += 32 * kAhead) {
+    const int u0 = c0 + lane;
     uint4 rp[kAhead], rq[kAhead];
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
       rq[k] = make_uint4(0u, 0u, 0u, 0u);
-      if (u0 + 32 * k < nv) {
-        rp[k] = __ldg(reinterpret_cast<const uint4*>(p + v0) + u0 + 32 * k);
-        if (q) rq[k] = __ldg(reinterpret_cast<const uint4*>(q + v0) + u0 + 32 * k);
+      if (u0 + 32 * k < x.nv) {
+        rp[k] = __ldg(reinterpret_cast<const uint4*>(p + x.v0) + u0 + 32 * k);
+        if (q) rq[k] = __ldg(reinterpret_cast<const uint4*>(q + x.v0) + u0 + 32 * k);
       }
     }
 #pragma unroll 1
-    for (int u = u0; u < min(nv, u0 + 32 * kAhead); u += 32) {
-      T x[N], y[N];
-      memcpy(x, &rp[0], 16);
-      memcpy(y, &rq[0], 16);
+    for (int u = u0; u < min(x.nv, u0 + 32 * kAhead); u += 32) {
+      T a[N], b[N];
+      memcpy(a, &rp[0], 16);
+      memcpy(b, &rq[0], 16);
 #pragma unroll
-      for (int c = 0; c < N; ++c) f(x[c], y[c]);
+      for (int c = 0; c < N; ++c) f(a[c], b[c]);
 #pragma unroll
       for (int k = 0; k + 1 < kAhead; ++k) {
         rp[k] = rp[k + 1];
         rq[k] = rq[k + 1];
       }
     }
-    g();
+    chunk();
   }
 #pragma unroll 1
   while (i < end) {
     f(ex, ey);
-    g();
-    i += 32;
     edge();
+    i += 32;
+    next();
   }
+  __syncwarp();
 }
 
 // The largest value of elements [i0, i1) of a row and the lowest place that has it, by the lanes of a warp (each
@@ -261,15 +277,24 @@ __device__ __forceinline__ bool came(uint64_t* bar, uint32_t parity) {
   return ok;
 }
 
+// which of a span's chunks token x is in: 0 before the vectors, then theirs, then what lies behind
+template <class T>
+__device__ __forceinline__ int chunk_of(const Span<T>& s, int x) {
+  return x < s.v0 ? 0 : (min(x, s.v1) - s.v0 + (x < s.v1 ? 0 : Span<T>::kChunk - 1)) / Span<T>::kChunk + 1;
+}
+
 enum Want : int { kMass, kDraw, kLargest, kDone };
 // of a node: its token is one, its first test (A = 0, Z = 1) passes, an earlier sibling has its token (POINT)
 enum Flag : int { kValid = 1, kPasses = 2, kAgain = 4 };
+constexpr int kChunks = KVSEL_MAX_VOCAB / kWarps / Span<float>::kChunk + 2;
 struct Shared {
   int par[KVSEL_MAX_TREE], tok[KVSEL_MAX_TREE], flag[KVSEL_MAX_TREE];
   float p[KVSEL_MAX_TREE], q[KVSEL_MAX_TREE], u[KVSEL_MAX_TREE];
   int out[KVSEL_MAX_TREE], nout;                     // POINT: nodes whose tokens have no weight in the draw
   // what every warp of the cluster found in its share of the vocabulary, written by that warp to all CTAs
   unsigned long long part[2][kMaxCluster * kWarps];
+  // the last draw: what every warp found before its vectors, in each chunk of them, and behind
+  unsigned long long chunk[kWarps][kChunks];
   uint64_t came[2];                                  // bytes of `part` that have come
   int cur, want, lost;
   unsigned long long A;
@@ -456,10 +481,22 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a)
     unsigned long long v, all, before;
     while (true) {
       v = 0;
-      int hi = 0, lo = 0;
+      unsigned long long sum = 0;
+      int hi = 0, lo = 0, chunks = 0;
+      const bool rest = sampled && off && first;
+      const Span<T> span(p, rest ? q : nullptr, w0, w1);
+      const bool wide = want == kDraw && span.wide();
       auto flush = [&] {
         v += static_cast<unsigned long long>(whole(hi, lo));
         hi = lo = 0;
+      };
+      auto chunk = [&] {
+        flush();
+        if (!wide) return;
+        const unsigned long long y = warp_sum(v);
+        if (lane == 0) s.chunk[warp][++chunks] = y;
+        sum += y;
+        v = 0;
       };
       if (greedy) {
         float top;
@@ -471,23 +508,37 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a)
           v = static_cast<unsigned long long>((k & 0x80000000u) ? ~k : (k | 0x80000000u)) << 32 | (0xFFFFFFFFu - static_cast<uint32_t>(at));
         }
         v = warp_max(v);
-      } else if (sampled && off && off != kOne && first) {
-        each_of(p, q, w0, w1, [&](T x, T y) { v += rest_units(value_of<T>(x), value_of<T>(y), off); }, [] {});
-        v = warp_sum(v);
+      } else if (rest && off != kOne) {
+        each_of(span, p, q, [&](T x, T y) { v += rest_units(value_of<T>(x), value_of<T>(y), off); }, chunk, [] {});
       } else {
         // p itself, or after the first rejection p - q where that is positive
-        each_of(p, sampled && off && first ? q : nullptr, w0, w1, [&](T x, T y) {
+        each_of(span, p, rest ? q : nullptr, [&](T x, T y) {
           const float xp = prob(value_of<T>(x)), xq = prob(value_of<T>(y));
           const Parts P = parts(xp), Q = parts(xq);
           hi += xp > xq ? P.hi - Q.hi : 0;
           lo += xp > xq ? P.lo - Q.lo : 0;
-        }, flush);
-        if (point && first)                          // POINT: what was rejected here has no weight any more
+        }, chunk, flush);
+      }
+      if (!greedy) {
+        // POINT: what was rejected here has no weight any more
+        unsigned long long gone = 0;
+        if (wide) {
+          const unsigned long long lead = warp_sum(span.apart || lane < 16 ? v : 0), tail = warp_sum(span.apart || lane < 16 ? 0 : v);
+          if (lane == 0) {
+            s.chunk[warp][0] = lead;
+            s.chunk[warp][(span.nv + 32 * kAhead - 1) / (32 * kAhead) + 1] = tail;
+          }
+          __syncwarp();
+        }
+        if (point && first)
           for (int k = lane; k < s.nout; k += 32) {
             const int x = s.tok[s.out[k]];
-            if (x >= w0 && x < w1) v -= units(s.p[s.out[k]]);
+            if (x < w0 || x >= w1) continue;
+            const unsigned long long y = units(s.p[s.out[k]]);
+            gone += y;
+            if (wide) atomicAdd(&s.chunk[warp][chunk_of(span, x)], 0 - y);
           }
-        v = warp_sum(v);
+        v = sum + warp_sum(v - gone);
       }
       // All CTAs get all numbers.  A warp sends those of the next pass when this CTA has got all of this one, so those of
       // the pass after that, which go to the same places, find these read.
@@ -540,13 +591,31 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a)
     const float u = fminf(fmaxf(s.u[0], 0.f), 0.99999994f);
     const unsigned long long goal = __umul64hi(all, __float2ull_rz(u * 18446744073709551616.f));
     if (all && before <= goal && goal < before + v) {
-      // In this warp's share: each lane sums a run of tokens, and the run that passes the goal is looked at again by all
-      // lanes.  (A vector per lane at a time, with a scan each, took 1 us per 256 tokens.)
+      // In this warp's share: the chunk that passes the goal, in which each lane sums a run of tokens, and the run that
+      // passes it is looked at again by all lanes.  (One warp that went over its whole share took 120 us of 150 for 512
+      // requests of 131072 tokens.)
       constexpr int N = 16 / sizeof(T);
       const bool rest = sampled && off && first;
-      const int lead = static_cast<int>((reinterpret_cast<uintptr_t>(p + w0) & 15) / sizeof(T));
-      const int per = ((w1 - w0 + lead + 31) / 32 + N - 1) / N * N, run = w0 - lead + lane * per;
-      const int l0 = max(run, w0), l1 = min(run + per, w1);
+      const Span<T> span(p, rest ? q : nullptr, w0, w1);
+      unsigned long long at = before;
+      int f0 = w0, f1 = w1;
+      if (span.wide()) {
+        const int chunks = (span.nv + 32 * kAhead - 1) / (32 * kAhead) + 2;
+        int here = 0;
+#pragma unroll 1
+        for (int c0 = 0; c0 < chunks; c0 += 32) {
+          const unsigned long long y = c0 + lane < chunks ? s.chunk[warp][c0 + lane] : 0, sum = at + warp_scan(y);
+          const unsigned hit = __ballot_sync(0xffffffffu, sum > goal);
+          here = c0 + (hit ? __ffs(hit) - 1 : 0);
+          at = __shfl_sync(0xffffffffu, hit ? sum - y : sum, hit ? here - c0 : 31);
+          if (hit) break;
+        }
+        f0 = here == 0 ? w0 : here == chunks - 1 ? span.v1 : span.v0 + (here - 1) * Span<T>::kChunk;
+        f1 = here == 0 ? span.v0 : here == chunks - 1 ? w1 : min(span.v1, span.v0 + here * Span<T>::kChunk);
+      }
+      const int lead = static_cast<int>((reinterpret_cast<uintptr_t>(p + f0) & 15) / sizeof(T));
+      const int per = ((f1 - f0 + lead + 31) / 32 + N - 1) / N * N, run = f0 - lead + lane * per;
+      const int l0 = max(run, f0), l1 = min(run + per, f1);
       unsigned long long y = 0;
 #pragma unroll 1
       for (int e = run; e < l1; e += N) {
@@ -560,7 +629,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a)
         const int t = s.out[k], x = s.tok[t];
         if (x >= l0 && x < l1) y -= units(s.p[t]);
       }
-      unsigned long long at = before + warp_scan(y) - y;
+      at += warp_scan(y) - y;
       unsigned hit = __ballot_sync(0xffffffffu, at + y > goal);
       const int who = __ffs(hit) - 1, r0 = __shfl_sync(0xffffffffu, l0, who), r1 = __shfl_sync(0xffffffffu, l1, who);
       at = __shfl_sync(0xffffffffu, at, who);

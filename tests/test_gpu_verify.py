@@ -62,6 +62,21 @@ def test_draft_on_another_boundary_than_target():
     c.check()
 
 
+@pytest.mark.parametrize("mode,dtype,near,pad,lead", [("sampled", "fp32", 0.1, 0, 0), ("sampled", "bf16", 2.0, 5, 3), ("point", "bf16", 0.1, 1, 1),
+                                                      ("point", "fp32", 0.1, 2, 1)])
+def test_draws_all_over_long_rows(mode, dtype, near, pad, lead):
+    # many requests: a CTA has a row to itself, a warp several stretches of it; the draws fall all over them
+    run(B=230, m=3, V=9001, mode=mode, dtype=dtype, kind="star", near=near, pad=pad, lead=lead, sharp=0.5, seed=pad)
+
+
+def test_draws_where_rows_do_not_share_a_boundary():
+    c = SH.VerifyCase(B=230, m=2, V=9001, kind="star", near=2.0, seed=6, sharp=0.5).upload()
+    d = SH.VerifyCase(B=230, m=2, V=9001, kind="star", near=2.0, seed=6, sharp=0.5).upload(lead=1)
+    c.t["draft"] = d.t["draft"]
+    assert CH.status(c.call()) == 0
+    c.check()
+
+
 def test_large_vocabulary():
     c = SH.VerifyCase(B=1, m=4, V=262144, kind="star", near=1.0, seed=2).upload()
     assert CH.status(c.call()) == 0
