@@ -316,11 +316,18 @@ def _refuse(where: str, why: str) -> None:
     raise KvselError(KVSEL_EINVAL, f"{where}: {why}")
 
 
+_BF16 = None   # torch's type, once it is loaded
+
+
 def _is_bf16(t) -> bool:
     """bf16, or its bit patterns in 16-bit integers."""
+    global _BF16
+    if t.dtype is _BF16:
+        return True
     import torch
 
-    return t.dtype is torch.bfloat16 or (t.element_size() == 2 and not t.is_floating_point())
+    _BF16 = torch.bfloat16
+    return t.dtype is _BF16 or (t.element_size() == 2 and not t.is_floating_point())
 
 
 def _same_rows(where: str, k, v) -> None:
@@ -868,9 +875,12 @@ def kvsel_rope_table(*, rot_dim: int = 128, layout: str = "half", theta: float =
 
 
 @functools.lru_cache(maxsize=256)
-def _rope_rows(q_shape, q, qo, k_shape, k, ko, pos_shape, pos) -> kvsel_rope_rows:
+def _rope_rows(q_shape, q, qo_shape, qo, k_shape, k, ko_shape, ko, pos_shape, pos) -> kvsel_rope_rows:
     """What kvsel_rope is told of tensors with these shapes and strides."""
-    where, (B, h, n, d) = "kvsel_rope", q_shape
+    where = "kvsel_rope"
+    if len(q_shape) != 4 or qo_shape != q_shape or (k_shape and (len(k_shape) != 4 or ko_shape != k_shape)):
+        _refuse(where, f"q {q_shape} to {qo_shape}, k {k_shape} to {ko_shape}")
+    B, h, n, d = q_shape
     hk = k_shape[1] if k_shape else 0
     if d != 128 or (k_shape and (k_shape[0], *k_shape[2:]) != (B, n, d)) or any(s[3] != 1 for s in (q, qo, k, ko) if s):
         _refuse(where, f"q {q_shape} with strides {q} and {qo}, k {k_shape} with strides {k} and {ko}")
@@ -885,20 +895,22 @@ def kvsel_rope(table: kvsel_rope_angles, q, pos, q_out=None, k=None, k_out=None,
     without an output in place."""
     where = "kvsel_rope"
     q_out = q if q_out is None else q_out
-    if k is not None and k_out is None:
-        k_out = k
-    if (k_out is not None) and k is None:
-        _refuse(where, "k_out without k")
-    for t, like in ((q, q), (q_out, q), (k, k), (k_out, k)):
-        if t is not None and (t.dim() != 4 or not _is_bf16(t) or t.shape != like.shape):
+    if k is None:
+        if k_out is not None:
+            _refuse(where, "k_out without k")
+        keys, k_ptr, ko_ptr = (None,) * 4, None, None
+    else:
+        k_out = k if k_out is None else k_out
+        keys, k_ptr, ko_ptr = (k.shape, k.stride(), k_out.shape, k_out.stride()), k.data_ptr(), k_out.data_ptr()
+    for t in (q, q_out) if k is None else (q, q_out, k, k_out):
+        if not _is_bf16(t):
             _refuse(where, f"{tuple(t.shape)} of {t.dtype}")
-    if pos.element_size() != 4 or pos.is_floating_point():
+    if pos.dtype is not _INT32 and (pos.element_size() != 4 or pos.is_floating_point()):
         _refuse(where, f"pos of {pos.dtype}")
-    p = _rope_rows(q.shape, q.stride(), q_out.stride(), *((k.shape, k.stride(), k_out.stride()) if k is not None else (None,) * 3),
-                   pos.shape, pos.stride())
+    p = _rope_rows(q.shape, q.stride(), q_out.shape, q_out.stride(), *keys, pos.shape, pos.stride())
     st = _place(q, stream, where)
-    rc = (_lib or load()).kvsel_rope(table, p, q.data_ptr(), q_out.data_ptr(), _ptr(k), _ptr(k_out), pos.data_ptr(),
-                                     _int32(new_lens, p.batch, where), st)
+    rc = (_lib or load()).kvsel_rope(table, p, q.data_ptr(), q_out.data_ptr(), k_ptr, ko_ptr, pos.data_ptr(),
+                                     new_lens if new_lens is None else _int32(new_lens, p.batch, where), st)
     if rc:
         _check(rc, where)
 
