@@ -40,7 +40,7 @@ namespace {
 
 constexpr int kTK = 128;                             // cached rows per tile
 constexpr int kQkWarp = 8, kPvWarp = 10, kLoadWarp = 12;   // + stream
-constexpr int kThreads = 512;                        // four warpgroups; warps 13 to 15 idle
+constexpr int kThreads = 512;                        // four warpgroups; warps 13 (but for BOTH) to 15 idle
 // registers per thread: 128 at launch (4 x 128 x 32 per sub-partition), then 184 for the two
 // softmax warpgroups and 72 for the others: 2 x 184 + 2 x 72 = 4 x 128
 constexpr int kSoftRegs = 184, kOtherRegs = 72;
