@@ -81,6 +81,9 @@ int check_tree(const kvsel_attn_params* p) {
 //   few       8.0 and the cache at 6.2 TB/s: 32 segments of 65536 rows 164.8
 //   cut       17.0 and the cache at 6.3 TB/s or the products at 1.3 PFLOP/s: 8 segments of 1024 rows 15.5, 64 of 4096 43,
 //             32 of 65536 182
+// With more items than SMs whole ones go in waves, 3 us and the times above for each, and cut ones cost 8 us for each that a
+// CTA has (5 for up to two tiles or of two blocks): 256 segments of 1024 rows, 32 query rows, 39.7 and 60.5; 512 of 256 rows
+// 43.4 and 41.3; 176 of 4096 rows 89 and 79; 256 query rows 51.6 and 55.3, 54.4 and 50.5, 117 and 88.
 // (Over those 210 shapes the calls take 1.11 times less than by the rules of kvsel_attend, and at most 15% more than by the
 // best of the three.)
 void plan_tree(const kvsel_attn_params* p, int sms, AttnPlan& pl) {
@@ -92,12 +95,12 @@ void plan_tree(const kvsel_attn_params* p, int sms, AttnPlan& pl) {
   const bool split = R <= block;
   const long long tiles = (rows + 127) / 128, items = segs * ((R + 2 * block - 1) / (2 * block));
   double best = 170.0 + std::max(segs * rows * 512.0 / 6.3e5, segs * rows * R * 512.0 / 1.3e8);
-  if (items <= sms) {
-    const double t = split ? 84.0 + 24.5 * ((tiles + 1) / 2) : 86.0 + 17.0 * tiles;
-    if (t < best) {
-      best = t;
-      pl.whole = true;
-    }
+  if (items > sms) best += (split && tiles > 2 ? 80.0 : 50.0) * items / sms;
+  const double one = split ? 84.0 + 24.5 * ((tiles + 1) / 2) : 86.0 + 17.0 * tiles;
+  const double each = items > sms ? 30.0 + one * ((items + sms - 1) / sms) : one;
+  if (each < best) {
+    best = each;
+    pl.whole = true;
   }
   const long long small = segs * ((R + attend_rows_tile() - 1) / attend_rows_tile()), steps = (rows + 63) / 64;
   for (int c = 8; c >= 1; c /= 2) {

@@ -39,6 +39,14 @@ def test_many_requests():
     SH.run_tree(B=300, H=1, G=2, m=3, lens=[3 + i for i in range(300)], layout="contiguous", seed=3)
 
 
+@pytest.mark.parametrize("m,G,long", [(8, 4, 500), (8, 4, 4000), (50, 4, 300), (50, 4, 4000), (4, 32, 900), (70, 2, 4100)])
+def test_more_items_than_ctas(m, G, long):
+    # whole items in waves, or cut ones where some are long; requests without nodes or rows among them
+    lens = [long if i == 77 else (i * 13) % 180 for i in range(200)]
+    SH.run_tree(B=200, H=1, G=G, m=m, lens=lens, new=[min(n, (i * 7) % (m + 1)) for i, n in enumerate(lens)], layout="paged", block=16, seed=m)
+    SH.run_tree(B=200, H=1, G=G, m=m, lens=lens, new=[min(n, m) for n in lens], layout="contiguous", window=90, n_sink=3, seed=m + 1)
+
+
 @pytest.mark.parametrize("B", [1, 500, 700])
 def test_many_requests_and_pages(B):
     # (up to 1024 touched entries in one launch, more in two)
