@@ -111,6 +111,18 @@ __device__ __forceinline__ int block_scan(int v, int* s_w, int& total) {
   return v;
 }
 
+// Entry u of those that the new rows of a request touch (rows [lo, end) are written to), or -1: none.  A request that is
+// not served touches none, whatever its lengths are: a negative one would lead to words before the table.
+__host__ __device__ constexpr long long touched_entry(bool ok, int lo, int end, int u, int shift) {
+  if (!ok || lo < 0) return -1;
+  const long long i = (lo >> shift) + static_cast<long long>(u);
+  return (i << shift) < end ? i : -1;
+}
+static_assert(touched_entry(true, 0, 1, 0, 3) == 0 && touched_entry(true, 17, 18, 0, 4) == 1 && touched_entry(true, 17, 33, 1, 4) == 2);
+static_assert(touched_entry(true, 17, 32, 1, 4) < 0 && touched_entry(true, 16, 0, 0, 4) < 0);
+static_assert(touched_entry(false, -1, 0, 0, 3) < 0 && touched_entry(false, -0x7FFFFFFF - 1, 0, 0, 3) < 0);
+static_assert(touched_entry(false, -1, 0, 1, 6) < 0 && touched_entry(true, -1, 0, 0, 3) < 0);
+
 struct Reserve {
   int lo, end, page0, m;          // first and last row that are written, the first's entry; new rows
   bool ok;
@@ -122,7 +134,7 @@ __device__ __forceinline__ Reserve reserve_of(const PagesArgs& a, int b) {
   r.m = min(max(raw, 0), a.m);
   r.ok = rows_of(a, a.lens, b, r.lo, hi) && raw == r.m &&
          static_cast<long long>(hi) + r.m <= static_cast<long long>(a.max_blocks) << a.shift;
-  r.page0 = r.lo >> a.shift;
+  r.page0 = r.ok ? r.lo >> a.shift : 0;
   r.end = r.ok ? hi + r.m : 0;
   // heads so far apart that their entries do not fit the plan
   if (r.ok && r.m > 0 && ((r.end - 1) >> a.shift) - r.page0 >= a.per) {
@@ -188,9 +200,9 @@ __device__ __forceinline__ int plan_pages(const PagesArgs& a, PlanShared& s, int
     const int b = it / a.per, u = it - b * a.per;
     range(b);
     int n = kNothing;
-    const int i = r.page0 + u;
+    const long long i = touched_entry(r.ok, r.lo, r.end, u, a.shift);
     if (!r.ok && u == 0) atomicOr(&s.bad[b >> 5], 1u << (b & 31));
-    if ((static_cast<long long>(i) << a.shift) < r.end) {
+    if (i >= 0) {
       const int page = a.table[static_cast<long long>(b) * a.max_blocks + i];
       if (page < 0) {
         n = kPage;

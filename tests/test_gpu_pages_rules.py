@@ -1,0 +1,65 @@
+"""Reservations of pages that have to be refused in part: lengths that no cache has, entries that no table has."""
+import numpy as np
+import pytest
+
+from tests import cache_harness as CH
+from tests import step_harness as SH
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    import __graft_entry__
+
+    __graft_entry__.build()
+    yield
+
+
+def lib():
+    from kv_cache_eviction_window_gb300 import binding
+
+    return binding
+
+
+def guarded(c):
+    """The table between words that name pages in use, so that a row before or behind it would be served or refused by
+    what lies there."""
+    import torch
+
+    B, cap = c.table.shape
+    wide = torch.full((B * cap + 128,), int(c.table.max()), dtype=torch.int32, device="cuda")
+    wide[64:-64] = c.table.reshape(-1)
+    c.table = wide[64:-64].view(B, cap)
+    return wide
+
+
+@pytest.mark.parametrize("n_new", [64, 8192])        # (one launch; two, with pages of 8)
+@pytest.mark.parametrize("bs", [8, 64])
+@pytest.mark.parametrize("where", [0, 1, 2])
+@pytest.mark.parametrize("length", [-1, -8, -1000, -2 ** 31])
+def test_a_negative_length_is_recorded_and_the_others_are_served(n_new, bs, where, length):
+    c = SH.PageCase(B=3, bs=bs, rows=[20, 33, 70], cap=16, spare=30, seed=bs).upload()
+    wide = guarded(c)
+    before, granted = wide.clone(), SH.ints([7, 7, 7])
+    c.d_lens[where] = length
+    lib().kvsel_pages_reserve(c.params(n_new), c.k, c.v, c.table, c.ref, c.d_lens, granted, c.ws, new_lens=SH.ints([9, 9, 9]))
+    assert CH.status(c.ws) == -7
+    new = [9, 9, 9]
+    new[where] = 0
+    assert np.array_equal(c.o.reserve(c.lens, new), granted.cpu().numpy())
+    c.check()
+    assert wide[:64].equal(before[:64]) and wide[-64:].equal(before[-64:])
+
+
+@pytest.mark.parametrize("n_new", [64, 8192])
+@pytest.mark.parametrize("length", [-1, -2 ** 31])
+def test_a_negative_length_of_one_head(n_new, length):
+    c = SH.PageCase(B=2, H=3, bs=8, rows=[[5, 20, 33], [16, 16, 0]], per_head=True, cap=16, spare=30, seed=2).upload()
+    guarded(c)
+    granted = SH.ints([7, 7])
+    c.d_lens[0, 1] = length
+    lib().kvsel_pages_reserve(c.params(n_new), c.k, c.v, c.table, c.ref, c.d_lens, granted, c.ws, new_lens=SH.ints([4, 4]))
+    assert CH.status(c.ws) == -7
+    assert np.array_equal(c.o.reserve(c.lens, [0, 4]), granted.cpu().numpy())
+    c.check()
