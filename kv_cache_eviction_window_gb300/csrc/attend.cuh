@@ -293,9 +293,9 @@ __device__ __forceinline__ int last_cta(const Share<Item>& sh, long long e) {
 }
 
 // Records for the join: at a kernel's start, and by the CTA that works on an item's first tile
-// (`follow` CTAs work on the others).
+// (`follow` CTAs work on the others).  Whole items have none: there may be more of them than `rec` has room for.
 __device__ __forceinline__ void rec_clear(const AttnArgs& a) {
-  if (threadIdx.x == 0 && !a.by_item) a.rec[blockIdx.x] = make_int2(-1, 0);
+  if (threadIdx.x == 0 && !a.by_item && !a.whole) a.rec[blockIdx.x] = make_int2(-1, 0);
 }
 __device__ __forceinline__ void rec_first(const AttnArgs& a, int item, int follow) {
   if (threadIdx.x != 0) return;
