@@ -594,7 +594,7 @@ int kvsel_attend_tree_workspace_size(const kvsel_attn_params* p, size_t* bytes);
  *   p        causal = 1, n_new <= KVSEL_MAX_TREE; acc_stride is not read
  *   tree     device uint32 [batch][n_new][ceil(n_new / 32)] as kvsel_tree_masks writes it; bits of rows at or
  *            behind m and the masks of nodes at or behind m are not used
- *   the other arguments, results, workspace and errors as kvsel_attend's
+ *   the other arguments, results, workspace and errors as kvsel_attend's (the weights' 2^-16 up to 16 query rows included)
  * The rows of the tree, and the cached rows that a token at row n - m sees, must be finite; the others
  * may hold anything.  (No accumulated weights: rows of nodes that are not accepted leave the cache.) */
 int kvsel_attend_tree(const kvsel_attn_params* p, const void* q, const kvsel_kv* kv, const int32_t* lens,

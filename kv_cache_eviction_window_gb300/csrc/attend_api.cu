@@ -73,8 +73,9 @@ int check_tree(const kvsel_attn_params* p) {
 
 // How the nodes of a tree go: in items of 16 rows by clusters of c CTAs (pl.cluster), each item of which reads the cache
 // again, from L2; up to 16 rows cut over the grid and joined (pl.few); in items of 128 rows or two such blocks, whole ones
-// to CTAs (pl.whole); or these cut over the grid and joined.  The estimate, in tenths of a microsecond, follows what was measured (8 to 512 rows per segment, 1 to 128
-// segments of 128 to 4096 rows, pages of 16, masks included, us):
+// to CTAs (pl.whole); or these cut over the grid and joined.  Up to 16 rows keep the softmax weights to 2^-16, as
+// kvsel_attend's do, and so never go to the tile kernel, which rounds them to bf16.  Otherwise the estimate, in tenths of a microsecond,
+// follows what was measured (8 to 512 rows per segment, 1 to 128 segments of 128 to 4096 rows, pages of 16, masks included, us):
 //   clusters  6.3 and 0.97 per tile of 64 rows, 7.8 and 1.06 where CTAs share an SM: 32 items of 1024 rows by clusters of
 //             eight 10.0, of four 10.2, of two 14.6; 96 items by clusters of two 16.6; more clusters than fit at once lose
 //   whole     8.4 and 2.45 per two tiles of 128 rows (one block), 8.6 and 1.7 per tile: 32 segments of 1024 rows 18.2
@@ -91,16 +92,22 @@ void plan_tree(const kvsel_attn_params* p, int sms, AttnPlan& pl) {
   // rows that a node may see, first ones and a window's apart
   long long rows = p->max_len;
   if (p->window > 0) rows = std::min(rows, p->n_sink + static_cast<long long>(p->window) + p->n_new + 128);
-  const int block = 128 / p->group * p->group;
-  const bool split = R <= block;
-  const long long tiles = (rows + 127) / 128, items = segs * ((R + 2 * block - 1) / (2 * block));
-  double best = 170.0 + std::max(segs * rows * 512.0 / 6.3e5, segs * rows * R * 512.0 / 1.3e8);
-  if (items > sms) best += (split && tiles > 2 ? 80.0 : 50.0) * items / sms;
-  const double one = split ? 84.0 + 24.5 * ((tiles + 1) / 2) : 86.0 + 17.0 * tiles;
-  const double each = items > sms ? 30.0 + one * ((items + sms - 1) / sms) : one;
-  if (each < best) {
-    best = each;
-    pl.whole = true;
+  double best;
+  if (R <= attend_rows_tile()) {
+    pl.few = true;
+    best = 80.0 + segs * rows * 512.0 / 6.2e5;
+  } else {
+    const int block = 128 / p->group * p->group;
+    const bool split = R <= block;
+    const long long tiles = (rows + 127) / 128, items = segs * ((R + 2 * block - 1) / (2 * block));
+    best = 170.0 + std::max(segs * rows * 512.0 / 6.3e5, segs * rows * R * 512.0 / 1.3e8);
+    if (items > sms) best += (split && tiles > 2 ? 80.0 : 50.0) * items / sms;
+    const double one = split ? 84.0 + 24.5 * ((tiles + 1) / 2) : 86.0 + 17.0 * tiles;
+    const double each = items > sms ? 30.0 + one * ((items + sms - 1) / sms) : one;
+    if (each < best) {
+      best = each;
+      pl.whole = true;
+    }
   }
   const long long small = segs * ((R + attend_rows_tile() - 1) / attend_rows_tile()), steps = (rows + 63) / 64;
   for (int c = 8; c >= 1; c /= 2) {
@@ -110,13 +117,9 @@ void plan_tree(const kvsel_attn_params* p, int sms, AttnPlan& pl) {
     if (t < best) {
       best = t;
       pl.cluster = c;
+      pl.few = pl.whole = false;
     }
   }
-  if (small == segs && 80.0 + segs * rows * 512.0 / 6.2e5 < best) {
-    pl.few = true;
-    pl.cluster = 0;
-  }
-  if (pl.cluster || pl.few) pl.whole = false;
 }
 
 int plan_attn(const kvsel_attn_params* p, bool with_acc, bool tree, AttnPlan& pl) {
