@@ -452,6 +452,8 @@ typedef struct kvsel_attn_params {
   int64_t n_rows;        /* PACKED: rows of k and v                                          */
   int64_t acc_stride;    /* acc: entries between segments, >= max_len                        */
   uint64_t wait_cycles;  /* as kvsel_params.wait_cycles                                      */
+  int32_t tree_window;   /* kvsel_attend_tree, with a window: 1 = it counts the tree's own rows
+                            too, as kvsel_attend's does; 0 = their masks alone decide        */
 } kvsel_attn_params;
 
 /* Bytes of device workspace that kvsel_attend needs on the current device (with_acc: the call
@@ -591,6 +593,9 @@ int kvsel_attend_tree_workspace_size(const kvsel_attn_params* p, size_t* bytes);
  *     j = n - m + u  and  bit u of its mask is set
  * (r is the row that the node would have in a chain of what it sees; a node with an empty mask counts as
  * n - m.)  Any mask will do: a node that sees nothing (an empty mask over an empty cache) gets zeros and -inf.
+ * So a node sees all its ancestors, however small the window.  For a model with a window set tree_window = 1: of the
+ * set bits of a node's mask, which lie at positions n - m, n - m + 1, ... in ascending order, it then sees those whose
+ * position i is i > r - window or i < n_sink.  (What an ancestor's row is in a chain: a chain's results are kvsel_attend's.)
  *   p        causal = 1, n_new <= KVSEL_MAX_TREE; acc_stride is not read
  *   tree     device uint32 [batch][n_new][ceil(n_new / 32)] as kvsel_tree_masks writes it; bits of rows at or
  *            behind m and the masks of nodes at or behind m are not used

@@ -106,6 +106,7 @@ class kvsel_attn_params(_RowParams):
         ("q_stride_req", ctypes.c_int64), ("q_stride_head", ctypes.c_int64), ("q_stride_tok", ctypes.c_int64),
         ("o_stride_req", ctypes.c_int64), ("o_stride_head", ctypes.c_int64), ("o_stride_tok", ctypes.c_int64),
         ("n_rows", ctypes.c_int64), ("acc_stride", ctypes.c_int64), ("wait_cycles", ctypes.c_uint64),
+        ("tree_window", ctypes.c_int32),
     ]
 
 
@@ -282,12 +283,12 @@ def make_attn_params(*, h_kv: int, group: int, batch: int, max_len: int, n_new: 
                      causal: bool = True, window: int = 0, n_sink: int = 0, scale: float = 0.0,
                      lens_per_head: bool = False, q_strides: Sequence[int] = (0, 0, 0),
                      o_strides: Sequence[int] = (0, 0, 0), n_rows: int = 0, acc_stride: int = 0,
-                     wait_cycles: int = 0) -> kvsel_attn_params:
+                     wait_cycles: int = 0, tree_window: bool = False) -> kvsel_attn_params:
     """q_strides / o_strides: (request, query head, token) in elements; zeros = dense
-    [batch][h_kv*group][n_new][head_dim]."""
+    [batch][h_kv*group][n_new][head_dim].  tree_window: the window counts a tree's own rows too."""
     return kvsel_attn_params(h_kv, group, head_dim, batch, n_new, max_len, int(bool(causal)), window, n_sink, scale,
                              int(bool(lens_per_head)), *[int(x) for x in q_strides], *[int(x) for x in o_strides],
-                             n_rows, acc_stride, int(wait_cycles))
+                             n_rows, acc_stride, int(wait_cycles), int(bool(tree_window)))
 
 
 def make_evict_params(*, h_kv: int, batch: int, capacity: int, budget: int, n_new: int = 1, head_dim: int = 128,

@@ -69,6 +69,7 @@ struct AttnArgs {
   int by_item;
   const uint32_t* tree;           // [B][m][tree_words]: which of the new tokens' rows a new token sees (TREE)
   int tree_words;
+  int tree_window;                // 1: the window and the first rows count there too (TREE)
   int whole;                      // attend_tile_kernel: a CTA per item, no plan, no join
   int grid;                       // CTAs of the kernel that works on the items
   WaitCtl wc;
@@ -316,23 +317,52 @@ __device__ __forceinline__ bool sees(const AttnArgs& a, int p, int j) {
   if (!a.causal) return true;
   return j <= p && (a.window <= 0 || j > p - a.window || j < a.n_sink);
 }
-// Node t of request b's tree: the words of its mask, and its position in a segment whose first row of the tree
-// is `base`: it follows the nodes that it sees, itself among them.
+// Node t of request b's tree: the words of its mask, and what follows from them in a segment whose first row of the tree
+// is `base`.
 __device__ __forceinline__ const uint32_t* tree_mask(const AttnArgs& a, int b, int t) {
   return a.tree + (static_cast<long long>(b) * a.m + t) * a.tree_words;
 }
-__device__ __forceinline__ int tree_position(const AttnArgs& a, const uint32_t* mask, int m, int base) {
-  int set = 0;
-  for (int w = 0; w * 32 < m; ++w) {
-    const int left = m - w * 32;
-    set += __popc(__ldg(mask + w) & (left < 32 ? (1u << left) - 1u : ~0u));
-  }
-  return base + max(set, 1) - 1;
+__device__ __forceinline__ uint32_t tree_word(const uint32_t* mask, int m, int w) {
+  const int left = m - w * 32;
+  return __ldg(mask + w) & (left < 32 ? (1u << left) - 1u : ~0u);
 }
-// whether the node with this mask and position p sees cached row j (j < hi of its tile)
-__device__ __forceinline__ bool tree_sees(const AttnArgs& a, const uint32_t* mask, int p, int base, int j) {
-  if (j >= base) return __ldg(mask + ((j - base) >> 5)) >> ((j - base) & 31) & 1u;
-  return a.window <= 0 || j > p - a.window || j < a.n_sink;
+// the node whose bit is number `rank` of the mask's (there are more of them than that)
+__device__ __forceinline__ int tree_bit(const uint32_t* mask, int m, int rank) {
+  int w = 0;
+  for (; (w + 1) * 32 < m; ++w) {
+    const int set = __popc(tree_word(mask, m, w));
+    if (rank < set) break;
+    rank -= set;
+  }
+  uint32_t x = tree_word(mask, m, w);
+  for (; rank > 0; --rank) x &= x - 1;
+  return w * 32 + __ffs(x) - 1;
+}
+// The node's position, behind the nodes that it sees (itself among them), which are at positions base, base + 1, ...
+// With tree_window the window hides the lowest of them: those before node `from`, but for first rows, those before
+// node `first` (both 0: none is hidden).
+struct TreeRow {
+  int p, from, first;
+};
+__device__ __forceinline__ TreeRow tree_row(const AttnArgs& a, const uint32_t* mask, int m, int base) {
+  int set = 0;
+  for (int w = 0; w * 32 < m; ++w) set += __popc(tree_word(mask, m, w));
+  TreeRow t{base + max(set, 1) - 1, 0, 0};
+  if (a.tree_window && a.window > 0 && set > a.window) {
+    const int gone = set - a.window, stay = a.n_sink - base;
+    t.from = tree_bit(mask, m, gone);
+    if (stay >= gone)
+      t.from = 0;
+    else if (stay > 0)
+      t.first = tree_bit(mask, m, stay);
+  }
+  return t;
+}
+// whether the node sees cached row j (j < hi of its tile)
+__device__ __forceinline__ bool tree_sees(const AttnArgs& a, const uint32_t* mask, const TreeRow& t, int base, int j) {
+  const int u = j - base;
+  if (u >= 0) return (u >= t.from || u < t.first) && (__ldg(mask + (u >> 5)) >> (u & 31) & 1u);
+  return a.window <= 0 || j > t.p - a.window || j < a.n_sink;
 }
 // 64 bits of a mask of m nodes from bit `at` on (at > -64); bit i of the result: node at + i
 __device__ __forceinline__ uint64_t tree_bits(const uint32_t* mask, int m, int at) {
@@ -341,8 +371,7 @@ __device__ __forceinline__ uint64_t tree_bits(const uint32_t* mask, int m, int a
   for (int i = 0; i < 3; ++i) {
     const int w = (at >> 5) + i, s = w * 32 - at;    // the word's place in the result: -31 to 95
     if (w < 0 || w * 32 >= m || s >= 64) continue;
-    const int left = m - w * 32;
-    const uint64_t x = __ldg(mask + w) & (left < 32 ? (1u << left) - 1u : ~0u);
+    const uint64_t x = tree_word(mask, m, w);
     y |= s < 0 ? x >> -s : x << s;
   }
   return y;

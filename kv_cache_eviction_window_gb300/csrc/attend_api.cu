@@ -68,6 +68,7 @@ int check_attn(const kvsel_attn_params* p) {
 int check_tree(const kvsel_attn_params* p) {
   const int rc = check_attn(p);
   if (rc) return rc;
+  if (p->tree_window < 0 || p->tree_window > 1) return KVSEL_EINVAL;
   return !p->causal || p->n_new > KVSEL_MAX_TREE ? KVSEL_EUNSUPPORTED : KVSEL_OK;
 }
 
@@ -355,6 +356,7 @@ static int attend(const kvsel_attn_params* p, const void* q, const kvsel_kv* kv,
   }
   a.tree = tree;
   a.tree_words = (p->n_new + 31) / 32;
+  a.tree_window = p->tree_window;
   a.by_rt = Div::by(pl.rt);
   a.by_H = Div::by(p->h_kv);
   a.by_G = Div::by(p->group);

@@ -152,6 +152,7 @@ __global__ void __launch_bounds__(kThreads, 2) attend_rows_kernel(const AttnArgs
     const int r0 = x.rt * kTR;
     int pos[2];
     const uint32_t* mask[2] = {a.tree, a.tree};
+    TreeRow node[2] = {};
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const int r = r0 + quad + 8 * u;
@@ -160,7 +161,7 @@ __global__ void __launch_bounds__(kThreads, 2) attend_rows_kernel(const AttnArgs
       pos[u] = live ? (a.causal ? x.n - x.m + t : x.n - 1) : -1;
       if (TREE && live) {
         mask[u] = tree_mask(a, x.b, t);
-        pos[u] = tree_position(a, mask[u], x.m, x.n - x.m);
+        node[u] = tree_row(a, mask[u], x.m, x.n - x.m);
       }
       const uint16_t* src = a.q + x.b * a.q_req + static_cast<long long>(x.h * a.G + g) * a.q_head +
                             static_cast<long long>(t) * a.q_tok;
@@ -215,7 +216,7 @@ __global__ void __launch_bounds__(kThreads, 2) attend_rows_kernel(const AttnArgs
           if (!whole) {
             const int j = j0 + nt * 8 + ql * 2 + (i & 1);
             if (j >= j1 ||
-                !(TREE ? tree_sees(a, mask[i >> 1], pos[i >> 1], x.n - x.m, j) : sees(a, pos[i >> 1], j)))
+                !(TREE ? tree_sees(a, mask[i >> 1], node[i >> 1], x.n - x.m, j) : sees(a, pos[i >> 1], j)))
               y = -INFINITY;
           }
           p[nt][i] = y;

@@ -47,6 +47,20 @@ def tree_visible(n: int, see: np.ndarray, window: int, n_sink: int) -> np.ndarra
     return out
 
 
+def tree_windowed(n: int, see: np.ndarray, window: int, n_sink: int) -> np.ndarray:
+    """The same where the window counts the tree's rows too: what a node sees of them lies, in order, at positions
+    n - m, n - m + 1, ..."""
+    m = see.shape[0]
+    out = tree_visible(n, see, window, n_sink)
+    for t in range(m):
+        line = [int(u) for u in np.flatnonzero(see[t])]
+        r = n - m + max(len(line), 1) - 1
+        for at, u in enumerate(line, start=n - m):
+            if n - m + u >= 0 and window and not (at > r - window or at < n_sink):
+                out[t, n - m + u] = False
+    return out
+
+
 def attend_seen(q, k, v, see, scale=None) -> dict:
     """q [G][m][d], k and v [n][d], see [m][n] -> out, lse, and what rounding errors scale with."""
     G, m, d = q.shape

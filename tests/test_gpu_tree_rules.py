@@ -2,6 +2,7 @@
 import numpy as np
 import pytest
 
+from oracle import step_oracle as SO
 from tests import cache_harness as CH
 from tests import step_harness as SH
 
@@ -45,3 +46,57 @@ def test_weights_of_few_rows_over_longer_texts(m, G, layout, block, n, pad):
     assert CH.status(c.call()) == 0
     c.check()
     CH.check_tokens(c)
+
+
+class Windowed(SH.TreeCase):
+    """The window counts the tree's rows too."""
+
+    def seen(self, b, h):
+        return SO.tree_windowed(int(self.lens[b][h]), self.masks[b], self.window, self.n_sink)
+
+    def run(self):
+        self.upload()
+        self.params["tree_window"] = True
+        assert CH.status(self.call()) == 0
+        self.check()
+
+
+@pytest.mark.parametrize("kind", ["chain", "tree"])
+@pytest.mark.parametrize("window,n_sink", [(1, 0), (2, 3), (5, 0), (16, 4), (31, 0), (33, 70), (64, 4), (100, 0)])
+@pytest.mark.parametrize("m,G", [(4, 4), (16, 1), (8, 4), (40, 4), (70, 3), (130, 4)])
+def test_a_window_that_ends_inside_the_tree(kind, window, n_sink, m, G):
+    Windowed(B=2, layout="paged", block=8, lens=[700, m + 2], H=2, G=G, m=m, window=window, n_sink=n_sink, kind=kind, seed=m).run()
+    Windowed(lens=m, H=1, G=G, m=m, window=window, n_sink=n_sink, kind=kind, seed=m + 1).run()
+
+
+@pytest.mark.parametrize("layout,block", [("contiguous", 0), ("packed", 0), ("paged", 16), ("paged", 64)])
+@pytest.mark.parametrize("m,window,n_sink", [(300, 40, 0), (1024, 512, 4), (257, 1, 1), (1024, 3, 1100)])
+def test_long_chains_under_a_window(layout, block, m, window, n_sink):
+    Windowed(B=2, lens=[[m + 70], [m]] if layout == "packed" else [m + 70, m], new=[m, m - 5], H=1, G=2, m=m, layout=layout, block=block, window=window, n_sink=n_sink, kind="chain", seed=m).run()
+
+
+@pytest.mark.parametrize("m", [3, 20, 64, 150])
+def test_any_mask_under_a_window(m):
+    g = CH.rng(m)
+    for density in (0.1, 0.5, 1.0):
+        masks = [g.random((m, m)) < density, np.zeros((m, m), bool), np.ones((m, m), bool)]
+        Windowed(B=3, lens=[m + 40, 90 + m, m + 1], m=m, G=4, window=7, n_sink=3, masks=masks, layout="paged", seed=m).run()
+    # fewer rows than nodes
+    masks = [np.tril(np.ones((m, m), bool))]
+    c = Windowed(lens=m - 1, m=m, G=4, masks=masks, window=2, n_sink=1)
+    c.seen = lambda b, h: np.array([[masks[0][t, u] and (u > t - 2 or u - 1 < 1) for u in range(1, m)] for t in range(m)])
+    c.seen_rows = lambda b, h: np.ones(m - 1, bool)
+    c.run()
+
+
+@pytest.mark.parametrize("m,G,window,n_sink", [(8, 2, 4, 0), (24, 4, 7, 2), (100, 4, 30, 4), (600, 2, 512, 4)])
+def test_a_chain_under_a_window_is_causal(m, G, window, n_sink):
+    kw = dict(B=2, H=2, G=G, m=m, lens=[1000, m + 3], new=[m, m // 2], layout="paged", window=window, n_sink=n_sink, seed=3)
+    c, t = CH.Case(**kw), Windowed(kind="chain", **kw)
+    c.upload().call()
+    t.upload()
+    t.params["tree_window"] = True
+    t.call()
+    want = c.oracle()
+    c.check(ora=want)
+    t.check(ora=want)
