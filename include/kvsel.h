@@ -700,7 +700,9 @@ int kvsel_pages_fork(const kvsel_pages_params* p, const int32_t* table_in, const
  *   lens     device int32 [batch] or [batch*h_kv], not changed (with lens_per_head the pages from the shortest
  *            head's rows to the longest's are made the request's own, with the rows of its longest)
  *   new_lens device int32 [batch], m of every request (0..n_new), or NULL = n_new for all
- *   granted  device int32 [batch], written: m, or 0 where the request was not served
+ *   granted  device int32 [batch], written: m, or 0 where the request was not served.  Made to be new_lens of every
+ *            call that follows, with lens + granted rows: a request that was not served has no page for new rows, or
+ *            one that others read, and may not write any
  * A length, table entry or row count out of range is recorded in the status word; such a request is not
  * served. */
 int kvsel_pages_reserve(const kvsel_pages_params* p, void* k, void* v, int32_t* table, int32_t* ref, const int32_t* lens,
@@ -714,7 +716,8 @@ int kvsel_pages_trim(const kvsel_pages_params* p, int32_t* table, int32_t* ref, 
 /* Moves the rows of the accepted nodes of a tree to its front, in every layer: with n = lens[b] rows, the
  * last m of them the tree's, row n - m + path[b][i] goes to row n - m + i for i < counts[b], and
  * lens_out[b] = n - m + counts[b].  (Then kvsel_pages_trim frees what lies behind.)
- *   k, v, table  as above, the rows n - m .. n - 1 reserved by kvsel_pages_reserve
+ *   k, v, table  as above, the rows n - m .. n - 1 reserved by kvsel_pages_reserve (which m are: its granted; whether a
+ *            page is the request's own is not looked at again here)
  *   lens     device int32 [batch] or [batch*h_kv]: rows with the tree's; lens_out likewise, written (may be lens)
  *   new_lens device int32 [batch], m of every request (0..n_new), or NULL = n_new for all
  *   path     device int32 [batch][n_new], counts device int32 [batch], as kvsel_verify writes them
