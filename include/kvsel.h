@@ -601,7 +601,8 @@ int kvsel_attend_tree_workspace_size(const kvsel_attn_params* p, size_t* bytes);
  *            behind m and the masks of nodes at or behind m are not used
  *   the other arguments, results, workspace and errors as kvsel_attend's (the weights' 2^-16 up to 16 query rows included)
  * The rows of the tree, and the cached rows that a token at row n - m sees, must be finite; the others
- * may hold anything.  (No accumulated weights: rows of nodes that are not accepted leave the cache.) */
+ * may hold anything.  (No accumulated weights: rows of nodes that are not accepted leave the cache.  What a
+ * cache that is evicted from needs then: kvsel_pages_accept.) */
 int kvsel_attend_tree(const kvsel_attn_params* p, const void* q, const kvsel_kv* kv, const int32_t* lens,
                       const int32_t* new_lens, const int64_t* offsets, const uint32_t* tree, void* out, float* lse,
                       void* ws, size_t ws_bytes, void* stream);
@@ -722,7 +723,13 @@ int kvsel_pages_trim(const kvsel_pages_params* p, int32_t* table, int32_t* ref, 
  *   new_lens device int32 [batch], m of every request (0..n_new), or NULL = n_new for all
  *   path     device int32 [batch][n_new], counts device int32 [batch], as kvsel_verify writes them
  * A count or length out of range is clamped, a path entry that is below its place, not above the
- * one before, or not below m moves nothing; each is recorded in the status word. */
+ * one before, or not below m moves nothing; each is recorded in the status word.
+ *
+ * In a cache that kvsel_evict_append keeps, that call appends the tree's rows (n_new = m; room is made for all of them), and
+ * this one takes its lens (lens_per_head = 1).  Their pos and acc need no move: row n - m + i has position seen + i and weight
+ * 0 whichever node it is.  But seen counts the rejected nodes: take m - counts[b] off every segment's.  kvsel_attend_tree
+ * adds no weights; kvsel_attend with acc and the accepted nodes' queries (new_lens = counts, lens = lens_out) does, and
+ * gives the same results for them.  Without it accepted rows weigh nothing and are the first to leave behind n_recent. */
 int kvsel_pages_accept(const kvsel_pages_params* p, void* k, void* v, const int32_t* table, const int32_t* lens,
                        const int32_t* new_lens, const int32_t* path, const int32_t* counts, int32_t* lens_out, void* ws,
                        size_t ws_bytes, void* stream);
