@@ -623,6 +623,7 @@ typedef struct kvsel_verify_params {
   int32_t dtype;         /* KVSEL_DTYPE_* of target and draft                                */
   int64_t stride_req, stride_node;   /* target and draft element (b, t, x) at b*stride_req +
                             t*stride_node + x; both 0 = [batch][n_new][vocab]                */
+  uint64_t wait_cycles;  /* as kvsel_params.wait_cycles                                      */
 } kvsel_verify_params;
 
 /* Bytes of device workspace that kvsel_verify needs (its status word).  Host-only. */
@@ -650,7 +651,8 @@ int kvsel_verify_workspace_size(const kvsel_verify_params* p, size_t* bytes);
  *   ws       workspace of kvsel_verify_workspace_size bytes, 256-byte aligned
  * Sums are exact (64-bit integers in units of 2^-45), so results do not depend on their order.  A token
  * outside [0, vocab) is never accepted, takes nothing from the rest, and is recorded in the status
- * word with a node count out of range (clamped) and a parent outside [0, t) (the node is ignored). */
+ * word with a node count out of range (clamped) and a parent outside [0, t) (the node is ignored).  A bounded wait
+ * that ran out (KVSEL_ETIMEOUT) leaves path, counts and next of its request undefined. */
 int kvsel_verify(const kvsel_verify_params* p, const int32_t* tokens, const int32_t* parents, const void* target,
                  const void* draft, const float* u, const int32_t* new_lens, int32_t* path, int32_t* counts,
                  int32_t* next, void* ws, size_t ws_bytes, void* stream);

@@ -123,6 +123,7 @@ class kvsel_verify_params(_RowParams):
     _fields_ = [
         ("batch", ctypes.c_int32), ("n_new", ctypes.c_int32), ("vocab", ctypes.c_int32), ("mode", ctypes.c_int32),
         ("dtype", ctypes.c_int32), ("stride_req", ctypes.c_int64), ("stride_node", ctypes.c_int64),
+        ("wait_cycles", ctypes.c_uint64),
     ]
 
 
@@ -301,9 +302,9 @@ def make_evict_params(*, h_kv: int, batch: int, capacity: int, budget: int, n_ne
 
 
 def make_verify_params(*, batch: int, n_new: int, vocab: int, mode: str = "sampled", dtype: str = "fp32",
-                       stride_req: int = 0, stride_node: int = 0) -> kvsel_verify_params:
+                       stride_req: int = 0, stride_node: int = 0, wait_cycles: int = 0) -> kvsel_verify_params:
     """Strides of target and draft in elements; zeros = dense [batch][n_new][vocab]."""
-    return kvsel_verify_params(batch, n_new, vocab, VERIFY[mode], DTYPE[dtype], stride_req, stride_node)
+    return kvsel_verify_params(batch, n_new, vocab, VERIFY[mode], DTYPE[dtype], stride_req, stride_node, int(wait_cycles))
 
 
 def make_pages_params(*, batch: int, max_blocks: int, num_blocks: int, block_size: int, h_kv: int, layers: int = 1,

@@ -20,6 +20,7 @@ struct VerifyArgs {
   int32_t* path;
   int32_t* counts;
   int32_t* next;
+  unsigned long long wait_cycles;
   int* status;
 };
 cudaError_t launch_verify(const VerifyArgs& a, int batch, bool bf16, int sms, cudaStream_t st);

@@ -11,6 +11,8 @@ using namespace kvsel;
 
 namespace {
 
+constexpr unsigned long long kDefaultWaitCycles = 2000000000ull;   // ~1 s at the boost clock
+
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 bool aligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 int launch_rc(cudaError_t e) { return e == cudaSuccess ? KVSEL_OK : KVSEL_ECUDA; }
@@ -151,6 +153,7 @@ int kvsel_verify(const kvsel_verify_params* p, const int32_t* tokens, const int3
   a.path = path;
   a.counts = counts;
   a.next = next;
+  a.wait_cycles = p->wait_cycles ? p->wait_cycles : kDefaultWaitCycles;
   a.status = static_cast<int*>(ws);
   int sms = 0;
   if ((rc = device_sms(&sms))) return rc;

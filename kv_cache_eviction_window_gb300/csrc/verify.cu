@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(1024) tree_masks_kernel(const int32_t* __restr
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kMaxCluster = 16;
-constexpr unsigned long long kWaitCycles = 2000000000ull;   // ~1 s at the boost clock
+constexpr long long kLandCycles = 1 << 17;           // after a wait that ran out: far longer than a remote store takes
 constexpr int kUnitBits = 45;                        // probabilities in units of 2^-45
 constexpr unsigned long long kOne = 1ull << kUnitBits;
 
@@ -265,15 +265,27 @@ __device__ __forceinline__ void send(unsigned long long* to, unsigned long long 
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(smem_u32(bar)), "r"(rank));
   asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.u64 [%0], %1, [%2];" ::"r"(at), "l"(v), "r"(there) : "memory");
 }
+// Whether a phase of the barrier, and with it what others have sent, has come: at once (NOW), or after some time that the
+// hardware waits itself.
+template <bool NOW>
 __device__ __forceinline__ bool came(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
+  if (NOW)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
   return ok;
 }
 
@@ -477,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a)
     const T* p = target + node * a.stride_node;
     const T* q = draft + node * a.stride_node;
     const unsigned long long off = s.A;
-    bool first = true;                               // the draw is from the rest, not from p itself
+    bool first = true, lost = false;                 // the draw is from the rest, not from p itself; a wait ran out
     unsigned long long v, all, before;
     while (true) {
       v = 0;
@@ -550,13 +562,18 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a)
         if (tid == 0) mbar_arrive_expect_tx(&s.came[side], cs * kWarps * 8);
         if (lane < cs) send(&s.part[side][mine], v, &s.came[side], lane);
         if (want == kDraw || warp == 0) {
+          const uint32_t parity = pass >> 1 & 1;
+          bool have = came<true>(&s.came[side], parity);
           const long long t0 = clock64();
-          while (!came(&s.came[side], pass >> 1 & 1) && !*static_cast<volatile int*>(&s.lost))
-            if (static_cast<unsigned long long>(clock64() - t0) > kWaitCycles) {
+          while (!have && !*static_cast<volatile int*>(&s.lost)) {
+            if (static_cast<unsigned long long>(clock64() - t0) > a.wait_cycles) {
               s.lost = 1;
               atomicOr(a.status, DEV_TIMEOUT_PIPE);
+            } else {
+              have = came<false>(&s.came[side], parity);
             }
-          __syncwarp();
+          }
+          lost = __any_sync(0xffffffffu, !have);
         }
       }
       const unsigned long long* part = s.part[side];
@@ -574,7 +591,8 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a)
         all = greedy ? warp_max(all) : warp_sum(all);
         if (!greedy && want == kDraw) before = warp_sum(before);
       }
-      if (want != kDraw || all || !first) break;
+      // (a warp that has not got all numbers makes no further pass: CTAs that have may be gone)
+      if (want != kDraw || all || !first || lost) break;
       first = false;                                 // nothing is left of the rest
     }
     if (greedy) {
@@ -590,7 +608,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a)
     best = all ? -2 : -1;                            // -2: written here
     const float u = fminf(fmaxf(s.u[0], 0.f), 0.99999994f);
     const unsigned long long goal = __umul64hi(all, __float2ull_rz(u * 18446744073709551616.f));
-    if (all && before <= goal && goal < before + v) {
+    if (!lost && all && before <= goal && goal < before + v) {
       // In this warp's share: the chunk that passes the goal, in which each lane sums a run of tokens, and the run that
       // passes it is looked at again by all lanes.  (One warp that went over its whole share took 120 us of 150 for 512
       // requests of 131072 tokens.)
@@ -651,7 +669,13 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a)
     }
     break;
   }
-  if (__any_sync(0xffffffffu, s.lost)) cl.sync();    // (nothing may still be on its way here)
+  // A wait ran out: what was sent from here lands, and no CTA ends before all that go on sending have given up, too.
+  if (cs > 1 && __any_sync(0xffffffffu, *static_cast<volatile int*>(&s.lost))) {
+    const long long t0 = clock64();
+    while (clock64() - t0 < kLandCycles) {
+    }
+    cl.sync();
+  }
   if (rank == 0 && tid == 0) {
     a.counts[b] = count;
     if (best != -2) a.next[b] = best;
