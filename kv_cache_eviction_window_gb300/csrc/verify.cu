@@ -91,10 +91,12 @@ __device__ __forceinline__ unsigned long long units(float x) {
   const Parts a = parts(prob(x));
   return whole(a.hi, a.lo);
 }
-// max(p - A q, 0) in units; A in units, below 2^55
+// max(p - A q, 0) in units.  A is the sum of up to 1023 masses of at most 17/16 (rows may sum to a sixteenth more than 1),
+// 1087 in all: below 2^56 units, and Q is 2^45 at most.
 __device__ __forceinline__ unsigned long long rest_units(float p, float q, unsigned long long A) {
+  static_assert((KVSEL_MAX_TREE - 1) * 17ull / 16 + 1 < 1ull << (56 - kUnitBits), "A << 8 fits 64 bits");
   const unsigned long long P = units(p), Q = units(q);
-  const unsigned long long AQ = A == kOne ? Q : __umul64hi(A << 9, Q << 10);
+  const unsigned long long AQ = A == kOne ? Q : __umul64hi(A << 8, Q << 11);
   return P > AQ ? P - AQ : 0;
 }
 

@@ -47,3 +47,27 @@ def test_a_request_of_one_cta_waits_for_nobody(monkeypatch):
     ws = with_wait(c, 1, monkeypatch)
     assert CH.status(ws) == 0
     c.check()
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("V", [8, 6000])
+@pytest.mark.parametrize("u0,token", [(0.25, 0), (0.99, 0)])
+def test_a_thousand_rejections_of_a_row_that_sums_to_more_than_one(dtype, V, u0, token):
+    # 1023 siblings, each with a token that the target never takes, and a target row that sums to 17/16: the masses
+    # before them sum to more than 1024.  Token 2 has 1/16 - 1024 * 2^-14 = 0 left by then, token 0 more than 1 - 1087 * 2^-16.
+    from oracle import step_oracle as SO
+
+    m = 1024
+    c = SH.VerifyCase(B=1, m=2, V=8, kind="star", dtype=dtype, seed=1)
+    c.m, c.V, c.new = m, V, np.array([m])
+    c.p, c.q = np.zeros((1, m, V)), np.zeros((1, m, V))
+    c.p[0, 0, [0, 2]] = 1.0, 2.0 ** -4
+    c.q[0, 0, [0, 1, 2]] = 2.0 ** -16, 1.0, 2.0 ** -14
+    c.parents, c.tokens = np.array([[-1] + [0] * (m - 1)]), np.ones((1, m), int)
+    c.u = np.full((1, m), 0.5, np.float32)
+    c.u[0, 0] = u0
+    want = SO.verify(c.tokens[0].tolist(), c.parents[0].tolist(), c.p[0, :, :8], c.q[0, :, :8], c.u[0], "sampled")
+    assert want == ([0], token)
+    c.upload()
+    assert CH.status(c.call()) == 0
+    c.check([want])
