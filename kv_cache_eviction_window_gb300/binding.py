@@ -769,13 +769,13 @@ def _values(t, params: kvsel_verify_params, where: str) -> Optional[int]:
         params.rows = _values_of(params)
     types, dense, req, node, need, shape = params.rows
     holds = t.dtype in types
-    if holds and not (dense and t.is_contiguous() and t.nbytes >= need):
+    if holds and not (t.shape == shape and dense and t.is_contiguous()):
         holds = t.stride()[-1] == 1 and t.untyped_storage().nbytes() - t.element_size() * t.storage_offset() >= need
         if holds and t.dim() == 3:
             holds = all(a >= b for a, b in zip(t.shape, shape)) and (shape[0] == 1 or t.stride(0) == req) and (
                 shape[1] == 1 or t.stride(1) == node)
-        elif holds and not t.is_contiguous():
-            holds = False
+        elif holds:                                  # rows one after another
+            holds = t.is_contiguous() and t.nbytes >= need and (t.dim() == 1 or t.shape[-1] % node == 0)
     if not holds:
         _refuse(where, f"{tuple(t.shape)} of {t.dtype} with strides {t.stride()}")
     return t.data_ptr()
