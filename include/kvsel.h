@@ -677,7 +677,8 @@ typedef struct kvsel_pages_params {
   int32_t n_new;         /* new rows of a request at most, 0..2^20;
                             batch * (n_new / block_size + 2) <= 2^20                         */
   int32_t lens_per_head; /* 0: lens [batch]; 1: lens [batch*h_kv], heads of a request may differ */
-  int64_t stride_layer;  /* elements between the pools of layers; 0 = dense                  */
+  int64_t stride_layer;  /* elements between the pools of layers, a multiple of 8 and a
+                            layer's pool at least; 0 = dense                                 */
 } kvsel_pages_params;
 
 /* Bytes of device workspace that the calls below need (one size serves all).  Host-only. */

@@ -308,10 +308,12 @@ def make_verify_params(*, batch: int, n_new: int, vocab: int, mode: str = "sampl
 
 
 def make_pages_params(*, batch: int, max_blocks: int, num_blocks: int, block_size: int, h_kv: int, layers: int = 1,
-                      n_new: int = 1, head_dim: int = 128, lens_per_head: bool = False) -> kvsel_pages_params:
-    """Pools [layers][num_blocks][block_size][h_kv][head_dim] under a table [batch][max_blocks]."""
+                      n_new: int = 1, head_dim: int = 128, lens_per_head: bool = False,
+                      stride_layer: int = 0) -> kvsel_pages_params:
+    """Pools [layers][num_blocks][block_size][h_kv][head_dim] under a table [batch][max_blocks]; stride_layer: elements
+    between layers (0: dense)."""
     return kvsel_pages_params(h_kv, head_dim, batch, block_size, max_blocks, num_blocks, layers, n_new,
-                              int(bool(lens_per_head)), 0)
+                              int(bool(lens_per_head)), stride_layer)
 
 
 def _refuse(where: str, why: str) -> None:
@@ -803,12 +805,18 @@ def kvsel_pages_workspace_size(params: kvsel_pages_params) -> int:
 def _pool(t, params: kvsel_pages_params, where: str) -> Optional[int]:
     if t.__class__ is int:
         return t
-    need = params.rows
-    if need is None:
+    if params.rows is None:
         p = params
-        need = params.rows = 2 * p.layers * p.num_blocks * p.block_size * p.h_kv * p.head_dim
-    if t.nbytes < need or not t.is_contiguous() or not _is_bf16(t):
-        _refuse(where, f"{tuple(t.shape)} of {t.dtype} with strides {t.stride()} for pools of {need} bytes")
+        layer = p.num_blocks * p.block_size * p.h_kv * p.head_dim
+        stride = p.stride_layer or layer
+        params.rows = 2 * ((p.layers - 1) * stride + layer), layer, stride if p.layers > 1 and stride != layer else 0
+    need, layer, stride = params.rows
+    holds = t.is_contiguous() and t.nbytes >= need
+    if stride and t.dim() > 1:                       # (else flat)
+        holds = t.shape[0] >= params.layers and t.stride(0) == stride and t[0].is_contiguous() and t[0].numel() >= layer and (
+            t.untyped_storage().nbytes() - 2 * t.storage_offset() >= need)
+    if not holds or not _is_bf16(t):
+        _refuse(where, f"{tuple(t.shape)} of {t.dtype} with strides {t.stride()} for pools of {need} bytes" + f", {stride} elements apart" * bool(stride))
     return t.data_ptr()
 
 

@@ -41,6 +41,11 @@ int check_verify(const kvsel_verify_params* p) {
 // table entries that the new rows of a request may touch
 long long reserve_entries(const kvsel_pages_params* p) { return p->n_new / p->block_size + 2ll; }
 
+// elements of a layer's pool
+long long layer_elems(const kvsel_pages_params* p) {
+  return static_cast<long long>(p->num_blocks) * p->block_size * p->h_kv * kHeadDim;
+}
+
 int check_pages(const kvsel_pages_params* p) {
   if (!p) return KVSEL_EINVAL;
   if (p->head_dim != kHeadDim) return KVSEL_EUNSUPPORTED;
@@ -51,7 +56,8 @@ int check_pages(const kvsel_pages_params* p) {
   if (p->batch > KVSEL_MAX_ATTN_BATCH || p->max_blocks > (1 << 20) || p->num_blocks > (1 << 28) || p->layers > 1024 ||
       p->n_new > (1 << 20) || p->batch * reserve_entries(p) > (1 << 20))
     return KVSEL_EUNSUPPORTED;
-  if (p->stride_layer && (p->layers > 1 && (p->stride_layer < 0 || p->stride_layer % 8))) return KVSEL_EINVAL;
+  // (pools of layers do not overlap)
+  if (p->stride_layer && p->layers > 1 && (p->stride_layer < layer_elems(p) || p->stride_layer % 8)) return KVSEL_EINVAL;
   return KVSEL_OK;
 }
 
@@ -82,8 +88,7 @@ PagesArgs pages_args(const kvsel_pages_params* p, void* ws) {
   a.m = p->n_new;
   a.per = static_cast<int>(reserve_entries(p));
   a.per_head = p->lens_per_head;
-  a.stride_layer = p->stride_layer ? p->stride_layer
-                                   : static_cast<long long>(p->num_blocks) * p->block_size * p->h_kv * kHeadDim;
+  a.stride_layer = p->stride_layer ? p->stride_layer : layer_elems(p);
   a.status = static_cast<int*>(ws);
   return a;
 }

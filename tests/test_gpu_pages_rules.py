@@ -63,3 +63,36 @@ def test_a_negative_length_of_one_head(n_new, length):
     assert CH.status(c.ws) == -7
     assert np.array_equal(c.o.reserve(c.lens, [0, 4]), granted.cpu().numpy())
     c.check()
+
+
+@pytest.mark.parametrize("n_new", [64, 8192])
+@pytest.mark.parametrize("gap", [0, 8])              # K and V of a layer side by side; elements between layers beside them
+def test_layers_further_apart_than_they_are_long(n_new, gap):
+    import torch
+
+    c = SH.PageCase(B=4, H=2, L=5, rows=[21, 21, 40, 16], share=[None, 0, None, None], cap=12, spare=30, seed=5).upload()
+    layer = c.k[0].numel()
+    stride = 2 * layer + gap
+    wide = torch.full((5, stride), 77, dtype=torch.int16, device="cuda")
+    k, v = (wide[:, i * layer:(i + 1) * layer].unflatten(1, c.k.shape[1:]) for i in range(2))
+    k.copy_(c.k)
+    v.copy_(c.v)
+
+    def params(n):
+        return lib().make_pages_params(batch=4, max_blocks=12, num_blocks=len(c.o.ref), block_size=16, h_kv=2, layers=5, n_new=n, stride_layer=stride)
+
+    granted, new = SH.ints([7] * 4), [9, 3, 9, 1]
+    lib().kvsel_pages_reserve(params(n_new), k, v, c.table, c.ref, c.d_lens, granted, c.ws, new_lens=SH.ints(new))
+    assert np.array_equal(c.o.reserve(c.lens, new), granted.cpu().numpy())
+    paths = [[0, 4, 8], [0], [0, 1, 2, 7], []]
+    path, out = np.full((4, 9), -1), SH.ints([0] * 4)
+    for b, x in enumerate(paths):
+        path[b, :len(x)] = x
+    rows = c.lens + new
+    lib().kvsel_pages_accept(params(9), k, v, c.table, SH.ints(rows), SH.ints(path), SH.ints([len(x) for x in paths]), out, c.ws,
+                             new_lens=SH.ints(new))
+    assert CH.status(c.ws) == 0
+    assert np.array_equal(c.o.accept(rows, new, paths), out.cpu().numpy())
+    c.k, c.v = k.contiguous(), v.contiguous()
+    c.check()
+    assert bool((wide[:, 2 * layer:] == 77).all())

@@ -34,3 +34,37 @@ def test_probabilities_of_other_numbers_of_nodes_or_tokens(B):
     for bad in (y, torch.zeros((2, 3, 12)), torch.zeros((2, 5, 12)), wide.view(16, 6)):
         with pytest.raises(B.KvselError):
             B._values(bad, s, "")
+
+
+def pools(layers=3, pages=6):
+    """K and V of a layer side by side: each a pool with twice a layer between layers."""
+    both = torch.zeros((layers, 2, pages, 8, 2, 128), dtype=torch.bfloat16)
+    return both, both[:, 0], both[:, 1]
+
+
+def test_pools_with_a_stride_of_layers(B):
+    both, k, v = pools()
+    layer = 6 * 8 * 2 * 128
+    kw = dict(batch=2, max_blocks=4, num_blocks=6, block_size=8, h_kv=2, layers=3)
+    p = B.make_pages_params(stride_layer=2 * layer, **kw)
+    assert p.stride_layer == 2 * layer
+    assert B._pool(k, p, "") == both.data_ptr() and B._pool(v, p, "") == both.data_ptr() + 2 * layer
+    B._pool(both.view(-1), p, "")
+    for bad in (both[:, 0].contiguous(), k[:2], k[:, :5], both[:2, 0], k.float(), both.view(-1)[:4 * layer], both[:, :, :3].reshape(3, -1)[:, :layer],
+                k.transpose(2, 3), torch.zeros((3, 6, 8, 2, 128), dtype=torch.bfloat16)):
+        with pytest.raises(B.KvselError):
+            B._pool(bad, p, "")
+    with pytest.raises(B.KvselError):
+        B._pool(k, B.make_pages_params(**kw), "")           # dense parameters
+    B._pool(k[:1], B.make_pages_params(**{**kw, "layers": 1}), "")
+    # layers that overlap, or begin between rows of 16 bytes
+    for stride, code in ((layer - 8, -1), (8, -1), (-layer, -1), (layer + 4, -1), (layer, 0), (layer + 8, 0)):
+        q = B.make_pages_params(stride_layer=stride, **kw)
+        if code:
+            with pytest.raises(B.KvselError) as e:
+                B.kvsel_pages_workspace_size(q)
+            assert e.value.code == code
+        else:
+            assert B.kvsel_pages_workspace_size(q) == B.kvsel_pages_workspace_size(p)
+    q.stride_layer = 2 * layer                               # (what was worked out for the other stride is not kept)
+    B._pool(k, q, "")
