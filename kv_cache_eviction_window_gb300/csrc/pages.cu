@@ -204,9 +204,9 @@ __device__ __forceinline__ int plan_pages(const PagesArgs& a, PlanShared& s, int
     if (!r.ok && u == 0) atomicOr(&s.bad[b >> 5], 1u << (b & 31));
     if (i >= 0) {
       const int page = a.table[static_cast<long long>(b) * a.max_blocks + i];
-      if (page < 0) {
+      if (page == -1) {
         n = kPage;
-      } else if (page >= a.num_blocks) {
+      } else if (page < 0 || page >= a.num_blocks) {
         atomicOr(&s.bad[b >> 5], 1u << (b & 31));
       } else if (a.ref[page] > 1) {
         n = kCopy;                                   // to be seen

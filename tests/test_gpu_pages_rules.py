@@ -66,6 +66,19 @@ def test_a_negative_length_of_one_head(n_new, length):
 
 
 @pytest.mark.parametrize("n_new", [64, 8192])
+@pytest.mark.parametrize("entry", [-2, -2 ** 31, 10 ** 6])
+def test_an_entry_that_no_table_has(n_new, entry):
+    c = SH.PageCase(B=3, bs=8, rows=[20, 20, 20], cap=8, spare=30, seed=1).upload()
+    granted, was = SH.ints([7, 7, 7]), c.table[1].clone()
+    c.table[1, 3] = entry
+    lib().kvsel_pages_reserve(c.params(n_new), c.k, c.v, c.table, c.ref, c.d_lens, granted, c.ws, new_lens=SH.ints([9, 9, 9]))
+    assert CH.status(c.ws) == -7
+    assert c.o.reserve(c.lens, [9, 0, 9]).tolist() == granted.tolist() and int(c.table[1, 3]) == entry
+    c.table[1] = was
+    c.check()
+
+
+@pytest.mark.parametrize("n_new", [64, 8192])
 @pytest.mark.parametrize("gap", [0, 8])              # K and V of a layer side by side; elements between layers beside them
 def test_layers_further_apart_than_they_are_long(n_new, gap):
     import torch
