@@ -698,8 +698,7 @@ int kvsel_pages_fork(const kvsel_pages_params* p, const int32_t* table_in, const
  * requests in order, only this one is left to use it.  Pages are the lowest free ones, in order of requests and
  * rows.  Where those run out, requests are served in order: one whose pages, together with all before
  * it, exceed the free ones gets none, nor does one that is to be left with a page by those before it (one
- * that needs neither is served).  Shared pages that new rows go to are ranked, in time with their number squared:
- * the last page of each request, as a rule.
+ * that needs neither is served).
  *   k, v     device bf16, the pools of layer 0, 16-byte aligned
  *   lens     device int32 [batch] or [batch*h_kv], not changed (with lens_per_head the pages from the shortest
  *            head's rows to the longest's are made the request's own, with the rows of its longest)

@@ -149,8 +149,8 @@ __device__ __forceinline__ Reserve reserve_of(const PagesArgs& a, int b) {
 enum Need : int { kNothing, kKeep, kPage, kCopy };
 __device__ __forceinline__ bool wants(int need) { return need >= kPage; }
 
-// What a reservation of up to ITEMS touched entries keeps in shared memory (larger ones: `need`, `pages`, `copies` and the
-// list of shared pages are in the workspace).
+// What a reservation of up to kItems touched entries keeps in shared memory (larger ones: `need`, `pages`, `copies` and the
+// list of shared entries are in the workspace).
 constexpr int kItems = 1024;
 struct PlanShared {
   int w[32];
@@ -167,7 +167,9 @@ struct PlanShared {
 
 // The plan of a reservation, by one CTA: needs, pages and copies {from, to, rows} of all entries, in their order.  It
 // writes nothing but these.  Returns the number of copies.
-// SMALL: up to kItems entries (two numbers of them in one scan).
+// SMALL: up to kItems entries: two numbers of them in one scan, and each shared page looked for among those before it.
+// Otherwise shared pages are counted in a table of at least twice as many places (open addressing, linear steps): 2^20 of
+// them, ranked against one another, would take a CTA half a minute.
 template <bool SMALL>
 __device__ __forceinline__ int plan_pages(const PagesArgs& a, PlanShared& s, int* need, int* pages, int4* copies, int* list) {
   constexpr int kMany = 1 << 15;                     // (kItems is less)
@@ -219,21 +221,49 @@ __device__ __forceinline__ int plan_pages(const PagesArgs& a, PlanShared& s, int
   int at = block_scan(shared, s.w, sharers) - shared;
   if (sharers) {
     // Of the requests that write to a shared page the last keeps it where no other uses it: as many of them before it
-    // as the page has other uses (requests that are not served for what their entries hold do not count).  The pages in
-    // order of entries:
+    // as the page has other uses (requests that are not served for what their entries hold do not count).  `list`, in
+    // order of entries: their pages, or the places that count them (-1: of a request that is not served).
+    int slots = 64;
+    if (!SMALL) {
+      while (slots < 2 * sharers) slots *= 2;
+      for (int i = tid; i < 3 * slots; i += kThreads) a.seats[i] = i < 2 * slots ? -1 : 0;
+      __syncthreads();
+    }
+    // of a place: the page, the last entry that writes to it, and the number of those
+    int32_t *key = a.seats, *last = a.seats + slots, *writers = a.seats + 2 * slots;
     int k = at;
-    for (int it = i0; it < i1; ++it)
-      if (need[it] == kCopy)
-        list[k++] = s.has(s.bad, it / a.per) ? -1 : a.table[static_cast<long long>(it / a.per) * a.max_blocks + range(it / a.per).page0 + it % a.per];
+    for (int it = i0; it < i1; ++it) {
+      if (need[it] != kCopy) continue;
+      const int b = it / a.per;
+      int y = s.has(s.bad, b) ? -1 : a.table[static_cast<long long>(b) * a.max_blocks + range(b).page0 + it % a.per];
+      if (!SMALL && y >= 0) {
+        const int page = y;
+        y = static_cast<int>(static_cast<unsigned>(page) * 2654435769u) & (slots - 1);   // 2^32 / golden ratio
+        while (true) {                               // (half of the places stay empty)
+          const int other = atomicCAS(key + y, -1, page);
+          if (other == -1 || other == page) break;
+          y = (y + 1) & (slots - 1);
+        }
+        atomicMax(last + y, it);
+        atomicAdd(writers + y, 1);
+      }
+      list[k++] = y;
+    }
     __syncthreads();
     for (int it = i0; it < i1; ++it) {
       if (need[it] != kCopy) continue;
-      const int page = list[at];
-      int before = 0;
+      const int y = list[at];
+      bool keeps = y >= 0;
+      if (SMALL && keeps) {
+        int before = 0;
 #pragma unroll 8
-      for (int c = 0; c < at; ++c) before += list[c] == page;
+        for (int c = 0; c < at; ++c) before += list[c] == y;
+        keeps = before >= a.ref[y] - 1;
+      } else if (keeps) {
+        keeps = __ldcg(last + y) == it && __ldcg(writers + y) >= a.ref[__ldcg(key + y)];
+      }
       ++at;
-      if (page < 0 || before < a.ref[page] - 1) continue;
+      if (!keeps) continue;
       need[it] = kKeep;
       atomicOr(&s.keeps[it / a.per >> 5], 1u << (it / a.per & 31));
     }

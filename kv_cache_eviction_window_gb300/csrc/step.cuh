@@ -48,6 +48,7 @@ struct PagesArgs {
   int32_t* need;                  // [B*per]
   int32_t* pages;                 // [B*per]
   int32_t* list;                  // [B*per]
+  int32_t* seats;                 // [3 * at least 2*B*per, a power of two]: shared pages and who writes to them
   int4* copies;                   // [1 + B*per]
   int* ticket;                    // zero between calls
   int* status;

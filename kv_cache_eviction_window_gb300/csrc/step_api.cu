@@ -62,7 +62,7 @@ int check_pages(const kvsel_pages_params* p) {
 }
 
 struct PagesLayout {
-  size_t need = 0, pages = 0, list = 0, copies = 0, total = 0;
+  size_t need = 0, pages = 0, list = 0, copies = 0, seats = 0, total = 0;
 };
 PagesLayout pages_layout(const kvsel_pages_params* p) {
   PagesLayout L;
@@ -72,7 +72,10 @@ PagesLayout pages_layout(const kvsel_pages_params* p) {
   L.pages = align256(L.need + items * sizeof(int32_t));
   L.list = align256(L.pages + items * sizeof(int32_t));
   L.copies = align256(L.list + items * sizeof(int32_t));
-  L.total = align256(L.copies + (items + 1) * sizeof(int4));
+  L.seats = align256(L.copies + (items + 1) * sizeof(int4));
+  size_t slots = 64;
+  while (slots < 2 * items) slots *= 2;
+  L.total = align256(L.seats + 3 * slots * sizeof(int32_t));
   return L;
 }
 
@@ -212,6 +215,7 @@ int kvsel_pages_reserve(const kvsel_pages_params* p, void* k, void* v, int32_t* 
   a.pages = reinterpret_cast<int32_t*>(wsb + L.pages);
   a.list = reinterpret_cast<int32_t*>(wsb + L.list);
   a.copies = reinterpret_cast<int4*>(wsb + L.copies);
+  a.seats = reinterpret_cast<int32_t*>(wsb + L.seats);
   a.ticket = reinterpret_cast<int*>(wsb + kStatusBytes);   // one of the counters that kvsel_workspace_init zeroes
   int sms = 0;
   if ((rc = device_sms(&sms))) return rc;

@@ -78,6 +78,26 @@ def test_an_entry_that_no_table_has(n_new, entry):
     c.check()
 
 
+@pytest.mark.parametrize("spare", [200, 9000, 13000])
+def test_thousands_of_shared_pages(spare):
+    # beams of four that set their lengths back: all their pages are shared, and new rows go to all of them
+    B, pages = 64, 256
+    share = [None if b % 4 == 0 else b - b % 4 for b in range(B)]
+    c = SH.PageCase(B=B, H=1, L=1, bs=8, rows=[8 * pages] * B, cap=pages + 4, spare=spare, share=share, seed=spare)
+    c.o.ref[np.flatnonzero(c.o.ref == 0)[spare:]] = 1   # (free pages: as many as are left so)
+    c.upload()
+    c.lens[:] = [3 + b for b in range(B)]
+    c.d_lens.copy_(SH.ints(c.lens))
+    new = [8 * pages - 3 - b if b % 7 else 5 for b in range(B)]
+    granted = SH.ints([7] * B)
+    for turn in range(2):                            # (and again: what is reserved already stays)
+        lib().kvsel_pages_reserve(c.params(8 * pages), c.k, c.v, c.table, c.ref, c.d_lens, granted, c.ws, new_lens=SH.ints(new))
+        assert CH.status(c.ws) == 0
+        assert np.array_equal(c.o.reserve(c.lens, new), granted.cpu().numpy())
+        c.check()
+    assert (spare > 12288) == all(granted.tolist())
+
+
 @pytest.mark.parametrize("n_new", [64, 8192])
 @pytest.mark.parametrize("gap", [0, 8])              # K and V of a layer side by side; elements between layers beside them
 def test_layers_further_apart_than_they_are_long(n_new, gap):
