@@ -113,15 +113,16 @@ __device__ __forceinline__ int block_scan(int v, int* s_w, int& total) {
 
 // Entry u of those that the new rows of a request touch (rows [lo, end) are written to), or -1: none.  A request that is
 // not served touches none, whatever its lengths are: a negative one would lead to words before the table.
-__host__ __device__ constexpr long long touched_entry(bool ok, int lo, int end, int u, int shift) {
-  if (!ok || lo < 0) return -1;
-  const long long i = (lo >> shift) + static_cast<long long>(u);
-  return (i << shift) < end ? i : -1;
+// (Of one that is, lo is at most 2^26, the rows of a table's row, and u at most 2^17: 32 bits will do.)
+__host__ __device__ constexpr int touched_entry(bool ok, int lo, int end, int u, int shift) {
+  const int i = (ok ? lo >> shift : 0) + u;
+  return ok && i << shift < end ? i : -1;
 }
 static_assert(touched_entry(true, 0, 1, 0, 3) == 0 && touched_entry(true, 17, 18, 0, 4) == 1 && touched_entry(true, 17, 33, 1, 4) == 2);
 static_assert(touched_entry(true, 17, 32, 1, 4) < 0 && touched_entry(true, 16, 0, 0, 4) < 0);
 static_assert(touched_entry(false, -1, 0, 0, 3) < 0 && touched_entry(false, -0x7FFFFFFF - 1, 0, 0, 3) < 0);
-static_assert(touched_entry(false, -1, 0, 1, 6) < 0 && touched_entry(true, -1, 0, 0, 3) < 0);
+static_assert(touched_entry(false, -1, 0, 1, 6) < 0 && touched_entry(false, -9, 5, 0, 3) < 0);
+static_assert(touched_entry(true, 1 << 26, 1 << 26, 1 << 17, 6) < 0 && touched_entry(true, (1 << 26) - 1, 1 << 26, 0, 6) == (1 << 20) - 1);
 
 struct Reserve {
   int lo, end, page0, m;          // first and last row that are written, the first's entry; new rows
@@ -202,7 +203,7 @@ __device__ __forceinline__ int plan_pages(const PagesArgs& a, PlanShared& s, int
     const int b = it / a.per, u = it - b * a.per;
     range(b);
     int n = kNothing;
-    const long long i = touched_entry(r.ok, r.lo, r.end, u, a.shift);
+    const int i = touched_entry(r.ok, r.lo, r.end, u, a.shift);
     if (!r.ok && u == 0) atomicOr(&s.bad[b >> 5], 1u << (b & 31));
     if (i >= 0) {
       const int page = a.table[static_cast<long long>(b) * a.max_blocks + i];
