@@ -182,7 +182,9 @@ int kvsel_pages_fork(const kvsel_pages_params* p, const int32_t* table_in, const
   if (rc) return rc;
   if (!words({table_in, lens_in, src, table_out, lens_out, ref})) return KVSEL_EINVAL;
   const long long entries = static_cast<long long>(p->batch) * p->max_blocks;
-  if ((table_in < table_out + entries && table_out < table_in + entries) || lens_in == lens_out) return KVSEL_EINVAL;
+  const int segs = p->lens_per_head ? p->batch * p->h_kv : p->batch;
+  if ((table_in < table_out + entries && table_out < table_in + entries) || (lens_in < lens_out + segs && lens_out < lens_in + segs))
+    return KVSEL_EINVAL;
   if ((rc = check_ws(ws, ws_bytes, pages_layout(p).total))) return rc;
   PagesArgs a = pages_args(p, ws);
   a.table_in = table_in;

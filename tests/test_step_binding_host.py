@@ -36,6 +36,15 @@ def test_probabilities_of_other_numbers_of_nodes_or_tokens(B):
             B._values(bad, s, "")
 
 
+def test_lengths_of_a_fork_that_overlap(B):
+    # a row may be written before another has read it
+    A = 1 << 20                                      # an address that nothing dereferences: all are refused first
+    for kw, most in ((dict(), 4), (dict(lens_per_head=True), 8)):
+        p = B.make_pages_params(batch=4, max_blocks=8, num_blocks=20, block_size=16, h_kv=2, **kw)
+        for shift in (0, 1, most - 1, -1, 1 - most):
+            assert B.load().kvsel_pages_fork(p, A, A + 4096, A, A + 65536, A + 4096 + 4 * shift, A, A, 1 << 30, None) == -1, shift
+
+
 def pools(layers=3, pages=6):
     """K and V of a layer side by side: each a pool with twice a layer between layers."""
     both = torch.zeros((layers, 2, pages, 8, 2, 128), dtype=torch.bfloat16)
