@@ -187,7 +187,8 @@ int kvsel_workspace_size(const kvsel_params* p, size_t* bytes);
  * (length of counts / offsets).  Any output pointer may be NULL. */
 int kvsel_output_size(const kvsel_params* p, int64_t* n_scores, int64_t* n_kept, int64_t* n_segments);
 
-/* Zero the workspace's device status word (do once after allocating a workspace). */
+/* Zero the workspace's device status word and the counters behind it (do once after allocating a workspace, with all
+ * its bytes). */
 int kvsel_workspace_init(void* ws, size_t ws_bytes, void* stream);
 
 /* ---- weights prepared once per model ------------------------------------------------------ */
@@ -681,7 +682,9 @@ typedef struct kvsel_pages_params {
                             layer's pool at least; 0 = dense                                 */
 } kvsel_pages_params;
 
-/* Bytes of device workspace that the calls below need (one size serves all).  Host-only. */
+/* Bytes of device workspace that the calls below need (one size serves all; about 52 to 76 per table entry that new rows may
+ * touch).  256-byte aligned, zeroed by kvsel_workspace_init once, one for every call that may run at the same time.
+ * Host-only. */
 int kvsel_pages_workspace_size(const kvsel_pages_params* p, size_t* bytes);
 
 /* New rows of the table from old ones: row b takes the pages and lens of old row src[b] (-1: none, its
