@@ -69,7 +69,7 @@ struct AttnArgs {
   int by_item;
   const uint32_t* tree;           // [B][m][tree_words]: which of the new tokens' rows a new token sees (TREE)
   int tree_words;
-  int tree_window;                // 1: the window and the first rows count there too (TREE)
+  int tree_window;                // 1: a window that is shorter than the trees counts their rows, too (TREE = kWindowed)
   int whole;                      // attend_tile_kernel: a CTA per item, no plan, no join
   int grid;                       // CTAs of the kernel that works on the items
   WaitCtl wc;
@@ -121,8 +121,10 @@ struct ItemRange {
   int skip;                       // the last of the segment's items where this and all behind it are empty, else the item
   long long row0;
 };
-// TREE: which of the new rows a token sees is in a.tree, and its position is anywhere from n - m to n - 1.
-template <int TK, bool TREE = false>
+// What says which of the new rows a token sees: the causal rule, the masks in a.tree, or these and the window.
+enum Tree : int { kCausal, kMasks, kWindowed };
+// TREE: a token's position is anywhere from n - m to n - 1.
+template <int TK, int TREE = kCausal>
 __device__ __forceinline__ ItemRange item_range(const AttnArgs& a, int item) {
   ItemRange x;
   const int TR = a.tr;
@@ -339,16 +341,17 @@ __device__ __forceinline__ int tree_bit(const uint32_t* mask, int m, int rank) {
   return w * 32 + __ffs(x) - 1;
 }
 // The node's position, behind the nodes that it sees (itself among them), which are at positions base, base + 1, ...
-// With tree_window the window hides the lowest of them: those before node `from`, but for first rows, those before
-// node `first` (both 0: none is hidden).
+// kWindowed: the window hides the lowest of them, those before node `from`, but for first rows, those before node
+// `first` (both 0: none is hidden).  (In one instance with kMasks this cost trees without it 0.2 us a call.)
 struct TreeRow {
   int p, from, first;
 };
+template <int TREE>
 __device__ __forceinline__ TreeRow tree_row(const AttnArgs& a, const uint32_t* mask, int m, int base) {
   int set = 0;
   for (int w = 0; w * 32 < m; ++w) set += __popc(tree_word(mask, m, w));
   TreeRow t{base + max(set, 1) - 1, 0, 0};
-  if (a.tree_window && a.window > 0 && set > a.window) {
+  if (TREE == kWindowed && set > a.window) {
     const int gone = set - a.window, stay = a.n_sink - base;
     t.from = tree_bit(mask, m, gone);
     if (stay >= gone)
@@ -359,9 +362,10 @@ __device__ __forceinline__ TreeRow tree_row(const AttnArgs& a, const uint32_t* m
   return t;
 }
 // whether the node sees cached row j (j < hi of its tile)
+template <int TREE>
 __device__ __forceinline__ bool tree_sees(const AttnArgs& a, const uint32_t* mask, const TreeRow& t, int base, int j) {
   const int u = j - base;
-  if (u >= 0) return (u >= t.from || u < t.first) && (__ldg(mask + (u >> 5)) >> (u & 31) & 1u);
+  if (u >= 0) return (TREE != kWindowed || u >= t.from || u < t.first) && (__ldg(mask + (u >> 5)) >> (u & 31) & 1u);
   return a.window <= 0 || j > t.p - a.window || j < a.n_sink;
 }
 // 64 bits of a mask of m nodes from bit `at` on (at > -64); bit i of the result: node at + i

@@ -75,7 +75,8 @@ int check_tree(const kvsel_attn_params* p) {
 // How the nodes of a tree go: in items of 16 rows by clusters of c CTAs (pl.cluster), each item of which reads the cache
 // again, from L2; up to 16 rows cut over the grid and joined (pl.few); in items of 128 rows or two such blocks, whole ones
 // to CTAs (pl.whole); or these cut over the grid and joined.  Up to 16 rows keep the softmax weights to 2^-16, as
-// kvsel_attend's do, and so never go to the tile kernel, which rounds them to bf16.  Otherwise the estimate, in tenths of a microsecond,
+// kvsel_attend's do, and so never go to the tile kernel, which rounds them to bf16 (384 segments of 8192 rows, 16 query rows:
+// 203 us, whole items 268; of 800 rows with that max_len 34 and 55).  Otherwise the estimate, in tenths of a microsecond,
 // follows what was measured (8 to 512 rows per segment, 1 to 128 segments of 128 to 4096 rows, pages of 16, masks included, us):
 //   clusters  6.3 and 0.97 per tile of 64 rows, 7.8 and 1.06 where CTAs share an SM: 32 items of 1024 rows by clusters of
 //             eight 10.0, of four 10.2, of two 14.6; 96 items by clusters of two 16.6; more clusters than fit at once lose
@@ -356,7 +357,7 @@ static int attend(const kvsel_attn_params* p, const void* q, const kvsel_kv* kv,
   }
   a.tree = tree;
   a.tree_words = (p->n_new + 31) / 32;
-  a.tree_window = p->tree_window;
+  a.tree_window = p->tree_window && p->window > 0 && p->window < p->n_new;
   a.by_rt = Div::by(pl.rt);
   a.by_H = Div::by(p->h_kv);
   a.by_G = Div::by(p->group);

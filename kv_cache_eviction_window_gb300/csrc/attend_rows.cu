@@ -81,8 +81,7 @@ __device__ __forceinline__ void mma16816(float c[4], const uint32_t a[4], uint32
 }
 
 // CLUSTER: an item's tiles are cut over the CTAs of a cluster instead, which join them.
-// TREE: the visibility of the new tokens' rows is in a.tree.
-template <bool CLUSTER, bool TREE>
+template <bool CLUSTER, int TREE>
 __global__ void __launch_bounds__(kThreads, 2) attend_rows_kernel(const AttnArgs a) {
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ float s_m[kWarps][kTR], s_l[kWarps][kTR];
@@ -161,7 +160,7 @@ __global__ void __launch_bounds__(kThreads, 2) attend_rows_kernel(const AttnArgs
       pos[u] = live ? (a.causal ? x.n - x.m + t : x.n - 1) : -1;
       if (TREE && live) {
         mask[u] = tree_mask(a, x.b, t);
-        node[u] = tree_row(a, mask[u], x.m, x.n - x.m);
+        node[u] = tree_row<TREE>(a, mask[u], x.m, x.n - x.m);
       }
       const uint16_t* src = a.q + x.b * a.q_req + static_cast<long long>(x.h * a.G + g) * a.q_head +
                             static_cast<long long>(t) * a.q_tok;
@@ -216,7 +215,7 @@ __global__ void __launch_bounds__(kThreads, 2) attend_rows_kernel(const AttnArgs
           if (!whole) {
             const int j = j0 + nt * 8 + ql * 2 + (i & 1);
             if (j >= j1 ||
-                !(TREE ? tree_sees(a, mask[i >> 1], node[i >> 1], x.n - x.m, j) : sees(a, pos[i >> 1], j)))
+                !(TREE ? tree_sees<TREE>(a, mask[i >> 1], node[i >> 1], x.n - x.m, j) : sees(a, pos[i >> 1], j)))
               y = -INFINITY;
           }
           p[nt][i] = y;
@@ -461,7 +460,7 @@ int clusters_at_once(int c) {
     const int n = known[dev][c].load(std::memory_order_relaxed);
     if (n) return n - 1;
   }
-  const void* kernel = reinterpret_cast<const void*>(attend_rows_kernel<true, false>);
+  const void* kernel = reinterpret_cast<const void*>(attend_rows_kernel<true, kCausal>);
   cudaLaunchAttribute attr[1];
   const cudaLaunchConfig_t cfg = cluster_config(c, c, nullptr, attr);
   int n = 0;
@@ -500,8 +499,9 @@ int attend_rows_cluster(long long items, long long tiles, bool window, int grid)
 }
 
 cudaError_t launch_attend_rows(const AttnArgs& a, int grid, int cluster, cudaStream_t st) {
-  const auto kernel = a.tree ? (cluster ? attend_rows_kernel<true, true> : attend_rows_kernel<false, true>)
-                             : (cluster ? attend_rows_kernel<true, false> : attend_rows_kernel<false, false>);
+  const auto kernel = !a.tree         ? (cluster ? attend_rows_kernel<true, kCausal> : attend_rows_kernel<false, kCausal>)
+                      : a.tree_window ? (cluster ? attend_rows_kernel<true, kWindowed> : attend_rows_kernel<false, kWindowed>)
+                                      : (cluster ? attend_rows_kernel<true, kMasks> : attend_rows_kernel<false, kMasks>);
   cudaError_t e = ensure_smem(reinterpret_cast<const void*>(kernel), kSmem);
   if (e != cudaSuccess) return e;
   if (cluster) {

@@ -149,7 +149,7 @@ __device__ __forceinline__ void load_pages(const AttnArgs& a, const CUtensorMap*
 // a stage, says where there is room: kvempty's phases pass for K's uses too, two of them look alike, and a warp that sees
 // every other use would take one for the other.  (It is never four V tiles of a ring ahead: the stage of the fourth needs
 // the first of them landed.)
-template <bool SPLIT, bool TREE, class Sh>
+template <bool SPLIT, int TREE, class Sh>
 __device__ __forceinline__ void load_values(const AttnArgs& a, const Sh& sh, const CUtensorMap* tv, uint8_t* sKV,
                                             uint64_t (&kvfull)[2][kStages], uint64_t (&vroom)[2][4], int* s_abort) {
   constexpr int kRows = SPLIT ? 64 : 128;
@@ -194,11 +194,10 @@ __device__ __forceinline__ void load_values(const AttnArgs& a, const Sh& sh, con
 
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// TREE: the visibility of the new tokens' rows is in a.tree
 // BOTH: small pages by two warps, 12 for K and 13 for V, with the table looked up two tiles ahead.  A box takes its warp
 // some 50 cycles beside its bytes.  8 segments of 8 requests of 2048 to 32768 rows, 32 nodes of 4 heads, pages of 16: one
 // warp for both, which looks a page up when it loads it, 150 us; two 125; V by 16-byte copies of three warps 136 to 264.
-template <bool SPLIT, bool TREE, bool BOTH>
+template <bool SPLIT, int TREE, bool BOTH>
 __global__ void __launch_bounds__(kThreads, 1)
     attend_tile_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                        const __grid_constant__ CUtensorMap tv, const AttnArgs a, const int block) {
@@ -461,7 +460,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int rr = x.rt * a.tr + first_row + row;  // row of the segment
       const int tree0 = x.n - x.m;                   // TREE: the first row of the tree
       const uint32_t* mask = TREE ? tree_mask(a, x.b, row < rows ? a.by_G(rr) : 0) : nullptr;
-      const int p = TREE ? tree_row(a, mask, x.m, tree0).p : a.causal ? x.n - x.m + a.by_G(rr) : x.n - 1;
+      const int p = TREE ? tree_row<TREE>(a, mask, x.m, tree0).p : a.causal ? x.n - x.m + a.by_G(rr) : x.n - 1;
       // cache rows of the block's first and last token (TREE: all see the rows up to pa; none is behind pb)
       const int pa = TREE ? tree0 - 1 : a.causal ? x.n - x.m + a.by_G(x.rt * a.tr + first_row) : x.n - 1;
       const int pb = TREE ? x.p1 : a.causal ? x.n - x.m + a.by_G(x.rt * a.tr + first_row + max(rows, 1) - 1) : x.n - 1;
@@ -491,8 +490,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int lo = a.window > 0 ? p - a.window + 1 - js : 0, first = a.window > 0 ? a.n_sink - js : 0;
           uint64_t see = (low_bits(hi) & ~(low_bits(lo) & ~low_bits(first))) |
                          (js + 64 > tree0 ? tree_bits(mask, x.m, js - tree0) & low_bits(j1 - js) : 0);
-          if (a.tree_window && js + 64 > tree0) {    // (worked out again: two numbers kept for it cost all steps 1%)
-            const TreeRow node = tree_row(a, mask, x.m, tree0);
+          if (TREE == kWindowed && js + 64 > tree0) {   // (worked out again: two numbers kept for it cost all steps 1%)
+            const TreeRow node = tree_row<TREE>(a, mask, x.m, tree0);
             see &= ~(low_bits(node.from - (js - tree0)) & ~low_bits(node.first - (js - tree0))) | low_bits(tree0 - js);
           }
           const uint32_t see0 = static_cast<uint32_t>(see), see1 = static_cast<uint32_t>(see >> 32);
@@ -745,11 +744,17 @@ bool attend_tile_whole(long long items, long long tiles, bool split, int grid) {
 // warp, 115).
 static bool attend_tile_both(const AttnArgs& a) { return a.src.paged && a.src.block_size < 64; }
 
+template <int TREE>
+static auto tree_kernel(bool split, bool both) {
+  return both ? (split ? attend_tile_kernel<true, TREE, true> : attend_tile_kernel<false, TREE, true>)
+              : (split ? attend_tile_kernel<true, TREE, false> : attend_tile_kernel<false, TREE, false>);
+}
+
 cudaError_t launch_attend_tile(const AttnArgs& a, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                                int block, bool split, int grid, cudaStream_t st) {
-  const auto kernel = !a.tree ? (split ? attend_tile_kernel<true, false, false> : attend_tile_kernel<false, false, false>)
-                      : attend_tile_both(a) ? (split ? attend_tile_kernel<true, true, true> : attend_tile_kernel<false, true, true>)
-                                            : (split ? attend_tile_kernel<true, true, false> : attend_tile_kernel<false, true, false>);
+  const auto kernel = !a.tree         ? (split ? attend_tile_kernel<true, kCausal, false> : attend_tile_kernel<false, kCausal, false>)
+                      : a.tree_window ? tree_kernel<kWindowed>(split, attend_tile_both(a))
+                                      : tree_kernel<kMasks>(split, attend_tile_both(a));
   cudaError_t e = ensure_smem(reinterpret_cast<const void*>(kernel), kSmem);
   if (e != cudaSuccess) return e;
   kernel<<<a.whole ? a.B * a.H * a.rt : grid, kThreads, kSmem, st>>>(tq, tk, tv, a, block);
