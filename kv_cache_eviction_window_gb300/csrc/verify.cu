@@ -64,6 +64,7 @@ __global__ void __launch_bounds__(1024) tree_masks_kernel(const int32_t* __restr
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kMaxCluster = 16;
 constexpr long long kLandCycles = 1 << 17;           // after a wait that ran out: far longer than a remote store takes
+constexpr unsigned long long kNapCycles = 1 << 16;   // shorter limits are not left to a wait of the hardware's own
 constexpr int kUnitBits = 45;                        // probabilities in units of 2^-45
 constexpr unsigned long long kOne = 1ull << kUnitBits;
 
@@ -565,14 +566,16 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a)
         if (lane < cs) send(&s.part[side][mine], v, &s.came[side], lane);
         if (want == kDraw || warp == 0) {
           const uint32_t parity = pass >> 1 & 1;
-          bool have = came<true>(&s.came[side], parity);
+          const bool brief = a.wait_cycles < kNapCycles;
+          auto here = [&] { return brief ? came<true>(&s.came[side], parity) : came<false>(&s.came[side], parity); };
+          bool have = here();
           const long long t0 = clock64();
           while (!have && !*static_cast<volatile int*>(&s.lost)) {
             if (static_cast<unsigned long long>(clock64() - t0) > a.wait_cycles) {
               s.lost = 1;
               atomicOr(a.status, DEV_TIMEOUT_PIPE);
             } else {
-              have = came<false>(&s.came[side], parity);
+              have = here();
             }
           }
           lost = __any_sync(0xffffffffu, !have);
