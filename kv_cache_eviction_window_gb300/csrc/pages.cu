@@ -111,18 +111,14 @@ __device__ __forceinline__ int block_scan(int v, int* s_w, int& total) {
   return v;
 }
 
-// Entry u of those that the new rows of a request touch (rows [lo, end) are written to), or -1: none.  A request that is
-// not served touches none, whatever its lengths are: a negative one would lead to words before the table.
-// (Of one that is, lo is at most 2^26, the rows of a table's row, and u at most 2^17: 32 bits will do.)
-__host__ __device__ constexpr int touched_entry(bool ok, int lo, int end, int u, int shift) {
-  const int i = (ok ? lo >> shift : 0) + u;
-  return ok && i << shift < end ? i : -1;
-}
-static_assert(touched_entry(true, 0, 1, 0, 3) == 0 && touched_entry(true, 17, 18, 0, 4) == 1 && touched_entry(true, 17, 33, 1, 4) == 2);
-static_assert(touched_entry(true, 17, 32, 1, 4) < 0 && touched_entry(true, 16, 0, 0, 4) < 0);
-static_assert(touched_entry(false, -1, 0, 0, 3) < 0 && touched_entry(false, -0x7FFFFFFF - 1, 0, 0, 3) < 0);
-static_assert(touched_entry(false, -1, 0, 1, 6) < 0 && touched_entry(false, -9, 5, 0, 3) < 0);
-static_assert(touched_entry(true, 1 << 26, 1 << 26, 1 << 17, 6) < 0 && touched_entry(true, (1 << 26) - 1, 1 << 26, 0, 6) == (1 << 20) - 1);
+// The first entry that the new rows of a request touch (rows [lo, end) are written to), and whether entry i is one.  A request
+// that is not served touches none (end = 0) whatever its lengths are: a negative one would lead to words before the table,
+// one near 2^31 to numbers that pass 32 bits.  (Where the entry is looked up does not wait for whether it is served.)
+__host__ __device__ constexpr int first_entry(int lo, int shift) { return (lo > 0 ? lo : 0) >> shift; }
+__host__ __device__ constexpr bool touched(int i, int end, int shift) { return static_cast<long long>(i) << shift < end; }
+static_assert(first_entry(17, 4) == 1 && touched(1, 18, 4) && touched(2, 33, 4) && !touched(2, 32, 4) && touched(0, 1, 3));
+static_assert(first_entry(-1, 3) == 0 && first_entry(-0x7FFFFFFF - 1, 6) == 0 && !touched(0, 0, 3) && !touched(1, 0, 6));
+static_assert(!touched(first_entry(0x7FFFFFFF, 3), 0, 3) && !touched(first_entry(0x7FFFFFFF, 6) + (1 << 17) + 1, 0, 6));
 
 struct Reserve {
   int lo, end, page0, m;          // first and last row that are written, the first's entry; new rows
@@ -135,7 +131,7 @@ __device__ __forceinline__ Reserve reserve_of(const PagesArgs& a, int b) {
   r.m = min(max(raw, 0), a.m);
   r.ok = rows_of(a, a.lens, b, r.lo, hi) && raw == r.m &&
          static_cast<long long>(hi) + r.m <= static_cast<long long>(a.max_blocks) << a.shift;
-  r.page0 = r.ok ? r.lo >> a.shift : 0;
+  r.page0 = first_entry(r.lo, a.shift);
   r.end = r.ok ? hi + r.m : 0;
   // heads so far apart that their entries do not fit the plan
   if (r.ok && r.m > 0 && ((r.end - 1) >> a.shift) - r.page0 >= a.per) {
@@ -203,9 +199,9 @@ __device__ __forceinline__ int plan_pages(const PagesArgs& a, PlanShared& s, int
     const int b = it / a.per, u = it - b * a.per;
     range(b);
     int n = kNothing;
-    const int i = touched_entry(r.ok, r.lo, r.end, u, a.shift);
+    const int i = r.page0 + u;
     if (!r.ok && u == 0) atomicOr(&s.bad[b >> 5], 1u << (b & 31));
-    if (i >= 0) {
+    if (touched(i, r.end, a.shift)) {
       const int page = a.table[static_cast<long long>(b) * a.max_blocks + i];
       if (page == -1) {
         n = kPage;
@@ -224,49 +220,57 @@ __device__ __forceinline__ int plan_pages(const PagesArgs& a, PlanShared& s, int
     // Of the requests that write to a shared page the last keeps it where no other uses it: as many of them before it
     // as the page has other uses (requests that are not served for what their entries hold do not count).  `list`, in
     // order of entries: their pages, or the places that count them (-1: of a request that is not served).
-    int slots = 64;
-    if (!SMALL) {
-      while (slots < 2 * sharers) slots *= 2;
-      for (int i = tid; i < 3 * slots; i += kThreads) a.seats[i] = i < 2 * slots ? -1 : 0;
-      __syncthreads();
-    }
-    // of a place: the page, the last entry that writes to it, and the number of those
-    int32_t *key = a.seats, *last = a.seats + slots, *writers = a.seats + 2 * slots;
-    int k = at;
-    for (int it = i0; it < i1; ++it) {
-      if (need[it] != kCopy) continue;
+    auto page_at = [&](int it) {
       const int b = it / a.per;
-      int y = s.has(s.bad, b) ? -1 : a.table[static_cast<long long>(b) * a.max_blocks + range(b).page0 + it % a.per];
-      if (!SMALL && y >= 0) {
-        const int page = y;
-        y = static_cast<int>(static_cast<unsigned>(page) * 2654435769u) & (slots - 1);   // 2^32 / golden ratio
-        while (true) {                               // (half of the places stay empty)
-          const int other = atomicCAS(key + y, -1, page);
-          if (other == -1 || other == page) break;
-          y = (y + 1) & (slots - 1);
-        }
-        atomicMax(last + y, it);
-        atomicAdd(writers + y, 1);
-      }
-      list[k++] = y;
-    }
-    __syncthreads();
-    for (int it = i0; it < i1; ++it) {
-      if (need[it] != kCopy) continue;
-      const int y = list[at];
-      bool keeps = y >= 0;
-      if (SMALL && keeps) {
-        int before = 0;
-#pragma unroll 8
-        for (int c = 0; c < at; ++c) before += list[c] == y;
-        keeps = before >= a.ref[y] - 1;
-      } else if (keeps) {
-        keeps = __ldcg(last + y) == it && __ldcg(writers + y) >= a.ref[__ldcg(key + y)];
-      }
-      ++at;
-      if (!keeps) continue;
+      return s.has(s.bad, b) ? -1 : a.table[static_cast<long long>(b) * a.max_blocks + range(b).page0 + it % a.per];
+    };
+    auto keep = [&](int it) {
       need[it] = kKeep;
       atomicOr(&s.keeps[it / a.per >> 5], 1u << (it / a.per & 31));
+    };
+    if constexpr (SMALL) {
+      for (int it = i0, k = at; it < i1; ++it)
+        if (need[it] == kCopy) list[k++] = page_at(it);
+      __syncthreads();
+      for (int it = i0; it < i1; ++it) {
+        if (need[it] != kCopy) continue;
+        const int page = list[at];
+        int before = 0;
+#pragma unroll 8
+        for (int c = 0; c < at; ++c) before += list[c] == page;
+        ++at;
+        if (page >= 0 && before >= a.ref[page] - 1) keep(it);
+      }
+    } else {
+      int log = 6;
+      while (1 << log < 2 * sharers) ++log;
+      const int slots = 1 << log;
+      // of a place: the page, the last entry that writes to it, and the number of those
+      int32_t *key = a.seats, *last = a.seats + slots, *writers = a.seats + 2 * slots;
+      for (int i = tid; i < 3 * slots; i += kThreads) a.seats[i] = i < 2 * slots ? -1 : 0;
+      __syncthreads();
+      for (int it = i0, k = at; it < i1; ++it) {
+        if (need[it] != kCopy) continue;
+        const int page = page_at(it);
+        int y = -1;
+        if (page >= 0) {
+          y = static_cast<int>(static_cast<unsigned>(page) * 2654435769u >> (32 - log));   // (2^32 by the golden ratio)
+          while (true) {                             // (half of the places stay empty)
+            const int other = atomicCAS(key + y, -1, page);
+            if (other == -1 || other == page) break;
+            y = (y + 1) & (slots - 1);
+          }
+          atomicMax(last + y, it);
+          atomicAdd(writers + y, 1);
+        }
+        list[k++] = y;
+      }
+      __syncthreads();
+      for (int it = i0; it < i1; ++it) {
+        if (need[it] != kCopy) continue;
+        const int y = list[at++];
+        if (y >= 0 && __ldcg(last + y) == it && __ldcg(writers + y) >= a.ref[__ldcg(key + y)]) keep(it);
+      }
     }
   }
   __syncthreads();
