@@ -460,7 +460,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int rr = x.rt * a.tr + first_row + row;  // row of the segment
       const int tree0 = x.n - x.m;                   // TREE: the first row of the tree
       const uint32_t* mask = TREE ? tree_mask(a, x.b, row < rows ? a.by_G(rr) : 0) : nullptr;
-      const int p = TREE ? tree_row<TREE>(a, mask, x.m, tree0).p : a.causal ? x.n - x.m + a.by_G(rr) : x.n - 1;
+      const TreeRow node = TREE ? tree_row<TREE>(a, mask, x.m, tree0) : TreeRow{};
+      const int p = TREE ? node.p : a.causal ? x.n - x.m + a.by_G(rr) : x.n - 1;
       // cache rows of the block's first and last token (TREE: all see the rows up to pa; none is behind pb)
       const int pa = TREE ? tree0 - 1 : a.causal ? x.n - x.m + a.by_G(x.rt * a.tr + first_row) : x.n - 1;
       const int pb = TREE ? x.p1 : a.causal ? x.n - x.m + a.by_G(x.rt * a.tr + first_row + max(rows, 1) - 1) : x.n - 1;
@@ -490,10 +491,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int lo = a.window > 0 ? p - a.window + 1 - js : 0, first = a.window > 0 ? a.n_sink - js : 0;
           uint64_t see = (low_bits(hi) & ~(low_bits(lo) & ~low_bits(first))) |
                          (js + 64 > tree0 ? tree_bits(mask, x.m, js - tree0) & low_bits(j1 - js) : 0);
-          if (TREE == kWindowed && js + 64 > tree0) {   // (worked out again: two numbers kept for it cost all steps 1%)
-            const TreeRow node = tree_row<TREE>(a, mask, x.m, tree0);
+          if (TREE == kWindowed)                     // (columns before the tree are not among those)
             see &= ~(low_bits(node.from - (js - tree0)) & ~low_bits(node.first - (js - tree0))) | low_bits(tree0 - js);
-          }
           const uint32_t see0 = static_cast<uint32_t>(see), see1 = static_cast<uint32_t>(see >> 32);
 #pragma unroll
           for (int c = 0; c < 64; ++c)
