@@ -6,7 +6,7 @@
 //
 // A thread turns eight pairs (32 bytes of a row) by the same sines for all heads of a token that fall
 // to it; cached keys have a position each.  Bound: HBM, a row read and written.  Measured: 8192 tokens of 32 + 8 heads
-// 27.5 us for 168 MB (24.7 at the copy rate); 32 segments of 13107 cached keys 42 us for 216 MB (31.9), of which the
+// 27.8 us for 168 MB (24.7 at the copy rate); 32 segments of 13107 cached keys 42 us for 216 MB (31.9), of which the
 // launch, the first places and the last stores are some 5; half the columns turned take as long.
 #include <algorithm>
 

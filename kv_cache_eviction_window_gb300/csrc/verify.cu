@@ -15,8 +15,8 @@
 // loads 1, the numbers to all CTAs of the cluster (which a barrier there counts; a barrier of the cluster took 0.35 longer)
 // and the walk.  A round is made for each rejection that a sibling follows, unless the sibling passes with the mass before,
 // and one for the last draw; GREEDY makes one per accepted node.  Measured on one GB300: 32 chains of five drafted tokens
-// over 50257 tokens, fp32, 9.9 us; 8 trees of 64 nodes over 131072, bf16, 13 to 28 us by what is rejected; 32 requests of
-// 26 nodes, GREEDY, 14.4 us; 512 requests of one node, bf16, 87 us for 134 MB (the sums' instructions).  (512 threads per
+// over 50257 tokens, fp32, 10.0 us; 8 trees of 64 nodes over 131072, bf16, 13 to 28 us by what is rejected; 32 requests of
+// 26 nodes, GREEDY, 14.6 us; 512 requests of one node, bf16, 87 us for 134 MB (the sums' instructions).  (512 threads per
 // CTA: a tenth to a quarter less for hundreds of requests, 1 to 5 us more for small vocabularies.)
 #include <cooperative_groups.h>
 
